@@ -1,0 +1,750 @@
+// Attention of a step's tokens over the dense paged cache (v4a_dense.h,
+// v4a_dense_attn): the form for few query rows per KV head (decode, short
+// chunks), which any shape may take.
+//
+// Mathematics: one pass over the keys with a running maximum m and sum l per
+// row; o = sum_j 2^{z_j - m} v_j is rescaled when m grows.  Scores are formed
+// transposed, S^T = K Q^T, so that the 16 rows of an mma.m16n8k16 are keys and
+// its 8 columns are query rows (the heads of a KV head's group, times tokens):
+// a group of up to 8 heads wastes nothing.  O^T = V^T P^T uses the same
+// columns, so the softmax factors of a column sit in the threads that hold the
+// column's accumulators.
+//
+// Bound: memory.  A KV head reads 2 dim elements per position for
+// 4 dim flops per query row, so with up to 16 rows the warp-level MMA (which
+// takes 8-column operands; tcgen05 needs 128 rows) is far from its rate and
+// the cache's bytes set the time.
+//
+// Layout: a CTA has one copying warp and four computing warps over a ring of
+// tiles of 64 positions (keys and values, TMA boxes in the 128-byte swizzle;
+// 64 divides the 256-position block, so a tile never crosses a page).
+// Computing warp w takes tiles w, w + 4, ... of the CTA's range with its own
+// m, l and o; the four are merged through shared memory when the range leaves
+// a (sequence, KV head, row group).  The tiles of all sequences and KV heads
+// form one line that the CTAs divide evenly, so ragged lengths balance and one
+// long sequence fills the machine; pieces of a unit that several CTAs hold go
+// to the workspace and are joined by a second kernel in CTA order.
+#include "dense_attn_common.cuh"
+
+namespace v4a {
+namespace {
+
+constexpr int kTile = 64;            // positions per tile
+constexpr int kWarps = 4;            // computing warps
+constexpr int kThreads = 32 * (kWarps + 1);
+constexpr int kMaxUnits = 1024;      // (sequence, row group) units that are split evenly
+constexpr int kRingBytes = 160 * 1024;
+constexpr int kCtas = 152;           // CTAs of an even split: one per SM
+
+struct JoinDesc { int valid, b, rg, hk, last, pad[3]; };
+
+struct MmaDev {
+  DenseAttnDev a;
+  int RG, U, split;                  // row groups per sequence, units, even split (else one CTA per unit and KV head)
+  float *part_o, *part_ml;           // [CTA][2][rows][D], [CTA][2][rows][2] (max in log2 units, sum)
+  JoinDesc* join;                    // [CTA]
+};
+
+template <int D, int NT, bool kFp8>
+struct Shape {
+  static constexpr int R = 8 * NT;
+  static constexpr int kElem = kFp8 ? 1 : 2;
+  static constexpr int kBox = kFp8 ? (D % 128 == 0 ? 128 : 64) : 64;     // elements of a box row
+  static constexpr int kBoxBytes = kBox * kElem;
+  static constexpr int kBoxes = D / kBox;
+  static constexpr int kTileBytes = kTile * D * kElem;                   // keys or values of a tile
+  static constexpr int kStage = 2 * kTileBytes;
+  static constexpr int kStages = kRingBytes / kStage < 16 ? kRingBytes / kStage : 16;
+  static constexpr int kPad = D + 4;                                     // merge rows: conflict-free columns
+  struct Tail {                                                          // behind the ring
+    uint64_t full[kStages], empty[kStages];
+    int skip[kStages];
+    int abort_flag;
+    int64_t total;
+    alignas(16) float scale[kStages][2][kFp8 ? kTile : 1];
+    float ml[kWarps][R][2];
+    alignas(16) float o[kWarps][R][kPad];
+    int64_t scan[kWarps + 1];
+  };
+};
+
+__device__ __forceinline__ void ldsm(uint32_t addr, uint32_t* r) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm_t(uint32_t addr, uint32_t* r) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+__device__ __forceinline__ void mma16816(float* c, const uint32_t* a, const uint32_t* b) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+// Codes b0 and b2 (or b1 and b3) of w as a bf16 pair times 2^-120 (sign to bit
+// 15, the 7 magnitude bits to bits 4..10: the code's value with the exponent
+// biased by 127 instead of 7), then times 2^120, exactly; subnormal codes too.
+__device__ __forceinline__ uint32_t e4m3_pair(uint32_t shifted) {      // codes in bits 8..15 and 24..31
+  const uint32_t m = ((shifted >> 4) & 0x07F007F0u) | (shifted & 0x80008000u);
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(m), "r"(0x7B807B80u));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&b);
+}
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, int c0, int c1, int c2, int c3, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(tc::smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(tc::smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ void compute_sync() {
+  __syncwarp();
+  asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory");
+}
+// compute_sync that also gives every computing thread whether all of them passed true.
+__device__ __forceinline__ bool compute_sync_and(bool ok) {
+  uint32_t r;
+  __syncwarp();
+  asm volatile(
+      "{\n.reg .pred p, q;\nsetp.ne.u32 p, %1, 0;\nbar.red.and.pred q, 1, %2, p;\nselp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(r) : "r"(uint32_t(ok)), "n"(32 * kWarps) : "memory");
+  return r != 0;
+}
+
+// A row group of one sequence: rows [row0, row0 + rows) of its tokens x group heads.
+struct Unit { int b, row0, rows, s0, m_lo, m_hi; TileRange<kTile> tr; };
+
+template <int R>
+__device__ __forceinline__ Unit make_unit(const DenseAttnDev& a, int b, int rg, const SeqRun& s) {
+  Unit u;
+  u.b = b;
+  u.row0 = rg * R;
+  u.rows = min(R, s.n * a.G - u.row0);
+  u.s0 = s.s0;
+  u.m_lo = u.m_hi = 0;
+  u.tr = TileRange<kTile>{0, 0, 0};
+  if (u.rows <= 0) return u;
+  u.m_lo = s.p0 + u.row0 / a.G;
+  u.m_hi = s.p0 + (u.row0 + u.rows - 1) / a.G;
+  u.tr = tile_range<kTile>(a, u.m_lo, u.m_hi);
+  return u;
+}
+
+// Where a CTA's tile x lies.
+struct Piece { int u, hk, tile; };
+
+template <int D, int NT, bool kFp8>
+__global__ void __launch_bounds__(kThreads, 1) dense_attn_mma(const MmaDev p, const __grid_constant__ CUtensorMap map) {
+  using S = Shape<D, NT, kFp8>;
+  constexpr int R = S::R;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  typename S::Tail& s = *reinterpret_cast<typename S::Tail*>(ring + S::kStages * S::kStage);
+  int64_t* pre = reinterpret_cast<int64_t*>(&s + 1);         // split: [U + 1] tiles before unit u, over its KV heads
+  SeqRun* runs = reinterpret_cast<SeqRun*>(pre + (p.split ? p.U + 1 : 0));   // [B], or one
+  const DenseAttnDev& a = p.a;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  volatile int* abort_flag = &s.abort_flag;
+
+  pdl_trigger();
+  if (tid == 0) {
+    for (int i = 0; i < S::kStages; ++i) {
+      tc::mbar_init(&s.full[i], 1);
+      tc::mbar_init(&s.empty[i], 1);
+    }
+    s.abort_flag = 0;
+    tc::mbar_fence_init();
+    tc::prefetch_tmap(&map);
+  }
+  pdl_wait();
+
+  // ---- the CTA's tiles [x0, x1) ----
+  int64_t x0, x1;
+  int u_direct = 0, hk_direct = 0, ctas = 0;
+  if (p.split) {
+    int32_t* st = blockIdx.x == 0 ? a.status : nullptr;     // one CTA reports the batch's faults
+    for (int b = tid; b < a.B; b += kThreads) runs[b] = seq_run(a, b, st);
+    __syncthreads();
+    // exclusive sums over the units: each thread a run of units, then the threads' totals
+    const int per = (p.U + kThreads - 1) / kThreads, u0 = tid * per, u1 = min(p.U, u0 + per);
+    int64_t sum = 0;
+    for (int u = u0; u < u1; ++u) {
+      pre[u] = sum;
+      sum += int64_t(make_unit<R>(a, u / p.RG, u % p.RG, runs[u / p.RG]).tr.tiles) * a.K;
+    }
+    int64_t v = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t w = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += w;
+    }
+    if (lane == 31) s.scan[warp] = v;
+    __syncthreads();
+    int64_t before = v - sum, total = 0;
+#pragma unroll
+    for (int w = 0; w <= kWarps; ++w) {
+      if (w < warp) before += s.scan[w];
+      total += s.scan[w];
+    }
+    for (int u = u0; u < u1; ++u) pre[u] += before;
+    if (tid == 0) { pre[p.U] = total; s.total = total; }
+    __syncthreads();
+    ctas = int(min(int64_t(gridDim.x), total));
+    if (int(blockIdx.x) >= ctas) {
+      if (tid == 0) p.join[blockIdx.x].valid = 0;
+      return;
+    }
+    x0 = blockIdx.x * total / ctas;
+    x1 = (blockIdx.x + 1) * total / ctas;
+  } else {
+    const int64_t c = blockIdx.x;
+    u_direct = int(c / a.K);
+    hk_direct = int(c % a.K);
+    if (tid == 0) runs[0] = seq_run(a, u_direct / p.RG, hk_direct == 0 && u_direct % p.RG == 0 ? a.status : nullptr);
+    __syncthreads();
+    x0 = 0;
+    x1 = make_unit<R>(a, u_direct / p.RG, u_direct % p.RG, runs[0]).tr.tiles;
+    if (x1 == 0) return;
+  }
+  auto unit_at = [&](int u) { return make_unit<R>(a, u / p.RG, u % p.RG, runs[p.split ? u / p.RG : 0]); };
+  auto locate = [&](int64_t x, Unit* un) {
+    if (!p.split) {
+      *un = unit_at(u_direct);
+      return Piece{u_direct, hk_direct, int(x)};
+    }
+    int lo = 0, hi = p.U;                       // largest u with pre[u] <= x (empty units precede)
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (pre[mid] <= x) lo = mid; else hi = mid;
+    }
+    *un = unit_at(lo);
+    const int64_t rem = x - pre[lo];
+    const int hk = int(rem / un->tr.tiles);
+    return Piece{lo, hk, int(rem - int64_t(hk) * un->tr.tiles)};
+  };
+
+  if (warp == kWarps) {
+    // ---- the copying warp: 32 tiles' pages are looked up at once, one lane each ----
+    auto page_of = [&](int64_t x, Piece* pc, int* row) {
+      if (x >= x1) return -1;
+      Unit un;
+      *pc = locate(x, &un);
+      const int kt = un.tr.at(pc->tile);
+      *row = kt % (kBlockPositions / kTile) * kTile;
+      const int32_t page = a.bt[int64_t(un.b) * a.max_blocks + kt / (kBlockPositions / kTile)];
+      if (page >= 0 && page < a.num_blocks) return int(page);
+      report(a.status, V4A_DEV_BAD_BLOCK);
+      return -1;
+    };
+    Piece pc{}, npc{};
+    int row = 0, nrow = 0, npage;
+    int page = page_of(x0 + lane, &pc, &row);
+    int stage = 0, use = 0;
+    bool ok = true;
+    int64_t issued = 0;
+    for (int64_t base = x0; base < x1 && ok; base += 32) {
+      npage = page_of(base + 32 + lane, &npc, &nrow);
+      const int n = int(min(int64_t(32), x1 - base));
+      for (int i = 0; i < n; ++i) {
+        if (lane == i) {
+          ok = tc::mbar_wait(&s.empty[stage], (use & 1) ^ 1, a.status, abort_flag);
+          if (ok && page < 0) {
+            s.skip[stage] = 1;
+            tc::mbar_arrive(&s.full[stage]);
+          } else if (ok) {
+            s.skip[stage] = 0;
+            uint8_t* dst = ring + stage * S::kStage;
+            tc::mbar_arrive_expect_tx(&s.full[stage], S::kStage + (kFp8 ? 2 * kTile * 4 : 0));
+#pragma unroll
+            for (int x = 0; x < S::kBoxes; ++x) {
+              tma_load_4d(dst + x * kTile * S::kBoxBytes, &map, x * S::kBox, row, pc.hk, page, &s.full[stage]);
+              tma_load_4d(dst + S::kTileBytes + x * kTile * S::kBoxBytes, &map, x * S::kBox, row, a.K + pc.hk, page, &s.full[stage]);
+            }
+            if (kFp8) {
+              const uint8_t* sc = a.pool + int64_t(page) * a.block_bytes + int64_t(2 * a.K) * kBlockPositions * D;
+              tc::bulk_load(s.scale[stage][0], sc + (int64_t(pc.hk) * kBlockPositions + row) * 4, kTile * 4, &s.full[stage]);
+              tc::bulk_load(s.scale[stage][1], sc + (int64_t(a.K + pc.hk) * kBlockPositions + row) * 4, kTile * 4, &s.full[stage]);
+            }
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, ok, i);
+        if (!ok) break;
+        ++issued;
+        if (++stage == S::kStages) { stage = 0; ++use; }
+      }
+      page = npage; pc = npc; row = nrow;
+    }
+    // after a timeout the copies in flight still land before the CTA ends
+    if (!ok && lane == 0)
+      for (int64_t i = max(int64_t(0), issued - S::kStages); i < issued; ++i)
+        tc::mbar_wait(&s.full[i % S::kStages], uint32_t(i / S::kStages) & 1, a.status, abort_flag);
+    return;
+  }
+
+  // ---- the computing warps ----
+  JoinDesc desc{};
+  const float f = a.scale_log2;
+  const uint32_t ring0 = tc::smem_u32(ring);
+  const int g4 = lane >> 2, c2 = (lane & 3) * 2;
+  int64_t x = x0;
+  bool ok = true;
+  while (x < x1 && ok) {
+    Unit un;
+    const Piece pc = locate(x, &un);
+    const int count = int(min(int64_t(un.tr.tiles - pc.tile), x1 - x));     // tiles of this segment
+    // the query rows as B operands: column g4 of n-tile nt, dims of step ks
+    uint32_t qf[D / 16][NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int r = nt * 8 + g4;
+      const bool live = r < un.rows;
+      const int tok = un.s0 + (un.row0 + r) / a.G, head = pc.hk * a.G + (un.row0 + r) % a.G;
+      const uint16_t* q = a.q + (int64_t(tok) * a.H + head) * D;
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks) {
+        if (kFp8) {           // fp8: a thread's four codes are dims 4 (lane % 4) .. + 3 of the step
+          const uint2 w = live ? *reinterpret_cast<const uint2*>(q + ks * 16 + 2 * c2) : make_uint2(0, 0);
+          qf[ks][nt][0] = w.x;
+          qf[ks][nt][1] = w.y;
+        } else {
+          qf[ks][nt][0] = live ? *reinterpret_cast<const uint32_t*>(q + ks * 16 + c2) : 0;
+          qf[ks][nt][1] = live ? *reinterpret_cast<const uint32_t*>(q + ks * 16 + 8 + c2) : 0;
+        }
+      }
+    }
+    float o[D / 16][NT][4], m[NT][2], l[NT][2];
+    int mrow[NT][2];                               // the columns' query positions
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        m[nt][e] = -INFINITY;
+        l[nt][e] = 0.f;
+        mrow[nt][e] = un.m_lo + ((un.row0 % a.G) + min(nt * 8 + c2 + e, un.rows - 1)) / a.G;
+      }
+#pragma unroll
+      for (int d = 0; d < D / 16; ++d)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[d][nt][e] = 0.f;
+    }
+
+    // this warp's tiles: CTA tile numbers that are warp modulo kWarps
+    const int done = int(x - x0);
+    for (int i = (warp - done % kWarps + kWarps) % kWarps; i < count; i += kWarps) {
+      const int n = done + i, stage = n % S::kStages;
+      ok = __all_sync(0xffffffffu, tc::mbar_wait(&s.full[stage], uint32_t(n / S::kStages) & 1, a.status, abort_flag));
+      if (!ok) break;
+      if (s.skip[stage]) {
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&s.empty[stage]);
+        continue;
+      }
+      const uint32_t kb = ring0 + stage * S::kStage, vb = kb + S::kTileBytes;
+      const int j0 = un.tr.at(pc.tile + i) * kTile;
+      float z[4][NT][4];
+#pragma unroll
+      for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) z[mt][nt][e] = 0.f;
+      // S^T = K Q^T
+      if constexpr (!kFp8) {
+        const int lr = (lane & 7) + ((lane >> 3) & 1) * 8;
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          const int ch = (ks & 3) * 2 + (lane >> 4);
+          const uint32_t at = kb + (ks >> 2) * (kTile * 128) + lr * 128 + ((ch ^ (lr & 7)) << 4);
+#pragma unroll
+          for (int mt = 0; mt < 4; ++mt) {
+            uint32_t k[4];
+            ldsm(at + mt * 16 * 128, k);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma16816(z[mt][nt], k, qf[ks][nt]);
+          }
+        }
+      } else {
+        // matrices: keys 0-7 and 8-15 of 16-code chunk 2c, then of chunk 2c + 1
+        const int lr = (lane & 7) + ((lane >> 3) & 1) * 8;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          const int byte = c * 32 + (lane >> 4) * 16, ch = byte % S::kBoxBytes / 16;
+          const int sw = S::kBoxBytes == 128 ? ch ^ (lr & 7) : ch ^ ((lr >> 1) & 3);
+          const uint32_t at = kb + byte / S::kBoxBytes * (kTile * S::kBoxBytes) + lr * S::kBoxBytes + (sw << 4);
+#pragma unroll
+          for (int mt = 0; mt < 4; ++mt) {
+            uint32_t w[4];
+            ldsm(at + mt * 16 * S::kBoxBytes, w);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t lo = w[2 * h], hi = w[2 * h + 1];
+              const uint32_t k[4] = {e4m3_pair(__byte_perm(lo, 0, 0x1404)), e4m3_pair(__byte_perm(hi, 0, 0x1404)),
+                                     e4m3_pair(__byte_perm(lo, 0, 0x3424)), e4m3_pair(__byte_perm(hi, 0, 0x3424))};
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) mma16816(z[mt][nt], k, qf[2 * c + h][nt]);
+            }
+          }
+        }
+#pragma unroll
+        for (int mt = 0; mt < 4; ++mt) {
+          const float k0 = s.scale[stage][0][mt * 16 + g4], k1 = s.scale[stage][0][mt * 16 + g4 + 8];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            z[mt][nt][0] *= k0; z[mt][nt][1] *= k0;
+            z[mt][nt][2] *= k1; z[mt][nt][3] *= k1;
+          }
+        }
+      }
+      // mask, running maximum
+      const bool full = all_visible(a, un.m_lo, un.m_hi, j0, kTile);
+      if (!full) {
+#pragma unroll
+        for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (!visible(a, mrow[nt][e & 1], j0 + mt * 16 + g4 + (e >> 1) * 8)) z[mt][nt][e] = -INFINITY;
+      }
+      bool grew = false;
+      float alpha[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float t = fmaxf(z[0][nt][e], z[0][nt][e + 2]);
+#pragma unroll
+          for (int mt = 1; mt < 4; ++mt) t = fmaxf(t, fmaxf(z[mt][nt][e], z[mt][nt][e + 2]));
+          t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
+          t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
+          t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
+          const float top = fmaxf(m[nt][e], t);
+          grew |= top > m[nt][e];
+          alpha[nt][e] = top == -INFINITY ? 1.f : exp2f((m[nt][e] - top) * f);
+          m[nt][e] = top;
+        }
+      if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          l[nt][0] *= alpha[nt][0];
+          l[nt][1] *= alpha[nt][1];
+#pragma unroll
+          for (int d = 0; d < D / 16; ++d) {
+            o[d][nt][0] *= alpha[nt][0]; o[d][nt][1] *= alpha[nt][1];
+            o[d][nt][2] *= alpha[nt][0]; o[d][nt][3] *= alpha[nt][1];
+          }
+        }
+      }
+      // P^T as B operands: keys are rows of the k step
+      uint32_t pf[4][NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const float b0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0] * f, b1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1] * f;
+#pragma unroll
+        for (int mt = 0; mt < 4; ++mt) {
+          float p0 = exp2f(fmaf(z[mt][nt][0], f, -b0)), p1 = exp2f(fmaf(z[mt][nt][1], f, -b1));
+          float p2 = exp2f(fmaf(z[mt][nt][2], f, -b0)), p3 = exp2f(fmaf(z[mt][nt][3], f, -b1));
+          l[nt][0] += p0 + p2;
+          l[nt][1] += p1 + p3;
+          if constexpr (kFp8) {        // the values' scales ride on P; a hidden row's scale may be anything
+            const float v0 = s.scale[stage][1][mt * 16 + g4], v1 = s.scale[stage][1][mt * 16 + g4 + 8];
+            p0 = p0 == 0.f ? 0.f : p0 * v0; p1 = p1 == 0.f ? 0.f : p1 * v0;
+            p2 = p2 == 0.f ? 0.f : p2 * v1; p3 = p3 == 0.f ? 0.f : p3 * v1;
+          }
+          pf[mt][nt][0] = transpose8(pack_bf16(p0, p1));
+          pf[mt][nt][1] = transpose8(pack_bf16(p2, p3));
+        }
+      }
+      // O^T += V^T P^T; value rows that no row of the unit sees become zeros
+#pragma unroll
+      for (int mt = 0; mt < 4; ++mt) {
+        uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
+        if (!full) {
+          uint32_t k[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int j = j0 + mt * 16 + c2 + (e & 1) + (e >> 1) * 8;
+            k[e] = j <= un.m_hi && (a.window == 0 || j > un.m_lo - a.window || j < a.sinks) ? 0xffffu : 0u;
+          }
+          keep0 = k[0] | k[1] << 16;
+          keep1 = k[2] | k[3] << 16;
+        }
+        if constexpr (!kFp8) {
+          const int key = mt * 16 + (lane & 7) + (lane >> 4) * 8;
+#pragma unroll
+          for (int d = 0; d < D / 16; ++d) {
+            const int ch = (d & 3) * 2 + ((lane >> 3) & 1);
+            uint32_t v[4];
+            ldsm_t(vb + (d >> 2) * (kTile * 128) + key * 128 + ((ch ^ (key & 7)) << 4), v);
+            if (!full) { v[0] &= keep0; v[1] &= keep0; v[2] &= keep1; v[3] &= keep1; }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma16816(o[d][nt], v, pf[mt][nt]);
+          }
+        } else {
+          // matrices: keys 0-7 and 8-15 of 16-code chunk 2c, then of chunk 2c + 1; a transposed
+          // word holds codes (key, dim 2 g4), (key, dim 2 g4 + 1) of two keys: the MMA's rows g4
+          // and g4 + 8 are dims 2 g4 and 2 g4 + 1 of the chunk
+          const int key = mt * 16 + (lane & 7) + ((lane >> 3) & 1) * 8;
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            const int byte = c * 32 + (lane >> 4) * 16, ch = byte % S::kBoxBytes / 16;
+            const int sw = S::kBoxBytes == 128 ? ch ^ (key & 7) : ch ^ ((key >> 1) & 3);
+            uint32_t w[4];
+            ldsm_t(vb + byte / S::kBoxBytes * (kTile * S::kBoxBytes) + key * S::kBoxBytes + (sw << 4), w);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t lo = w[2 * h], hi = w[2 * h + 1];
+              uint32_t v[4] = {e4m3_pair(__byte_perm(lo, 0, 0x2404)), e4m3_pair(__byte_perm(lo, 0, 0x3414)),
+                               e4m3_pair(__byte_perm(hi, 0, 0x2404)), e4m3_pair(__byte_perm(hi, 0, 0x3414))};
+              if (!full) { v[0] &= keep0; v[1] &= keep0; v[2] &= keep1; v[3] &= keep1; }
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) mma16816(o[2 * c + h][nt], v, pf[mt][nt]);
+            }
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&s.empty[stage]);
+    }
+
+    // ---- the four warps' results meet ----
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float t = l[nt][e];
+        t += __shfl_xor_sync(0xffffffffu, t, 4);
+        t += __shfl_xor_sync(0xffffffffu, t, 8);
+        t += __shfl_xor_sync(0xffffffffu, t, 16);
+        const int r = nt * 8 + c2 + e;
+        if (g4 == 0) {
+          s.ml[warp][r][0] = m[nt][e] == -INFINITY ? -INFINITY : m[nt][e] * f;
+          s.ml[warp][r][1] = t;
+        }
+#pragma unroll
+        for (int d = 0; d < D / 16; ++d) {
+          // rows of the accumulator: dims g4, g4 + 8 (fp8: dims 2 g4, 2 g4 + 1)
+          s.o[warp][r][d * 16 + (kFp8 ? 2 * g4 : g4)] = o[d][nt][e];
+          s.o[warp][r][d * 16 + (kFp8 ? 2 * g4 + 1 : g4 + 8)] = o[d][nt][e + 2];
+        }
+      }
+    }
+    compute_sync();
+    const bool begins = pc.tile == 0, ends = pc.tile + count == un.tr.tiles;
+    const int64_t part = int64_t(blockIdx.x) * 2 + (begins ? 1 : 0);
+    for (int i = tid; i < R * D / 4; i += 32 * kWarps) {
+      const int r = i / (D / 4), d = i % (D / 4) * 4;
+      if (r >= un.rows) continue;
+      float top = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s.ml[w][r][0]);
+      float sum = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float wt = s.ml[w][r][0] == -INFINITY ? 0.f : exp2f(s.ml[w][r][0] - top);
+        sum = fmaf(wt, s.ml[w][r][1], sum);
+        const float4 t = *reinterpret_cast<const float4*>(&s.o[w][r][d]);
+        v[0] = fmaf(wt, t.x, v[0]); v[1] = fmaf(wt, t.y, v[1]);
+        v[2] = fmaf(wt, t.z, v[2]); v[3] = fmaf(wt, t.w, v[3]);
+      }
+      if (begins && ends) {
+        const int64_t row = int64_t(un.s0 + (un.row0 + r) / a.G) * a.H + pc.hk * a.G + (un.row0 + r) % a.G;
+        const float inv = sum > 0.f ? 1.f / sum : sum == 0.f ? 0.f : sum;     // NaN stays NaN
+        *reinterpret_cast<uint2*>(a.out + row * D + d) =
+            make_uint2(pack_bf16(v[0] * inv, v[1] * inv), pack_bf16(v[2] * inv, v[3] * inv));
+        if (d == 0 && a.lse) a.lse[row] = (top + log2f(sum)) * 0.6931471805599453f;
+      } else {
+        *reinterpret_cast<float4*>(p.part_o + (part * R + r) * D + d) = make_float4(v[0], v[1], v[2], v[3]);
+        if (d == 0) {
+          p.part_ml[(part * R + r) * 2] = top;
+          p.part_ml[(part * R + r) * 2 + 1] = sum;
+        }
+      }
+    }
+    if (begins && !ends) {        // the unit goes on in the next CTAs: this one describes it for the join
+      const int64_t end = pre[pc.u] + int64_t(pc.hk + 1) * un.tr.tiles;
+      desc = JoinDesc{1, un.b, pc.u % p.RG, pc.hk, int((end * ctas - 1) / s.total), {0, 0, 0}};
+    }
+    ok = compute_sync_and(ok);     // all four warps go on or stop together
+    x += count;
+  }
+  if (p.split && tid == 0) p.join[blockIdx.x] = ok ? desc : JoinDesc{};
+}
+
+// Joins the pieces of a unit that several CTAs hold: piece c's slot 1, then
+// slot 0 of the CTAs behind it, in CTA order; weights 2^{m - max} of the
+// pieces' maxima.  One CTA per (describing CTA, row); 8 groups of lanes share
+// the pieces and meet in group order, so the result does not depend on timing.
+template <int D, int R>
+__global__ void __launch_bounds__(256) dense_attn_join(const MmaDev p) {
+  constexpr int kLanes = D / 4, kGroups = 256 / kLanes > 8 ? 8 : 256 / kLanes;
+  __shared__ float4 acc[kGroups][kLanes];
+  __shared__ float red[8];
+  const int c = blockIdx.x, r = blockIdx.y, tid = threadIdx.x;
+  const DenseAttnDev& a = p.a;
+  pdl_trigger();
+  pdl_wait();
+  const JoinDesc j = p.join[c];
+  if (!j.valid) return;
+  const int s0 = a.starts[j.b], n = a.starts[j.b + 1] - s0;
+  const int row = j.rg * R + r;
+  if (row >= n * a.G) return;
+  auto part = [&](int k) { return (int64_t(c + k) * 2 + (k == 0 ? 1 : 0)) * R + r; };
+  const int pieces = j.last - c + 1;
+  float top = -INFINITY;
+  for (int k = tid; k < pieces; k += 256) top = fmaxf(top, p.part_ml[part(k) * 2]);
+  top = warp_max(top);
+  if ((tid & 31) == 0) red[tid >> 5] = top;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < 8; ++w) top = fmaxf(top, red[w]);
+  const int g = tid / kLanes, l = tid % kLanes;
+  float sum = 0.f;
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (g < kGroups) {
+#pragma unroll 4
+    for (int k = g; k < pieces; k += kGroups) {
+      const float m = p.part_ml[part(k) * 2], s = p.part_ml[part(k) * 2 + 1];
+      const float4 o = *reinterpret_cast<const float4*>(p.part_o + part(k) * D + 4 * l);
+      const float w = m == -INFINITY ? 0.f : exp2f(m - top);
+      sum = fmaf(w, s, sum);
+      v.x = fmaf(w, o.x, v.x); v.y = fmaf(w, o.y, v.y); v.z = fmaf(w, o.z, v.z); v.w = fmaf(w, o.w, v.w);
+    }
+  }
+  __syncthreads();                         // red is read above
+  if (g < kGroups) {
+    acc[g][l] = v;
+    if (l == 0) red[g] = sum;
+  }
+  __syncthreads();
+  if (tid >= kLanes) return;
+  sum = 0.f;
+  v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int k = 0; k < kGroups; ++k) {
+    const float4 t = acc[k][l];
+    sum += red[k];
+    v.x += t.x; v.y += t.y; v.z += t.z; v.w += t.w;
+  }
+  const int64_t at = int64_t(s0 + row / a.G) * a.H + j.hk * a.G + row % a.G;
+  const float inv = sum > 0.f ? 1.f / sum : sum == 0.f ? 0.f : sum;
+  *reinterpret_cast<uint2*>(a.out + at * D + 4 * l) = make_uint2(pack_bf16(v.x * inv, v.y * inv), pack_bf16(v.z * inv, v.w * inv));
+  if (l == 0 && a.lse) a.lse[at] = (top + log2f(sum)) * 0.6931471805599453f;
+}
+
+int rows_of(const v4a_dense_attn_args* a) {
+  const int64_t rows = int64_t(a->max_new_per_seq) * (a->num_heads / a->kv.num_kv_heads);
+  return rows > 8 && a->kv.dim <= 192 ? 16 : 8;      // 16 rows of dim 256 would not fit the registers
+}
+
+int64_t row_groups(const v4a_dense_attn_args* a) {
+  const int64_t rows = int64_t(a->max_new_per_seq) * (a->num_heads / a->kv.num_kv_heads);
+  return (rows + rows_of(a) - 1) / rows_of(a);
+}
+
+size_t workspace_of(const v4a_dense_attn_args* a) {
+  const size_t R = rows_of(a), n = size_t(kCtas) * 2 * R;
+  return 16 + kCtas * sizeof(JoinDesc) + n * a->kv.dim * 4 + n * 2 * 4;
+}
+
+template <int D, int NT, bool kFp8>
+int launch(MmaDev& p, const v4a_dense_attn_args* a, cudaStream_t stream) {
+  using S = Shape<D, NT, kFp8>;
+  CUtensorMap map;
+  const auto sw = S::kBoxBytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+  if (!dense_rows_map(&map, a->kv, p.a.block_bytes, S::kBox, kTile, sw)) return V4A_ERR_CUDA;
+  const size_t smem = 1024 + S::kStages * S::kStage + sizeof(typename S::Tail) +
+                      (p.split ? p.a.B * sizeof(SeqRun) + (p.U + 1) * sizeof(int64_t) : sizeof(SeqRun));
+  if (smem > 227 * 1024) return V4A_ERR_UNSUPPORTED;
+  auto kern = dense_attn_mma<D, NT, kFp8>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024) != cudaSuccess) return V4A_ERR_CUDA;
+  const int64_t grid = p.split ? kCtas : int64_t(p.U) * p.a.K;
+  if (grid > INT32_MAX) return V4A_ERR_UNSUPPORTED;
+  cudaError_t e = launch_pdl(kern, dim3(unsigned(grid)), dim3(kThreads), smem, stream, p, map);
+  if (e == cudaSuccess && p.split) e = launch_pdl(dense_attn_join<D, S::R>, dim3(unsigned(grid), S::R), dim3(256), 0, stream, p);
+  return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? V4A_OK : V4A_ERR_CUDA;
+}
+
+template <bool kFp8>
+int launch_dim(MmaDev& p, const v4a_dense_attn_args* a, cudaStream_t stream) {
+  const bool two = rows_of(a) == 16;
+  switch (a->kv.dim) {
+    case 64: return two ? launch<64, 2, kFp8>(p, a, stream) : launch<64, 1, kFp8>(p, a, stream);
+    case 128: return two ? launch<128, 2, kFp8>(p, a, stream) : launch<128, 1, kFp8>(p, a, stream);
+    case 192: return two ? launch<192, 2, kFp8>(p, a, stream) : launch<192, 1, kFp8>(p, a, stream);
+    default: return launch<256, 1, kFp8>(p, a, stream);
+  }
+}
+
+// Everything but the pointers of the call's own tensors.
+int check_shape(const v4a_dense_attn_args* a) {
+  if (!a || a->num_tokens < 0 || a->num_seqs < 0 || a->max_new_per_seq < 1 || a->num_heads < 1 || a->window < 0 || a->sinks < 0)
+    return V4A_ERR_INVALID_ARG;
+  const v4a_dense_cache& c = a->kv;
+  if (c.num_kv_heads < 1 || c.num_kv_heads > 1024 || a->num_heads % c.num_kv_heads) return V4A_ERR_INVALID_ARG;
+  if (c.dim != 64 && c.dim != 128 && c.dim != 192 && c.dim != 256) return V4A_ERR_UNSUPPORTED;
+  if (c.format != V4A_KV_BF16 && c.format != V4A_KV_FP8_TOKEN) return V4A_ERR_UNSUPPORTED;
+  if (a->num_heads > 1024 || a->max_new_per_seq > (1 << 22) || c.max_blocks > (1 << 22)) return V4A_ERR_UNSUPPORTED;
+  if (int64_t(a->num_seqs) * row_groups(a) > INT32_MAX) return V4A_ERR_UNSUPPORTED;
+  return V4A_OK;
+}
+
+}  // namespace
+
+bool dense_rows_map(CUtensorMap* map, const v4a_dense_cache& c, int64_t block_bytes, int box, int rows,
+                    CUtensorMapSwizzle swizzle) {
+  auto encode = tc::encode_fn();
+  if (!encode) return false;
+  const bool fp8 = c.format == V4A_KV_FP8_TOKEN;
+  const cuuint64_t row = cuuint64_t(c.dim) * (fp8 ? 1 : 2);
+  const cuuint64_t dims[4] = {cuuint64_t(c.dim), 256, cuuint64_t(2 * c.num_kv_heads), cuuint64_t(c.num_blocks)};
+  const cuuint64_t strides[3] = {row, 256 * row, cuuint64_t(block_bytes)};
+  const cuuint32_t boxes[4] = {cuuint32_t(box), cuuint32_t(rows), 1, 1}, es[4] = {1, 1, 1, 1};
+  return encode(map, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, c.pool, dims, strides, boxes,
+                es, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+size_t dense_attn_workspace_size(const v4a_dense_attn_args* a) { return check_shape(a) ? 0 : workspace_of(a); }
+
+int dense_attn(const v4a_dense_attn_args* a, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  int rc = check_shape(a);
+  if (rc) return rc;
+  MmaDev p{};
+  rc = dense_cache_check(a->kv, &p.a.block_bytes);
+  if (rc) return rc;
+  if (!(a->softmax_scale > 0.f) || !std::isfinite(a->softmax_scale) || a->kv.max_blocks < 1) return V4A_ERR_INVALID_ARG;
+  if (a->num_tokens == 0 || a->num_seqs == 0) return V4A_OK;
+  if (!a->positions || !a->token_starts || !a->kv.block_table || !a->q || !a->out) return V4A_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(a->q) & 15) || (reinterpret_cast<uintptr_t>(a->out) & 15) ||
+      static_cast<const void*>(a->q) == static_cast<const void*>(a->out))
+    return V4A_ERR_INVALID_ARG;
+  if (!ws || (reinterpret_cast<uintptr_t>(ws) & 15) || ws_bytes < workspace_of(a)) return V4A_ERR_WORKSPACE;
+  DenseAttnDev& d = p.a;
+  d.T = a->num_tokens; d.B = a->num_seqs; d.H = a->num_heads; d.K = a->kv.num_kv_heads; d.G = d.H / d.K;
+  d.max_new = a->max_new_per_seq; d.max_blocks = a->kv.max_blocks; d.window = a->window; d.sinks = a->sinks;
+  d.num_blocks = a->kv.num_blocks;
+  d.positions = a->positions; d.starts = a->token_starts; d.bt = a->kv.block_table;
+  d.pool = static_cast<const uint8_t*>(a->kv.pool);
+  d.q = a->q; d.out = a->out; d.lse = a->lse; d.status = a->status;
+  d.scale_log2 = a->softmax_scale * 1.4426950408889634f;
+  p.RG = int(row_groups(a));
+  p.U = d.B * p.RG;
+  p.split = p.U <= kMaxUnits;
+  const size_t R = rows_of(a), n = size_t(kCtas) * 2 * R;
+  p.join = static_cast<JoinDesc*>(ws);
+  p.part_o = reinterpret_cast<float*>(p.join + kCtas);
+  p.part_ml = p.part_o + n * a->kv.dim;
+  return a->kv.format == V4A_KV_FP8_TOKEN ? launch_dim<true>(p, a, stream) : launch_dim<false>(p, a, stream);
+}
+
+}  // namespace v4a

@@ -1,0 +1,255 @@
+// Per-head RMSNorm of queries and keys, the position rotation, and the keys'
+// and values' insert into the dense paged cache, in one pass
+// (v4a_dense.h, v4a_dense_insert).
+//
+// Mathematics: y = x / sqrt(mean(x^2) + eps) * gamma over a head's dims, then
+// pairs (a, b) turn by the angle p f_j.  The angle is formed in turns as a
+// 64-bit fraction: F_j = f_j / (2 pi) 2^64 on the host, p F_j mod 2^64 is one
+// integer product, and its top 32 bits are the signed fraction of a turn, so
+// no fp64 and no range reduction runs on the device and far positions lose
+// nothing.
+//
+// Bound: memory.  Every row is read once and written once; a row of dim
+// elements is held by dim / 8 lanes as one 16-byte load each, the norm and the
+// fp8 row maximum are shuffles inside those lanes, and the halves of a
+// half-split pair meet by a shuffle.  A CTA takes one token (or part of its
+// rows when tokens are few): its cos and sin are computed once and shared by
+// all its heads, and all its loads are issued before the first use.
+#include "tc_common.cuh"
+#include "v4a_dense.h"
+#include "v4a_dense_internal.h"
+
+namespace v4a {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kPasses = 4;        // rows per lane group held in registers (16 bytes a lane each)
+
+struct InsertDev {
+  uint64_t turn[128];             // F_j: turns per position as a 64-bit fraction
+  float magnitude;
+  int R, first, half;
+  int D, H, K, NR, passes;        // NR = H + 2K rows a token
+  float eps;
+  const int32_t* positions;
+  const int64_t* slots;
+  const uint16_t *q, *k, *v;
+  uint16_t* q_out;
+  int64_t qs, qos, ks, vs;
+  const float *qg, *kg;
+  uint8_t* pool;
+  int64_t num_slots, block_bytes;
+  int32_t* status;
+};
+
+// kLanes: lanes of one row (dim / 8, or 32 with the last eight idle at dim 192).
+template <int kLanes, bool kFp8>
+__global__ void __launch_bounds__(kThreads) dense_insert_kernel(const __grid_constant__ InsertDev p) {
+  constexpr int kRows = kThreads / kLanes;      // rows per pass
+  __shared__ float cs[256];                     // cos [0, R/2), sin [R/2, R)
+  const int t = blockIdx.x, tid = threadIdx.x;
+  const int l = tid % kLanes, r0 = blockIdx.y * (kRows * p.passes) + tid / kLanes;
+  const int D = p.D;
+  const bool live = 8 * l < D;
+  pdl_trigger();
+  pdl_wait();
+  const int64_t slot = p.slots[t];
+  const int P = p.positions[t];
+  uint4 raw[kPasses];
+#pragma unroll
+  for (int i = 0; i < kPasses; ++i) {
+    const int r = r0 + i * kRows;
+    raw[i] = make_uint4(0, 0, 0, 0);
+    if (i < p.passes && r < p.NR && live) {
+      const uint16_t* src = r < p.H ? p.q + int64_t(t) * p.qs + r * D
+                            : r < p.H + p.K ? p.k + int64_t(t) * p.ks + (r - p.H) * D
+                                            : p.v + int64_t(t) * p.vs + (r - p.H - p.K) * D;
+      raw[i] = *reinterpret_cast<const uint4*>(src + 8 * l);
+    }
+  }
+  if (slot < 0 || slot >= p.num_slots || P < 0) {   // the whole CTA
+    if (tid == 0 && slot != -1) report(p.status, slot < 0 || slot >= p.num_slots ? V4A_DEV_BAD_BLOCK : V4A_DEV_BAD_BATCH);
+    return;
+  }
+  for (int j = tid; j < p.R / 2; j += kThreads) {
+    const int32_t frac = int32_t((uint64_t(uint32_t(P)) * p.turn[j]) >> 32);
+    float sn, co;
+    sincospif(float(frac) * 0x1p-31f, &sn, &co);
+    cs[j] = co * p.magnitude;
+    cs[p.R / 2 + j] = sn * p.magnitude;
+  }
+  __syncthreads();
+  const int d0 = 8 * l, rel = d0 - p.first;
+  const bool rot = live && rel >= 0 && rel < p.R;
+  const bool upper = rel >= p.R / 2;             // half layout: this lane holds the pairs' second halves
+  const int mate = p.half && rot ? (upper ? l - p.R / 16 : l + p.R / 16) : l;
+  uint8_t* block = p.pool + (slot / kBlockPositions) * p.block_bytes;
+  const int at = int(slot % kBlockPositions);
+#pragma unroll
+  for (int i = 0; i < kPasses; ++i) {
+    const int r = r0 + i * kRows;
+    if (i >= p.passes) break;                    // the same for the whole CTA
+    const bool is_q = r < p.H, is_v = r >= p.H + p.K, row_ok = r < p.NR;
+    const uint32_t u[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+    float x[8];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      x[2 * e] = __uint_as_float(u[e] << 16);
+      x[2 * e + 1] = __uint_as_float(u[e] & 0xffff0000u);
+    }
+    const float* gamma = is_q ? p.qg : is_v ? nullptr : p.kg;
+    float ss = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
+#pragma unroll
+    for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    if (gamma && live) {
+      const float inv = rsqrtf(ss / float(D) + p.eps);
+      const float4 g0 = *reinterpret_cast<const float4*>(gamma + d0), g1 = *reinterpret_cast<const float4*>(gamma + d0 + 4);
+      x[0] *= inv * g0.x; x[1] *= inv * g0.y; x[2] *= inv * g0.z; x[3] *= inv * g0.w;
+      x[4] *= inv * g1.x; x[5] *= inv * g1.y; x[6] *= inv * g1.z; x[7] *= inv * g1.w;
+    }
+    if (p.half) {
+      float y[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] = __shfl_sync(0xffffffffu, x[e], mate, kLanes);
+      if (rot && !is_v) {
+        const int j = upper ? rel - p.R / 2 : rel;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float co = cs[j + e], sn = cs[p.R / 2 + j + e];
+          x[e] = upper ? fmaf(y[e], sn, x[e] * co) : fmaf(-y[e], sn, x[e] * co);
+        }
+      }
+    } else if (rot && !is_v) {
+      const int j = rel / 2;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float co = cs[j + e], sn = cs[p.R / 2 + j + e], a = x[2 * e], b = x[2 * e + 1];
+        x[2 * e] = fmaf(-b, sn, a * co);
+        x[2 * e + 1] = fmaf(b, co, a * sn);
+      }
+    }
+    // row maximum of |x| as bits: a NaN is the largest of them, and makes the
+    // row's scale NaN (readers may decode the code itself as a number)
+    uint32_t top = 0;
+    if (kFp8) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(x[e]) & 0x7fffffffu);
+#pragma unroll
+      for (int o = kLanes / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    }
+    if (!row_ok || !live) continue;
+    if (is_q || !kFp8) {
+      uint32_t w[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * e], x[2 * e + 1]);
+        w[e] = *reinterpret_cast<const uint32_t*>(&b);
+      }
+      const int64_t row = int64_t(r - p.H) * kBlockPositions + at;     // keys' heads, then values'
+      uint16_t* dst = is_q ? p.q_out + int64_t(t) * p.qos + r * D : reinterpret_cast<uint16_t*>(block) + row * D;
+      *reinterpret_cast<uint4*>(dst + d0) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+      // exact divisions: the codes are those of the definition in fp32
+      const float s = top ? __fdiv_rn(__uint_as_float(top), 448.f) : 1.f;
+      uint32_t w[2] = {0, 0};
+#pragma unroll
+      for (int e = 0; e < 8; ++e) w[e >> 2] |= uint32_t(f32_to_e4m3(__fdiv_rn(x[e], s))) << (8 * (e & 3));
+      const int64_t row = int64_t(r - p.H) * kBlockPositions + at;
+      *reinterpret_cast<uint2*>(block + row * D + d0) = make_uint2(w[0], w[1]);
+      if (l == 0) reinterpret_cast<float*>(block + int64_t(2 * p.K) * kBlockPositions * D)[row] = s;
+    }
+  }
+}
+
+bool aligned(const void* p, uintptr_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
+
+// The turns per position of each pair; V4A_OK or V4A_ERR_INVALID_ARG.
+int fill_rope(const v4a_rope& r, int dim, InsertDev* d) {
+  if (r.dims < 0 || r.dims > 256 || r.dims % 16 || r.first < 0 || r.first % 8 || r.first + r.dims > dim) return V4A_ERR_INVALID_ARG;
+  d->R = r.dims;
+  d->first = r.first;
+  d->half = r.layout == V4A_ROPE_HALF;
+  d->magnitude = float(r.magnitude);
+  if (r.dims == 0) {
+    d->half = 0;
+    return V4A_OK;
+  }
+  if (r.layout != V4A_ROPE_INTERLEAVED && r.layout != V4A_ROPE_HALF) return V4A_ERR_INVALID_ARG;
+  if (r.scaling < V4A_ROPE_PLAIN || r.scaling > V4A_ROPE_TABLE) return V4A_ERR_INVALID_ARG;
+  if (!std::isfinite(r.magnitude)) return V4A_ERR_INVALID_ARG;
+  if (r.scaling == V4A_ROPE_TABLE ? !r.inv_freq : !(r.theta > 0)) return V4A_ERR_INVALID_ARG;
+  if ((r.scaling == V4A_ROPE_LINEAR || r.scaling == V4A_ROPE_YARN) && !(r.factor > 0)) return V4A_ERR_INVALID_ARG;
+  if (r.scaling == V4A_ROPE_YARN && (!(r.original > 0) || !(r.beta_fast > r.beta_slow))) return V4A_ERR_INVALID_ARG;
+  const double two_pi = 6.283185307179586476925286766559;
+  for (int j = 0; j < r.dims / 2; ++j) {
+    double f = r.scaling == V4A_ROPE_TABLE ? r.inv_freq[j] : std::pow(r.theta, -2.0 * j / r.dims);
+    if (r.scaling == V4A_ROPE_LINEAR) f /= r.factor;
+    if (r.scaling == V4A_ROPE_YARN) {
+      double g = (r.original * f / two_pi - r.beta_slow) / (r.beta_fast - r.beta_slow);
+      g = g < 0 ? 0 : g > 1 ? 1 : g;
+      f = f * g + f / r.factor * (1 - g);
+    }
+    if (!(f >= 0 && f <= two_pi / 2)) return V4A_ERR_INVALID_ARG;     // at most half a turn a position
+    d->turn[j] = uint64_t(std::ldexp(f / two_pi, 64));
+  }
+  return V4A_OK;
+}
+
+}  // namespace
+
+int dense_cache_check(const v4a_dense_cache& c, int64_t* block_bytes) {
+  if (c.num_kv_heads < 1 || c.num_kv_heads > 1024 || c.num_blocks < 1 || !c.pool) return V4A_ERR_INVALID_ARG;
+  if (c.format != V4A_KV_BF16 && c.format != V4A_KV_FP8_TOKEN) return V4A_ERR_UNSUPPORTED;
+  if (c.dim != 64 && c.dim != 128 && c.dim != 192 && c.dim != 256) return V4A_ERR_UNSUPPORTED;
+  const int64_t need = v4a_dense_block_bytes(c.num_kv_heads, c.dim, c.format);
+  *block_bytes = c.block_bytes ? c.block_bytes : need;
+  if (*block_bytes < need || *block_bytes % 16 || !aligned(c.pool, 16)) return V4A_ERR_INVALID_ARG;
+  if (c.num_blocks > INT32_MAX) return V4A_ERR_UNSUPPORTED;
+  return V4A_OK;
+}
+
+int dense_insert(const v4a_dense_insert_args* a, cudaStream_t stream) {
+  if (!a || a->num_tokens < 0 || a->num_heads < 0 || !(a->eps >= 0.f)) return V4A_ERR_INVALID_ARG;
+  if (a->num_heads > 1024) return V4A_ERR_UNSUPPORTED;
+  InsertDev d{};
+  int rc = dense_cache_check(a->kv, &d.block_bytes);
+  if (rc) return rc;
+  const int D = a->kv.dim, K = a->kv.num_kv_heads, H = a->num_heads;
+  if (H % K) return V4A_ERR_INVALID_ARG;
+  rc = fill_rope(a->rope, D, &d);
+  if (rc) return rc;
+  if (a->num_tokens == 0) return V4A_OK;
+  if (!a->positions || !a->slots || !a->k || !a->v || (H > 0 && (!a->q || !a->q_out))) return V4A_ERR_INVALID_ARG;
+  if (!aligned(a->q, 16) || !aligned(a->q_out, 16) || !aligned(a->k, 16) || !aligned(a->v, 16) ||
+      !aligned(a->q_gamma, 16) || !aligned(a->k_gamma, 16))
+    return V4A_ERR_INVALID_ARG;
+  if ((H > 0 && (a->q_stride < int64_t(H) * D || a->q_out_stride < int64_t(H) * D || a->q_stride % 8 || a->q_out_stride % 8)) ||
+      a->k_stride < int64_t(K) * D || a->v_stride < int64_t(K) * D || a->k_stride % 8 || a->v_stride % 8)
+    return V4A_ERR_INVALID_ARG;
+  if (H > 0 && a->q == a->q_out && a->q_stride != a->q_out_stride) return V4A_ERR_INVALID_ARG;
+  d.D = D; d.H = H; d.K = K; d.NR = H + 2 * K; d.eps = a->eps;
+  d.positions = a->positions; d.slots = a->slots;
+  d.q = a->q; d.k = a->k; d.v = a->v; d.q_out = a->q_out;
+  d.qs = a->q_stride; d.qos = a->q_out_stride; d.ks = a->k_stride; d.vs = a->v_stride;
+  d.qg = a->q_gamma; d.kg = a->k_gamma;
+  d.pool = static_cast<uint8_t*>(a->kv.pool);
+  d.num_slots = a->kv.num_blocks * kBlockPositions;
+  d.status = a->status;
+  const int lanes = D == 64 ? 8 : D == 128 ? 16 : 32;
+  const int rows = kThreads / lanes, need = (d.NR + rows - 1) / rows;
+  // few tokens: one pass per CTA, so that a token's rows spread over more SMs
+  int y = (need + kPasses - 1) / kPasses;
+  if (int64_t(a->num_tokens) * y < 2 * 152) y = need;
+  d.passes = (need + y - 1) / y;
+  y = (need + d.passes - 1) / d.passes;
+  const bool fp8 = a->kv.format == V4A_KV_FP8_TOKEN;
+  auto kern = lanes == 8    ? (fp8 ? dense_insert_kernel<8, true> : dense_insert_kernel<8, false>)
+              : lanes == 16 ? (fp8 ? dense_insert_kernel<16, true> : dense_insert_kernel<16, false>)
+                            : (fp8 ? dense_insert_kernel<32, true> : dense_insert_kernel<32, false>);
+  const cudaError_t e = launch_pdl(kern, dim3(a->num_tokens, y), dim3(kThreads), 0, stream, d);
+  return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? V4A_OK : V4A_ERR_CUDA;
+}
+
+}  // namespace v4a
