@@ -15,25 +15,24 @@
 // takes 8-column operands; tcgen05 needs 128 rows) is far from its rate and
 // the cache's bytes set the time.
 //
-// Layout: a CTA has one copying warp and four computing warps over a ring of
-// tiles of 64 positions (keys and values, TMA boxes in the 128-byte swizzle;
-// 64 divides the 256-position block, so a tile never crosses a page).
-// Computing warp w takes tiles w, w + 4, ... of the CTA's range with its own
-// m, l and o; the four are merged through shared memory when the range leaves
-// a (sequence, KV head, row group).  The tiles of all sequences and KV heads
-// form one line that the CTAs divide evenly, so ragged lengths balance and one
-// long sequence fills the machine; pieces of a unit that several CTAs hold go
-// to the workspace and are joined by a second kernel in CTA order.
+// Layout: the positions of all sequences and KV heads, in tiles, form one line
+// that the CTAs divide evenly, so ragged lengths balance and one long sequence
+// fills the machine.  A tile is 64 dim bytes of keys and values (16 positions
+// of bf16, 32 of fp8): contiguous runs of one page, since both divide the
+// 256-position block.  Warp w of a CTA takes tiles w, w + kWarps, ... of the
+// CTA's range and streams them by itself through a private ring of stages in
+// shared memory (16-byte cp.async, rows swizzled for ldmatrix), with its own
+// m, l and o, so the main loop has no barrier.  The warps meet when the range
+// leaves a (sequence, KV head, row group): each leaves o in the stage that it
+// has just read.  Pieces of a unit that several CTAs hold go to the workspace
+// and are joined by a second kernel in CTA order.
 #include "dense_attn_common.cuh"
 
 namespace v4a {
 namespace {
 
-constexpr int kTile = 64;            // positions per tile
-constexpr int kWarps = 4;            // computing warps
-constexpr int kThreads = 32 * (kWarps + 1);
 constexpr int kMaxUnits = 1024;      // (sequence, row group) units that are split evenly
-constexpr int kRingBytes = 160 * 1024;
+constexpr int kRingBytes = 192 * 1024;
 constexpr int kCtas = 152;           // CTAs of an even split: one per SM
 
 struct JoinDesc { int valid, b, rg, hk, last, pad[3]; };
@@ -47,26 +46,29 @@ struct MmaDev {
 
 template <int D, int NT, bool kFp8>
 struct Shape {
-  static constexpr int R = 8 * NT;
-  static constexpr int kElem = kFp8 ? 1 : 2;
-  static constexpr int kBox = kFp8 ? (D % 128 == 0 ? 128 : 64) : 64;     // elements of a box row
-  static constexpr int kBoxBytes = kBox * kElem;
-  static constexpr int kBoxes = D / kBox;
-  static constexpr int kTileBytes = kTile * D * kElem;                   // keys or values of a tile
-  static constexpr int kStage = 2 * kTileBytes;
-  static constexpr int kStages = kRingBytes / kStage < 16 ? kRingBytes / kStage : 16;
-  static constexpr int kPad = D + 4;                                     // merge rows: conflict-free columns
-  struct Tail {                                                          // behind the ring
-    uint64_t full[kStages], empty[kStages];
-    int skip[kStages];
-    int abort_flag;
-    int64_t total;
-    alignas(16) float scale[kStages][2][kFp8 ? kTile : 1];
+  static constexpr int R = 8 * NT;                               // query rows of a unit
+  static constexpr int kKeys = kFp8 ? 32 : 16;                   // positions per tile
+  static constexpr int kRow = kFp8 ? D : 2 * D;                  // bytes of a row
+  static constexpr int kHalf = kKeys * kRow;                     // keys (or values) of a tile: 32 D bytes
+  static constexpr int kScales = kFp8 ? 2 * kKeys * 4 : 0;
+  static constexpr int kStage = 2 * kHalf + kScales;             // holds R x D fp32 for the merge as well
+  static constexpr int kWarps = D <= 128 ? 8 : 4;
+  static constexpr int kThreads = 32 * kWarps;
+  static constexpr int kStages = kRingBytes / (kWarps * 2 * kHalf);
+  static_assert(R * D * 4 <= 2 * kHalf && kStages >= 3, "a stage holds the merge rows");
+  struct Tail {                                                  // behind the rings
+    int64_t total, scan[kWarps];
+    int buf[kWarps];                                             // the stage a warp left its o in
     float ml[kWarps][R][2];
-    alignas(16) float o[kWarps][R][kPad];
-    int64_t scan[kWarps + 1];
   };
 };
+
+// 16-byte chunk `ch` of row r: rows of a multiple of 128 bytes rotate over the
+// eight bank groups, rows of 64 and 192 bytes over four (two rows apart).
+template <int kRow>
+__device__ __forceinline__ uint32_t chunk_at(int r, int ch) {
+  return uint32_t(r * kRow + ((ch ^ (kRow % 128 == 0 ? r & 7 : (r >> 1) & 3)) << 4));
+}
 
 __device__ __forceinline__ void ldsm(uint32_t addr, uint32_t* r) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -99,43 +101,23 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&b);
 }
-__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, int c0, int c1, int c2, int c3, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(tc::smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(tc::smem_u32(bar))
-      : "memory");
-}
-__device__ __forceinline__ void compute_sync() {
-  __syncwarp();
-  asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory");
-}
-// compute_sync that also gives every computing thread whether all of them passed true.
-__device__ __forceinline__ bool compute_sync_and(bool ok) {
-  uint32_t r;
-  __syncwarp();
-  asm volatile(
-      "{\n.reg .pred p, q;\nsetp.ne.u32 p, %1, 0;\nbar.red.and.pred q, 1, %2, p;\nselp.u32 %0, 1, 0, q;\n}\n"
-      : "=r"(r) : "r"(uint32_t(ok)), "n"(32 * kWarps) : "memory");
-  return r != 0;
-}
-
 // A row group of one sequence: rows [row0, row0 + rows) of its tokens x group heads.
-struct Unit { int b, row0, rows, s0, m_lo, m_hi; TileRange<kTile> tr; };
+template <int kKeys>
+struct Unit { int b, row0, rows, s0, m_lo, m_hi; TileRange<kKeys> tr; };
 
-template <int R>
-__device__ __forceinline__ Unit make_unit(const DenseAttnDev& a, int b, int rg, const SeqRun& s) {
-  Unit u;
+template <int R, int kKeys>
+__device__ __forceinline__ Unit<kKeys> make_unit(const DenseAttnDev& a, int b, int rg, const SeqRun& s) {
+  Unit<kKeys> u;
   u.b = b;
   u.row0 = rg * R;
   u.rows = min(R, s.n * a.G - u.row0);
   u.s0 = s.s0;
   u.m_lo = u.m_hi = 0;
-  u.tr = TileRange<kTile>{0, 0, 0};
+  u.tr = TileRange<kKeys>{0, 0, 0};
   if (u.rows <= 0) return u;
   u.m_lo = s.p0 + u.row0 / a.G;
   u.m_hi = s.p0 + (u.row0 + u.rows - 1) / a.G;
-  u.tr = tile_range<kTile>(a, u.m_lo, u.m_hi);
+  u.tr = tile_range<kKeys>(a, u.m_lo, u.m_hi);
   return u;
 }
 
@@ -143,28 +125,16 @@ __device__ __forceinline__ Unit make_unit(const DenseAttnDev& a, int b, int rg, 
 struct Piece { int u, hk, tile; };
 
 template <int D, int NT, bool kFp8>
-__global__ void __launch_bounds__(kThreads, 1) dense_attn_mma(const MmaDev p, const __grid_constant__ CUtensorMap map) {
+__global__ void __launch_bounds__(Shape<D, NT, kFp8>::kThreads, 1) dense_attn_mma(const MmaDev p) {
   using S = Shape<D, NT, kFp8>;
-  constexpr int R = S::R;
-  extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  typename S::Tail& s = *reinterpret_cast<typename S::Tail*>(ring + S::kStages * S::kStage);
+  constexpr int R = S::R, kWarps = S::kWarps, kThreads = S::kThreads, kKeys = S::kKeys, MT = kKeys / 16;
+  extern __shared__ __align__(128) uint8_t smem[];
+  typename S::Tail& s = *reinterpret_cast<typename S::Tail*>(smem + kWarps * S::kStages * S::kStage);
   int64_t* pre = reinterpret_cast<int64_t*>(&s + 1);         // split: [U + 1] tiles before unit u, over its KV heads
   SeqRun* runs = reinterpret_cast<SeqRun*>(pre + (p.split ? p.U + 1 : 0));   // [B], or one
   const DenseAttnDev& a = p.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  volatile int* abort_flag = &s.abort_flag;
-
-  pdl_trigger();
-  if (tid == 0) {
-    for (int i = 0; i < S::kStages; ++i) {
-      tc::mbar_init(&s.full[i], 1);
-      tc::mbar_init(&s.empty[i], 1);
-    }
-    s.abort_flag = 0;
-    tc::mbar_fence_init();
-    tc::prefetch_tmap(&map);
-  }
+  auto unit_of = [&](int u, int run) { return make_unit<R, kKeys>(a, u / p.RG, u % p.RG, runs[run]); };
   pdl_wait();
 
   // ---- the CTA's tiles [x0, x1) ----
@@ -175,11 +145,11 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_mma(const MmaDev p, co
     for (int b = tid; b < a.B; b += kThreads) runs[b] = seq_run(a, b, st);
     __syncthreads();
     // exclusive sums over the units: each thread a run of units, then the threads' totals
-    const int per = (p.U + kThreads - 1) / kThreads, u0 = tid * per, u1 = min(p.U, u0 + per);
+    const int per = (p.U + kThreads - 1) / kThreads, u0 = min(p.U, tid * per), u1 = min(p.U, u0 + per);
     int64_t sum = 0;
     for (int u = u0; u < u1; ++u) {
       pre[u] = sum;
-      sum += int64_t(make_unit<R>(a, u / p.RG, u % p.RG, runs[u / p.RG]).tr.tiles) * a.K;
+      sum += int64_t(unit_of(u, u / p.RG).tr.tiles) * a.K;
     }
     int64_t v = sum;
 #pragma unroll
@@ -191,20 +161,21 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_mma(const MmaDev p, co
     __syncthreads();
     int64_t before = v - sum, total = 0;
 #pragma unroll
-    for (int w = 0; w <= kWarps; ++w) {
+    for (int w = 0; w < kWarps; ++w) {
       if (w < warp) before += s.scan[w];
       total += s.scan[w];
     }
     for (int u = u0; u < u1; ++u) pre[u] += before;
     if (tid == 0) { pre[p.U] = total; s.total = total; }
     __syncthreads();
-    ctas = int(min(int64_t(gridDim.x), total));
+    // a tile per warp at least
+    ctas = int(min(int64_t(gridDim.x), (total + kWarps - 1) / kWarps));
     if (int(blockIdx.x) >= ctas) {
       if (tid == 0) p.join[blockIdx.x].valid = 0;
       return;
     }
-    x0 = blockIdx.x * total / ctas;
-    x1 = (blockIdx.x + 1) * total / ctas;
+    x0 = int64_t(blockIdx.x) * total / ctas;
+    x1 = (int64_t(blockIdx.x) + 1) * total / ctas;
   } else {
     const int64_t c = blockIdx.x;
     u_direct = int(c / a.K);
@@ -212,13 +183,12 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_mma(const MmaDev p, co
     if (tid == 0) runs[0] = seq_run(a, u_direct / p.RG, hk_direct == 0 && u_direct % p.RG == 0 ? a.status : nullptr);
     __syncthreads();
     x0 = 0;
-    x1 = make_unit<R>(a, u_direct / p.RG, u_direct % p.RG, runs[0]).tr.tiles;
+    x1 = unit_of(u_direct, 0).tr.tiles;
     if (x1 == 0) return;
   }
-  auto unit_at = [&](int u) { return make_unit<R>(a, u / p.RG, u % p.RG, runs[p.split ? u / p.RG : 0]); };
-  auto locate = [&](int64_t x, Unit* un) {
+  auto locate = [&](int64_t x, Unit<kKeys>* un) {
     if (!p.split) {
-      *un = unit_at(u_direct);
+      *un = unit_of(u_direct, 0);
       return Piece{u_direct, hk_direct, int(x)};
     }
     int lo = 0, hi = p.U;                       // largest u with pre[u] <= x (empty units precede)
@@ -226,79 +196,74 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_mma(const MmaDev p, co
       const int mid = (lo + hi) >> 1;
       if (pre[mid] <= x) lo = mid; else hi = mid;
     }
-    *un = unit_at(lo);
+    *un = unit_of(lo, lo / p.RG);
     const int64_t rem = x - pre[lo];
     const int hk = int(rem / un->tr.tiles);
     return Piece{lo, hk, int(rem - int64_t(hk) * un->tr.tiles)};
   };
 
-  if (warp == kWarps) {
-    // ---- the copying warp: 32 tiles' pages are looked up at once, one lane each ----
-    auto page_of = [&](int64_t x, Piece* pc, int* row) {
-      if (x >= x1) return -1;
-      Unit un;
-      *pc = locate(x, &un);
-      const int kt = un.tr.at(pc->tile);
-      *row = kt % (kBlockPositions / kTile) * kTile;
-      const int32_t page = a.bt[int64_t(un.b) * a.max_blocks + kt / (kBlockPositions / kTile)];
-      if (page >= 0 && page < a.num_blocks) return int(page);
-      report(a.status, V4A_DEV_BAD_BLOCK);
-      return -1;
-    };
-    Piece pc{}, npc{};
-    int row = 0, nrow = 0, npage;
-    int page = page_of(x0 + lane, &pc, &row);
-    int stage = 0, use = 0;
-    bool ok = true;
-    int64_t issued = 0;
-    for (int64_t base = x0; base < x1 && ok; base += 32) {
-      npage = page_of(base + 32 + lane, &npc, &nrow);
-      const int n = int(min(int64_t(32), x1 - base));
-      for (int i = 0; i < n; ++i) {
-        if (lane == i) {
-          ok = tc::mbar_wait(&s.empty[stage], (use & 1) ^ 1, a.status, abort_flag);
-          if (ok && page < 0) {
-            s.skip[stage] = 1;
-            tc::mbar_arrive(&s.full[stage]);
-          } else if (ok) {
-            s.skip[stage] = 0;
-            uint8_t* dst = ring + stage * S::kStage;
-            tc::mbar_arrive_expect_tx(&s.full[stage], S::kStage + (kFp8 ? 2 * kTile * 4 : 0));
+  // ---- this warp's stream: tiles x0 + warp + j kWarps, j = 0, 1, ... ----
+  // Lane l looks up tile j0 + l of a batch of 32, one batch ahead of its use:
+  // its page (-1: missing) and its first row in the page (KV head x 256 + position).
+  struct Where { int page, row; };
+  const int mine = int((x1 - x0 - warp + kWarps - 1) / kWarps);
+  const int64_t to_values = int64_t(a.K) * kBlockPositions * S::kRow;
+  auto lookup = [&](int j) -> Where {
+    if (j >= mine) return {-1, 0};
+    Unit<kKeys> un;
+    const Piece pc = locate(x0 + warp + int64_t(j) * kWarps, &un);
+    const int kt = un.tr.at(pc.tile);
+    const int32_t page = a.bt[int64_t(un.b) * a.max_blocks + kt / (kBlockPositions / kKeys)];
+    const int row = pc.hk * kBlockPositions + kt % (kBlockPositions / kKeys) * kKeys;
+    if (page >= 0 && page < a.num_blocks) return {page, row};
+    report(a.status, V4A_DEV_BAD_BLOCK);
+    return {-1, row};
+  };
+  uint8_t* ring = smem + warp * (S::kStages * S::kStage);
+  const uint32_t ring0 = tc::smem_u32(ring);
+  Where now = lookup(lane), next = lookup(32 + lane);
+  uint32_t missing = 0;                          // bit per stage
+  int issued = 0, istage = 0;
+  auto issue = [&]() {                           // copies tile `issued` into stage istage; one group per call
+    if (issued < mine) {
+      const int page = __shfl_sync(0xffffffffu, now.page, issued & 31);
+      const int row = __shfl_sync(0xffffffffu, now.row, issued & 31);
+      missing = page < 0 ? missing | (1u << istage) : missing & ~(1u << istage);
+      if (page >= 0) {
+        const uint8_t* block = a.pool + page * a.block_bytes;
+        const uint8_t* src = block + int64_t(row) * S::kRow;
+        uint8_t* dst = ring + istage * S::kStage;
 #pragma unroll
-            for (int x = 0; x < S::kBoxes; ++x) {
-              tma_load_4d(dst + x * kTile * S::kBoxBytes, &map, x * S::kBox, row, pc.hk, page, &s.full[stage]);
-              tma_load_4d(dst + S::kTileBytes + x * kTile * S::kBoxBytes, &map, x * S::kBox, row, a.K + pc.hk, page, &s.full[stage]);
-            }
-            if (kFp8) {
-              const uint8_t* sc = a.pool + int64_t(page) * a.block_bytes + int64_t(2 * a.K) * kBlockPositions * D;
-              tc::bulk_load(s.scale[stage][0], sc + (int64_t(pc.hk) * kBlockPositions + row) * 4, kTile * 4, &s.full[stage]);
-              tc::bulk_load(s.scale[stage][1], sc + (int64_t(a.K + pc.hk) * kBlockPositions + row) * 4, kTile * 4, &s.full[stage]);
-            }
-          }
+        for (int i = 0; i < S::kHalf / 512; ++i) {
+          const int c = lane + 32 * i, r = c / (S::kRow / 16), ch = c % (S::kRow / 16);
+          const uint32_t to = chunk_at<S::kRow>(r, ch);
+          tc::cp_async16(dst + to, src + c * 16);
+          tc::cp_async16(dst + S::kHalf + to, src + to_values + c * 16);
         }
-        ok = __shfl_sync(0xffffffffu, ok, i);
-        if (!ok) break;
-        ++issued;
-        if (++stage == S::kStages) { stage = 0; ++use; }
+        if (kFp8 && lane < kKeys / 2) {          // the rows' scales: keys' from lanes 0..7, values' from 8..15
+          const int which = lane / (kKeys / 4), q = lane % (kKeys / 4);
+          const uint8_t* sc = block + 2 * to_values + (row + int64_t(which) * a.K * kBlockPositions) * 4;
+          tc::cp_async16(dst + 2 * S::kHalf + which * kKeys * 4 + q * 16, sc + q * 16);
+        }
       }
-      page = npage; pc = npc; row = nrow;
+      if ((++issued & 31) == 0) {
+        now = next;
+        next = lookup(issued + 32 + lane);
+      }
+      if (++istage == S::kStages) istage = 0;
     }
-    // after a timeout the copies in flight still land before the CTA ends
-    if (!ok && lane == 0)
-      for (int64_t i = max(int64_t(0), issued - S::kStages); i < issued; ++i)
-        tc::mbar_wait(&s.full[i % S::kStages], uint32_t(i / S::kStages) & 1, a.status, abort_flag);
-    return;
-  }
+    tc::cp_async_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < S::kStages - 1; ++i) issue();
 
-  // ---- the computing warps ----
   JoinDesc desc{};
   const float f = a.scale_log2;
-  const uint32_t ring0 = tc::smem_u32(ring);
   const int g4 = lane >> 2, c2 = (lane & 3) * 2;
+  int stage = 0;                                 // of this warp's next tile
   int64_t x = x0;
-  bool ok = true;
-  while (x < x1 && ok) {
-    Unit un;
+  while (x < x1) {
+    Unit<kKeys> un;
     const Piece pc = locate(x, &un);
     const int count = int(min(int64_t(un.tr.tiles - pc.tile), x1 - x));     // tiles of this segment
     // the query rows as B operands: column g4 of n-tile nt, dims of step ks
@@ -337,53 +302,45 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_mma(const MmaDev p, co
         for (int e = 0; e < 4; ++e) o[d][nt][e] = 0.f;
     }
 
-    // this warp's tiles: CTA tile numbers that are warp modulo kWarps
-    const int done = int(x - x0);
-    for (int i = (warp - done % kWarps + kWarps) % kWarps; i < count; i += kWarps) {
-      const int n = done + i, stage = n % S::kStages;
-      ok = __all_sync(0xffffffffu, tc::mbar_wait(&s.full[stage], uint32_t(n / S::kStages) & 1, a.status, abort_flag));
-      if (!ok) break;
-      if (s.skip[stage]) {
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&s.empty[stage]);
-        continue;
-      }
-      const uint32_t kb = ring0 + stage * S::kStage, vb = kb + S::kTileBytes;
-      const int j0 = un.tr.at(pc.tile + i) * kTile;
-      float z[4][NT][4];
+    int last = stage;                              // the stage read last: free until the next issue()
+    const int phase = int((x - x0) % kWarps);
+    for (int i = (warp - phase + kWarps) % kWarps; i < count; i += kWarps) {
+      tc::cp_async_wait_group<S::kStages - 2>();
+      __syncwarp();                                // every lane's copies of the tile; every lane has left the stage read last
+      const bool gone = missing >> stage & 1;
+      const int cur = stage;
+      if (++stage == S::kStages) stage = 0;
+      last = cur;
+      issue();                                     // into the stage read last
+      if (gone) continue;
+      const uint32_t kb = ring0 + cur * S::kStage, vb = kb + S::kHalf;
+      const float* scale = reinterpret_cast<const float*>(ring + cur * S::kStage + 2 * S::kHalf);
+      const int j0 = un.tr.at(pc.tile + i) * kKeys;
+      float z[MT][NT][4];
 #pragma unroll
-      for (int mt = 0; mt < 4; ++mt)
+      for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 4; ++e) z[mt][nt][e] = 0.f;
       // S^T = K Q^T
-      if constexpr (!kFp8) {
-        const int lr = (lane & 7) + ((lane >> 3) & 1) * 8;
+      const int lr = (lane & 7) + ((lane >> 3) & 1) * 8;
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-          const int ch = (ks & 3) * 2 + (lane >> 4);
-          const uint32_t at = kb + (ks >> 2) * (kTile * 128) + lr * 128 + ((ch ^ (lr & 7)) << 4);
+      for (int mt = 0; mt < MT; ++mt) {
+        if constexpr (!kFp8) {
 #pragma unroll
-          for (int mt = 0; mt < 4; ++mt) {
+          for (int ks = 0; ks < D / 16; ++ks) {
             uint32_t k[4];
-            ldsm(at + mt * 16 * 128, k);
+            ldsm(kb + chunk_at<S::kRow>(mt * 16 + lr, 2 * ks + (lane >> 4)), k);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) mma16816(z[mt][nt], k, qf[ks][nt]);
           }
-        }
-      } else {
-        // matrices: keys 0-7 and 8-15 of 16-code chunk 2c, then of chunk 2c + 1
-        const int lr = (lane & 7) + ((lane >> 3) & 1) * 8;
+        } else {
+          // matrices: keys 0-7 and 8-15 of 16-code chunk 2c, then of chunk 2c + 1
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-          const int byte = c * 32 + (lane >> 4) * 16, ch = byte % S::kBoxBytes / 16;
-          const int sw = S::kBoxBytes == 128 ? ch ^ (lr & 7) : ch ^ ((lr >> 1) & 3);
-          const uint32_t at = kb + byte / S::kBoxBytes * (kTile * S::kBoxBytes) + lr * S::kBoxBytes + (sw << 4);
-#pragma unroll
-          for (int mt = 0; mt < 4; ++mt) {
+          for (int c = 0; c < D / 32; ++c) {
             uint32_t w[4];
-            ldsm(at + mt * 16 * S::kBoxBytes, w);
+            ldsm(kb + chunk_at<S::kRow>(mt * 16 + lr, 2 * c + (lane >> 4)), w);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const uint32_t lo = w[2 * h], hi = w[2 * h + 1];
@@ -393,10 +350,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_mma(const MmaDev p, co
               for (int nt = 0; nt < NT; ++nt) mma16816(z[mt][nt], k, qf[2 * c + h][nt]);
             }
           }
-        }
-#pragma unroll
-        for (int mt = 0; mt < 4; ++mt) {
-          const float k0 = s.scale[stage][0][mt * 16 + g4], k1 = s.scale[stage][0][mt * 16 + g4 + 8];
+          const float k0 = scale[mt * 16 + g4], k1 = scale[mt * 16 + g4 + 8];
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             z[mt][nt][0] *= k0; z[mt][nt][1] *= k0;
@@ -405,10 +359,10 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_mma(const MmaDev p, co
         }
       }
       // mask, running maximum
-      const bool full = all_visible(a, un.m_lo, un.m_hi, j0, kTile);
+      const bool full = all_visible(a, un.m_lo, un.m_hi, j0, kKeys);
       if (!full) {
 #pragma unroll
-        for (int mt = 0; mt < 4; ++mt)
+        for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -423,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_mma(const MmaDev p, co
         for (int e = 0; e < 2; ++e) {
           float t = fmaxf(z[0][nt][e], z[0][nt][e + 2]);
 #pragma unroll
-          for (int mt = 1; mt < 4; ++mt) t = fmaxf(t, fmaxf(z[mt][nt][e], z[mt][nt][e + 2]));
+          for (int mt = 1; mt < MT; ++mt) t = fmaxf(t, fmaxf(z[mt][nt][e], z[mt][nt][e + 2]));
           t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
           t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
           t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
@@ -445,18 +399,18 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_mma(const MmaDev p, co
         }
       }
       // P^T as B operands: keys are rows of the k step
-      uint32_t pf[4][NT][2];
+      uint32_t pf[MT][NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         const float b0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0] * f, b1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1] * f;
 #pragma unroll
-        for (int mt = 0; mt < 4; ++mt) {
+        for (int mt = 0; mt < MT; ++mt) {
           float p0 = exp2f(fmaf(z[mt][nt][0], f, -b0)), p1 = exp2f(fmaf(z[mt][nt][1], f, -b1));
           float p2 = exp2f(fmaf(z[mt][nt][2], f, -b0)), p3 = exp2f(fmaf(z[mt][nt][3], f, -b1));
           l[nt][0] += p0 + p2;
           l[nt][1] += p1 + p3;
           if constexpr (kFp8) {        // the values' scales ride on P; a hidden row's scale may be anything
-            const float v0 = s.scale[stage][1][mt * 16 + g4], v1 = s.scale[stage][1][mt * 16 + g4 + 8];
+            const float v0 = scale[kKeys + mt * 16 + g4], v1 = scale[kKeys + mt * 16 + g4 + 8];
             p0 = p0 == 0.f ? 0.f : p0 * v0; p1 = p1 == 0.f ? 0.f : p1 * v0;
             p2 = p2 == 0.f ? 0.f : p2 * v1; p3 = p3 == 0.f ? 0.f : p3 * v1;
           }
@@ -466,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_mma(const MmaDev p, co
       }
       // O^T += V^T P^T; value rows that no row of the unit sees become zeros
 #pragma unroll
-      for (int mt = 0; mt < 4; ++mt) {
+      for (int mt = 0; mt < MT; ++mt) {
         uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
         if (!full) {
           uint32_t k[4];
@@ -482,9 +436,8 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_mma(const MmaDev p, co
           const int key = mt * 16 + (lane & 7) + (lane >> 4) * 8;
 #pragma unroll
           for (int d = 0; d < D / 16; ++d) {
-            const int ch = (d & 3) * 2 + ((lane >> 3) & 1);
             uint32_t v[4];
-            ldsm_t(vb + (d >> 2) * (kTile * 128) + key * 128 + ((ch ^ (key & 7)) << 4), v);
+            ldsm_t(vb + chunk_at<S::kRow>(key, 2 * d + ((lane >> 3) & 1)), v);
             if (!full) { v[0] &= keep0; v[1] &= keep0; v[2] &= keep1; v[3] &= keep1; }
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) mma16816(o[d][nt], v, pf[mt][nt]);
@@ -493,13 +446,10 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_mma(const MmaDev p, co
           // matrices: keys 0-7 and 8-15 of 16-code chunk 2c, then of chunk 2c + 1; a transposed
           // word holds codes (key, dim 2 g4), (key, dim 2 g4 + 1) of two keys: the MMA's rows g4
           // and g4 + 8 are dims 2 g4 and 2 g4 + 1 of the chunk
-          const int key = mt * 16 + (lane & 7) + ((lane >> 3) & 1) * 8;
 #pragma unroll
           for (int c = 0; c < D / 32; ++c) {
-            const int byte = c * 32 + (lane >> 4) * 16, ch = byte % S::kBoxBytes / 16;
-            const int sw = S::kBoxBytes == 128 ? ch ^ (key & 7) : ch ^ ((key >> 1) & 3);
             uint32_t w[4];
-            ldsm_t(vb + byte / S::kBoxBytes * (kTile * S::kBoxBytes) + key * S::kBoxBytes + (sw << 4), w);
+            ldsm_t(vb + chunk_at<S::kRow>(mt * 16 + lr, 2 * c + (lane >> 4)), w);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const uint32_t lo = w[2 * h], hi = w[2 * h + 1];
@@ -512,11 +462,14 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_mma(const MmaDev p, co
           }
         }
       }
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&s.empty[stage]);
     }
 
-    // ---- the four warps' results meet ----
+    // ---- the warps' results meet: o [R][D] fp32 in the stage read last ----
+    // (float index r D + (d with bits 3..4 turned by r / 2): the rows that one
+    // store touches lie in different banks)
+    __syncwarp();
+    float* mine_o = reinterpret_cast<float*>(ring + last * S::kStage);
+    if (lane == 0) s.buf[warp] = int(ring - smem) + last * S::kStage;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -525,24 +478,29 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_mma(const MmaDev p, co
         t += __shfl_xor_sync(0xffffffffu, t, 4);
         t += __shfl_xor_sync(0xffffffffu, t, 8);
         t += __shfl_xor_sync(0xffffffffu, t, 16);
-        const int r = nt * 8 + c2 + e;
+        const int r = nt * 8 + c2 + e, turn = ((r >> 1) & 3) << 3;
+        // a column without a key leaves nothing (a warp without a tile of this segment has no free
+        // stage either); one whose logits are all NaN has m = -inf and a NaN sum, and is passed on
+        const bool none = m[nt][e] == -INFINITY && t == 0.f;
         if (g4 == 0) {
-          s.ml[warp][r][0] = m[nt][e] == -INFINITY ? -INFINITY : m[nt][e] * f;
+          s.ml[warp][r][0] = none ? -INFINITY : m[nt][e] == -INFINITY ? 0.f : m[nt][e] * f;
           s.ml[warp][r][1] = t;
         }
+        if (!none) {
 #pragma unroll
-        for (int d = 0; d < D / 16; ++d) {
-          // rows of the accumulator: dims g4, g4 + 8 (fp8: dims 2 g4, 2 g4 + 1)
-          s.o[warp][r][d * 16 + (kFp8 ? 2 * g4 : g4)] = o[d][nt][e];
-          s.o[warp][r][d * 16 + (kFp8 ? 2 * g4 + 1 : g4 + 8)] = o[d][nt][e + 2];
+          for (int d = 0; d < D / 16; ++d) {
+            // rows of the accumulator: dims g4, g4 + 8 (fp8: dims 2 g4, 2 g4 + 1)
+            mine_o[r * D + ((d * 16 + (kFp8 ? 2 * g4 : g4)) ^ turn)] = o[d][nt][e];
+            mine_o[r * D + ((d * 16 + (kFp8 ? 2 * g4 + 1 : g4 + 8)) ^ turn)] = o[d][nt][e + 2];
+          }
         }
       }
     }
-    compute_sync();
+    __syncthreads();
     const bool begins = pc.tile == 0, ends = pc.tile + count == un.tr.tiles;
     const int64_t part = int64_t(blockIdx.x) * 2 + (begins ? 1 : 0);
-    for (int i = tid; i < R * D / 4; i += 32 * kWarps) {
-      const int r = i / (D / 4), d = i % (D / 4) * 4;
+    for (int i = tid; i < R * D / 4; i += kThreads) {
+      const int r = i / (D / 4), d = i % (D / 4) * 4, turn = ((r >> 1) & 3) << 3;
       if (r >= un.rows) continue;
       float top = -INFINITY;
 #pragma unroll
@@ -550,9 +508,10 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_mma(const MmaDev p, co
       float sum = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        const float wt = s.ml[w][r][0] == -INFINITY ? 0.f : exp2f(s.ml[w][r][0] - top);
+        if (s.ml[w][r][0] == -INFINITY) continue;
+        const float wt = exp2f(s.ml[w][r][0] - top);
         sum = fmaf(wt, s.ml[w][r][1], sum);
-        const float4 t = *reinterpret_cast<const float4*>(&s.o[w][r][d]);
+        const float4 t = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(smem + s.buf[w]) + r * D + (d ^ turn));
         v[0] = fmaf(wt, t.x, v[0]); v[1] = fmaf(wt, t.y, v[1]);
         v[2] = fmaf(wt, t.z, v[2]); v[3] = fmaf(wt, t.w, v[3]);
       }
@@ -574,10 +533,11 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_mma(const MmaDev p, co
       const int64_t end = pre[pc.u] + int64_t(pc.hk + 1) * un.tr.tiles;
       desc = JoinDesc{1, un.b, pc.u % p.RG, pc.hk, int((end * ctas - 1) / s.total), {0, 0, 0}};
     }
-    ok = compute_sync_and(ok);     // all four warps go on or stop together
+    __syncthreads();              // the stages are read
     x += count;
   }
-  if (p.split && tid == 0) p.join[blockIdx.x] = ok ? desc : JoinDesc{};
+  if (p.split && tid == 0) p.join[blockIdx.x] = desc;
+  pdl_trigger();
 }
 
 // Joins the pieces of a unit that several CTAs hold: piece c's slot 1, then
@@ -591,8 +551,8 @@ __global__ void __launch_bounds__(256) dense_attn_join(const MmaDev p) {
   __shared__ float red[8];
   const int c = blockIdx.x, r = blockIdx.y, tid = threadIdx.x;
   const DenseAttnDev& a = p.a;
-  pdl_trigger();
   pdl_wait();
+  pdl_trigger();
   const JoinDesc j = p.join[c];
   if (!j.valid) return;
   const int s0 = a.starts[j.b], n = a.starts[j.b + 1] - s0;
@@ -657,19 +617,16 @@ size_t workspace_of(const v4a_dense_attn_args* a) {
 }
 
 template <int D, int NT, bool kFp8>
-int launch(MmaDev& p, const v4a_dense_attn_args* a, cudaStream_t stream) {
+int launch(MmaDev& p, cudaStream_t stream) {
   using S = Shape<D, NT, kFp8>;
-  CUtensorMap map;
-  const auto sw = S::kBoxBytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
-  if (!dense_rows_map(&map, a->kv, p.a.block_bytes, S::kBox, kTile, sw)) return V4A_ERR_CUDA;
-  const size_t smem = 1024 + S::kStages * S::kStage + sizeof(typename S::Tail) +
+  const size_t smem = S::kWarps * S::kStages * S::kStage + sizeof(typename S::Tail) +
                       (p.split ? p.a.B * sizeof(SeqRun) + (p.U + 1) * sizeof(int64_t) : sizeof(SeqRun));
   if (smem > 227 * 1024) return V4A_ERR_UNSUPPORTED;
   auto kern = dense_attn_mma<D, NT, kFp8>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024) != cudaSuccess) return V4A_ERR_CUDA;
   const int64_t grid = p.split ? kCtas : int64_t(p.U) * p.a.K;
   if (grid > INT32_MAX) return V4A_ERR_UNSUPPORTED;
-  cudaError_t e = launch_pdl(kern, dim3(unsigned(grid)), dim3(kThreads), smem, stream, p, map);
+  cudaError_t e = launch_pdl(kern, dim3(unsigned(grid)), dim3(S::kThreads), smem, stream, p);
   if (e == cudaSuccess && p.split) e = launch_pdl(dense_attn_join<D, S::R>, dim3(unsigned(grid), S::R), dim3(256), 0, stream, p);
   return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? V4A_OK : V4A_ERR_CUDA;
 }
@@ -678,10 +635,10 @@ template <bool kFp8>
 int launch_dim(MmaDev& p, const v4a_dense_attn_args* a, cudaStream_t stream) {
   const bool two = rows_of(a) == 16;
   switch (a->kv.dim) {
-    case 64: return two ? launch<64, 2, kFp8>(p, a, stream) : launch<64, 1, kFp8>(p, a, stream);
-    case 128: return two ? launch<128, 2, kFp8>(p, a, stream) : launch<128, 1, kFp8>(p, a, stream);
-    case 192: return two ? launch<192, 2, kFp8>(p, a, stream) : launch<192, 1, kFp8>(p, a, stream);
-    default: return launch<256, 1, kFp8>(p, a, stream);
+    case 64: return two ? launch<64, 2, kFp8>(p, stream) : launch<64, 1, kFp8>(p, stream);
+    case 128: return two ? launch<128, 2, kFp8>(p, stream) : launch<128, 1, kFp8>(p, stream);
+    case 192: return two ? launch<192, 2, kFp8>(p, stream) : launch<192, 1, kFp8>(p, stream);
+    default: return launch<256, 1, kFp8>(p, stream);
   }
 }
 
@@ -699,20 +656,6 @@ int check_shape(const v4a_dense_attn_args* a) {
 }
 
 }  // namespace
-
-bool dense_rows_map(CUtensorMap* map, const v4a_dense_cache& c, int64_t block_bytes, int box, int rows,
-                    CUtensorMapSwizzle swizzle) {
-  auto encode = tc::encode_fn();
-  if (!encode) return false;
-  const bool fp8 = c.format == V4A_KV_FP8_TOKEN;
-  const cuuint64_t row = cuuint64_t(c.dim) * (fp8 ? 1 : 2);
-  const cuuint64_t dims[4] = {cuuint64_t(c.dim), 256, cuuint64_t(2 * c.num_kv_heads), cuuint64_t(c.num_blocks)};
-  const cuuint64_t strides[3] = {row, 256 * row, cuuint64_t(block_bytes)};
-  const cuuint32_t boxes[4] = {cuuint32_t(box), cuuint32_t(rows), 1, 1}, es[4] = {1, 1, 1, 1};
-  return encode(map, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, c.pool, dims, strides, boxes,
-                es, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
 
 size_t dense_attn_workspace_size(const v4a_dense_attn_args* a) { return check_shape(a) ? 0 : workspace_of(a); }
 

@@ -67,9 +67,4 @@ __device__ __forceinline__ bool all_visible(const DenseAttnDev& a, int m_lo, int
   return j + n - 1 <= m_lo && (a.window == 0 || j > m_hi - a.window || j + n <= a.sinks);
 }
 
-// The tensor map of a cache's rows: [block][key heads, value heads][256][dim],
-// boxes of `box` elements x `rows` positions.  False when the encoder fails.
-bool dense_rows_map(CUtensorMap* map, const v4a_dense_cache& c, int64_t block_bytes, int box, int rows,
-                    CUtensorMapSwizzle swizzle);
-
 }  // namespace v4a

@@ -510,6 +510,67 @@ def test_chunk_equals_single_tokens():
     layer.check(q, out, lse, pos, starts, 0, 0, op.args.softmax_scale, tokens=set(range(0, 130, 9)))
 
 
+def _reference(pool, table, b, m, q, K, dim, fp8, h):
+    """fp64 on the GPU for one query head group: (o, lse) over positions 0..m (bf16 or fp8 caches of long tests)."""
+    n, body = m + 1, 2 * K * 256 * dim
+    page = table[b, :(n + 255) // 256].long()
+    if fp8:
+        rows = pool[page][:, :body].view(torch.float8_e4m3fn).double().view(-1, 2, K, 256, dim)[:, :, h]
+        rows = rows * pool[page][:, body:body + 8 * K * 256].contiguous().view(torch.float32).double().view(-1, 2, K, 256, 1)[:, :, h]
+    else:
+        rows = pool[page][:, :2 * body].contiguous().view(torch.bfloat16).view(-1, 2, K, 256, dim)[:, :, h].double()
+    k, v = (rows[:, i].reshape(-1, dim)[:n] for i in (0, 1))
+    z = q.double() @ k.T / math.sqrt(dim)
+    p = torch.softmax(z, -1)
+    return p @ v, torch.logsumexp(z, -1), p @ v.abs(), (q.double().abs() @ k.abs().T).amax(-1) / math.sqrt(dim)
+
+
+@pytest.mark.parametrize("lengths,H,K,dim,fp8", [((30000, 20011, 1), 16, 4, 128, False), ((40001, 255), 16, 2, 128, True),
+                                                  ((25000,), 4, 4, 64, False), ((9000, 14000), 2, 2, 256, False)])
+def test_long_caches(lengths, H, K, dim, fp8):
+    """Hundreds of tiles per CTA, ranges over several sequences and KV heads."""
+    D = _dense()
+    g = torch.Generator(device=DEV).manual_seed(H + dim)
+    held = [-(-n // 256) for n in lengths]
+    ids = torch.randperm(sum(held) + 2, generator=g, device=DEV).to(torch.int32)
+    table = torch.full((len(lengths), max(held)), -1, dtype=torch.int32, device=DEV)
+    for b, n in enumerate(held):
+        table[b, :n] = ids[sum(held[:b]):sum(held[:b]) + n]
+    body = 2 * K * 256 * dim
+    x = torch.randn((len(ids), body), generator=g, device=DEV)
+    if fp8:
+        sc = (torch.rand((len(ids), 2 * K * 256), generator=g, device=DEV) + 0.5) / 100
+        pool = torch.cat([(x * 100).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8), sc.view(torch.uint8)], 1)
+    else:
+        pool = x.to(torch.bfloat16).view(torch.uint8)
+    T = len(lengths)
+    q = torch.randn((T, H, dim), generator=g, device=DEV).mul_(2).to(torch.bfloat16)
+    out, lse = torch.empty_like(q), torch.empty((T, H), device=DEV)
+    op = D.DenseAttention(D.DenseCache(pool, table, K, dim, D.KV_FP8_TOKEN if fp8 else D.KV_BF16), H, T)
+    op.run(q, out, torch.tensor([n - 1 for n in lengths], dtype=torch.int32, device=DEV), torch.arange(T + 1, dtype=torch.int32, device=DEV), lse)
+    torch.cuda.synchronize()
+    assert int(op.status.item()) == 0
+    G = H // K
+    for b, n in enumerate(lengths):
+        for h in range(K):
+            s = slice(h * G, (h + 1) * G)
+            o, l, av, amp = _reference(pool, table, b, n - 1, q[b, s], K, dim, fp8, h)
+            dz, dn = (dim + 8) * 2.0 ** -24 * amp[:, None], (n + 32) * 2.0 ** -24
+            assert ((out[b, s].double() - o).abs() <= (2.0 ** -8 + 2 * dz + 2 * dn) * av + 2.0 ** -8 * o.abs()).all(), (b, h)
+            assert ((lse[b, s].double() - l).abs() <= dz[:, 0] + dn + 2.0 ** -22 * l.abs() + 2.0 ** -20).all(), (b, h)
+
+
+def test_nan_query_gives_nan():
+    layer = Layer((300, 90), 8, 2, 64, False, seed=30)
+    op = _dense().DenseAttention(layer.cache, 8, 2)
+    q = layer.query(2)
+    q[0, 3, 5] = math.nan
+    out, lse = torch.zeros_like(q), torch.zeros((2, 8), device=DEV)
+    op.run(q, out, torch.tensor([299, 89], dtype=torch.int32, device=DEV), torch.arange(3, dtype=torch.int32, device=DEV), lse)
+    assert out[0, 3].isnan().all() and lse[0, 3].isnan()
+    assert int(out.isnan().sum()) == 64 and int(lse.isnan().sum()) == 1
+
+
 def test_same_call_same_bytes():
     layer = Layer((5000, 100, 2600), 16, 2, 128, False, seed=12)
     op, q, out, lse = _attend(layer, [4999, 99, 2599], [0, 1, 2, 3], tokens={1})
