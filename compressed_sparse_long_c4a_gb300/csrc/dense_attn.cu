@@ -88,6 +88,24 @@ __device__ __forceinline__ void mma16816(float* c, const uint32_t* a, const uint
                : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
 }
+// The same product with f16 operands.
+__device__ __forceinline__ void mma16816_f16(float* c, const uint32_t* a, const uint32_t* b) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+// Two e4m3 codes (low byte first) as f16, exactly.
+__device__ __forceinline__ uint32_t e4m3_f16(uint32_t codes) {
+  uint32_t r;
+  asm("{\n.reg .b16 c;\ncvt.u16.u32 c, %1;\ncvt.rn.f16x2.e4m3x2 %0, c;\n}\n" : "=r"(r) : "r"(codes));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+// log2 of a value row's scale, at least -100 (a NaN stays one).
+__device__ __forceinline__ float scale_log2(float s) { return s > 0x1p-100f ? log2f(s) : s <= 0x1p-100f ? -100.f : s; }
 // Codes b0 and b2 (or b1 and b3) of w as a bf16 pair times 2^-120 (sign to bit
 // 15, the 7 magnitude bits to bits 4..10: the code's value with the exponent
 // biased by 127 instead of 7), then times 2^120, exactly; subnormal codes too.
@@ -369,21 +387,35 @@ __global__ void __launch_bounds__(Shape<D, NT, kFp8>::kThreads, 1) dense_attn_mm
             for (int e = 0; e < 4; ++e)
               if (!visible(a, mrow[nt][e & 1], j0 + mt * 16 + g4 + (e >> 1) * 8)) z[mt][nt][e] = -INFINITY;
       }
+      // In log2 units from here.  fp8: the values' scales are a part of the exponent (w_j = z_j + log2
+      // sv_j, whose running maximum is taken), so that P = 2^{w - m} is 1 at its largest whatever the
+      // scales are and fits f16, whose 11 bits keep the single dominating key exact to 2^-12 (a bf16
+      // product p sv lost up to 2^-9 there); 2^15 P uses f16's upper range, so that keys down to
+      // 2^-39 of the largest count.  l sums 2^{z - m} itself: at most 2^100 a key.
+      float ls[MT][2];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        ls[mt][0] = kFp8 ? scale_log2(scale[kKeys + mt * 16 + g4]) : 0.f;
+        ls[mt][1] = kFp8 ? scale_log2(scale[kKeys + mt * 16 + g4 + 8]) : 0.f;
+      }
       bool grew = false;
       float alpha[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float t = fmaxf(z[0][nt][e], z[0][nt][e + 2]);
+          float t = -INFINITY;
 #pragma unroll
-          for (int mt = 1; mt < MT; ++mt) t = fmaxf(t, fmaxf(z[mt][nt][e], z[mt][nt][e + 2]));
+          for (int mt = 0; mt < MT; ++mt)
+            t = kFp8 ? fmaxf(t, fmaxf(fmaf(z[mt][nt][e], f, ls[mt][0]), fmaf(z[mt][nt][e + 2], f, ls[mt][1])))
+                     : fmaxf(t, fmaxf(z[mt][nt][e], z[mt][nt][e + 2]));
           t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
           t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
           t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
+          if (!kFp8) t *= f;
           const float top = fmaxf(m[nt][e], t);
           grew |= top > m[nt][e];
-          alpha[nt][e] = top == -INFINITY ? 1.f : exp2f((m[nt][e] - top) * f);
+          alpha[nt][e] = top == -INFINITY ? 1.f : exp2f(m[nt][e] - top);
           m[nt][e] = top;
         }
       if (__any_sync(0xffffffffu, grew)) {
@@ -402,20 +434,23 @@ __global__ void __launch_bounds__(Shape<D, NT, kFp8>::kThreads, 1) dense_attn_mm
       uint32_t pf[MT][NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        const float b0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0] * f, b1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1] * f;
+        const float b0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0], b1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
-          float p0 = exp2f(fmaf(z[mt][nt][0], f, -b0)), p1 = exp2f(fmaf(z[mt][nt][1], f, -b1));
-          float p2 = exp2f(fmaf(z[mt][nt][2], f, -b0)), p3 = exp2f(fmaf(z[mt][nt][3], f, -b1));
+          const float y0 = fmaf(z[mt][nt][0], f, -b0), y1 = fmaf(z[mt][nt][1], f, -b1);
+          const float y2 = fmaf(z[mt][nt][2], f, -b0), y3 = fmaf(z[mt][nt][3], f, -b1);
+          const float p0 = exp2f(y0), p1 = exp2f(y1), p2 = exp2f(y2), p3 = exp2f(y3);
           l[nt][0] += p0 + p2;
           l[nt][1] += p1 + p3;
-          if constexpr (kFp8) {        // the values' scales ride on P; a hidden row's scale may be anything
-            const float v0 = scale[kKeys + mt * 16 + g4], v1 = scale[kKeys + mt * 16 + g4 + 8];
-            p0 = p0 == 0.f ? 0.f : p0 * v0; p1 = p1 == 0.f ? 0.f : p1 * v0;
-            p2 = p2 == 0.f ? 0.f : p2 * v1; p3 = p3 == 0.f ? 0.f : p3 * v1;
+          if constexpr (kFp8) {        // a hidden row has y = -inf; its scale may be anything
+            auto weight = [](float y, float s) { return y == -INFINITY ? 0.f : exp2f(y + s); };
+            const float s0 = ls[mt][0] + 15.f, s1 = ls[mt][1] + 15.f;
+            pf[mt][nt][0] = transpose8(pack_f16(weight(y0, s0), weight(y1, s0)));
+            pf[mt][nt][1] = transpose8(pack_f16(weight(y2, s1), weight(y3, s1)));
+          } else {
+            pf[mt][nt][0] = transpose8(pack_bf16(p0, p1));
+            pf[mt][nt][1] = transpose8(pack_bf16(p2, p3));
           }
-          pf[mt][nt][0] = transpose8(pack_bf16(p0, p1));
-          pf[mt][nt][1] = transpose8(pack_bf16(p2, p3));
         }
       }
       // O^T += V^T P^T; value rows that no row of the unit sees become zeros
@@ -453,11 +488,11 @@ __global__ void __launch_bounds__(Shape<D, NT, kFp8>::kThreads, 1) dense_attn_mm
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const uint32_t lo = w[2 * h], hi = w[2 * h + 1];
-              uint32_t v[4] = {e4m3_pair(__byte_perm(lo, 0, 0x2404)), e4m3_pair(__byte_perm(lo, 0, 0x3414)),
-                               e4m3_pair(__byte_perm(hi, 0, 0x2404)), e4m3_pair(__byte_perm(hi, 0, 0x3414))};
+              const uint32_t pl = __byte_perm(lo, 0, 0x3120), ph = __byte_perm(hi, 0, 0x3120);
+              uint32_t v[4] = {e4m3_f16(pl), e4m3_f16(pl >> 16), e4m3_f16(ph), e4m3_f16(ph >> 16)};
               if (!full) { v[0] &= keep0; v[1] &= keep0; v[2] &= keep1; v[3] &= keep1; }
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt) mma16816(o[2 * c + h][nt], v, pf[mt][nt]);
+              for (int nt = 0; nt < NT; ++nt) mma16816_f16(o[2 * c + h][nt], v, pf[mt][nt]);
             }
           }
         }
@@ -483,15 +518,16 @@ __global__ void __launch_bounds__(Shape<D, NT, kFp8>::kThreads, 1) dense_attn_mm
         // stage either); one whose logits are all NaN has m = -inf and a NaN sum, and is passed on
         const bool none = m[nt][e] == -INFINITY && t == 0.f;
         if (g4 == 0) {
-          s.ml[warp][r][0] = none ? -INFINITY : m[nt][e] == -INFINITY ? 0.f : m[nt][e] * f;
+          s.ml[warp][r][0] = none ? -INFINITY : m[nt][e] == -INFINITY ? 0.f : m[nt][e];
           s.ml[warp][r][1] = t;
         }
         if (!none) {
 #pragma unroll
           for (int d = 0; d < D / 16; ++d) {
             // rows of the accumulator: dims g4, g4 + 8 (fp8: dims 2 g4, 2 g4 + 1)
-            mine_o[r * D + ((d * 16 + (kFp8 ? 2 * g4 : g4)) ^ turn)] = o[d][nt][e];
-            mine_o[r * D + ((d * 16 + (kFp8 ? 2 * g4 + 1 : g4 + 8)) ^ turn)] = o[d][nt][e + 2];
+            constexpr float unit = kFp8 ? 0x1p-15f : 1.f;
+            mine_o[r * D + ((d * 16 + (kFp8 ? 2 * g4 : g4)) ^ turn)] = o[d][nt][e] * unit;
+            mine_o[r * D + ((d * 16 + (kFp8 ? 2 * g4 + 1 : g4 + 8)) ^ turn)] = o[d][nt][e + 2] * unit;
           }
         }
       }
@@ -680,6 +716,7 @@ int dense_attn(const v4a_dense_attn_args* a, void* ws, size_t ws_bytes, cudaStre
   d.pool = static_cast<const uint8_t*>(a->kv.pool);
   d.q = a->q; d.out = a->out; d.lse = a->lse; d.status = a->status;
   d.scale_log2 = a->softmax_scale * 1.4426950408889634f;
+  if (dense_prefill_takes(a)) return dense_prefill(d, a->kv.dim, stream);
   p.RG = int(row_groups(a));
   p.U = d.B * p.RG;
   p.split = p.U <= kMaxUnits;

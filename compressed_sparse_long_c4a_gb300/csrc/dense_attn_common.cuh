@@ -67,4 +67,8 @@ __device__ __forceinline__ bool all_visible(const DenseAttnDev& a, int m_lo, int
   return j + n - 1 <= m_lo && (a.window == 0 || j > m_hi - a.window || j + n <= a.sinks);
 }
 
+// The tensor-core form for many rows (dense_prefill.cu): whether it takes the shape, and its launch.
+bool dense_prefill_takes(const v4a_dense_attn_args* a);
+int dense_prefill(const DenseAttnDev& d, int dim, cudaStream_t stream);
+
 }  // namespace v4a

@@ -1,0 +1,370 @@
+// Attention of chunks over the dense paged cache on the tensor cores
+// (v4a_dense_attn with many query rows per KV head; bf16 caches, dim 64 and
+// 128): tcgen05 kind::f16 with the accumulators in TMEM.
+//
+// Mathematics: as dense_attn.cu, one pass over the keys with a running
+// maximum and sum per row.  The rows of a CTA are 256 consecutive (token,
+// head of the group) pairs of one sequence and KV head, as two tiles of 128:
+// both read each key tile, and while one tile is in its softmax the tensor
+// cores work for the other.  The maximum that P is formed against is raised
+// only when a row's logits pass it by more than 2^8, so the output
+// accumulator is rescaled a few times per row instead of once per key tile;
+// P <= 2^8 then, which bf16 holds as well as values up to one, and l uses the
+// same maximum.
+//
+//   S_t = Q_t K^T   M = 128, N = 128 keys, K = dim     TMEM columns [128 t, +128)
+//   P_t = 2^{S f - m} in bf16, over S_t's columns       [128 t, +64)
+//   O_t += P_t V    M = 128, N = dim, K = 128 keys      [256 + 128 t, +dim)
+//                   (P from TMEM, V as an MN-major operand)
+//
+// Roles (12 warps): 0-3 and 4-7 the two tiles' softmax (a thread owns a row),
+// 8 and 9 one MMA issuer per tile, 10 and 11 copy keys and values (16-byte
+// cp.async into the 128-byte swizzle; rows that no row of the CTA sees are
+// filled with zeros, so what they hold cannot reach a product).  Keys and
+// values have two buffers each.
+//
+// Bound: the tensor cores (4 dim flops per visible pair), and beside them the
+// exponentials: 128 x 128 per tile and step.
+#include "dense_attn_common.cuh"
+
+namespace v4a {
+namespace {
+
+constexpr int kRows = 128;           // rows of a tile (MMA M)
+constexpr int kKeys = 128;           // keys per step
+constexpr int kThreads = 384;
+constexpr int kLoaders = 64;
+constexpr float kRaise = 8.f;        // log2 units by which logits may pass the maximum in use
+
+struct PreSmem {
+  uint64_t q_full, k_full[2], v_full[2], k_free[2], v_free[2], s_full[2], p_full[2], o_full[2], drain[2];
+  uint32_t tmem_base;
+  int abort_flag;
+  int missing[4];                    // step i's page is missing: [i % 4]
+  SeqRun run;
+};
+
+// MN-major operand (as in attn_tc.cu): 64-element rows along N, 8-row groups
+// 1024 bytes apart, the next 64 columns `lbo` bytes further.
+__device__ __forceinline__ uint64_t desc_mn(uint32_t saddr, uint32_t lbo) {
+  return uint64_t((saddr & 0x3FFFFu) >> 4) | (uint64_t((lbo >> 4) & 0x3FFFu) << 16) | (uint64_t(1024 >> 4) << 32) |
+         (uint64_t(1) << 46) | (uint64_t(2) << 61);
+}
+// D += A B with A in TMEM (bf16 pairs, one row per lane).
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// 32 lanes x 32 columns of 32 bits into TMEM (not waited for).
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};\n" ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]),
+      "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]),
+      "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]),
+      "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+      "tcgen05.wait::ld.sync.aligned;\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]),
+        "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]),
+        "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// 16 bytes global -> shared, or zeros.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool live) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&b);
+}
+
+// Byte offset of 16-byte chunk `ch` of row r in an operand of [dim / 64][128 rows][128 bytes], swizzled.
+__device__ __forceinline__ uint32_t chunk_at(int r, int ch) {
+  return uint32_t((ch >> 3) * (128 * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4));
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) dense_prefill_kernel(const DenseAttnDev a) {
+  constexpr int kTileBytes = 128 * D * 2;      // a Q tile, a step's keys or its values
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t q0 = tc::smem_u32(base), k0 = q0 + 2 * kTileBytes, v0 = k0 + 2 * kTileBytes;
+  PreSmem& s = *reinterpret_cast<PreSmem*>(base + 6 * kTileBytes);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int hk = blockIdx.x % a.K, b = blockIdx.x / a.K;
+  const int row0 = int(gridDim.y - 1 - blockIdx.y) * (2 * kRows);     // later rows see more keys: first
+  volatile int* abort_flag = &s.abort_flag;
+
+  pdl_wait();
+  if (tid == 0) s.run = seq_run(a, b, hk == 0 && row0 == 0 ? a.status : nullptr);
+  __syncthreads();
+  const SeqRun run = s.run;
+  const int rows = min(2 * kRows, run.n * a.G - row0);
+  if (rows <= 0) return;
+  const int tiles = rows > kRows ? 2 : 1;
+  const int m_lo = run.p0 + row0 / a.G, m_hi = run.p0 + (row0 + rows - 1) / a.G;
+  const TileRange<kKeys> tr = tile_range<kKeys>(a, m_lo, m_hi);
+
+  if (tid == 0) {
+    tc::mbar_init(&s.q_full, 256);
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(&s.k_full[i], kLoaders);
+      tc::mbar_init(&s.v_full[i], kLoaders);
+      tc::mbar_init(&s.k_free[i], tiles);
+      tc::mbar_init(&s.v_free[i], tiles);
+      tc::mbar_init(&s.s_full[i], 1);
+      tc::mbar_init(&s.p_full[i], 4);
+      tc::mbar_init(&s.o_full[i], 1);
+      tc::mbar_init(&s.drain[i], 1);
+    }
+    s.abort_flag = 0;
+    tc::mbar_fence_init();
+  }
+  __syncwarp();
+  if (warp == 0) tc::tmem_alloc(&s.tmem_base, 512);
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = s.tmem_base;
+
+  if (warp < 8) {
+    // ---- Q into shared memory (rows behind the last are zeros), then the softmax of one tile ----
+    for (int c = tid; c < tiles * kRows * (D / 8); c += 256) {
+      const int r = c / (D / 8), ch = c % (D / 8), i = row0 + min(r, rows - 1);
+      const uint16_t* q = a.q + (int64_t(run.s0 + i / a.G) * a.H + hk * a.G + i % a.G) * D;
+      copy16(q0 + (r >> 7) * kTileBytes + chunk_at(r & 127, ch), q + ch * 8, r < rows);
+    }
+    tc::cp_async_wait_all();
+    tc::fence_proxy_async();
+    tc::mbar_arrive(&s.q_full);
+    const int t = warp >> 2, r = tid & 127;
+    if (t < tiles) {
+      const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
+      const uint32_t s_at = tmem + 128 * t + lanes, o_at = tmem + 256 + 128 * t + lanes;
+      const float f = a.scale_log2;
+      const int row = t * kRows + r, m = run.p0 + (row0 + min(row, rows - 1)) / a.G;
+      float top = -INFINITY, ref = 0.f, l = 0.f;       // largest logit, the maximum in use, the sum against it
+      bool any = false;                                // `ref` is set (a key has been seen)
+      bool ok = true;
+      for (int i = 0; i < tr.tiles; ++i) {
+        ok = __all_sync(0xffffffffu, tc::mbar_wait(&s.s_full[t], i & 1, a.status, abort_flag));
+        if (!ok) break;
+        tc::tc_fence_after();
+        float z[128];
+        tc::tmem_ld64(s_at, z);
+        tc::tmem_ld64(s_at + 64, z + 64);
+        const int j0 = tr.at(i) * kKeys;
+        const bool gone = s.missing[i & 3] != 0;
+        if (gone || !all_visible(a, m_lo, m_hi, j0, kKeys)) {
+          const int hi = gone ? -1 : m - j0, lo = a.window ? m - a.window - j0 : -1, sk = a.window ? a.sinks - j0 : 0;
+#pragma unroll
+          for (int c = 0; c < 128; ++c)
+            if (c > hi || (c <= lo && c >= sk)) z[c] = -INFINITY;
+        }
+        float mx[4] = {z[0], z[1], z[2], z[3]};
+#pragma unroll
+        for (int c = 4; c < 128; ++c) mx[c & 3] = fmaxf(mx[c & 3], z[c]);
+        top = fmaxf(top, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * f);
+        const bool raise = top > -INFINITY && (!any || top > ref + kRaise);
+        if (__any_sync(0xffffffffu, raise && any)) {   // the step before has left the accumulator: its MMAs precede S
+          const float w = raise && any ? exp2f(ref - top) : 1.f;
+          l *= w;
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            float o[32];
+            tmem_ld32(o_at + c, o);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] *= w;
+            tmem_st32(o_at + c, reinterpret_cast<const uint32_t*>(o));
+          }
+          tmem_wait_st();
+        }
+        if (raise) {
+          ref = top;
+          any = true;
+        }
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c0 = 0; c0 < 128; c0 += 64) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int c = 0; c < 64; c += 2) {
+            const float p0 = exp2f(fmaf(z[c0 + c], f, -ref)), p1 = exp2f(fmaf(z[c0 + c + 1], f, -ref));
+            sum[c & 2] += p0;
+            sum[(c & 2) + 1] += p1;
+            pk[c >> 1] = pack_bf16(p0, p1);
+          }
+          tmem_st32(s_at + c0 / 2, pk);
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        tmem_wait_st();
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&s.p_full[t]);
+      }
+      // ---- the output ----
+      if (ok) ok = __all_sync(0xffffffffu, tc::mbar_wait(&s.o_full[t], 0, a.status, abort_flag));
+      if (ok) {
+        tc::tc_fence_after();
+        const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;
+        const int i = row0 + row;
+        const int64_t at = int64_t(run.s0 + i / a.G) * a.H + hk * a.G + i % a.G;
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          float o[32];
+          tmem_ld32(o_at + c, o);
+          if (row < rows) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 8)
+              *reinterpret_cast<uint4*>(a.out + at * D + c + e) =
+                  make_uint4(pack_bf16(o[e] * inv, o[e + 1] * inv), pack_bf16(o[e + 2] * inv, o[e + 3] * inv),
+                             pack_bf16(o[e + 4] * inv, o[e + 5] * inv), pack_bf16(o[e + 6] * inv, o[e + 7] * inv));
+          }
+          __syncwarp();
+        }
+        if (row < rows && a.lse) a.lse[at] = any ? (ref + log2f(l)) * 0.6931471805599453f : l == 0.f ? -INFINITY : l;
+      }
+      tc::tc_fence_before();
+    }
+  } else if (warp < 10) {
+    // ---- one MMA issuer per tile ----
+    const int t = warp - 8;
+    if (t < tiles && lane == 0) {
+      const uint32_t idesc_s = tc::make_idesc(1, 1, kRows, kKeys);
+      const uint32_t idesc_o = tc::make_idesc(1, 1, kRows, D) | (1u << 16);       // B is MN-major
+      const uint32_t st = tmem + 128 * t, ot = tmem + 256 + 128 * t, qa = q0 + t * kTileBytes;
+      auto scores = [&](int i) {
+        const uint32_t kb = k0 + (i & 1) * kTileBytes;
+#pragma unroll
+        for (int e = 0; e < D / 16; ++e)
+          tc::mma_f16(st, tc::desc_sw128(qa + (e >> 2) * (128 * 128)) + 2 * (e & 3),
+                      tc::desc_sw128(kb + (e >> 2) * (128 * 128)) + 2 * (e & 3), idesc_s, e > 0);
+        tc::mma_commit(&s.s_full[t]);
+        tc::mma_commit(&s.k_free[i & 1]);
+      };
+      bool ok = tc::mbar_wait(&s.q_full, 0, a.status, abort_flag) && tc::mbar_wait(&s.k_full[0], 0, a.status, abort_flag);
+      if (ok) {
+        tc::tc_fence_after();
+        scores(0);
+      }
+      for (int i = 0; i < tr.tiles && ok; ++i) {
+        ok = tc::mbar_wait(&s.v_full[i & 1], (i >> 1) & 1, a.status, abort_flag) &&
+             tc::mbar_wait(&s.p_full[t], i & 1, a.status, abort_flag);
+        if (!ok) break;
+        tc::tc_fence_after();
+        const uint32_t vb = v0 + (i & 1) * kTileBytes;
+#pragma unroll
+        for (int e = 0; e < kKeys / 16; ++e)
+          mma_ts(ot, st + 8 * e, desc_mn(vb + e * 16 * 128, 128 * 128), idesc_o, i > 0 || e > 0);
+        tc::mma_commit(&s.v_free[i & 1]);
+        if (i + 1 < tr.tiles) {
+          ok = tc::mbar_wait(&s.k_full[(i + 1) & 1], ((i + 1) >> 1) & 1, a.status, abort_flag);
+          if (ok) {
+            tc::tc_fence_after();
+            scores(i + 1);
+          }
+        } else {
+          tc::mma_commit(&s.o_full[t]);
+        }
+      }
+      if (!ok) {                      // after a timeout: what was issued ends before TMEM is freed
+        tc::mma_commit(&s.drain[t]);
+        for (int n = 0; n < (1 << 22) && !tc::mbar_test(&s.drain[t], 0); ++n) {
+        }
+      }
+    }
+    __syncwarp();
+  } else {
+    // ---- the copying warps: groups K_0, V_0, K_1, V_1, ...; a group is announced when the second
+    // one behind it has been issued, so up to three are in flight ----
+    const int lt = tid - 10 * 32;
+    bool ok = true;
+    auto page_of = [&](int i) {
+      if (i >= tr.tiles) return -1;
+      const int kt = tr.at(i);
+      const int32_t page = a.bt[int64_t(b) * a.max_blocks + kt / (kBlockPositions / kKeys)];
+      if (page >= 0 && page < a.num_blocks) return int(page);
+      if (lt == 0) report(a.status, V4A_DEV_BAD_BLOCK);
+      return -1;
+    };
+    auto announce = [&](int g) {      // group g of the line has landed
+      tc::fence_proxy_async();
+      tc::mbar_arrive(g & 1 ? &s.v_full[(g >> 1) & 1] : &s.k_full[(g >> 1) & 1]);
+    };
+    int page = page_of(0);
+    int g = 0;
+    for (int i = 0; i < tr.tiles && ok; ++i) {
+      const int next = page_of(i + 1);
+      const int j0 = tr.at(i) * kKeys;
+      const uint8_t* rows_k = a.pool + (page < 0 ? 0 : page * a.block_bytes + (int64_t(hk) * kBlockPositions + j0 % kBlockPositions) * (2 * D));
+      if (lt == 0) s.missing[i & 3] = page < 0;
+#pragma unroll 1
+      for (int half = 0; half < 2 && ok; ++half, ++g) {
+        ok = tc::mbar_wait(half ? &s.v_free[i & 1] : &s.k_free[i & 1], ((i >> 1) & 1) ^ 1, a.status, abort_flag);
+        if (!ok) break;
+        const uint8_t* src = rows_k + (page < 0 ? 0 : half * (int64_t(a.K) * kBlockPositions * (2 * D)));
+        const uint32_t dst = (half ? v0 : k0) + (i & 1) * kTileBytes;
+#pragma unroll 8
+        for (int c = lt; c < kKeys * (D / 8); c += kLoaders) {
+          const int r = c / (D / 8), ch = c % (D / 8), j = j0 + r;
+          const bool live = page >= 0 && j <= m_hi && (a.window == 0 || j > m_lo - a.window || j < a.sinks);
+          copy16(dst + chunk_at(r, ch), src + (page < 0 ? 0 : c * 16), live);
+        }
+        tc::cp_async_commit();
+        tc::cp_async_wait_group<2>();
+        if (g >= 2) announce(g - 2);
+      }
+      page = next;
+    }
+    tc::cp_async_wait_all();
+    if (ok)
+      for (int e = g - 2; e < g; ++e) announce(e);
+  }
+  __syncthreads();
+  tc::tc_fence_after();
+  if (warp == 0) tc::tmem_dealloc(tmem, 512);
+  pdl_trigger();
+}
+
+template <int D>
+int launch(const DenseAttnDev& d, cudaStream_t stream) {
+  constexpr int smem = 1024 + 6 * 128 * D * 2 + int(sizeof(PreSmem));
+  // at least 116 KB: no two CTAs that allocate TMEM share an SM
+  constexpr int bytes = smem < 116 * 1024 ? 116 * 1024 : smem;
+  static_assert(bytes <= 227 * 1024, "shared memory");
+  if (cudaFuncSetAttribute(dense_prefill_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+    return V4A_ERR_CUDA;
+  const int64_t rows = int64_t(d.max_new) * d.G, blocks = (rows + 2 * kRows - 1) / (2 * kRows);
+  if (blocks > 65535 || int64_t(d.K) * d.B > INT32_MAX) return V4A_ERR_UNSUPPORTED;
+  const cudaError_t e = launch_pdl(dense_prefill_kernel<D>, dim3(unsigned(d.K * d.B), unsigned(blocks)), dim3(kThreads), bytes, stream, d);
+  return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? V4A_OK : V4A_ERR_CUDA;
+}
+
+}  // namespace
+
+bool dense_prefill_takes(const v4a_dense_attn_args* a) {
+  const int64_t rows = int64_t(a->max_new_per_seq) * (a->num_heads / a->kv.num_kv_heads);
+  return a->kv.format == V4A_KV_BF16 && (a->kv.dim == 64 || a->kv.dim == 128) && rows > 64 && rows <= int64_t(65535) * 256;
+}
+
+int dense_prefill(const DenseAttnDev& d, int dim, cudaStream_t stream) {
+  return dim == 64 ? launch<64>(d, stream) : launch<128>(d, stream);
+}
+
+}  // namespace v4a

@@ -207,8 +207,9 @@ V4A_API int v4a_dense_insert(const v4a_dense_insert_args* args, void* stream);
  * behind the last sequence.  Cache rows that no query of the call sees do not
  * reach the outputs whatever they hold; a NaN or infinity in a row that one
  * query sees may reach the same sequence's other queries of the same call.
- * Dot products and sums are fp32; the probabilities are rounded to bf16 as an
- * operand of the tensor cores.
+ * Dot products and sums are fp32; the probabilities are rounded to bf16 (bf16
+ * caches) or f16 (fp8 caches) as an operand of the tensor cores.  fp8 value
+ * scales below 2^-100 are read as 2^-100.
  */
 typedef struct {
   int32_t num_tokens;          /* T >= 0: rows of q and out */
