@@ -37,7 +37,7 @@ constexpr int kLoaders = 64;
 constexpr float kRaise = 8.f;        // log2 units by which logits may pass the maximum in use
 
 struct PreSmem {
-  uint64_t q_full, k_full[2], v_full[2], k_free[2], v_free[2], s_full[2], p_full[2], o_full[2], drain[2];
+  uint64_t q_full, k_full[2], v_full[2], k_free[2], v_free[2], s_full[2], p_full[2][2], o_full[2], drain[2];
   uint32_t tmem_base;
   int abort_flag;
   int missing[4];                    // step i's page is missing: [i % 4]
@@ -89,6 +89,30 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool live)
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
 }
 
+// Arrives on `bar` when this thread's copies so far have landed.
+__device__ __forceinline__ void arrive_copies(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(tc::smem_u32(bar)) : "memory");
+}
+
+// (x, y) * (f, f) + (b, b), (x, y) + (u, v): one instruction for two values.
+__device__ __forceinline__ float2 fma2(float2 x, float2 f, float2 b) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(r) : "l"(*reinterpret_cast<uint64_t*>(&x)), "l"(*reinterpret_cast<uint64_t*>(&f)), "l"(*reinterpret_cast<uint64_t*>(&b)));
+  return *reinterpret_cast<float2*>(&r);
+}
+__device__ __forceinline__ float2 add2(float2 x, float2 y) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(*reinterpret_cast<uint64_t*>(&x)), "l"(*reinterpret_cast<uint64_t*>(&y)));
+  return *reinterpret_cast<float2*>(&r);
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&b);
@@ -129,7 +153,8 @@ __global__ void __launch_bounds__(kThreads, 1) dense_prefill_kernel(const DenseA
       tc::mbar_init(&s.k_free[i], tiles);
       tc::mbar_init(&s.v_free[i], tiles);
       tc::mbar_init(&s.s_full[i], 1);
-      tc::mbar_init(&s.p_full[i], 4);
+      tc::mbar_init(&s.p_full[i][0], 4);
+      tc::mbar_init(&s.p_full[i][1], 4);
       tc::mbar_init(&s.o_full[i], 1);
       tc::mbar_init(&s.drain[i], 1);
     }
@@ -143,6 +168,9 @@ __global__ void __launch_bounds__(kThreads, 1) dense_prefill_kernel(const DenseA
   tc::tc_fence_after();
   const uint32_t tmem = s.tmem_base;
 
+  // registers: 256 threads x 208 + 128 x 88 = the launch's 384 x 168 (checked by the host)
+  if (warp < 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+  else asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
   if (warp < 8) {
     // ---- Q into shared memory (rows behind the last are zeros), then the softmax of one tile ----
     for (int c = tid; c < tiles * kRows * (D / 8); c += 256) {
@@ -179,8 +207,10 @@ __global__ void __launch_bounds__(kThreads, 1) dense_prefill_kernel(const DenseA
         }
         float mx[4] = {z[0], z[1], z[2], z[3]};
 #pragma unroll
-        for (int c = 4; c < 128; ++c) mx[c & 3] = fmaxf(mx[c & 3], z[c]);
-        top = fmaxf(top, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * f);
+        for (int c = 4; c < 124; c += 8)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], z[c + e], z[c + e + 4]);
+        top = fmaxf(top, max3(max3(mx[0], mx[1], mx[2]), mx[3], fmaxf(max3(z[124], z[125], z[126]), z[127])) * f);
         const bool raise = top > -INFINITY && (!any || top > ref + kRaise);
         if (__any_sync(0xffffffffu, raise && any)) {   // the step before has left the accumulator: its MMAs precede S
           const float w = raise && any ? exp2f(ref - top) : 1.f;
@@ -199,24 +229,26 @@ __global__ void __launch_bounds__(kThreads, 1) dense_prefill_kernel(const DenseA
           ref = top;
           any = true;
         }
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        const float2 f2 = make_float2(f, f), r2 = make_float2(-ref, -ref);
 #pragma unroll
-        for (int c0 = 0; c0 < 128; c0 += 64) {
+        for (int h = 0; h < 2; ++h) {          // the first 64 keys' product runs while the other 64 are exponentiated
           uint32_t pk[32];
 #pragma unroll
           for (int c = 0; c < 64; c += 2) {
-            const float p0 = exp2f(fmaf(z[c0 + c], f, -ref)), p1 = exp2f(fmaf(z[c0 + c + 1], f, -ref));
-            sum[c & 2] += p0;
-            sum[(c & 2) + 1] += p1;
-            pk[c >> 1] = pack_bf16(p0, p1);
+            float2 y = fma2(make_float2(z[64 * h + c], z[64 * h + c + 1]), f2, r2);
+            y.x = exp2f(y.x);
+            y.y = exp2f(y.y);
+            sum[(c >> 1) & 1] = add2(sum[(c >> 1) & 1], y);
+            pk[c >> 1] = pack_bf16(y.x, y.y);
           }
-          tmem_st32(s_at + c0 / 2, pk);
+          tmem_st32(s_at + 32 * h, pk);
+          tmem_wait_st();
+          tc::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&s.p_full[t][h]);
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        tmem_wait_st();
-        tc::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&s.p_full[t]);
+        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
       }
       // ---- the output ----
       if (ok) ok = __all_sync(0xffffffffu, tc::mbar_wait(&s.o_full[t], 0, a.status, abort_flag));
@@ -260,28 +292,30 @@ __global__ void __launch_bounds__(kThreads, 1) dense_prefill_kernel(const DenseA
       };
       bool ok = tc::mbar_wait(&s.q_full, 0, a.status, abort_flag) && tc::mbar_wait(&s.k_full[0], 0, a.status, abort_flag);
       if (ok) {
+        tc::fence_proxy_async();     // the copying threads' writes, seen through the barrier, -> the tensor cores' reads
         tc::tc_fence_after();
         scores(0);
       }
       for (int i = 0; i < tr.tiles && ok; ++i) {
+        // the copies are waited for ahead of P, so that nothing but P separates the products
+        const bool more = i + 1 < tr.tiles;
         ok = tc::mbar_wait(&s.v_full[i & 1], (i >> 1) & 1, a.status, abort_flag) &&
-             tc::mbar_wait(&s.p_full[t], i & 1, a.status, abort_flag);
-        if (!ok) break;
-        tc::tc_fence_after();
+             (!more || tc::mbar_wait(&s.k_full[(i + 1) & 1], ((i + 1) >> 1) & 1, a.status, abort_flag));
+        tc::fence_proxy_async();
         const uint32_t vb = v0 + (i & 1) * kTileBytes;
 #pragma unroll
-        for (int e = 0; e < kKeys / 16; ++e)
-          mma_ts(ot, st + 8 * e, desc_mn(vb + e * 16 * 128, 128 * 128), idesc_o, i > 0 || e > 0);
-        tc::mma_commit(&s.v_free[i & 1]);
-        if (i + 1 < tr.tiles) {
-          ok = tc::mbar_wait(&s.k_full[(i + 1) & 1], ((i + 1) >> 1) & 1, a.status, abort_flag);
-          if (ok) {
-            tc::tc_fence_after();
-            scores(i + 1);
-          }
-        } else {
-          tc::mma_commit(&s.o_full[t]);
+        for (int h = 0; h < 2; ++h) {
+          ok = ok && tc::mbar_wait(&s.p_full[t][h], i & 1, a.status, abort_flag);
+          if (!ok) break;
+          tc::tc_fence_after();
+#pragma unroll
+          for (int e = 4 * h; e < 4 * h + 4; ++e)
+            mma_ts(ot, st + 8 * e, desc_mn(vb + e * 16 * 128, 128 * 128), idesc_o, i > 0 || e > 0);
         }
+        if (!ok) break;
+        if (more) scores(i + 1);
+        else tc::mma_commit(&s.o_full[t]);
+        tc::mma_commit(&s.v_free[i & 1]);
       }
       if (!ok) {                      // after a timeout: what was issued ends before TMEM is freed
         tc::mma_commit(&s.drain[t]);
@@ -291,8 +325,8 @@ __global__ void __launch_bounds__(kThreads, 1) dense_prefill_kernel(const DenseA
     }
     __syncwarp();
   } else {
-    // ---- the copying warps: groups K_0, V_0, K_1, V_1, ...; a group is announced when the second
-    // one behind it has been issued, so up to three are in flight ----
+    // ---- the copying warps: K_0, V_0, K_1, V_1, ... each as soon as its buffer is free; a buffer's
+    // barrier completes when every thread's copies into it have landed ----
     const int lt = tid - 10 * 32;
     bool ok = true;
     auto page_of = [&](int i) {
@@ -303,38 +337,38 @@ __global__ void __launch_bounds__(kThreads, 1) dense_prefill_kernel(const DenseA
       if (lt == 0) report(a.status, V4A_DEV_BAD_BLOCK);
       return -1;
     };
-    auto announce = [&](int g) {      // group g of the line has landed
-      tc::fence_proxy_async();
-      tc::mbar_arrive(g & 1 ? &s.v_full[(g >> 1) & 1] : &s.k_full[(g >> 1) & 1]);
-    };
     int page = page_of(0);
-    int g = 0;
     for (int i = 0; i < tr.tiles && ok; ++i) {
       const int next = page_of(i + 1);
       const int j0 = tr.at(i) * kKeys;
       const uint8_t* rows_k = a.pool + (page < 0 ? 0 : page * a.block_bytes + (int64_t(hk) * kBlockPositions + j0 % kBlockPositions) * (2 * D));
+      const bool whole = page >= 0 && j0 + kKeys - 1 <= m_hi && (a.window == 0 || j0 > m_lo - a.window);
       if (lt == 0) s.missing[i & 3] = page < 0;
 #pragma unroll 1
-      for (int half = 0; half < 2 && ok; ++half, ++g) {
+      for (int half = 0; half < 2; ++half) {
         ok = tc::mbar_wait(half ? &s.v_free[i & 1] : &s.k_free[i & 1], ((i >> 1) & 1) ^ 1, a.status, abort_flag);
         if (!ok) break;
         const uint8_t* src = rows_k + (page < 0 ? 0 : half * (int64_t(a.K) * kBlockPositions * (2 * D)));
         const uint32_t dst = (half ? v0 : k0) + (i & 1) * kTileBytes;
-#pragma unroll 8
-        for (int c = lt; c < kKeys * (D / 8); c += kLoaders) {
-          const int r = c / (D / 8), ch = c % (D / 8), j = j0 + r;
-          const bool live = page >= 0 && j <= m_hi && (a.window == 0 || j > m_lo - a.window || j < a.sinks);
-          copy16(dst + chunk_at(r, ch), src + (page < 0 ? 0 : c * 16), live);
+        if (whole) {
+#pragma unroll
+          for (int e = 0; e < kKeys * (D / 8) / kLoaders; ++e) {
+            const int c = lt + e * kLoaders;
+            copy16(dst + chunk_at(c / (D / 8), c % (D / 8)), src + c * 16, true);
+          }
+        } else {
+#pragma unroll 4
+          for (int e = 0; e < kKeys * (D / 8) / kLoaders; ++e) {
+            const int c = lt + e * kLoaders, j = j0 + c / (D / 8);
+            const bool live = page >= 0 && j <= m_hi && (a.window == 0 || j > m_lo - a.window || j < a.sinks);
+            copy16(dst + chunk_at(c / (D / 8), c % (D / 8)), src + (page < 0 ? 0 : c * 16), live);
+          }
         }
-        tc::cp_async_commit();
-        tc::cp_async_wait_group<2>();
-        if (g >= 2) announce(g - 2);
+        arrive_copies(half ? &s.v_full[i & 1] : &s.k_full[i & 1]);
       }
       page = next;
     }
     tc::cp_async_wait_all();
-    if (ok)
-      for (int e = g - 2; e < g; ++e) announce(e);
   }
   __syncthreads();
   tc::tc_fence_after();
@@ -350,6 +384,9 @@ int launch(const DenseAttnDev& d, cudaStream_t stream) {
   static_assert(bytes <= 227 * 1024, "shared memory");
   if (cudaFuncSetAttribute(dense_prefill_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
     return V4A_ERR_CUDA;
+  cudaFuncAttributes attr;
+  if (cudaFuncGetAttributes(&attr, dense_prefill_kernel<D>) != cudaSuccess) return V4A_ERR_CUDA;
+  if (attr.numRegs != 168) return V4A_ERR_UNSUPPORTED;     // the register split would not add up
   const int64_t rows = int64_t(d.max_new) * d.G, blocks = (rows + 2 * kRows - 1) / (2 * kRows);
   if (blocks > 65535 || int64_t(d.K) * d.B > INT32_MAX) return V4A_ERR_UNSUPPORTED;
   const cudaError_t e = launch_pdl(dense_prefill_kernel<D>, dim3(unsigned(d.K * d.B), unsigned(blocks)), dim3(kThreads), bytes, stream, d);
