@@ -31,18 +31,7 @@
 namespace v4a {
 namespace {
 
-constexpr int kMaxUnits = 1024;      // (sequence, row group) units that are split evenly
 constexpr int kRingBytes = 192 * 1024;
-constexpr int kCtas = 152;           // CTAs of an even split: one per SM
-
-struct JoinDesc { int valid, b, rg, hk, last, pad[3]; };
-
-struct MmaDev {
-  DenseAttnDev a;
-  int RG, U, split;                  // row groups per sequence, units, even split (else one CTA per unit and KV head)
-  float *part_o, *part_ml;           // [CTA][2][rows][D], [CTA][2][rows][2] (max in log2 units, sum)
-  JoinDesc* join;                    // [CTA]
-};
 
 template <int D, int NT, bool kFp8>
 struct Shape {
@@ -57,7 +46,7 @@ struct Shape {
   static constexpr int kStages = kRingBytes / (kWarps * 2 * kHalf);
   static_assert(R * D * 4 <= 2 * kHalf && kStages >= 3, "a stage holds the merge rows");
   struct Tail {                                                  // behind the rings
-    int64_t total, scan[kWarps];
+    int64_t scan[kWarps];
     int buf[kWarps];                                             // the stage a warp left its o in
     float ml[kWarps][R][2];
   };
@@ -119,106 +108,17 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&b);
 }
-// A row group of one sequence: rows [row0, row0 + rows) of its tokens x group heads.
-template <int kKeys>
-struct Unit { int b, row0, rows, s0, m_lo, m_hi; TileRange<kKeys> tr; };
-
-template <int R, int kKeys>
-__device__ __forceinline__ Unit<kKeys> make_unit(const DenseAttnDev& a, int b, int rg, const SeqRun& s) {
-  Unit<kKeys> u;
-  u.b = b;
-  u.row0 = rg * R;
-  u.rows = min(R, s.n * a.G - u.row0);
-  u.s0 = s.s0;
-  u.m_lo = u.m_hi = 0;
-  u.tr = TileRange<kKeys>{0, 0, 0};
-  if (u.rows <= 0) return u;
-  u.m_lo = s.p0 + u.row0 / a.G;
-  u.m_hi = s.p0 + (u.row0 + u.rows - 1) / a.G;
-  u.tr = tile_range<kKeys>(a, u.m_lo, u.m_hi);
-  return u;
-}
-
-// Where a CTA's tile x lies.
-struct Piece { int u, hk, tile; };
-
 template <int D, int NT, bool kFp8>
-__global__ void __launch_bounds__(Shape<D, NT, kFp8>::kThreads, 1) dense_attn_mma(const MmaDev p) {
+__global__ void __launch_bounds__(Shape<D, NT, kFp8>::kThreads, 1) dense_attn_mma(const DenseAttnDev a, const SplitDev p) {
   using S = Shape<D, NT, kFp8>;
   constexpr int R = S::R, kWarps = S::kWarps, kThreads = S::kThreads, kKeys = S::kKeys, MT = kKeys / 16;
   extern __shared__ __align__(128) uint8_t smem[];
   typename S::Tail& s = *reinterpret_cast<typename S::Tail*>(smem + kWarps * S::kStages * S::kStage);
-  int64_t* pre = reinterpret_cast<int64_t*>(&s + 1);         // split: [U + 1] tiles before unit u, over its KV heads
-  SeqRun* runs = reinterpret_cast<SeqRun*>(pre + (p.split ? p.U + 1 : 0));   // [B], or one
-  const DenseAttnDev& a = p.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  auto unit_of = [&](int u, int run) { return make_unit<R, kKeys>(a, u / p.RG, u % p.RG, runs[run]); };
   pdl_wait();
-
-  // ---- the CTA's tiles [x0, x1) ----
-  int64_t x0, x1;
-  int u_direct = 0, hk_direct = 0, ctas = 0;
-  if (p.split) {
-    int32_t* st = blockIdx.x == 0 ? a.status : nullptr;     // one CTA reports the batch's faults
-    for (int b = tid; b < a.B; b += kThreads) runs[b] = seq_run(a, b, st);
-    __syncthreads();
-    // exclusive sums over the units: each thread a run of units, then the threads' totals
-    const int per = (p.U + kThreads - 1) / kThreads, u0 = min(p.U, tid * per), u1 = min(p.U, u0 + per);
-    int64_t sum = 0;
-    for (int u = u0; u < u1; ++u) {
-      pre[u] = sum;
-      sum += int64_t(unit_of(u, u / p.RG).tr.tiles) * a.K;
-    }
-    int64_t v = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t w = __shfl_up_sync(0xffffffffu, v, o);
-      if (lane >= o) v += w;
-    }
-    if (lane == 31) s.scan[warp] = v;
-    __syncthreads();
-    int64_t before = v - sum, total = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) before += s.scan[w];
-      total += s.scan[w];
-    }
-    for (int u = u0; u < u1; ++u) pre[u] += before;
-    if (tid == 0) { pre[p.U] = total; s.total = total; }
-    __syncthreads();
-    // a tile per warp at least
-    ctas = int(min(int64_t(gridDim.x), (total + kWarps - 1) / kWarps));
-    if (int(blockIdx.x) >= ctas) {
-      if (tid == 0) p.join[blockIdx.x].valid = 0;
-      return;
-    }
-    x0 = int64_t(blockIdx.x) * total / ctas;
-    x1 = (int64_t(blockIdx.x) + 1) * total / ctas;
-  } else {
-    const int64_t c = blockIdx.x;
-    u_direct = int(c / a.K);
-    hk_direct = int(c % a.K);
-    if (tid == 0) runs[0] = seq_run(a, u_direct / p.RG, hk_direct == 0 && u_direct % p.RG == 0 ? a.status : nullptr);
-    __syncthreads();
-    x0 = 0;
-    x1 = unit_of(u_direct, 0).tr.tiles;
-    if (x1 == 0) return;
-  }
-  auto locate = [&](int64_t x, Unit<kKeys>* un) {
-    if (!p.split) {
-      *un = unit_of(u_direct, 0);
-      return Piece{u_direct, hk_direct, int(x)};
-    }
-    int lo = 0, hi = p.U;                       // largest u with pre[u] <= x (empty units precede)
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (pre[mid] <= x) lo = mid; else hi = mid;
-    }
-    *un = unit_of(lo, lo / p.RG);
-    const int64_t rem = x - pre[lo];
-    const int hk = int(rem / un->tr.tiles);
-    return Piece{lo, hk, int(rem - int64_t(hk) * un->tr.tiles)};
-  };
+  Line<R, kKeys, kThreads> line(a, p, &s + 1);
+  if (!line.init(s.scan, kWarps)) return;          // a tile per warp at least
+  const int64_t x0 = line.x0, x1 = line.x1;
 
   // ---- this warp's stream: tiles x0 + warp + j kWarps, j = 0, 1, ... ----
   // Lane l looks up tile j0 + l of a batch of 32, one batch ahead of its use:
@@ -229,7 +129,7 @@ __global__ void __launch_bounds__(Shape<D, NT, kFp8>::kThreads, 1) dense_attn_mm
   auto lookup = [&](int j) -> Where {
     if (j >= mine) return {-1, 0};
     Unit<kKeys> un;
-    const Piece pc = locate(x0 + warp + int64_t(j) * kWarps, &un);
+    const auto pc = line.locate(x0 + warp + int64_t(j) * kWarps, &un);
     const int kt = un.tr.at(pc.tile);
     const int32_t page = a.bt[int64_t(un.b) * a.max_blocks + kt / (kBlockPositions / kKeys)];
     const int row = pc.hk * kBlockPositions + kt % (kBlockPositions / kKeys) * kKeys;
@@ -282,7 +182,7 @@ __global__ void __launch_bounds__(Shape<D, NT, kFp8>::kThreads, 1) dense_attn_mm
   int64_t x = x0;
   while (x < x1) {
     Unit<kKeys> un;
-    const Piece pc = locate(x, &un);
+    const auto pc = line.locate(x, &un);
     const int count = int(min(int64_t(un.tr.tiles - pc.tile), x1 - x));     // tiles of this segment
     // the query rows as B operands: column g4 of n-tile nt, dims of step ks
     uint32_t qf[D / 16][NT][2];
@@ -290,8 +190,7 @@ __global__ void __launch_bounds__(Shape<D, NT, kFp8>::kThreads, 1) dense_attn_mm
     for (int nt = 0; nt < NT; ++nt) {
       const int r = nt * 8 + g4;
       const bool live = r < un.rows;
-      const int tok = un.s0 + (un.row0 + r) / a.G, head = pc.hk * a.G + (un.row0 + r) % a.G;
-      const uint16_t* q = a.q + (int64_t(tok) * a.H + head) * D;
+      const uint16_t* q = a.q + row_of(a, un, pc.hk, r) * D;
 #pragma unroll
       for (int ks = 0; ks < D / 16; ++ks) {
         if (kFp8) {           // fp8: a thread's four codes are dims 4 (lane % 4) .. + 3 of the step
@@ -552,7 +451,7 @@ __global__ void __launch_bounds__(Shape<D, NT, kFp8>::kThreads, 1) dense_attn_mm
         v[2] = fmaf(wt, t.z, v[2]); v[3] = fmaf(wt, t.w, v[3]);
       }
       if (begins && ends) {
-        const int64_t row = int64_t(un.s0 + (un.row0 + r) / a.G) * a.H + pc.hk * a.G + (un.row0 + r) % a.G;
+        const int64_t row = row_of(a, un, pc.hk, r);
         const float inv = sum > 0.f ? 1.f / sum : sum == 0.f ? 0.f : sum;     // NaN stays NaN
         *reinterpret_cast<uint2*>(a.out + row * D + d) =
             make_uint2(pack_bf16(v[0] * inv, v[1] * inv), pack_bf16(v[2] * inv, v[3] * inv));
@@ -565,10 +464,7 @@ __global__ void __launch_bounds__(Shape<D, NT, kFp8>::kThreads, 1) dense_attn_mm
         }
       }
     }
-    if (begins && !ends) {        // the unit goes on in the next CTAs: this one describes it for the join
-      const int64_t end = pre[pc.u] + int64_t(pc.hk + 1) * un.tr.tiles;
-      desc = JoinDesc{1, un.b, pc.u % p.RG, pc.hk, int((end * ctas - 1) / s.total), {0, 0, 0}};
-    }
+    if (begins && !ends) desc = line.describe(pc, un);     // the unit goes on in the next CTAs
     __syncthreads();              // the stages are read
     x += count;
   }
@@ -577,24 +473,24 @@ __global__ void __launch_bounds__(Shape<D, NT, kFp8>::kThreads, 1) dense_attn_mm
 }
 
 // Joins the pieces of a unit that several CTAs hold: piece c's slot 1, then
-// slot 0 of the CTAs behind it, in CTA order; weights 2^{m - max} of the
-// pieces' maxima.  One CTA per (describing CTA, row); 8 groups of lanes share
-// the pieces and meet in group order, so the result does not depend on timing.
-template <int D, int R>
-__global__ void __launch_bounds__(256) dense_attn_join(const MmaDev p) {
+// slot 0 of the CTAs behind it; weights 2^{m - max} of the pieces' maxima.  A
+// CTA takes one row (grid.y = rows) of the unit that CTA blockIdx.x of the
+// launch before describes; 8 groups of lanes share the pieces and meet in
+// group order, so the result does not depend on timing.
+template <int D>
+__global__ void __launch_bounds__(256) dense_join_kernel(const DenseAttnDev a, const SplitDev p) {
   constexpr int kLanes = D / 4, kGroups = 256 / kLanes > 8 ? 8 : 256 / kLanes;
   __shared__ float4 acc[kGroups][kLanes];
   __shared__ float red[8];
   const int c = blockIdx.x, r = blockIdx.y, tid = threadIdx.x;
-  const DenseAttnDev& a = p.a;
   pdl_wait();
   pdl_trigger();
   const JoinDesc j = p.join[c];
   if (!j.valid) return;
   const int s0 = a.starts[j.b], n = a.starts[j.b + 1] - s0;
-  const int row = j.rg * R + r;
-  if (row >= n * a.G) return;
-  auto part = [&](int k) { return (int64_t(c + k) * 2 + (k == 0 ? 1 : 0)) * R + r; };
+  const int64_t row = int64_t(j.rg) * p.rows + r;
+  if (row >= int64_t(n) * a.G) return;
+  auto part = [&](int k) { return (int64_t(c + k) * 2 + (k == 0 ? 1 : 0)) * p.rows + r; };
   const int pieces = j.last - c + 1;
   float top = -INFINITY;
   for (int k = tid; k < pieces; k += 256) top = fmaxf(top, p.part_ml[part(k) * 2]);
@@ -611,7 +507,8 @@ __global__ void __launch_bounds__(256) dense_attn_join(const MmaDev p) {
     for (int k = g; k < pieces; k += kGroups) {
       const float m = p.part_ml[part(k) * 2], s = p.part_ml[part(k) * 2 + 1];
       const float4 o = *reinterpret_cast<const float4*>(p.part_o + part(k) * D + 4 * l);
-      const float w = m == -INFINITY ? 0.f : exp2f(m - top);
+      if (m == -INFINITY) continue;          // its o was not written
+      const float w = exp2f(m - top);
       sum = fmaf(w, s, sum);
       v.x = fmaf(w, o.x, v.x); v.y = fmaf(w, o.y, v.y); v.z = fmaf(w, o.z, v.z); v.w = fmaf(w, o.w, v.w);
     }
@@ -634,7 +531,54 @@ __global__ void __launch_bounds__(256) dense_attn_join(const MmaDev p) {
   const int64_t at = int64_t(s0 + row / a.G) * a.H + j.hk * a.G + row % a.G;
   const float inv = sum > 0.f ? 1.f / sum : sum == 0.f ? 0.f : sum;
   *reinterpret_cast<uint2*>(a.out + at * D + 4 * l) = make_uint2(pack_bf16(v.x * inv, v.y * inv), pack_bf16(v.z * inv, v.w * inv));
-  if (l == 0 && a.lse) a.lse[at] = (top + log2f(sum)) * 0.6931471805599453f;
+  if (l == 0 && a.lse) a.lse[at] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+}
+
+// The same for units of 256 rows (dense_prefill.cu), whose pieces are few and
+// lie as [slot][dim / 4][row][4]: a thread takes a row's 16 dims (grid.y =
+// dim / 16) through the pieces in order.
+template <int D>
+__global__ void __launch_bounds__(256) dense_join_rows(const DenseAttnDev a, const SplitDev p) {
+  const int c = blockIdx.x, r = threadIdx.x, d0 = blockIdx.y * 4;
+  pdl_wait();
+  pdl_trigger();
+  const JoinDesc j = p.join[c];
+  if (!j.valid) return;
+  const int s0 = a.starts[j.b], n = a.starts[j.b + 1] - s0;
+  const int64_t row = int64_t(j.rg) * 256 + r;
+  if (row >= int64_t(n) * a.G) return;
+  auto slot = [&](int k) { return int64_t(c + k) * 2 + (k == 0 ? 1 : 0); };
+  auto ml = [&](int k) { return *reinterpret_cast<const float2*>(p.part_ml + (slot(k) * 256 + r) * 2); };
+  const int pieces = j.last - c + 1;
+  float top = -INFINITY, sum = 0.f;
+#pragma unroll 4
+  for (int k = 0; k < pieces; ++k) top = fmaxf(top, ml(k).x);
+  float4 v[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+  for (int k = 0; k < pieces; ++k) {
+    const float2 t = ml(k);
+    float4 o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = reinterpret_cast<const float4*>(p.part_o)[(slot(k) * (D / 4) + d0 + i) * 256 + r];
+    if (t.x == -INFINITY) continue;
+    const float w = exp2f(t.x - top);
+    sum = fmaf(w, t.y, sum);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[i].x = fmaf(w, o[i].x, v[i].x); v[i].y = fmaf(w, o[i].y, v[i].y);
+      v[i].z = fmaf(w, o[i].z, v[i].z); v[i].w = fmaf(w, o[i].w, v[i].w);
+    }
+  }
+  const int64_t at = int64_t(s0 + row / a.G) * a.H + j.hk * a.G + row % a.G;
+  const float inv = sum > 0.f ? 1.f / sum : sum == 0.f ? 0.f : sum;
+#pragma unroll
+  for (int i = 0; i < 4; i += 2)
+    *reinterpret_cast<uint4*>(a.out + at * D + 4 * (d0 + i)) =
+        make_uint4(pack_bf16(v[i].x * inv, v[i].y * inv), pack_bf16(v[i].z * inv, v[i].w * inv),
+                   pack_bf16(v[i + 1].x * inv, v[i + 1].y * inv), pack_bf16(v[i + 1].z * inv, v[i + 1].w * inv));
+  if (blockIdx.y == 0 && a.lse) a.lse[at] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
 }
 
 int rows_of(const v4a_dense_attn_args* a) {
@@ -648,33 +592,31 @@ int64_t row_groups(const v4a_dense_attn_args* a) {
 }
 
 size_t workspace_of(const v4a_dense_attn_args* a) {
-  const size_t R = rows_of(a), n = size_t(kCtas) * 2 * R;
-  return 16 + kCtas * sizeof(JoinDesc) + n * a->kv.dim * 4 + n * 2 * 4;
+  return dense_prefill_takes(a) ? dense_prefill_workspace(a) : split_workspace(rows_of(a), a->kv.dim);
 }
 
 template <int D, int NT, bool kFp8>
-int launch(MmaDev& p, cudaStream_t stream) {
+int launch(const DenseAttnDev& a, const SplitDev& p, cudaStream_t stream) {
   using S = Shape<D, NT, kFp8>;
-  const size_t smem = S::kWarps * S::kStages * S::kStage + sizeof(typename S::Tail) +
-                      (p.split ? p.a.B * sizeof(SeqRun) + (p.U + 1) * sizeof(int64_t) : sizeof(SeqRun));
+  const size_t smem = S::kWarps * S::kStages * S::kStage + sizeof(typename S::Tail) + split_smem(p.split, p.U, a.B);
   if (smem > 227 * 1024) return V4A_ERR_UNSUPPORTED;
   auto kern = dense_attn_mma<D, NT, kFp8>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024) != cudaSuccess) return V4A_ERR_CUDA;
-  const int64_t grid = p.split ? kCtas : int64_t(p.U) * p.a.K;
+  const int64_t grid = p.split ? kSplitCtas : int64_t(p.U) * a.K;
   if (grid > INT32_MAX) return V4A_ERR_UNSUPPORTED;
-  cudaError_t e = launch_pdl(kern, dim3(unsigned(grid)), dim3(S::kThreads), smem, stream, p);
-  if (e == cudaSuccess && p.split) e = launch_pdl(dense_attn_join<D, S::R>, dim3(unsigned(grid), S::R), dim3(256), 0, stream, p);
-  return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? V4A_OK : V4A_ERR_CUDA;
+  const cudaError_t e = launch_pdl(kern, dim3(unsigned(grid)), dim3(S::kThreads), smem, stream, a, p);
+  if (e != cudaSuccess || cudaGetLastError() != cudaSuccess) return V4A_ERR_CUDA;
+  return p.split ? dense_join(a, p, D, stream) : V4A_OK;
 }
 
 template <bool kFp8>
-int launch_dim(MmaDev& p, const v4a_dense_attn_args* a, cudaStream_t stream) {
-  const bool two = rows_of(a) == 16;
-  switch (a->kv.dim) {
-    case 64: return two ? launch<64, 2, kFp8>(p, stream) : launch<64, 1, kFp8>(p, stream);
-    case 128: return two ? launch<128, 2, kFp8>(p, stream) : launch<128, 1, kFp8>(p, stream);
-    case 192: return two ? launch<192, 2, kFp8>(p, stream) : launch<192, 1, kFp8>(p, stream);
-    default: return launch<256, 1, kFp8>(p, stream);
+int launch_dim(const DenseAttnDev& a, const SplitDev& p, int dim, cudaStream_t stream) {
+  const bool two = p.rows == 16;
+  switch (dim) {
+    case 64: return two ? launch<64, 2, kFp8>(a, p, stream) : launch<64, 1, kFp8>(a, p, stream);
+    case 128: return two ? launch<128, 2, kFp8>(a, p, stream) : launch<128, 1, kFp8>(a, p, stream);
+    case 192: return two ? launch<192, 2, kFp8>(a, p, stream) : launch<192, 1, kFp8>(a, p, stream);
+    default: return launch<256, 1, kFp8>(a, p, stream);
   }
 }
 
@@ -693,13 +635,22 @@ int check_shape(const v4a_dense_attn_args* a) {
 
 }  // namespace
 
+int dense_join(const DenseAttnDev& a, const SplitDev& p, int dim, cudaStream_t stream) {
+  const bool many = p.rows > 16;
+  auto kern = many ? (dim == 64 ? dense_join_rows<64> : dense_join_rows<128>)
+                   : (dim == 64 ? dense_join_kernel<64> : dim == 128 ? dense_join_kernel<128> : dim == 192 ? dense_join_kernel<192> : dense_join_kernel<256>);
+  const int y = many ? dim / 16 : p.rows;
+  const cudaError_t e = launch_pdl(kern, dim3(kSplitCtas, unsigned(y)), dim3(256), 0, stream, a, p);
+  return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? V4A_OK : V4A_ERR_CUDA;
+}
+
 size_t dense_attn_workspace_size(const v4a_dense_attn_args* a) { return check_shape(a) ? 0 : workspace_of(a); }
 
 int dense_attn(const v4a_dense_attn_args* a, void* ws, size_t ws_bytes, cudaStream_t stream) {
   int rc = check_shape(a);
   if (rc) return rc;
-  MmaDev p{};
-  rc = dense_cache_check(a->kv, &p.a.block_bytes);
+  DenseAttnDev d{};
+  rc = dense_cache_check(a->kv, &d.block_bytes);
   if (rc) return rc;
   if (!(a->softmax_scale > 0.f) || !std::isfinite(a->softmax_scale) || a->kv.max_blocks < 1) return V4A_ERR_INVALID_ARG;
   if (a->num_tokens == 0 || a->num_seqs == 0) return V4A_OK;
@@ -708,7 +659,6 @@ int dense_attn(const v4a_dense_attn_args* a, void* ws, size_t ws_bytes, cudaStre
       static_cast<const void*>(a->q) == static_cast<const void*>(a->out))
     return V4A_ERR_INVALID_ARG;
   if (!ws || (reinterpret_cast<uintptr_t>(ws) & 15) || ws_bytes < workspace_of(a)) return V4A_ERR_WORKSPACE;
-  DenseAttnDev& d = p.a;
   d.T = a->num_tokens; d.B = a->num_seqs; d.H = a->num_heads; d.K = a->kv.num_kv_heads; d.G = d.H / d.K;
   d.max_new = a->max_new_per_seq; d.max_blocks = a->kv.max_blocks; d.window = a->window; d.sinks = a->sinks;
   d.num_blocks = a->kv.num_blocks;
@@ -716,15 +666,13 @@ int dense_attn(const v4a_dense_attn_args* a, void* ws, size_t ws_bytes, cudaStre
   d.pool = static_cast<const uint8_t*>(a->kv.pool);
   d.q = a->q; d.out = a->out; d.lse = a->lse; d.status = a->status;
   d.scale_log2 = a->softmax_scale * 1.4426950408889634f;
-  if (dense_prefill_takes(a)) return dense_prefill(d, a->kv.dim, stream);
+  if (dense_prefill_takes(a)) return dense_prefill(a, d, ws, stream);
+  SplitDev p{};
   p.RG = int(row_groups(a));
   p.U = d.B * p.RG;
-  p.split = p.U <= kMaxUnits;
-  const size_t R = rows_of(a), n = size_t(kCtas) * 2 * R;
-  p.join = static_cast<JoinDesc*>(ws);
-  p.part_o = reinterpret_cast<float*>(p.join + kCtas);
-  p.part_ml = p.part_o + n * a->kv.dim;
-  return a->kv.format == V4A_KV_FP8_TOKEN ? launch_dim<true>(p, a, stream) : launch_dim<false>(p, a, stream);
+  p.split = p.U <= kMaxSplitUnits;
+  split_carve(&p, ws, rows_of(a), a->kv.dim);
+  return a->kv.format == V4A_KV_FP8_TOKEN ? launch_dim<true>(d, p, a->kv.dim, stream) : launch_dim<false>(d, p, a->kv.dim, stream);
 }
 
 }  // namespace v4a

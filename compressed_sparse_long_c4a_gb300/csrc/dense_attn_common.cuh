@@ -67,8 +67,163 @@ __device__ __forceinline__ bool all_visible(const DenseAttnDev& a, int m_lo, int
   return j + n - 1 <= m_lo && (a.window == 0 || j > m_hi - a.window || j + n <= a.sinks);
 }
 
+// ---- units and the line of their tiles ---------------------------------------------
+// A unit is up to R consecutive rows (token, head of the group) of one sequence
+// and one KV head; its row group `rg` starts at row rg * R of the sequence.
+template <int kTile>
+struct Unit { int b, row0, rows, s0, m_lo, m_hi; TileRange<kTile> tr; };
+
+template <int R, int kTile>
+__device__ __forceinline__ Unit<kTile> make_unit(const DenseAttnDev& a, int b, int rg, const SeqRun& s) {
+  Unit<kTile> u;
+  u.b = b;
+  u.row0 = rg * R;
+  u.rows = int(min(int64_t(R), int64_t(s.n) * a.G - u.row0));
+  u.s0 = s.s0;
+  u.m_lo = u.m_hi = 0;
+  u.tr = TileRange<kTile>{0, 0, 0};
+  if (u.rows <= 0) return u;
+  u.m_lo = s.p0 + u.row0 / a.G;
+  u.m_hi = s.p0 + (u.row0 + u.rows - 1) / a.G;
+  u.tr = tile_range<kTile>(a, u.m_lo, u.m_hi);
+  return u;
+}
+
+// Row r of a unit in the [T][H] order of q and out.
+template <int kTile>
+__device__ __forceinline__ int64_t row_of(const DenseAttnDev& a, const Unit<kTile>& u, int hk, int r) {
+  return int64_t(u.s0 + (u.row0 + r) / a.G) * a.H + hk * a.G + (u.row0 + r) % a.G;
+}
+
+// How a launch divides the units: split = 1: the tiles of all units and KV
+// heads form one line (unit by unit, KV head by KV head) that `ctas` CTAs
+// divide evenly; split = 0: one CTA per unit and KV head.
+struct SplitDev {
+  int RG, U, split;               // row groups per sequence, units (sequences x row groups)
+  int rows;                       // R
+  struct JoinDesc* join;          // [CTA]
+  float *part_o, *part_ml;        // [CTA][2][R][dim], [CTA][2][R][2] (maximum in log2 units, sum)
+};
+
+// A unit that starts in a CTA's range and goes on in the next CTAs' up to `last`:
+// its pieces are this CTA's slot 1 and slot 0 of the others.
+struct JoinDesc { int valid, b, rg, hk, last, pad[3]; };
+
+constexpr int kMaxSplitUnits = 1024;
+constexpr int kSplitCtas = 152;   // one CTA per SM
+
+__host__ __device__ constexpr size_t split_smem(int split, int U, int B) {
+  return split ? (U + 1) * sizeof(int64_t) + B * sizeof(SeqRun) : sizeof(SeqRun);
+}
+__host__ __device__ constexpr size_t split_workspace(int R, int dim) {
+  return 16 + kSplitCtas * (sizeof(JoinDesc) + size_t(2) * R * (dim + 2) * sizeof(float));
+}
+inline void split_carve(SplitDev* p, void* ws, int R, int dim) {
+  p->rows = R;
+  p->join = static_cast<JoinDesc*>(ws);
+  p->part_o = reinterpret_cast<float*>(p->join + kSplitCtas);
+  p->part_ml = p->part_o + size_t(kSplitCtas) * 2 * R * dim;
+}
+
+// The CTA's part of the line (or its unit), kept in shared memory behind `mem`.
+template <int R, int kTile, int kThreads>
+struct Line {
+  const DenseAttnDev& a;
+  const SplitDev& p;
+  int64_t* pre;                   // [U + 1] tiles before unit u, over its KV heads
+  SeqRun* runs;                   // [B], or the one
+  int64_t x0, x1, total;
+  int ctas, u_direct, hk_direct;
+
+  struct Piece { int u, hk, tile; };
+
+  // `scan`: kThreads / 32 words of shared memory.  At least min_tiles tiles per
+  // CTA.  Called by the whole CTA; false when it has no tiles.
+  __device__ __forceinline__ Line(const DenseAttnDev& a_, const SplitDev& p_, void* mem) : a(a_), p(p_) {
+    pre = static_cast<int64_t*>(mem);
+    runs = reinterpret_cast<SeqRun*>(pre + (p.split ? p.U + 1 : 0));
+  }
+  __device__ __forceinline__ bool init(int64_t* scan, int min_tiles) {
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    u_direct = hk_direct = ctas = 0;
+    total = 0;
+    if (!p.split) {
+      u_direct = int(blockIdx.x / unsigned(a.K));
+      hk_direct = int(blockIdx.x % unsigned(a.K));
+      if (tid == 0) runs[0] = seq_run(a, u_direct / p.RG, hk_direct == 0 && u_direct % p.RG == 0 ? a.status : nullptr);
+      __syncthreads();
+      x0 = 0;
+      x1 = unit(u_direct).tr.tiles;
+      return x1 > 0;
+    }
+    int32_t* st = blockIdx.x == 0 ? a.status : nullptr;     // one CTA reports the batch's faults
+    for (int b = tid; b < a.B; b += kThreads) runs[b] = seq_run(a, b, st);
+    __syncthreads();
+    // exclusive sums over the units: each thread a run of units, then the threads' totals
+    const int per = (p.U + kThreads - 1) / kThreads, u0 = min(p.U, tid * per), u1 = min(p.U, u0 + per);
+    int64_t sum = 0;
+    for (int u = u0; u < u1; ++u) {
+      pre[u] = sum;
+      sum += int64_t(unit(u).tr.tiles) * a.K;
+    }
+    int64_t v = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t w = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += w;
+    }
+    if (lane == 31) scan[warp] = v;
+    __syncthreads();
+    int64_t before = v - sum;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) before += scan[w];
+      total += scan[w];
+    }
+    for (int u = u0; u < u1; ++u) pre[u] += before;
+    if (tid == 0) pre[p.U] = total;
+    __syncthreads();
+    ctas = int(min(int64_t(gridDim.x), (total + min_tiles - 1) / min_tiles));
+    if (int(blockIdx.x) >= ctas) {
+      if (tid == 0) p.join[blockIdx.x].valid = 0;
+      return false;
+    }
+    x0 = int64_t(blockIdx.x) * total / ctas;
+    x1 = (int64_t(blockIdx.x) + 1) * total / ctas;
+    return true;
+  }
+  __device__ __forceinline__ Unit<kTile> unit(int u) const {
+    return make_unit<R, kTile>(a, u / p.RG, u % p.RG, runs[p.split ? u / p.RG : 0]);
+  }
+  // Where tile x of the line lies.
+  __device__ __forceinline__ Piece locate(int64_t x, Unit<kTile>* un) const {
+    if (!p.split) {
+      *un = unit(u_direct);
+      return Piece{u_direct, hk_direct, int(x)};
+    }
+    int lo = 0, hi = p.U;                       // largest u with pre[u] <= x (empty units precede)
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (pre[mid] <= x) lo = mid; else hi = mid;
+    }
+    *un = unit(lo);
+    const int64_t rem = x - pre[lo];
+    const int hk = int(rem / un->tr.tiles);
+    return Piece{lo, hk, int(rem - int64_t(hk) * un->tr.tiles)};
+  }
+  // The description of a unit that leaves the CTA's range.
+  __device__ __forceinline__ JoinDesc describe(const Piece& pc, const Unit<kTile>& un) const {
+    const int64_t end = pre[pc.u] + int64_t(pc.hk + 1) * un.tr.tiles;
+    return JoinDesc{1, un.b, pc.u % p.RG, pc.hk, int((end * ctas - 1) / total), {0, 0, 0}};
+  }
+};
+
+// Joins the pieces of every split unit (dense_attn.cu).
+int dense_join(const DenseAttnDev& a, const SplitDev& p, int dim, cudaStream_t stream);
+
 // The tensor-core form for many rows (dense_prefill.cu): whether it takes the shape, and its launch.
 bool dense_prefill_takes(const v4a_dense_attn_args* a);
-int dense_prefill(const DenseAttnDev& d, int dim, cudaStream_t stream);
+size_t dense_prefill_workspace(const v4a_dense_attn_args* a);
+int dense_prefill(const v4a_dense_attn_args* a, const DenseAttnDev& d, void* ws, cudaStream_t stream);
 
 }  // namespace v4a

@@ -18,7 +18,7 @@
 //                   (P from TMEM, V as an MN-major operand)
 //
 // Roles (12 warps): 0-3 and 4-7 the two tiles' softmax (a thread owns a row),
-// 8 and 9 one MMA issuer per tile, 10 and 11 copy keys and values (16-byte
+// 8 issues the MMAs, 9 to 11 copy keys and values (16-byte
 // cp.async into the 128-byte swizzle; rows that no row of the CTA sees are
 // filled with zeros, so what they hold cannot reach a product).  Keys and
 // values have two buffers each.
@@ -33,15 +33,17 @@ namespace {
 constexpr int kRows = 128;           // rows of a tile (MMA M)
 constexpr int kKeys = 128;           // keys per step
 constexpr int kThreads = 384;
-constexpr int kLoaders = 64;
+constexpr int kUnit = 2 * kRows;     // rows of a unit
+constexpr int kLoaders = 96;
+constexpr int kMinSteps = 4;         // steps a CTA of an even split has at least
 constexpr float kRaise = 8.f;        // log2 units by which logits may pass the maximum in use
 
 struct PreSmem {
-  uint64_t q_full, k_full[2], v_full[2], k_free[2], v_free[2], s_full[2], p_full[2][2], o_full[2], drain[2];
+  uint64_t q_full[2], k_full[2], v_full[2], k_free[2], v_free[2], s_full[2], p_full[2][2], o_full[2], drain;
+  int64_t scan[kThreads / 32];
   uint32_t tmem_base;
   int abort_flag;
-  int missing[4];                    // step i's page is missing: [i % 4]
-  SeqRun run;
+  int missing[4];                    // step n's page is missing: [n % 4]
 };
 
 // MN-major operand (as in attn_tc.cu): 64-element rows along N, 8-row groups
@@ -124,40 +126,33 @@ __device__ __forceinline__ uint32_t chunk_at(int r, int ch) {
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1) dense_prefill_kernel(const DenseAttnDev a) {
+__global__ void __launch_bounds__(kThreads, 1) dense_prefill_kernel(const DenseAttnDev a, const SplitDev p) {
   constexpr int kTileBytes = 128 * D * 2;      // a Q tile, a step's keys or its values
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t q0 = tc::smem_u32(base), k0 = q0 + 2 * kTileBytes, v0 = k0 + 2 * kTileBytes;
   PreSmem& s = *reinterpret_cast<PreSmem*>(base + 6 * kTileBytes);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int hk = blockIdx.x % a.K, b = blockIdx.x / a.K;
-  const int row0 = int(gridDim.y - 1 - blockIdx.y) * (2 * kRows);     // later rows see more keys: first
   volatile int* abort_flag = &s.abort_flag;
 
   pdl_wait();
-  if (tid == 0) s.run = seq_run(a, b, hk == 0 && row0 == 0 ? a.status : nullptr);
-  __syncthreads();
-  const SeqRun run = s.run;
-  const int rows = min(2 * kRows, run.n * a.G - row0);
-  if (rows <= 0) return;
-  const int tiles = rows > kRows ? 2 : 1;
-  const int m_lo = run.p0 + row0 / a.G, m_hi = run.p0 + (row0 + rows - 1) / a.G;
-  const TileRange<kKeys> tr = tile_range<kKeys>(a, m_lo, m_hi);
+  Line<kUnit, kKeys, kThreads> line(a, p, &s + 1);
+  if (!line.init(s.scan, kMinSteps)) return;
+  const int64_t x0 = line.x0, x1 = line.x1;
 
   if (tid == 0) {
-    tc::mbar_init(&s.q_full, 256);
     for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(&s.q_full[i], kRows);
       tc::mbar_init(&s.k_full[i], kLoaders);
       tc::mbar_init(&s.v_full[i], kLoaders);
-      tc::mbar_init(&s.k_free[i], tiles);
-      tc::mbar_init(&s.v_free[i], tiles);
+      tc::mbar_init(&s.k_free[i], 1);
+      tc::mbar_init(&s.v_free[i], 1);
       tc::mbar_init(&s.s_full[i], 1);
       tc::mbar_init(&s.p_full[i][0], 4);
       tc::mbar_init(&s.p_full[i][1], 4);
       tc::mbar_init(&s.o_full[i], 1);
-      tc::mbar_init(&s.drain[i], 1);
     }
+    tc::mbar_init(&s.drain, 1);
     s.abort_flag = 0;
     tc::mbar_fence_init();
   }
@@ -168,240 +163,322 @@ __global__ void __launch_bounds__(kThreads, 1) dense_prefill_kernel(const DenseA
   tc::tc_fence_after();
   const uint32_t tmem = s.tmem_base;
 
-  // registers: 256 threads x 208 + 128 x 88 = the launch's 384 x 168 (checked by the host)
-  if (warp < 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-  else asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+  // Every role walks the CTA's segments (the parts of units in [x0, x1)) by
+  // itself.  Counters: n = steps of the CTA (key and value buffers), e = steps
+  // of a tile (its S and P), g = segments of a tile (its Q and O).
+  // registers: 256 threads x 200 + 128 x 104 = the launch's 384 x 168 (checked by the host)
+  if (warp < 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+  else asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
   if (warp < 8) {
-    // ---- Q into shared memory (rows behind the last are zeros), then the softmax of one tile ----
-    for (int c = tid; c < tiles * kRows * (D / 8); c += 256) {
-      const int r = c / (D / 8), ch = c % (D / 8), i = row0 + min(r, rows - 1);
-      const uint16_t* q = a.q + (int64_t(run.s0 + i / a.G) * a.H + hk * a.G + i % a.G) * D;
-      copy16(q0 + (r >> 7) * kTileBytes + chunk_at(r & 127, ch), q + ch * 8, r < rows);
-    }
-    tc::cp_async_wait_all();
-    tc::fence_proxy_async();
-    tc::mbar_arrive(&s.q_full);
+    // ---- a tile's queries, softmax and output ----
     const int t = warp >> 2, r = tid & 127;
-    if (t < tiles) {
-      const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
-      const uint32_t s_at = tmem + 128 * t + lanes, o_at = tmem + 256 + 128 * t + lanes;
-      const float f = a.scale_log2;
-      const int row = t * kRows + r, m = run.p0 + (row0 + min(row, rows - 1)) / a.G;
-      float top = -INFINITY, ref = 0.f, l = 0.f;       // largest logit, the maximum in use, the sum against it
-      bool any = false;                                // `ref` is set (a key has been seen)
-      bool ok = true;
-      for (int i = 0; i < tr.tiles; ++i) {
-        ok = __all_sync(0xffffffffu, tc::mbar_wait(&s.s_full[t], i & 1, a.status, abort_flag));
-        if (!ok) break;
-        tc::tc_fence_after();
-        float z[128];
-        tc::tmem_ld64(s_at, z);
-        tc::tmem_ld64(s_at + 64, z + 64);
-        const int j0 = tr.at(i) * kKeys;
-        const bool gone = s.missing[i & 3] != 0;
-        if (gone || !all_visible(a, m_lo, m_hi, j0, kKeys)) {
-          const int hi = gone ? -1 : m - j0, lo = a.window ? m - a.window - j0 : -1, sk = a.window ? a.sinks - j0 : 0;
-#pragma unroll
-          for (int c = 0; c < 128; ++c)
-            if (c > hi || (c <= lo && c >= sk)) z[c] = -INFINITY;
+    const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
+    const uint32_t s_at = tmem + 128 * t + lanes, o_at = tmem + 256 + 128 * t + lanes;
+    const float f = a.scale_log2;
+    bool ok = true;
+    int n0 = 0, e = 0, g = 0;
+    for (int64_t x = x0; x < x1 && ok;) {
+      Unit<kKeys> un;
+      const auto pc = line.locate(x, &un);
+      const int count = int(min(int64_t(un.tr.tiles - pc.tile), x1 - x));
+      if (un.rows > t * kRows) {
+        // Q rows behind the last are zeros
+#pragma unroll 4
+        for (int c = r; c < kRows * (D / 8); c += kRows) {
+          const int qr = c / (D / 8), ch = c % (D / 8), i = t * kRows + qr;
+          const uint16_t* q = a.q + row_of(a, un, pc.hk, min(i, un.rows - 1)) * D;
+          copy16(q0 + t * kTileBytes + chunk_at(qr, ch), q + ch * 8, i < un.rows);
         }
-        float mx[4] = {z[0], z[1], z[2], z[3]};
+        tc::cp_async_wait_all();
+        tc::fence_proxy_async();
+        tc::mbar_arrive(&s.q_full[t]);
+        const int row = t * kRows + r, m = un.m_lo + (un.row0 % a.G + min(row, un.rows - 1)) / a.G;
+        float top = -INFINITY, ref = 0.f, l = 0.f;       // largest logit, the maximum in use, the sum against it
+        bool any = false;                                // `ref` is set (a key has been seen)
+        for (int i = 0; i < count; ++i, ++e) {
+          ok = __all_sync(0xffffffffu, tc::mbar_wait(&s.s_full[t], e & 1, a.status, abort_flag));
+          if (!ok) break;
+          tc::tc_fence_after();
+          float z[128];
+          tc::tmem_ld64(s_at, z);
+          tc::tmem_ld64(s_at + 64, z + 64);
+          const int j0 = un.tr.at(pc.tile + i) * kKeys;
+          const bool gone = s.missing[(n0 + i) & 3] != 0;
+          if (gone || !all_visible(a, un.m_lo, un.m_hi, j0, kKeys)) {
+            // columns up to hi, and of those the ones behind lo or before sk; a warp whose rows see all skips each side
+            const int hi = gone ? -1 : m - j0, lo = a.window ? m - a.window - j0 : -1, sk = a.window ? a.sinks - j0 : 0;
+            if (__any_sync(0xffffffffu, hi < kKeys - 1)) {
 #pragma unroll
-        for (int c = 4; c < 124; c += 8)
+              for (int c = 0; c < 128; ++c) z[c] = c <= hi ? z[c] : -INFINITY;
+            }
+            if (__any_sync(0xffffffffu, lo >= 0)) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], z[c + e], z[c + e + 4]);
-        top = fmaxf(top, max3(max3(mx[0], mx[1], mx[2]), mx[3], fmaxf(max3(z[124], z[125], z[126]), z[127])) * f);
-        const bool raise = top > -INFINITY && (!any || top > ref + kRaise);
-        if (__any_sync(0xffffffffu, raise && any)) {   // the step before has left the accumulator: its MMAs precede S
-          const float w = raise && any ? exp2f(ref - top) : 1.f;
-          l *= w;
+              for (int c = 0; c < 128; ++c) z[c] = c > lo || c < sk ? z[c] : -INFINITY;
+            }
+          }
+          float mx[4] = {z[0], z[1], z[2], z[3]};
+#pragma unroll
+          for (int c = 4; c < 124; c += 8)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mx[k] = max3(mx[k], z[c + k], z[c + k + 4]);
+          top = fmaxf(top, max3(max3(mx[0], mx[1], mx[2]), mx[3], fmaxf(max3(z[124], z[125], z[126]), z[127])) * f);
+          const bool raise = top > -INFINITY && (!any || top > ref + kRaise);
+          if (__any_sync(0xffffffffu, raise && any)) {   // the step before has left the accumulator: its MMAs precede S
+            const float w = raise && any ? exp2f(ref - top) : 1.f;
+            l *= w;
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+              float o[32];
+              tmem_ld32(o_at + c, o);
+#pragma unroll
+              for (int k = 0; k < 32; ++k) o[k] *= w;
+              tmem_st32(o_at + c, reinterpret_cast<const uint32_t*>(o));
+            }
+            tmem_wait_st();
+          }
+          if (raise) {
+            ref = top;
+            any = true;
+          }
+          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          const float2 f2 = make_float2(f, f), r2 = make_float2(-ref, -ref);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {          // the first 64 keys' product runs while the other 64 are exponentiated
+            uint32_t pk[32];
+#pragma unroll
+            for (int c = 0; c < 64; c += 2) {
+              float2 y = fma2(make_float2(z[64 * h + c], z[64 * h + c + 1]), f2, r2);
+              y.x = exp2f(y.x);
+              y.y = exp2f(y.y);
+              sum[(c >> 1) & 1] = add2(sum[(c >> 1) & 1], y);
+              pk[c >> 1] = pack_bf16(y.x, y.y);
+            }
+            tmem_st32(s_at + 32 * h, pk);
+            tmem_wait_st();
+            tc::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&s.p_full[t][h]);
+          }
+          l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+        }
+        // ---- the output, or the piece for the join ----
+        if (ok) ok = __all_sync(0xffffffffu, tc::mbar_wait(&s.o_full[t], g & 1, a.status, abort_flag));
+        ++g;
+        if (ok) {
+          tc::tc_fence_after();
+          const bool begins = pc.tile == 0, whole = begins && pc.tile + count == un.tr.tiles;
+          const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;
+          const int64_t at = row_of(a, un, pc.hk, min(row, un.rows - 1));
+          const int64_t slot = int64_t(blockIdx.x) * 2 + (begins ? 1 : 0), part = slot * kUnit + row;
 #pragma unroll 1
           for (int c = 0; c < D; c += 32) {
             float o[32];
             tmem_ld32(o_at + c, o);
+            if (row < un.rows && whole) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] *= w;
-            tmem_st32(o_at + c, reinterpret_cast<const uint32_t*>(o));
+              for (int k = 0; k < 32; k += 8)
+                *reinterpret_cast<uint4*>(a.out + at * D + c + k) =
+                    make_uint4(pack_bf16(o[k] * inv, o[k + 1] * inv), pack_bf16(o[k + 2] * inv, o[k + 3] * inv),
+                               pack_bf16(o[k + 4] * inv, o[k + 5] * inv), pack_bf16(o[k + 6] * inv, o[k + 7] * inv));
+            } else if (row < un.rows) {
+#pragma unroll
+              for (int k = 0; k < 32; k += 4)      // [slot][dim / 4][row][4]: a warp's rows side by side
+                *reinterpret_cast<float4*>(p.part_o + (slot * (D / 4) + (c + k) / 4) * (kUnit * 4) + row * 4) =
+                    make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+            }
+            __syncwarp();
           }
-          tmem_wait_st();
-        }
-        if (raise) {
-          ref = top;
-          any = true;
-        }
-        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-        const float2 f2 = make_float2(f, f), r2 = make_float2(-ref, -ref);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {          // the first 64 keys' product runs while the other 64 are exponentiated
-          uint32_t pk[32];
-#pragma unroll
-          for (int c = 0; c < 64; c += 2) {
-            float2 y = fma2(make_float2(z[64 * h + c], z[64 * h + c + 1]), f2, r2);
-            y.x = exp2f(y.x);
-            y.y = exp2f(y.y);
-            sum[(c >> 1) & 1] = add2(sum[(c >> 1) & 1], y);
-            pk[c >> 1] = pack_bf16(y.x, y.y);
+          if (row < un.rows) {
+            if (whole) {
+              if (a.lse) a.lse[at] = any ? (ref + log2f(l)) * 0.6931471805599453f : l == 0.f ? -INFINITY : l;
+            } else {       // a piece without a key leaves nothing; one whose logits are all NaN is passed on
+              p.part_ml[part * 2] = any || l != 0.f ? ref : -INFINITY;
+              p.part_ml[part * 2 + 1] = l;
+            }
           }
-          tmem_st32(s_at + 32 * h, pk);
-          tmem_wait_st();
-          tc::tc_fence_before();
-          __syncwarp();
-          if (lane == 0) tc::mbar_arrive(&s.p_full[t][h]);
+          tc::tc_fence_before();       // O and Q are free for the next segment (announced by its q_full)
         }
-        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
       }
-      // ---- the output ----
-      if (ok) ok = __all_sync(0xffffffffu, tc::mbar_wait(&s.o_full[t], 0, a.status, abort_flag));
-      if (ok) {
-        tc::tc_fence_after();
-        const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;
-        const int i = row0 + row;
-        const int64_t at = int64_t(run.s0 + i / a.G) * a.H + hk * a.G + i % a.G;
-#pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
-          float o[32];
-          tmem_ld32(o_at + c, o);
-          if (row < rows) {
-#pragma unroll
-            for (int e = 0; e < 32; e += 8)
-              *reinterpret_cast<uint4*>(a.out + at * D + c + e) =
-                  make_uint4(pack_bf16(o[e] * inv, o[e + 1] * inv), pack_bf16(o[e + 2] * inv, o[e + 3] * inv),
-                             pack_bf16(o[e + 4] * inv, o[e + 5] * inv), pack_bf16(o[e + 6] * inv, o[e + 7] * inv));
-          }
-          __syncwarp();
-        }
-        if (row < rows && a.lse) a.lse[at] = any ? (ref + log2f(l)) * 0.6931471805599453f : l == 0.f ? -INFINITY : l;
-      }
-      tc::tc_fence_before();
+      n0 += count;
+      x += count;
     }
-  } else if (warp < 10) {
-    // ---- one MMA issuer per tile ----
-    const int t = warp - 8;
-    if (t < tiles && lane == 0) {
+  } else if (warp == 8) {
+    // ---- the MMA issuer: tile 0's products, then tile 1's, so that one tile's run while the other is
+    // in its softmax (with an issuer per tile the two ran in step: 4100 against 3100 clocks a step) ----
+    if (lane == 0) {
       const uint32_t idesc_s = tc::make_idesc(1, 1, kRows, kKeys);
       const uint32_t idesc_o = tc::make_idesc(1, 1, kRows, D) | (1u << 16);       // B is MN-major
-      const uint32_t st = tmem + 128 * t, ot = tmem + 256 + 128 * t, qa = q0 + t * kTileBytes;
-      auto scores = [&](int i) {
-        const uint32_t kb = k0 + (i & 1) * kTileBytes;
+      auto scores = [&](int t, int n) {
+        const uint32_t st = tmem + 128 * t, qa = q0 + t * kTileBytes, kb = k0 + (n & 1) * kTileBytes;
 #pragma unroll
-        for (int e = 0; e < D / 16; ++e)
-          tc::mma_f16(st, tc::desc_sw128(qa + (e >> 2) * (128 * 128)) + 2 * (e & 3),
-                      tc::desc_sw128(kb + (e >> 2) * (128 * 128)) + 2 * (e & 3), idesc_s, e > 0);
+        for (int k = 0; k < D / 16; ++k)
+          tc::mma_f16(st, tc::desc_sw128(qa + (k >> 2) * (128 * 128)) + 2 * (k & 3),
+                      tc::desc_sw128(kb + (k >> 2) * (128 * 128)) + 2 * (k & 3), idesc_s, k > 0);
         tc::mma_commit(&s.s_full[t]);
-        tc::mma_commit(&s.k_free[i & 1]);
       };
-      bool ok = tc::mbar_wait(&s.q_full, 0, a.status, abort_flag) && tc::mbar_wait(&s.k_full[0], 0, a.status, abort_flag);
-      if (ok) {
-        tc::fence_proxy_async();     // the copying threads' writes, seen through the barrier, -> the tensor cores' reads
-        tc::tc_fence_after();
-        scores(0);
-      }
-      for (int i = 0; i < tr.tiles && ok; ++i) {
-        // the copies are waited for ahead of P, so that nothing but P separates the products
-        const bool more = i + 1 < tr.tiles;
-        ok = tc::mbar_wait(&s.v_full[i & 1], (i >> 1) & 1, a.status, abort_flag) &&
-             (!more || tc::mbar_wait(&s.k_full[(i + 1) & 1], ((i + 1) >> 1) & 1, a.status, abort_flag));
-        tc::fence_proxy_async();
-        const uint32_t vb = v0 + (i & 1) * kTileBytes;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          ok = ok && tc::mbar_wait(&s.p_full[t][h], i & 1, a.status, abort_flag);
+      auto wait_keys = [&](int n) { return tc::mbar_wait(&s.k_full[n & 1], (n >> 1) & 1, a.status, abort_flag); };
+      auto wait_values = [&](int n) { return tc::mbar_wait(&s.v_full[n & 1], (n >> 1) & 1, a.status, abort_flag); };
+      bool ok = true;
+      int n = 0, e[2] = {0, 0}, g[2] = {0, 0};
+      for (int64_t x = x0; x < x1 && ok;) {
+        Unit<kKeys> un;
+        const auto pc = line.locate(x, &un);
+        const int count = int(min(int64_t(un.tr.tiles - pc.tile), x1 - x));
+        x += count;
+        const int tiles = un.rows > kRows ? 2 : 1;
+        ok = wait_keys(n);
+        for (int t = 0; t < tiles && ok; ++t) {
+          ok = tc::mbar_wait(&s.q_full[t], g[t] & 1, a.status, abort_flag);
+          ++g[t];
           if (!ok) break;
+          tc::fence_proxy_async();     // the copying threads' writes, seen through the barrier, -> the tensor cores' reads
           tc::tc_fence_after();
-#pragma unroll
-          for (int e = 4 * h; e < 4 * h + 4; ++e)
-            mma_ts(ot, st + 8 * e, desc_mn(vb + e * 16 * 128, 128 * 128), idesc_o, i > 0 || e > 0);
+          scores(t, n);
         }
-        if (!ok) break;
-        if (more) scores(i + 1);
-        else tc::mma_commit(&s.o_full[t]);
-        tc::mma_commit(&s.v_free[i & 1]);
+        tc::mma_commit(&s.k_free[n & 1]);
+        for (int i = 0; i < count && ok; ++i, ++n) {
+          // the copies are waited for ahead of P, so that nothing but P separates the products
+          const bool more = i + 1 < count;
+          ok = wait_values(n) && (!more || wait_keys(n + 1));
+          tc::fence_proxy_async();
+          const uint32_t vb = v0 + (n & 1) * kTileBytes;
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            if (t >= tiles) break;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              ok = ok && tc::mbar_wait(&s.p_full[t][h], e[t] & 1, a.status, abort_flag);
+              if (!ok) break;
+              tc::tc_fence_after();
+#pragma unroll
+              for (int k = 4 * h; k < 4 * h + 4; ++k)
+                mma_ts(tmem + 256 + 128 * t, tmem + 128 * t + 8 * k, desc_mn(vb + k * 16 * 128, 128 * 128), idesc_o, i > 0 || k > 0);
+            }
+            if (!ok) break;
+            ++e[t];
+            if (more) scores(t, n + 1);
+            else tc::mma_commit(&s.o_full[t]);
+          }
+          if (!ok) break;
+          if (more) tc::mma_commit(&s.k_free[(n + 1) & 1]);
+          tc::mma_commit(&s.v_free[n & 1]);
+        }
       }
       if (!ok) {                      // after a timeout: what was issued ends before TMEM is freed
-        tc::mma_commit(&s.drain[t]);
-        for (int n = 0; n < (1 << 22) && !tc::mbar_test(&s.drain[t], 0); ++n) {
+        tc::mma_commit(&s.drain);
+        for (int k = 0; k < (1 << 22) && !tc::mbar_test(&s.drain, 0); ++k) {
         }
       }
     }
     __syncwarp();
   } else {
-    // ---- the copying warps: K_0, V_0, K_1, V_1, ... each as soon as its buffer is free; a buffer's
-    // barrier completes when every thread's copies into it have landed ----
-    const int lt = tid - 10 * 32;
+    // ---- the copying warps: each step's keys, then its values, as soon as a buffer is free; a
+    // buffer's barrier completes when every thread's copies into it have landed ----
+    const int lt = tid - 9 * 32;
     bool ok = true;
-    auto page_of = [&](int i) {
-      if (i >= tr.tiles) return -1;
-      const int kt = tr.at(i);
-      const int32_t page = a.bt[int64_t(b) * a.max_blocks + kt / (kBlockPositions / kKeys)];
-      if (page >= 0 && page < a.num_blocks) return int(page);
-      if (lt == 0) report(a.status, V4A_DEV_BAD_BLOCK);
-      return -1;
-    };
-    int page = page_of(0);
-    for (int i = 0; i < tr.tiles && ok; ++i) {
-      const int next = page_of(i + 1);
-      const int j0 = tr.at(i) * kKeys;
-      const uint8_t* rows_k = a.pool + (page < 0 ? 0 : page * a.block_bytes + (int64_t(hk) * kBlockPositions + j0 % kBlockPositions) * (2 * D));
-      const bool whole = page >= 0 && j0 + kKeys - 1 <= m_hi && (a.window == 0 || j0 > m_lo - a.window);
-      if (lt == 0) s.missing[i & 3] = page < 0;
-#pragma unroll 1
-      for (int half = 0; half < 2; ++half) {
-        ok = tc::mbar_wait(half ? &s.v_free[i & 1] : &s.k_free[i & 1], ((i >> 1) & 1) ^ 1, a.status, abort_flag);
-        if (!ok) break;
-        const uint8_t* src = rows_k + (page < 0 ? 0 : half * (int64_t(a.K) * kBlockPositions * (2 * D)));
-        const uint32_t dst = (half ? v0 : k0) + (i & 1) * kTileBytes;
-        if (whole) {
-#pragma unroll
-          for (int e = 0; e < kKeys * (D / 8) / kLoaders; ++e) {
-            const int c = lt + e * kLoaders;
-            copy16(dst + chunk_at(c / (D / 8), c % (D / 8)), src + c * 16, true);
-          }
-        } else {
-#pragma unroll 4
-          for (int e = 0; e < kKeys * (D / 8) / kLoaders; ++e) {
-            const int c = lt + e * kLoaders, j = j0 + c / (D / 8);
-            const bool live = page >= 0 && j <= m_hi && (a.window == 0 || j > m_lo - a.window || j < a.sinks);
-            copy16(dst + chunk_at(c / (D / 8), c % (D / 8)), src + (page < 0 ? 0 : c * 16), live);
-          }
+    int n = 0;
+    for (int64_t x = x0; x < x1 && ok;) {
+      Unit<kKeys> un;
+      const auto pc = line.locate(x, &un);
+      const int count = int(min(int64_t(un.tr.tiles - pc.tile), x1 - x));
+      x += count;
+      auto entry = [&](int i) {      // step i's table entry, read a step ahead of its use
+        return i < count ? a.bt[int64_t(un.b) * a.max_blocks + un.tr.at(pc.tile + i) / (kBlockPositions / kKeys)] : -1;
+      };
+      int32_t next = entry(0);
+      for (int i = 0; i < count && ok; ++i, ++n) {
+        int32_t page = next;
+        next = entry(i + 1);
+        if (page < 0 || page >= a.num_blocks) {
+          if (lt == 0) report(a.status, V4A_DEV_BAD_BLOCK);
+          page = -1;
         }
-        arrive_copies(half ? &s.v_full[i & 1] : &s.k_full[i & 1]);
+        const int j0 = un.tr.at(pc.tile + i) * kKeys;
+        const uint8_t* rows_k =
+            a.pool + (page < 0 ? 0 : page * a.block_bytes + (int64_t(pc.hk) * kBlockPositions + j0 % kBlockPositions) * (2 * D));
+        const bool whole = page >= 0 && j0 + kKeys - 1 <= un.m_hi && (a.window == 0 || j0 > un.m_lo - a.window);
+        if (lt == 0) s.missing[n & 3] = page < 0;
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+          ok = tc::mbar_wait(half ? &s.v_free[n & 1] : &s.k_free[n & 1], ((n >> 1) & 1) ^ 1, a.status, abort_flag);
+          if (!ok) break;
+          const uint8_t* src = rows_k + (page < 0 ? 0 : half * (int64_t(a.K) * kBlockPositions * (2 * D)));
+          const uint32_t dst = (half ? v0 : k0) + (n & 1) * kTileBytes;
+          // thread lt: chunk lt % (dim / 8) of rows lt / (dim / 8) + k * (96 / (dim / 8))
+          constexpr int kChunks = kKeys * (D / 8), kPasses = (kChunks + kLoaders - 1) / kLoaders;
+          if (whole) {
+#pragma unroll
+            for (int k = 0; k < kPasses; ++k) {
+              const int c = lt + k * kLoaders;
+              if (c < kChunks) copy16(dst + chunk_at(c / (D / 8), c % (D / 8)), src + c * 16, true);
+            }
+          } else {
+            const int hi = page < 0 ? -1 : un.m_hi - j0, lo = a.window ? un.m_lo - a.window - j0 : -1, sk = a.window ? a.sinks - j0 : 0;
+            const int step = page < 0 ? 0 : kLoaders * 16;
+            src += page < 0 ? 0 : lt * 16;
+#pragma unroll
+            for (int k = 0; k < kPasses; ++k) {
+              const int c = lt + k * kLoaders, r = c / (D / 8);
+              if (c < kChunks) copy16(dst + chunk_at(r, c % (D / 8)), src + k * step, r <= hi && (r > lo || r < sk));
+            }
+          }
+          arrive_copies(half ? &s.v_full[n & 1] : &s.k_full[n & 1]);
+        }
       }
-      page = next;
     }
     tc::cp_async_wait_all();
   }
   __syncthreads();
   tc::tc_fence_after();
   if (warp == 0) tc::tmem_dealloc(tmem, 512);
+  if (p.split && tid == 0) {          // at most the last unit goes on in the next CTAs
+    Unit<kKeys> un;
+    const auto pc = line.locate(x1 - 1, &un);
+    // (its first tile has to lie in the range, its last one behind it)
+    const bool tail = pc.tile + 1 < un.tr.tiles && x1 - 1 - pc.tile >= x0;
+    p.join[blockIdx.x] = tail ? line.describe(pc, un) : JoinDesc{};
+  }
   pdl_trigger();
 }
 
 template <int D>
-int launch(const DenseAttnDev& d, cudaStream_t stream) {
-  constexpr int smem = 1024 + 6 * 128 * D * 2 + int(sizeof(PreSmem));
+int launch(const DenseAttnDev& d, const SplitDev& p, cudaStream_t stream) {
   // at least 116 KB: no two CTAs that allocate TMEM share an SM
-  constexpr int bytes = smem < 116 * 1024 ? 116 * 1024 : smem;
-  static_assert(bytes <= 227 * 1024, "shared memory");
-  if (cudaFuncSetAttribute(dense_prefill_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
-    return V4A_ERR_CUDA;
+  size_t bytes = 1024 + 6 * 128 * D * 2 + sizeof(PreSmem) + split_smem(p.split, p.U, d.B);
+  if (bytes < 116 * 1024) bytes = 116 * 1024;
+  if (bytes > 227 * 1024) return V4A_ERR_UNSUPPORTED;
+  auto kern = dense_prefill_kernel<D>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024) != cudaSuccess) return V4A_ERR_CUDA;
   cudaFuncAttributes attr;
-  if (cudaFuncGetAttributes(&attr, dense_prefill_kernel<D>) != cudaSuccess) return V4A_ERR_CUDA;
+  if (cudaFuncGetAttributes(&attr, kern) != cudaSuccess) return V4A_ERR_CUDA;
   if (attr.numRegs != 168) return V4A_ERR_UNSUPPORTED;     // the register split would not add up
-  const int64_t rows = int64_t(d.max_new) * d.G, blocks = (rows + 2 * kRows - 1) / (2 * kRows);
-  if (blocks > 65535 || int64_t(d.K) * d.B > INT32_MAX) return V4A_ERR_UNSUPPORTED;
-  const cudaError_t e = launch_pdl(dense_prefill_kernel<D>, dim3(unsigned(d.K * d.B), unsigned(blocks)), dim3(kThreads), bytes, stream, d);
-  return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? V4A_OK : V4A_ERR_CUDA;
+  const int64_t grid = p.split ? kSplitCtas : int64_t(p.U) * d.K;
+  if (grid > INT32_MAX) return V4A_ERR_UNSUPPORTED;
+  const cudaError_t e = launch_pdl(kern, dim3(unsigned(grid)), dim3(kThreads), bytes, stream, d, p);
+  if (e != cudaSuccess || cudaGetLastError() != cudaSuccess) return V4A_ERR_CUDA;
+  return p.split ? dense_join(d, p, D, stream) : V4A_OK;
+}
+
+int64_t row_blocks(const v4a_dense_attn_args* a) {
+  return (int64_t(a->max_new_per_seq) * (a->num_heads / a->kv.num_kv_heads) + kUnit - 1) / kUnit;
 }
 
 }  // namespace
 
 bool dense_prefill_takes(const v4a_dense_attn_args* a) {
   const int64_t rows = int64_t(a->max_new_per_seq) * (a->num_heads / a->kv.num_kv_heads);
-  return a->kv.format == V4A_KV_BF16 && (a->kv.dim == 64 || a->kv.dim == 128) && rows > 64 && rows <= int64_t(65535) * 256;
+  return a->kv.format == V4A_KV_BF16 && (a->kv.dim == 64 || a->kv.dim == 128) && rows > 64;
 }
 
-int dense_prefill(const DenseAttnDev& d, int dim, cudaStream_t stream) {
-  return dim == 64 ? launch<64>(d, stream) : launch<128>(d, stream);
+size_t dense_prefill_workspace(const v4a_dense_attn_args* a) { return split_workspace(kUnit, a->kv.dim); }
+
+int dense_prefill(const v4a_dense_attn_args* a, const DenseAttnDev& d, void* ws, cudaStream_t stream) {
+  SplitDev p{};
+  p.RG = int(row_blocks(a));
+  p.U = d.B * p.RG;
+  p.split = p.U <= kMaxSplitUnits;
+  split_carve(&p, ws, kUnit, a->kv.dim);
+  return a->kv.dim == 64 ? launch<64>(d, p, stream) : launch<128>(d, p, stream);
 }
 
 }  // namespace v4a
