@@ -41,9 +41,10 @@ struct Shape {
   static constexpr int kHalf = kKeys * kRow;                     // keys (or values) of a tile: 32 D bytes
   static constexpr int kScales = kFp8 ? 2 * kKeys * 4 : 0;
   static constexpr int kStage = 2 * kHalf + kScales;             // holds R x D fp32 for the merge as well
-  static constexpr int kWarps = D <= 128 ? 8 : 4;
+  static constexpr int kWarps = 4;
   static constexpr int kThreads = 32 * kWarps;
-  static constexpr int kStages = kRingBytes / (kWarps * 2 * kHalf);
+  static constexpr int kPerSm = D <= 128 ? 2 : 1;                // CTAs per SM: while one's warps meet, the other's stream
+  static constexpr int kStages = kRingBytes / kPerSm / (kWarps * 2 * kHalf);
   static_assert(R * D * 4 <= 2 * kHalf && kStages >= 3, "a stage holds the merge rows");
   struct Tail {                                                  // behind the rings
     int64_t scan[kWarps];
@@ -109,7 +110,7 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&b);
 }
 template <int D, int NT, bool kFp8>
-__global__ void __launch_bounds__(Shape<D, NT, kFp8>::kThreads, 1) dense_attn_mma(const DenseAttnDev a, const SplitDev p) {
+__global__ void __launch_bounds__(Shape<D, NT, kFp8>::kThreads, Shape<D, NT, kFp8>::kPerSm) dense_attn_mma(const DenseAttnDev a, const SplitDev p) {
   using S = Shape<D, NT, kFp8>;
   constexpr int R = S::R, kWarps = S::kWarps, kThreads = S::kThreads, kKeys = S::kKeys, MT = kKeys / 16;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -179,18 +180,14 @@ __global__ void __launch_bounds__(Shape<D, NT, kFp8>::kThreads, 1) dense_attn_mm
   const float f = a.scale_log2;
   const int g4 = lane >> 2, c2 = (lane & 3) * 2;
   int stage = 0;                                 // of this warp's next tile
-  int64_t x = x0;
-  while (x < x1) {
-    Unit<kKeys> un;
-    const auto pc = line.locate(x, &un);
-    const int count = int(min(int64_t(un.tr.tiles - pc.tile), x1 - x));     // tiles of this segment
+  uint32_t qf[D / 16][NT][2];
+  auto load_q = [&](const Unit<kKeys>& un, int hk) {
     // the query rows as B operands: column g4 of n-tile nt, dims of step ks
-    uint32_t qf[D / 16][NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int r = nt * 8 + g4;
       const bool live = r < un.rows;
-      const uint16_t* q = a.q + row_of(a, un, pc.hk, r) * D;
+      const uint16_t* q = a.q + row_of(a, un, hk, live ? r : 0) * D;
 #pragma unroll
       for (int ks = 0; ks < D / 16; ++ks) {
         if (kFp8) {           // fp8: a thread's four codes are dims 4 (lane % 4) .. + 3 of the step
@@ -203,6 +200,15 @@ __global__ void __launch_bounds__(Shape<D, NT, kFp8>::kThreads, 1) dense_attn_mm
         }
       }
     }
+  };
+  int64_t x = x0;
+  Unit<kKeys> next_un;
+  auto next_pc = line.locate(x, &next_un);
+  load_q(next_un, next_pc.hk);
+  while (x < x1) {
+    const Unit<kKeys> un = next_un;
+    const auto pc = next_pc;
+    const int count = int(min(int64_t(un.tr.tiles - pc.tile), x1 - x));     // tiles of this segment
     float o[D / 16][NT][4], m[NT][2], l[NT][2];
     int mrow[NT][2];                               // the columns' query positions
 #pragma unroll
@@ -401,6 +407,10 @@ __global__ void __launch_bounds__(Shape<D, NT, kFp8>::kThreads, 1) dense_attn_mm
     // ---- the warps' results meet: o [R][D] fp32 in the stage read last ----
     // (float index r D + (d with bits 3..4 turned by r / 2): the rows that one
     // store touches lie in different banks)
+    if (x + count < x1) {          // the next segment's queries are on their way meanwhile
+      next_pc = line.locate(x + count, &next_un);
+      load_q(next_un, next_pc.hk);
+    }
     __syncwarp();
     float* mine_o = reinterpret_cast<float*>(ring + last * S::kStage);
     if (lane == 0) s.buf[warp] = int(ring - smem) + last * S::kStage;
@@ -591,8 +601,10 @@ int64_t row_groups(const v4a_dense_attn_args* a) {
   return (rows + rows_of(a) - 1) / rows_of(a);
 }
 
+int ctas_of(const v4a_dense_attn_args* a) { return a->kv.dim <= 128 ? 2 * kSms : kSms; }
+
 size_t workspace_of(const v4a_dense_attn_args* a) {
-  return dense_prefill_takes(a) ? dense_prefill_workspace(a) : split_workspace(rows_of(a), a->kv.dim);
+  return dense_prefill_takes(a) ? dense_prefill_workspace(a) : split_workspace(rows_of(a), a->kv.dim, ctas_of(a));
 }
 
 template <int D, int NT, bool kFp8>
@@ -602,7 +614,7 @@ int launch(const DenseAttnDev& a, const SplitDev& p, cudaStream_t stream) {
   if (smem > 227 * 1024) return V4A_ERR_UNSUPPORTED;
   auto kern = dense_attn_mma<D, NT, kFp8>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024) != cudaSuccess) return V4A_ERR_CUDA;
-  const int64_t grid = p.split ? kSplitCtas : int64_t(p.U) * a.K;
+  const int64_t grid = p.split ? p.grid : int64_t(p.U) * a.K;
   if (grid > INT32_MAX) return V4A_ERR_UNSUPPORTED;
   const cudaError_t e = launch_pdl(kern, dim3(unsigned(grid)), dim3(S::kThreads), smem, stream, a, p);
   if (e != cudaSuccess || cudaGetLastError() != cudaSuccess) return V4A_ERR_CUDA;
@@ -640,7 +652,7 @@ int dense_join(const DenseAttnDev& a, const SplitDev& p, int dim, cudaStream_t s
   auto kern = many ? (dim == 64 ? dense_join_rows<64> : dense_join_rows<128>)
                    : (dim == 64 ? dense_join_kernel<64> : dim == 128 ? dense_join_kernel<128> : dim == 192 ? dense_join_kernel<192> : dense_join_kernel<256>);
   const int y = many ? dim / 16 : p.rows;
-  const cudaError_t e = launch_pdl(kern, dim3(kSplitCtas, unsigned(y)), dim3(256), 0, stream, a, p);
+  const cudaError_t e = launch_pdl(kern, dim3(unsigned(p.grid), unsigned(y)), dim3(256), 0, stream, a, p);
   return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? V4A_OK : V4A_ERR_CUDA;
 }
 
@@ -671,7 +683,7 @@ int dense_attn(const v4a_dense_attn_args* a, void* ws, size_t ws_bytes, cudaStre
   p.RG = int(row_groups(a));
   p.U = d.B * p.RG;
   p.split = p.U <= kMaxSplitUnits;
-  split_carve(&p, ws, rows_of(a), a->kv.dim);
+  split_carve(&p, ws, rows_of(a), a->kv.dim, ctas_of(a));
   return a->kv.format == V4A_KV_FP8_TOKEN ? launch_dim<true>(d, p, a->kv.dim, stream) : launch_dim<false>(d, p, a->kv.dim, stream);
 }
 

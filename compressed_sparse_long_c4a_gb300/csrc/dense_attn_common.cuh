@@ -100,7 +100,7 @@ __device__ __forceinline__ int64_t row_of(const DenseAttnDev& a, const Unit<kTil
 // divide evenly; split = 0: one CTA per unit and KV head.
 struct SplitDev {
   int RG, U, split;               // row groups per sequence, units (sequences x row groups)
-  int rows;                       // R
+  int rows, grid;                 // R; CTAs of the launch (split)
   struct JoinDesc* join;          // [CTA]
   float *part_o, *part_ml;        // [CTA][2][R][dim], [CTA][2][R][2] (maximum in log2 units, sum)
 };
@@ -109,20 +109,21 @@ struct SplitDev {
 // its pieces are this CTA's slot 1 and slot 0 of the others.
 struct JoinDesc { int valid, b, rg, hk, last, pad[3]; };
 
-constexpr int kMaxSplitUnits = 1024;
-constexpr int kSplitCtas = 152;   // one CTA per SM
+constexpr int kMaxSplitUnits = 512;   // more units than these fill the machine one by one
+constexpr int kSms = 152;
 
 __host__ __device__ constexpr size_t split_smem(int split, int U, int B) {
   return split ? (U + 1) * sizeof(int64_t) + B * sizeof(SeqRun) : sizeof(SeqRun);
 }
-__host__ __device__ constexpr size_t split_workspace(int R, int dim) {
-  return 16 + kSplitCtas * (sizeof(JoinDesc) + size_t(2) * R * (dim + 2) * sizeof(float));
+__host__ __device__ constexpr size_t split_workspace(int R, int dim, int ctas) {
+  return 16 + ctas * (sizeof(JoinDesc) + size_t(2) * R * (dim + 2) * sizeof(float));
 }
-inline void split_carve(SplitDev* p, void* ws, int R, int dim) {
+inline void split_carve(SplitDev* p, void* ws, int R, int dim, int ctas) {
   p->rows = R;
+  p->grid = ctas;
   p->join = static_cast<JoinDesc*>(ws);
-  p->part_o = reinterpret_cast<float*>(p->join + kSplitCtas);
-  p->part_ml = p->part_o + size_t(kSplitCtas) * 2 * R * dim;
+  p->part_o = reinterpret_cast<float*>(p->join + ctas);
+  p->part_ml = p->part_o + size_t(ctas) * 2 * R * dim;
 }
 
 // The CTA's part of the line (or its unit), kept in shared memory behind `mem`.

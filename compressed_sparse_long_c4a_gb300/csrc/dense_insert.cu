@@ -9,12 +9,14 @@
 // no fp64 and no range reduction runs on the device and far positions lose
 // nothing.
 //
-// Bound: memory.  Every row is read once and written once; a row of dim
-// elements is held by dim / 8 lanes as one 16-byte load each, the norm and the
-// fp8 row maximum are shuffles inside those lanes, and the halves of a
-// half-split pair meet by a shuffle.  A CTA takes one token (or part of its
-// rows when tokens are few): its cos and sin are computed once and shared by
-// all its heads, and all its loads are issued before the first use.
+// Bound: memory, if the arithmetic keeps out of its way.  Every row is read
+// once and written once.  A row is held by dim / 8 lanes, each with two runs of
+// four dims: in the half layout a lane takes the two halves of its pairs, so
+// the rotation needs no exchange, and its cosines and sines are the same for
+// every row that it handles and stay in registers.  The norm
+// and the fp8 row maximum are shuffles inside the row's lanes.  A CTA takes one
+// token (or part of its rows when tokens are few): its angles are computed once
+// and shared by all its heads, and all its loads are issued before the first use.
 #include "tc_common.cuh"
 #include "v4a_dense.h"
 #include "v4a_dense_internal.h"
@@ -22,8 +24,8 @@
 namespace v4a {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kPasses = 4;        // rows per lane group held in registers (16 bytes a lane each)
+constexpr int kThreads = 128;     // eight CTAs an SM: 121 us for 16384 tokens of 64 + 8 + 8 heads; four of 256 threads took 124
+constexpr int kPasses = 5;        // rows per lane group held in registers (16 bytes a lane each)
 
 struct InsertDev {
   uint64_t turn[128];             // F_j: turns per position as a 64-bit fraction
@@ -42,123 +44,145 @@ struct InsertDev {
   int32_t* status;
 };
 
+__device__ __forceinline__ void unpack4(uint2 w, float* x) {
+  x[0] = __uint_as_float(w.x << 16);
+  x[1] = __uint_as_float(w.x & 0xffff0000u);
+  x[2] = __uint_as_float(w.y << 16);
+  x[3] = __uint_as_float(w.y & 0xffff0000u);
+}
+__device__ __forceinline__ uint2 pack4(const float* x) {
+  const __nv_bfloat162 a = __floats2bfloat162_rn(x[0], x[1]), b = __floats2bfloat162_rn(x[2], x[3]);
+  return make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+}
+
 // kLanes: lanes of one row (dim / 8, or 32 with the last eight idle at dim 192).
 template <int kLanes, bool kFp8>
-__global__ void __launch_bounds__(kThreads) dense_insert_kernel(const __grid_constant__ InsertDev p) {
+__global__ void __launch_bounds__(kThreads, 8) dense_insert_kernel(const __grid_constant__ InsertDev p) {
   constexpr int kRows = kThreads / kLanes;      // rows per pass
-  __shared__ float cs[256];                     // cos [0, R/2), sin [R/2, R)
+  __shared__ alignas(16) float cs[256];         // cos [0, R/2), sin [R/2, R)
   const int t = blockIdx.x, tid = threadIdx.x;
   const int l = tid % kLanes, r0 = blockIdx.y * (kRows * p.passes) + tid / kLanes;
   const int D = p.D;
   const bool live = 8 * l < D;
+  // this lane's dims: d0 .. d0 + 3 and d1 .. d1 + 3; with `rot` their pairs' cosines start at cs[j]
+  int d0 = 8 * l, d1 = 8 * l + 4, j = 0;
+  bool rot;
+  if (p.half) {
+    rot = l < p.R / 8;
+    if (rot) {
+      j = 4 * l;
+      d0 = p.first + j;
+      d1 = d0 + p.R / 2;
+    } else {                                    // the dims beside the rotated ones, eight at a time
+      d0 = 8 * l - p.R;
+      if (d0 >= p.first) d0 += p.R;
+      d1 = d0 + 4;
+    }
+  } else {
+    rot = d0 >= p.first && d0 < p.first + p.R;
+    if (rot) j = (d0 - p.first) / 2;
+  }
+  rot = rot && live;
   pdl_trigger();
   pdl_wait();
   const int64_t slot = p.slots[t];
   const int P = p.positions[t];
-  uint4 raw[kPasses];
+  uint2 lo[kPasses], hi[kPasses];
 #pragma unroll
   for (int i = 0; i < kPasses; ++i) {
     const int r = r0 + i * kRows;
-    raw[i] = make_uint4(0, 0, 0, 0);
+    lo[i] = hi[i] = make_uint2(0, 0);
     if (i < p.passes && r < p.NR && live) {
       const uint16_t* src = r < p.H ? p.q + int64_t(t) * p.qs + r * D
                             : r < p.H + p.K ? p.k + int64_t(t) * p.ks + (r - p.H) * D
                                             : p.v + int64_t(t) * p.vs + (r - p.H - p.K) * D;
-      raw[i] = *reinterpret_cast<const uint4*>(src + 8 * l);
+      lo[i] = *reinterpret_cast<const uint2*>(src + d0);
+      hi[i] = *reinterpret_cast<const uint2*>(src + d1);
     }
   }
   if (slot < 0 || slot >= p.num_slots || P < 0) {   // the whole CTA
     if (tid == 0 && slot != -1) report(p.status, slot < 0 || slot >= p.num_slots ? V4A_DEV_BAD_BLOCK : V4A_DEV_BAD_BATCH);
     return;
   }
-  for (int j = tid; j < p.R / 2; j += kThreads) {
-    const int32_t frac = int32_t((uint64_t(uint32_t(P)) * p.turn[j]) >> 32);
+  for (int i = tid; i < p.R / 2; i += kThreads) {
+    const int32_t frac = int32_t((uint64_t(uint32_t(P)) * p.turn[i]) >> 32);
     float sn, co;
     sincospif(float(frac) * 0x1p-31f, &sn, &co);
-    cs[j] = co * p.magnitude;
-    cs[p.R / 2 + j] = sn * p.magnitude;
+    cs[i] = co * p.magnitude;
+    cs[p.R / 2 + i] = sn * p.magnitude;
   }
   __syncthreads();
-  const int d0 = 8 * l, rel = d0 - p.first;
-  const bool rot = live && rel >= 0 && rel < p.R;
-  const bool upper = rel >= p.R / 2;             // half layout: this lane holds the pairs' second halves
-  const int mate = p.half && rot ? (upper ? l - p.R / 16 : l + p.R / 16) : l;
+  float co[4] = {1.f, 1.f, 1.f, 1.f}, sn[4] = {0.f, 0.f, 0.f, 0.f};
+  if (rot) {
+    const float4 c = *reinterpret_cast<const float4*>(cs + j), s = *reinterpret_cast<const float4*>(cs + p.R / 2 + j);
+    co[0] = c.x; co[1] = c.y; co[2] = c.z; co[3] = c.w;
+    sn[0] = s.x; sn[1] = s.y; sn[2] = s.z; sn[3] = s.w;
+  }
   uint8_t* block = p.pool + (slot / kBlockPositions) * p.block_bytes;
   const int at = int(slot % kBlockPositions);
 #pragma unroll
   for (int i = 0; i < kPasses; ++i) {
     const int r = r0 + i * kRows;
     if (i >= p.passes) break;                    // the same for the whole CTA
-    const bool is_q = r < p.H, is_v = r >= p.H + p.K, row_ok = r < p.NR;
-    const uint32_t u[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+    const bool is_q = r < p.H, is_v = r >= p.H + p.K;
     float x[8];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      x[2 * e] = __uint_as_float(u[e] << 16);
-      x[2 * e + 1] = __uint_as_float(u[e] & 0xffff0000u);
-    }
+    unpack4(lo[i], x);
+    unpack4(hi[i], x + 4);
     const float* gamma = is_q ? p.qg : is_v ? nullptr : p.kg;
-    float ss = 0.f;
+    if (gamma) {
+      float ss = 0.f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
+      for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
+      // a group of lanes that shares a row is here together
+      const uint32_t group = kLanes == 32 ? 0xffffffffu : ((1u << (kLanes & 31)) - 1u) << ((tid & 31) / kLanes * kLanes);
 #pragma unroll
-    for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    if (gamma && live) {
+      for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(group, ss, o);
       const float inv = rsqrtf(ss / float(D) + p.eps);
-      const float4 g0 = *reinterpret_cast<const float4*>(gamma + d0), g1 = *reinterpret_cast<const float4*>(gamma + d0 + 4);
+      const int at0 = live ? d0 : 0, at1 = live ? d1 : 0;
+      const float4 g0 = __ldg(reinterpret_cast<const float4*>(gamma + at0)), g1 = __ldg(reinterpret_cast<const float4*>(gamma + at1));
       x[0] *= inv * g0.x; x[1] *= inv * g0.y; x[2] *= inv * g0.z; x[3] *= inv * g0.w;
       x[4] *= inv * g1.x; x[5] *= inv * g1.y; x[6] *= inv * g1.z; x[7] *= inv * g1.w;
     }
-    if (p.half) {
-      float y[8];
+    if (rot && !is_v) {
+      auto turn = [](float& u, float& w, float c, float s) {
+        const float a = fmaf(-w, s, u * c), b = fmaf(w, c, u * s);
+        u = a;
+        w = b;
+      };
+      if (p.half) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] = __shfl_sync(0xffffffffu, x[e], mate, kLanes);
-      if (rot && !is_v) {
-        const int j = upper ? rel - p.R / 2 : rel;
+        for (int e = 0; e < 4; ++e) turn(x[e], x[4 + e], co[e], sn[e]);
+      } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float co = cs[j + e], sn = cs[p.R / 2 + j + e];
-          x[e] = upper ? fmaf(y[e], sn, x[e] * co) : fmaf(-y[e], sn, x[e] * co);
-        }
-      }
-    } else if (rot && !is_v) {
-      const int j = rel / 2;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float co = cs[j + e], sn = cs[p.R / 2 + j + e], a = x[2 * e], b = x[2 * e + 1];
-        x[2 * e] = fmaf(-b, sn, a * co);
-        x[2 * e + 1] = fmaf(b, co, a * sn);
+        for (int e = 0; e < 4; ++e) turn(x[2 * e], x[2 * e + 1], co[e], sn[e]);
       }
     }
-    // row maximum of |x| as bits: a NaN is the largest of them, and makes the
-    // row's scale NaN (readers may decode the code itself as a number)
-    uint32_t top = 0;
-    if (kFp8) {
+    const int64_t row = int64_t(r - p.H) * kBlockPositions + at;     // keys' heads, then values'
+    if (is_q || !kFp8) {
+      if (r < p.NR && live) {
+        uint16_t* dst = is_q ? p.q_out + int64_t(t) * p.qos + r * D : reinterpret_cast<uint16_t*>(block) + row * D;
+        *reinterpret_cast<uint2*>(dst + d0) = pack4(x);
+        *reinterpret_cast<uint2*>(dst + d1) = pack4(x + 4);
+      }
+    } else {
+      // row maximum of |x| as bits: a NaN is the largest of them, and makes the
+      // row's scale NaN (readers may decode the code itself as a number)
+      const uint32_t group = kLanes == 32 ? 0xffffffffu : ((1u << (kLanes & 31)) - 1u) << ((tid & 31) / kLanes * kLanes);
+      uint32_t top = 0;
 #pragma unroll
       for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(x[e]) & 0x7fffffffu);
 #pragma unroll
-      for (int o = kLanes / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-    }
-    if (!row_ok || !live) continue;
-    if (is_q || !kFp8) {
-      uint32_t w[4];
+      for (int o = kLanes / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(group, top, o));
+      if (r < p.NR && live) {
+        // exact divisions: the codes are those of the definition in fp32
+        const float s = top ? __fdiv_rn(__uint_as_float(top), 448.f) : 1.f;
+        uint32_t w[2] = {0, 0};
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * e], x[2 * e + 1]);
-        w[e] = *reinterpret_cast<const uint32_t*>(&b);
+        for (int e = 0; e < 8; ++e) w[e >> 2] |= uint32_t(f32_to_e4m3(__fdiv_rn(x[e], s))) << (8 * (e & 3));
+        *reinterpret_cast<uint32_t*>(block + row * D + d0) = w[0];
+        *reinterpret_cast<uint32_t*>(block + row * D + d1) = w[1];
+        if (l == 0) reinterpret_cast<float*>(block + int64_t(2 * p.K) * kBlockPositions * D)[row] = s;
       }
-      const int64_t row = int64_t(r - p.H) * kBlockPositions + at;     // keys' heads, then values'
-      uint16_t* dst = is_q ? p.q_out + int64_t(t) * p.qos + r * D : reinterpret_cast<uint16_t*>(block) + row * D;
-      *reinterpret_cast<uint4*>(dst + d0) = make_uint4(w[0], w[1], w[2], w[3]);
-    } else {
-      // exact divisions: the codes are those of the definition in fp32
-      const float s = top ? __fdiv_rn(__uint_as_float(top), 448.f) : 1.f;
-      uint32_t w[2] = {0, 0};
-#pragma unroll
-      for (int e = 0; e < 8; ++e) w[e >> 2] |= uint32_t(f32_to_e4m3(__fdiv_rn(x[e], s))) << (8 * (e & 3));
-      const int64_t row = int64_t(r - p.H) * kBlockPositions + at;
-      *reinterpret_cast<uint2*>(block + row * D + d0) = make_uint2(w[0], w[1]);
-      if (l == 0) reinterpret_cast<float*>(block + int64_t(2 * p.K) * kBlockPositions * D)[row] = s;
     }
   }
 }

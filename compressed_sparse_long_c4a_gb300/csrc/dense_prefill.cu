@@ -471,7 +471,7 @@ int launch(const DenseAttnDev& d, const SplitDev& p, cudaStream_t stream) {
   cudaFuncAttributes attr;
   if (cudaFuncGetAttributes(&attr, kern) != cudaSuccess) return V4A_ERR_CUDA;
   if (attr.numRegs != 168) return V4A_ERR_UNSUPPORTED;     // the register split would not add up
-  const int64_t grid = p.split ? kSplitCtas : int64_t(p.U) * d.K;
+  const int64_t grid = p.split ? p.grid : int64_t(p.U) * d.K;
   if (grid > INT32_MAX) return V4A_ERR_UNSUPPORTED;
   const cudaError_t e = launch_pdl(kern, dim3(unsigned(grid)), dim3(kThreads), bytes, stream, d, p);
   if (e != cudaSuccess || cudaGetLastError() != cudaSuccess) return V4A_ERR_CUDA;
@@ -489,14 +489,14 @@ bool dense_prefill_takes(const v4a_dense_attn_args* a) {
   return a->kv.format == V4A_KV_BF16 && (a->kv.dim == 64 || a->kv.dim == 128) && rows > 64;
 }
 
-size_t dense_prefill_workspace(const v4a_dense_attn_args* a) { return split_workspace(kUnit, a->kv.dim); }
+size_t dense_prefill_workspace(const v4a_dense_attn_args* a) { return split_workspace(kUnit, a->kv.dim, kSms); }
 
 int dense_prefill(const v4a_dense_attn_args* a, const DenseAttnDev& d, void* ws, cudaStream_t stream) {
   SplitDev p{};
   p.RG = int(row_blocks(a));
   p.U = d.B * p.RG;
   p.split = p.U <= kMaxSplitUnits;
-  split_carve(&p, ws, kUnit, a->kv.dim);
+  split_carve(&p, ws, kUnit, a->kv.dim, kSms);
   return a->kv.dim == 64 ? launch<64>(d, p, stream) : launch<128>(d, p, stream);
 }
 
