@@ -407,6 +407,7 @@ __global__ void __launch_bounds__(Shape<D, NT, kFp8>::kThreads, Shape<D, NT, kFp
     // ---- the warps' results meet: o [R][D] fp32 in the stage read last ----
     // (float index r D + (d with bits 3..4 turned by r / 2): the rows that one
     // store touches lie in different banks)
+    if (x + count >= x1) pdl_trigger();      // the join may be set up (it waits for this kernel's end)
     if (x + count < x1) {          // the next segment's queries are on their way meanwhile
       next_pc = line.locate(x + count, &next_un);
       load_q(next_un, next_pc.hk);
@@ -479,7 +480,6 @@ __global__ void __launch_bounds__(Shape<D, NT, kFp8>::kThreads, Shape<D, NT, kFp
     x += count;
   }
   if (p.split && tid == 0) p.join[blockIdx.x] = desc;
-  pdl_trigger();
 }
 
 // Joins the pieces of a unit that several CTAs hold: piece c's slot 1, then
@@ -491,54 +491,50 @@ template <int D>
 __global__ void __launch_bounds__(256) dense_join_kernel(const DenseAttnDev a, const SplitDev p) {
   constexpr int kLanes = D / 4, kGroups = 256 / kLanes > 8 ? 8 : 256 / kLanes;
   __shared__ float4 acc[kGroups][kLanes];
-  __shared__ float red[8];
+  __shared__ float2 red[kGroups];
   const int c = blockIdx.x, r = blockIdx.y, tid = threadIdx.x;
   pdl_wait();
   pdl_trigger();
   const JoinDesc j = p.join[c];
-  if (!j.valid) return;
-  const int s0 = a.starts[j.b], n = a.starts[j.b + 1] - s0;
-  const int64_t row = int64_t(j.rg) * p.rows + r;
-  if (row >= int64_t(n) * a.G) return;
-  auto part = [&](int k) { return (int64_t(c + k) * 2 + (k == 0 ? 1 : 0)) * p.rows + r; };
-  const int pieces = j.last - c + 1;
-  float top = -INFINITY;
-  for (int k = tid; k < pieces; k += 256) top = fmaxf(top, p.part_ml[part(k) * 2]);
-  top = warp_max(top);
-  if ((tid & 31) == 0) red[tid >> 5] = top;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < 8; ++w) top = fmaxf(top, red[w]);
-  const int g = tid / kLanes, l = tid % kLanes;
-  float sum = 0.f;
+  if (r >= j.rows) return;
+  // each group goes once through its pieces with a running maximum
+  const int pieces = j.last - c + 1, g = tid / kLanes, l = tid % kLanes;
+  float top = -INFINITY, sum = 0.f;
   float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
   if (g < kGroups) {
 #pragma unroll 4
     for (int k = g; k < pieces; k += kGroups) {
-      const float m = p.part_ml[part(k) * 2], s = p.part_ml[part(k) * 2 + 1];
-      const float4 o = *reinterpret_cast<const float4*>(p.part_o + part(k) * D + 4 * l);
-      if (m == -INFINITY) continue;          // its o was not written
-      const float w = exp2f(m - top);
-      sum = fmaf(w, s, sum);
-      v.x = fmaf(w, o.x, v.x); v.y = fmaf(w, o.y, v.y); v.z = fmaf(w, o.z, v.z); v.w = fmaf(w, o.w, v.w);
+      const int64_t part = (int64_t(c + k) * 2 + (k == 0 ? 1 : 0)) * p.rows + r;
+      const float2 t = *reinterpret_cast<const float2*>(p.part_ml + part * 2);
+      const float4 o = *reinterpret_cast<const float4*>(p.part_o + part * D + 4 * l);
+      if (t.x == -INFINITY) continue;        // a piece without a key
+      const float m = fmaxf(top, t.x), w0 = exp2f(top - m), w1 = exp2f(t.x - m);
+      top = m;
+      sum = fmaf(sum, w0, w1 * t.y);
+      v.x = fmaf(v.x, w0, w1 * o.x); v.y = fmaf(v.y, w0, w1 * o.y);
+      v.z = fmaf(v.z, w0, w1 * o.z); v.w = fmaf(v.w, w0, w1 * o.w);
     }
-  }
-  __syncthreads();                         // red is read above
-  if (g < kGroups) {
     acc[g][l] = v;
-    if (l == 0) red[g] = sum;
+    if (l == 0) red[g] = make_float2(top, sum);
   }
   __syncthreads();
   if (tid >= kLanes) return;
+  top = -INFINITY;
+#pragma unroll
+  for (int k = 0; k < kGroups; ++k) top = fmaxf(top, red[k].x);
   sum = 0.f;
   v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
   for (int k = 0; k < kGroups; ++k) {
-    const float4 t = acc[k][l];
-    sum += red[k];
-    v.x += t.x; v.y += t.y; v.z += t.z; v.w += t.w;
+    const float2 t = red[k];
+    if (t.x == -INFINITY) continue;
+    const float w = exp2f(t.x - top);
+    const float4 o = acc[k][l];
+    sum = fmaf(w, t.y, sum);
+    v.x = fmaf(w, o.x, v.x); v.y = fmaf(w, o.y, v.y); v.z = fmaf(w, o.z, v.z); v.w = fmaf(w, o.w, v.w);
   }
-  const int64_t at = int64_t(s0 + row / a.G) * a.H + j.hk * a.G + row % a.G;
+  const int i = j.row0 + r;
+  const int64_t at = int64_t(j.s0 + i / a.G) * a.H + j.hk * a.G + i % a.G;
   const float inv = sum > 0.f ? 1.f / sum : sum == 0.f ? 0.f : sum;
   *reinterpret_cast<uint2*>(a.out + at * D + 4 * l) = make_uint2(pack_bf16(v.x * inv, v.y * inv), pack_bf16(v.z * inv, v.w * inv));
   if (l == 0 && a.lse) a.lse[at] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
@@ -553,10 +549,7 @@ __global__ void __launch_bounds__(256) dense_join_rows(const DenseAttnDev a, con
   pdl_wait();
   pdl_trigger();
   const JoinDesc j = p.join[c];
-  if (!j.valid) return;
-  const int s0 = a.starts[j.b], n = a.starts[j.b + 1] - s0;
-  const int64_t row = int64_t(j.rg) * 256 + r;
-  if (row >= int64_t(n) * a.G) return;
+  if (r >= j.rows) return;
   auto slot = [&](int k) { return int64_t(c + k) * 2 + (k == 0 ? 1 : 0); };
   auto ml = [&](int k) { return *reinterpret_cast<const float2*>(p.part_ml + (slot(k) * 256 + r) * 2); };
   const int pieces = j.last - c + 1;
@@ -581,13 +574,14 @@ __global__ void __launch_bounds__(256) dense_join_rows(const DenseAttnDev a, con
       v[i].z = fmaf(w, o[i].z, v[i].z); v[i].w = fmaf(w, o[i].w, v[i].w);
     }
   }
-  const int64_t at = int64_t(s0 + row / a.G) * a.H + j.hk * a.G + row % a.G;
+  const int i = j.row0 + r;
+  const int64_t at = int64_t(j.s0 + i / a.G) * a.H + j.hk * a.G + i % a.G;
   const float inv = sum > 0.f ? 1.f / sum : sum == 0.f ? 0.f : sum;
 #pragma unroll
-  for (int i = 0; i < 4; i += 2)
-    *reinterpret_cast<uint4*>(a.out + at * D + 4 * (d0 + i)) =
-        make_uint4(pack_bf16(v[i].x * inv, v[i].y * inv), pack_bf16(v[i].z * inv, v[i].w * inv),
-                   pack_bf16(v[i + 1].x * inv, v[i + 1].y * inv), pack_bf16(v[i + 1].z * inv, v[i + 1].w * inv));
+  for (int k = 0; k < 4; k += 2)
+    *reinterpret_cast<uint4*>(a.out + at * D + 4 * (d0 + k)) =
+        make_uint4(pack_bf16(v[k].x * inv, v[k].y * inv), pack_bf16(v[k].z * inv, v[k].w * inv),
+                   pack_bf16(v[k + 1].x * inv, v[k + 1].y * inv), pack_bf16(v[k + 1].z * inv, v[k + 1].w * inv));
   if (blockIdx.y == 0 && a.lse) a.lse[at] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
 }
 
@@ -613,7 +607,8 @@ int launch(const DenseAttnDev& a, const SplitDev& p, cudaStream_t stream) {
   const size_t smem = S::kWarps * S::kStages * S::kStage + sizeof(typename S::Tail) + split_smem(p.split, p.U, a.B);
   if (smem > 227 * 1024) return V4A_ERR_UNSUPPORTED;
   auto kern = dense_attn_mma<D, NT, kFp8>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024) != cudaSuccess) return V4A_ERR_CUDA;
+  static std::atomic<uint64_t> done{0};
+  if (!raise_smem(kern, 227 * 1024, &done)) return V4A_ERR_CUDA;
   const int64_t grid = p.split ? p.grid : int64_t(p.U) * a.K;
   if (grid > INT32_MAX) return V4A_ERR_UNSUPPORTED;
   const cudaError_t e = launch_pdl(kern, dim3(unsigned(grid)), dim3(S::kThreads), smem, stream, a, p);

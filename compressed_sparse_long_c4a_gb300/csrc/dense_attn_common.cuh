@@ -1,6 +1,8 @@
 // What the dense attention kernels share: the arguments on the device, which
 // keys a group of rows sees, and the tiles that cover them.
 #pragma once
+#include <atomic>
+
 #include "tc_common.cuh"
 #include "v4a_dense.h"
 #include "v4a_dense_internal.h"
@@ -106,8 +108,8 @@ struct SplitDev {
 };
 
 // A unit that starts in a CTA's range and goes on in the next CTAs' up to `last`:
-// its pieces are this CTA's slot 1 and slot 0 of the others.
-struct JoinDesc { int valid, b, rg, hk, last, pad[3]; };
+// its pieces are this CTA's slot 1 and slot 0 of the others.  rows = 0: none.
+struct alignas(32) JoinDesc { int rows, row0, s0, hk, last, pad[3]; };
 
 constexpr int kMaxSplitUnits = 512;   // more units than these fill the machine one by one
 constexpr int kSms = 152;
@@ -118,6 +120,17 @@ __host__ __device__ constexpr size_t split_smem(int split, int U, int B) {
 __host__ __device__ constexpr size_t split_workspace(int R, int dim, int ctas) {
   return 16 + ctas * (sizeof(JoinDesc) + size_t(2) * R * (dim + 2) * sizeof(float));
 }
+// Raises a kernel's dynamic shared memory limit, once per device (`done`: the devices it is done on).
+template <typename K>
+inline bool raise_smem(K kern, int bytes, std::atomic<uint64_t>* done) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  if (dev < 64 && (done->load() >> dev & 1)) return true;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
+  if (dev < 64) done->fetch_or(uint64_t(1) << dev);
+  return true;
+}
+
 inline void split_carve(SplitDev* p, void* ws, int R, int dim, int ctas) {
   p->rows = R;
   p->grid = ctas;
@@ -186,7 +199,7 @@ struct Line {
     __syncthreads();
     ctas = int(min(int64_t(gridDim.x), (total + min_tiles - 1) / min_tiles));
     if (int(blockIdx.x) >= ctas) {
-      if (tid == 0) p.join[blockIdx.x].valid = 0;
+      if (tid == 0) p.join[blockIdx.x].rows = 0;
       return false;
     }
     x0 = int64_t(blockIdx.x) * total / ctas;
@@ -215,7 +228,7 @@ struct Line {
   // The description of a unit that leaves the CTA's range.
   __device__ __forceinline__ JoinDesc describe(const Piece& pc, const Unit<kTile>& un) const {
     const int64_t end = pre[pc.u] + int64_t(pc.hk + 1) * un.tr.tiles;
-    return JoinDesc{1, un.b, pc.u % p.RG, pc.hk, int((end * ctas - 1) / total), {0, 0, 0}};
+    return JoinDesc{un.rows, un.row0, un.s0, pc.hk, int((end * ctas - 1) / total), {0, 0, 0}};
   }
 };
 

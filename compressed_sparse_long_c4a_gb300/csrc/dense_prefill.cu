@@ -467,7 +467,8 @@ int launch(const DenseAttnDev& d, const SplitDev& p, cudaStream_t stream) {
   if (bytes < 116 * 1024) bytes = 116 * 1024;
   if (bytes > 227 * 1024) return V4A_ERR_UNSUPPORTED;
   auto kern = dense_prefill_kernel<D>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024) != cudaSuccess) return V4A_ERR_CUDA;
+  static std::atomic<uint64_t> done{0};
+  if (!raise_smem(kern, 227 * 1024, &done)) return V4A_ERR_CUDA;
   cudaFuncAttributes attr;
   if (cudaFuncGetAttributes(&attr, kern) != cudaSuccess) return V4A_ERR_CUDA;
   if (attr.numRegs != 168) return V4A_ERR_UNSUPPORTED;     // the register split would not add up

@@ -95,19 +95,25 @@ def _want(t, name, dtype, device, shape=None, contiguous=True):
 class _Op:
     """Launches on the tensors' device, whatever the current one is."""
 
-    def _launch(self, where, fn, args, ws, stream):
+    def _launch(self, stream):
+        """Calls the C entry on the kept argument struct."""
         dev = self.device
         if stream is None:
             stream = torch.cuda.current_stream(dev)
         elif stream.device != dev:
-            raise ValueError(f"{where}: the stream is on {stream.device}, the tensors on {dev}")
-        extra = () if ws is None else (ws.data_ptr(), ws.numel())
+            raise ValueError(f"{self._where}: the stream is on {stream.device}, the tensors on {dev}")
         if torch.cuda.current_device() == dev.index:
-            rc = fn(C.byref(args), *extra, stream.cuda_stream)
+            rc = self._fn(*self._call, stream.cuda_stream)
         else:
             with torch.cuda.device(dev):
-                rc = fn(C.byref(args), *extra, stream.cuda_stream)
-        v4a._check(where, rc)
+                rc = self._fn(*self._call, stream.cuda_stream)
+        if rc:
+            v4a._check(self._where, rc)
+
+    def _bind(self, where, fn, workspace=None):
+        self._where, self._fn, self.workspace = where, fn, workspace
+        ws = () if workspace is None else (workspace.data_ptr(), workspace.numel())
+        self._call = (C.byref(self.args), *ws)
 
 
 class StepPlan(_Op):
@@ -136,8 +142,7 @@ class StepPlan(_Op):
         need = lib().v4a_plan_workspace_size(C.byref(self.args))
         if need == 0:
             raise ValueError("StepPlan: sizes outside v4a_step_plan's limits")
-        self.workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        self._fn = lib().v4a_step_plan
+        self._bind("v4a_step_plan", lib().v4a_step_plan, torch.empty(need, dtype=torch.uint8, device=dev))
 
     def run(self, cached: torch.Tensor, fresh: torch.Tensor, free_in: torch.Tensor, free_out: torch.Tensor | None = None,
             stream=None):
@@ -145,9 +150,10 @@ class StepPlan(_Op):
         a, dev = self.args, self.device
         free_out = free_in if free_out is None else free_out
         for n, t, k in (("cached", cached, a.num_seqs), ("fresh", fresh, a.num_seqs), ("free_in", free_in, 2), ("free_out", free_out, 2)):
-            _want(t, n, torch.int32, dev, (k,))
+            if not (t.dtype is torch.int32 and t.device == dev and t.shape == (k,) and t.is_contiguous()):
+                _want(t, n, torch.int32, dev, (k,))
         a.cached, a.fresh, a.free_in, a.free_out = cached.data_ptr(), fresh.data_ptr(), free_in.data_ptr(), free_out.data_ptr()
-        self._launch("v4a_step_plan", self._fn, a, self.workspace, stream)
+        self._launch(stream)
 
 
 @dataclass
@@ -199,10 +205,12 @@ class DenseCache:
 
 def _rows(t, name, device, heads, dim, tokens):
     """Token stride of a [tokens][heads][dim] bf16 tensor whose heads are contiguous."""
-    _want(t, name, torch.bfloat16, device, (tokens, heads, dim), contiguous=False)
-    if t.stride(2) != 1 or t.stride(1) != dim:
+    if not (isinstance(t, torch.Tensor) and t.dtype is torch.bfloat16 and t.device == device and t.shape == (tokens, heads, dim)):
+        _want(t, name, torch.bfloat16, device, (tokens, heads, dim), contiguous=False)
+    st = t.stride()
+    if st[2] != 1 or st[1] != dim and heads > 1:
         raise ValueError(f"{name}: heads and dims must be contiguous")
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), heads * dim)
+    return st[0] if tokens > 1 else max(st[0], heads * dim)
 
 
 class DenseInsert(_Op):
@@ -220,7 +228,7 @@ class DenseInsert(_Op):
         self.args = InsertArgs(0, None, None, num_heads, None, 0, None, 0, None, 0, None, 0,
                                None if q_gamma is None else q_gamma.data_ptr(), None if k_gamma is None else k_gamma.data_ptr(),
                                eps, self._rope, cache.struct(), self.status.data_ptr())
-        self._fn = lib().v4a_dense_insert
+        self._bind("v4a_dense_insert", lib().v4a_dense_insert)
 
     def run(self, q, k, v, q_out, positions: torch.Tensor, slots: torch.Tensor, stream=None):
         """q, q_out [T][heads][dim], k, v [T][KV heads][dim] bf16 (any token
@@ -236,10 +244,11 @@ class DenseInsert(_Op):
         a.k_stride = _rows(k, "k", dev, c.num_kv_heads, c.dim, n)
         a.v_stride = _rows(v, "v", dev, c.num_kv_heads, c.dim, n)
         a.k, a.v = k.data_ptr(), v.data_ptr()
-        _want(positions, "positions", torch.int32, dev, (n,))
-        _want(slots, "slots", torch.int64, dev, (n,))
+        for name, t, dtype in (("positions", positions, torch.int32), ("slots", slots, torch.int64)):
+            if not (t.dtype is dtype and t.device == dev and t.shape == (n,) and t.is_contiguous()):
+                _want(t, name, dtype, dev, (n,))
         a.positions, a.slots = positions.data_ptr(), slots.data_ptr()
-        self._launch("v4a_dense_insert", self._fn, a, None, stream)
+        self._launch(stream)
 
 
 class DenseAttention(_Op):
@@ -262,8 +271,7 @@ class DenseAttention(_Op):
         need = lib().v4a_dense_attn_workspace_size(C.byref(self.args))
         if need == 0:
             raise ValueError("DenseAttention: sizes outside v4a_dense_attn's limits")
-        self.workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
-        self._fn = lib().v4a_dense_attn
+        self._bind("v4a_dense_attn", lib().v4a_dense_attn, torch.empty(need, dtype=torch.uint8, device=self.device))
 
     def run(self, q: torch.Tensor, out: torch.Tensor, positions: torch.Tensor, token_starts: torch.Tensor, lse=None, stream=None):
         """q, out [T][heads][dim] bf16, T <= max_tokens; positions int32 [T];
@@ -272,13 +280,16 @@ class DenseAttention(_Op):
         n = q.shape[0]
         if n > self.max_tokens:
             raise ValueError(f"q: {n} tokens, at most {self.max_tokens}")
-        _want(q, "q", torch.bfloat16, dev, (n, a.num_heads, self.cache.dim))
-        _want(out, "out", torch.bfloat16, dev, (n, a.num_heads, self.cache.dim))
-        _want(positions, "positions", torch.int32, dev, (n,))
-        _want(token_starts, "token_starts", torch.int32, dev, (a.num_seqs + 1,))
-        if lse is not None:
-            _want(lse, "lse", torch.float32, dev, (n, a.num_heads))
+        for name, t, dtype, shape in (("q", q, torch.bfloat16, (n, a.num_heads, self.cache.dim)),
+                                      ("out", out, torch.bfloat16, (n, a.num_heads, self.cache.dim)),
+                                      ("positions", positions, torch.int32, (n,)),
+                                      ("token_starts", token_starts, torch.int32, (a.num_seqs + 1,)),
+                                      ("lse", lse, torch.float32, (n, a.num_heads))):
+            if t is None and name == "lse":
+                continue
+            if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.device == dev and t.shape == shape and t.is_contiguous()):
+                _want(t, name, dtype, dev, shape)
         a.num_tokens = n
         a.q, a.out, a.positions, a.token_starts = q.data_ptr(), out.data_ptr(), positions.data_ptr(), token_starts.data_ptr()
         a.lse = None if lse is None else lse.data_ptr()
-        self._launch("v4a_dense_attn", self._fn, a, self.workspace, stream)
+        self._launch(stream)
