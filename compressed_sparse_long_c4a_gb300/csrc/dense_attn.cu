@@ -17,8 +17,8 @@
 //
 // Layout: the positions of all sequences and KV heads, in tiles, form one line
 // that the CTAs divide evenly, so ragged lengths balance and one long sequence
-// fills the machine.  A tile is 64 dim bytes of keys and values (16 positions
-// of bf16, 32 of fp8): contiguous runs of one page, since both divide the
+// fills the machine.  A tile is 16 positions of bf16 or 32 of fp8 (twice that
+// at dim 64): contiguous runs of one page, since both divide the
 // 256-position block.  Warp w of a CTA takes tiles w, w + kWarps, ... of the
 // CTA's range and streams them by itself through a private ring of stages in
 // shared memory (16-byte cp.async, rows swizzled for ldmatrix), with its own
@@ -32,13 +32,14 @@ namespace v4a {
 namespace {
 
 constexpr int kRingBytes = 192 * 1024;
+constexpr int kUnitCost = 16;        // tiles that a unit's set-up and merge take the time of
 
 template <int D, int NT, bool kFp8>
 struct Shape {
   static constexpr int R = 8 * NT;                               // query rows of a unit
-  static constexpr int kKeys = kFp8 ? 32 : 16;                   // positions per tile
+  static constexpr int kKeys = (kFp8 ? 32 : 16) * (D == 64 ? 2 : 1);   // positions per tile
   static constexpr int kRow = kFp8 ? D : 2 * D;                  // bytes of a row
-  static constexpr int kHalf = kKeys * kRow;                     // keys (or values) of a tile: 32 D bytes
+  static constexpr int kHalf = kKeys * kRow;                     // keys (or values) of a tile: 32 D bytes (64 D at dim 64)
   static constexpr int kScales = kFp8 ? 2 * kKeys * 4 : 0;
   static constexpr int kStage = 2 * kHalf + kScales;             // holds R x D fp32 for the merge as well
   static constexpr int kWarps = 4;
@@ -96,15 +97,6 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
 }
 // log2 of a value row's scale, at least -100 (a NaN stays one).
 __device__ __forceinline__ float scale_log2(float s) { return s > 0x1p-100f ? log2f(s) : s <= 0x1p-100f ? -100.f : s; }
-// Codes b0 and b2 (or b1 and b3) of w as a bf16 pair times 2^-120 (sign to bit
-// 15, the 7 magnitude bits to bits 4..10: the code's value with the exponent
-// biased by 127 instead of 7), then times 2^120, exactly; subnormal codes too.
-__device__ __forceinline__ uint32_t e4m3_pair(uint32_t shifted) {      // codes in bits 8..15 and 24..31
-  const uint32_t m = ((shifted >> 4) & 0x07F007F0u) | (shifted & 0x80008000u);
-  uint32_t r;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(m), "r"(0x7B807B80u));
-  return r;
-}
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&b);
@@ -159,7 +151,7 @@ __global__ void __launch_bounds__(Shape<D, NT, kFp8>::kThreads, Shape<D, NT, kFp
           tc::cp_async16(dst + to, src + c * 16);
           tc::cp_async16(dst + S::kHalf + to, src + to_values + c * 16);
         }
-        if (kFp8 && lane < kKeys / 2) {          // the rows' scales: keys' from lanes 0..7, values' from 8..15
+        if (kFp8 && lane < kKeys / 2) {          // the rows' scales: keys' from the first half of these lanes, values' from the rest
           const int which = lane / (kKeys / 4), q = lane % (kKeys / 4);
           const uint8_t* sc = block + 2 * to_values + (row + int64_t(which) * a.K * kBlockPositions) * 4;
           tc::cp_async16(dst + 2 * S::kHalf + which * kKeys * 4 + q * 16, sc + q * 16);
@@ -181,6 +173,7 @@ __global__ void __launch_bounds__(Shape<D, NT, kFp8>::kThreads, Shape<D, NT, kFp
   const int g4 = lane >> 2, c2 = (lane & 3) * 2;
   int stage = 0;                                 // of this warp's next tile
   uint32_t qf[D / 16][NT][2];
+  float fq[NT][2];                               // f for the columns c2, c2 + 1 (fp8: with their rows' powers of two)
   auto load_q = [&](const Unit<kKeys>& un, int hk) {
     // the query rows as B operands: column g4 of n-tile nt, dims of step ks
 #pragma unroll
@@ -201,6 +194,34 @@ __global__ void __launch_bounds__(Shape<D, NT, kFp8>::kThreads, Shape<D, NT, kFp
       }
     }
   };
+  // fp8: e4m3 codes are exact in f16, so the query joins them there: its row times the power of two
+  // that brings its largest element to [2^14, 2^15) is exact down to 2^-31 of that element (and
+  // within 2^-40 of it below).
+  auto fit_q = [&]() {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      fq[nt][0] = fq[nt][1] = f;
+      if constexpr (kFp8) {
+        uint32_t top = 0;                        // |q| as bf16 bits, two at a time
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) top = __vmaxu2(top, __vmaxu2(qf[ks][nt][0] & 0x7fff7fffu, qf[ks][nt][1] & 0x7fff7fffu));
+        top = max(top >> 16, top & 0xffffu);
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const int e = top == 0 ? 127 : min(253, max(1, 268 - int(top >> 7)));      // the power's exponent field
+        const float up = __int_as_float(e << 23), down = __int_as_float((254 - e) << 23);
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t w = qf[ks][nt][i];
+            qf[ks][nt][i] = pack_f16(__uint_as_float(w << 16) * up, __uint_as_float(w & 0xffff0000u) * up);
+          }
+        fq[nt][0] = f * __shfl_sync(0xffffffffu, down, 4 * c2);
+        fq[nt][1] = f * __shfl_sync(0xffffffffu, down, 4 * c2 + 4);
+      }
+    }
+  };
   int64_t x = x0;
   Unit<kKeys> next_un;
   auto next_pc = line.locate(x, &next_un);
@@ -209,6 +230,7 @@ __global__ void __launch_bounds__(Shape<D, NT, kFp8>::kThreads, Shape<D, NT, kFp
     const Unit<kKeys> un = next_un;
     const auto pc = next_pc;
     const int count = int(min(int64_t(un.tr.tiles - pc.tile), x1 - x));     // tiles of this segment
+    fit_q();
     float o[D / 16][NT][4], m[NT][2], l[NT][2];
     int mrow[NT][2];                               // the columns' query positions
 #pragma unroll
@@ -267,10 +289,9 @@ __global__ void __launch_bounds__(Shape<D, NT, kFp8>::kThreads, Shape<D, NT, kFp
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const uint32_t lo = w[2 * h], hi = w[2 * h + 1];
-              const uint32_t k[4] = {e4m3_pair(__byte_perm(lo, 0, 0x1404)), e4m3_pair(__byte_perm(hi, 0, 0x1404)),
-                                     e4m3_pair(__byte_perm(lo, 0, 0x3424)), e4m3_pair(__byte_perm(hi, 0, 0x3424))};
+              const uint32_t k[4] = {e4m3_f16(lo), e4m3_f16(hi), e4m3_f16(lo >> 16), e4m3_f16(hi >> 16)};
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt) mma16816(z[mt][nt], k, qf[2 * c + h][nt]);
+              for (int nt = 0; nt < NT; ++nt) mma16816_f16(z[mt][nt], k, qf[2 * c + h][nt]);
             }
           }
           const float k0 = scale[mt * 16 + g4], k1 = scale[mt * 16 + g4 + 8];
@@ -312,7 +333,7 @@ __global__ void __launch_bounds__(Shape<D, NT, kFp8>::kThreads, Shape<D, NT, kFp
           float t = -INFINITY;
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt)
-            t = kFp8 ? fmaxf(t, fmaxf(fmaf(z[mt][nt][e], f, ls[mt][0]), fmaf(z[mt][nt][e + 2], f, ls[mt][1])))
+            t = kFp8 ? fmaxf(t, fmaxf(fmaf(z[mt][nt][e], fq[nt][e], ls[mt][0]), fmaf(z[mt][nt][e + 2], fq[nt][e], ls[mt][1])))
                      : fmaxf(t, fmaxf(z[mt][nt][e], z[mt][nt][e + 2]));
           t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
           t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
@@ -342,8 +363,8 @@ __global__ void __launch_bounds__(Shape<D, NT, kFp8>::kThreads, Shape<D, NT, kFp
         const float b0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0], b1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
-          const float y0 = fmaf(z[mt][nt][0], f, -b0), y1 = fmaf(z[mt][nt][1], f, -b1);
-          const float y2 = fmaf(z[mt][nt][2], f, -b0), y3 = fmaf(z[mt][nt][3], f, -b1);
+          const float y0 = fmaf(z[mt][nt][0], fq[nt][0], -b0), y1 = fmaf(z[mt][nt][1], fq[nt][1], -b1);
+          const float y2 = fmaf(z[mt][nt][2], fq[nt][0], -b0), y3 = fmaf(z[mt][nt][3], fq[nt][1], -b1);
           const float p0 = exp2f(y0), p1 = exp2f(y1), p2 = exp2f(y2), p3 = exp2f(y3);
           l[nt][0] += p0 + p2;
           l[nt][1] += p1 + p3;
@@ -677,8 +698,12 @@ int dense_attn(const v4a_dense_attn_args* a, void* ws, size_t ws_bytes, cudaStre
   SplitDev p{};
   p.RG = int(row_groups(a));
   p.U = d.B * p.RG;
-  p.split = p.U <= kMaxSplitUnits;
-  split_carve(&p, ws, rows_of(a), a->kv.dim, ctas_of(a));
+  // One CTA per unit and KV head when there are enough of them and a window bounds their lengths (64
+  // sequences x 8 heads x 1024 positions: 29 us, the even split 34); an even split otherwise, since the
+  // lengths are the device's (200 sequences of 1 to 600 x 8: 47 us unsplit, 50 split; but one long
+  // sequence among short ones would run alone).
+  p.split = p.U <= kMaxSplitUnits && (a->window == 0 || int64_t(p.U) * d.K < 256);
+  split_carve(&p, ws, rows_of(a), a->kv.dim, ctas_of(a), kUnitCost);
   return a->kv.format == V4A_KV_FP8_TOKEN ? launch_dim<true>(d, p, a->kv.dim, stream) : launch_dim<false>(d, p, a->kv.dim, stream);
 }
 

@@ -98,11 +98,12 @@ __device__ __forceinline__ int64_t row_of(const DenseAttnDev& a, const Unit<kTil
 }
 
 // How a launch divides the units: split = 1: the tiles of all units and KV
-// heads form one line (unit by unit, KV head by KV head) that `ctas` CTAs
-// divide evenly; split = 0: one CTA per unit and KV head.
+// heads form one line (unit by unit, KV head by KV head) that the CTAs divide
+// evenly, each unit counted with `cost` tiles more than it has (its set-up and
+// its end take about that long); split = 0: one CTA per unit and KV head.
 struct SplitDev {
   int RG, U, split;               // row groups per sequence, units (sequences x row groups)
-  int rows, grid;                 // R; CTAs of the launch (split)
+  int rows, grid, cost;           // R; CTAs of the launch and a unit's extra tiles (split)
   struct JoinDesc* join;          // [CTA]
   float *part_o, *part_ml;        // [CTA][2][R][dim], [CTA][2][R][2] (maximum in log2 units, sum)
 };
@@ -131,9 +132,10 @@ inline bool raise_smem(K kern, int bytes, std::atomic<uint64_t>* done) {
   return true;
 }
 
-inline void split_carve(SplitDev* p, void* ws, int R, int dim, int ctas) {
+inline void split_carve(SplitDev* p, void* ws, int R, int dim, int ctas, int cost) {
   p->rows = R;
   p->grid = ctas;
+  p->cost = cost;
   p->join = static_cast<JoinDesc*>(ws);
   p->part_o = reinterpret_cast<float*>(p->join + ctas);
   p->part_ml = p->part_o + size_t(ctas) * 2 * R * dim;
@@ -146,7 +148,7 @@ struct Line {
   const SplitDev& p;
   int64_t* pre;                   // [U + 1] tiles before unit u, over its KV heads
   SeqRun* runs;                   // [B], or the one
-  int64_t x0, x1, total;
+  int64_t x0, x1, total, weight;
   int ctas, u_direct, hk_direct;
 
   struct Piece { int u, hk, tile; };
@@ -197,14 +199,29 @@ struct Line {
     for (int u = u0; u < u1; ++u) pre[u] += before;
     if (tid == 0) pre[p.U] = total;
     __syncthreads();
+    weight = total + int64_t(p.cost) * a.K * p.U;
     ctas = int(min(int64_t(gridDim.x), (total + min_tiles - 1) / min_tiles));
-    if (int(blockIdx.x) >= ctas) {
-      if (tid == 0) p.join[blockIdx.x].rows = 0;
-      return false;
+    x0 = x1 = 0;
+    if (int(blockIdx.x) < ctas) {
+      x0 = place(int64_t(blockIdx.x) * weight / ctas);
+      x1 = place((int64_t(blockIdx.x) + 1) * weight / ctas);
     }
-    x0 = int64_t(blockIdx.x) * total / ctas;
-    x1 = (int64_t(blockIdx.x) + 1) * total / ctas;
-    return true;
+    if (x0 == x1 && tid == 0) p.join[blockIdx.x].rows = 0;
+    return x0 < x1;
+  }
+  // The first tile at or behind position w of the line with the units' costs,
+  // which are in front of their tiles.
+  __device__ __forceinline__ int64_t place(int64_t w) const {
+    const int64_t each = int64_t(p.cost) * a.K;
+    if (w >= weight) return total;
+    int lo = 0, hi = p.U;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (pre[mid] + each * mid <= w) lo = mid; else hi = mid;
+    }
+    const int tiles = unit(lo).tr.tiles;
+    const int64_t rem = w - pre[lo] - each * lo, hk = rem / (tiles + p.cost);
+    return pre[lo] + hk * tiles + max(int64_t(0), rem - hk * (tiles + p.cost) - p.cost);
   }
   __device__ __forceinline__ Unit<kTile> unit(int u) const {
     return make_unit<R, kTile>(a, u / p.RG, u % p.RG, runs[p.split ? u / p.RG : 0]);
@@ -222,13 +239,13 @@ struct Line {
     }
     *un = unit(lo);
     const int64_t rem = x - pre[lo];
-    const int hk = int(rem / un->tr.tiles);
+    const int hk = rem <= INT32_MAX ? int(rem) / un->tr.tiles : int(rem / un->tr.tiles);
     return Piece{lo, hk, int(rem - int64_t(hk) * un->tr.tiles)};
   }
   // The description of a unit that leaves the CTA's range.
   __device__ __forceinline__ JoinDesc describe(const Piece& pc, const Unit<kTile>& un) const {
-    const int64_t end = pre[pc.u] + int64_t(pc.hk + 1) * un.tr.tiles;
-    return JoinDesc{un.rows, un.row0, un.s0, pc.hk, int((end * ctas - 1) / total), {0, 0, 0}};
+    const int64_t end = pre[pc.u] + int64_t(p.cost) * a.K * pc.u + int64_t(pc.hk + 1) * (un.tr.tiles + p.cost);
+    return JoinDesc{un.rows, un.row0, un.s0, pc.hk, int((end * ctas - 1) / weight), {0, 0, 0}};
   }
 };
 

@@ -35,6 +35,7 @@ constexpr int kKeys = 128;           // keys per step
 constexpr int kThreads = 384;
 constexpr int kUnit = 2 * kRows;     // rows of a unit
 constexpr int kLoaders = 96;
+constexpr int kUnitCost = 3;         // steps that a unit's set-up and output take the time of
 constexpr int kMinSteps = 4;         // steps a CTA of an even split has at least
 constexpr float kRaise = 8.f;        // log2 units by which logits may pass the maximum in use
 
@@ -497,7 +498,7 @@ int dense_prefill(const v4a_dense_attn_args* a, const DenseAttnDev& d, void* ws,
   p.RG = int(row_blocks(a));
   p.U = d.B * p.RG;
   p.split = p.U <= kMaxSplitUnits;
-  split_carve(&p, ws, kUnit, a->kv.dim, kSms);
+  split_carve(&p, ws, kUnit, a->kv.dim, kSms, kUnitCost);
   return a->kv.dim == 64 ? launch<64>(d, p, stream) : launch<128>(d, p, stream);
 }
 
