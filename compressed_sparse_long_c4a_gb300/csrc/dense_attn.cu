@@ -357,7 +357,7 @@ __global__ void __launch_bounds__(Shape<D, NT, kFp8>::kThreads, Shape<D, NT, kFp
         }
       }
       // P^T as B operands: keys are rows of the k step
-      uint32_t pf[MT][NT][2];
+      uint32_t pf[MT][NT][2], pl[kFp8 ? 1 : MT][NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         const float b0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0], b1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
@@ -374,8 +374,14 @@ __global__ void __launch_bounds__(Shape<D, NT, kFp8>::kThreads, Shape<D, NT, kFp
             pf[mt][nt][0] = transpose8(pack_f16(weight(y0, s0), weight(y1, s0)));
             pf[mt][nt][1] = transpose8(pack_f16(weight(y2, s1), weight(y3, s1)));
           } else {
-            pf[mt][nt][0] = transpose8(pack_bf16(p0, p1));
-            pf[mt][nt][1] = transpose8(pack_bf16(p2, p3));
+            // two bf16 operands, p and what its rounding left: 16 bits (the products wait on memory anyway)
+            auto split = [](float u, float w, uint32_t* hi, uint32_t* lo) {
+              const uint32_t h = pack_bf16(u, w);
+              *hi = transpose8(h);
+              *lo = transpose8(pack_bf16(u - __uint_as_float(h << 16), w - __uint_as_float(h & 0xffff0000u)));
+            };
+            split(p0, p1, &pf[mt][nt][0], &pl[mt][nt][0]);
+            split(p2, p3, &pf[mt][nt][1], &pl[mt][nt][1]);
           }
         }
       }
@@ -401,7 +407,10 @@ __global__ void __launch_bounds__(Shape<D, NT, kFp8>::kThreads, Shape<D, NT, kFp
             ldsm_t(vb + chunk_at<S::kRow>(key, 2 * d + ((lane >> 3) & 1)), v);
             if (!full) { v[0] &= keep0; v[1] &= keep0; v[2] &= keep1; v[3] &= keep1; }
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma16816(o[d][nt], v, pf[mt][nt]);
+            for (int nt = 0; nt < NT; ++nt) {
+              mma16816(o[d][nt], v, pf[mt][nt]);
+              mma16816(o[d][nt], v, pl[mt][nt]);
+            }
           }
         } else {
           // matrices: keys 0-7 and 8-15 of 16-code chunk 2c, then of chunk 2c + 1; a transposed
@@ -414,8 +423,8 @@ __global__ void __launch_bounds__(Shape<D, NT, kFp8>::kThreads, Shape<D, NT, kFp
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const uint32_t lo = w[2 * h], hi = w[2 * h + 1];
-              const uint32_t pl = __byte_perm(lo, 0, 0x3120), ph = __byte_perm(hi, 0, 0x3120);
-              uint32_t v[4] = {e4m3_f16(pl), e4m3_f16(pl >> 16), e4m3_f16(ph), e4m3_f16(ph >> 16)};
+              const uint32_t wl = __byte_perm(lo, 0, 0x3120), wh = __byte_perm(hi, 0, 0x3120);
+              uint32_t v[4] = {e4m3_f16(wl), e4m3_f16(wl >> 16), e4m3_f16(wh), e4m3_f16(wh >> 16)};
               if (!full) { v[0] &= keep0; v[1] &= keep0; v[2] &= keep1; v[3] &= keep1; }
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) mma16816_f16(o[2 * c + h][nt], v, pf[mt][nt]);
