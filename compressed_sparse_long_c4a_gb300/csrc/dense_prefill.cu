@@ -38,6 +38,7 @@ constexpr int kLoaders = 96;
 constexpr int kUnitCost = 3;         // steps that a unit's set-up and output take the time of
 constexpr int kMinSteps = 4;         // steps a CTA of an even split has at least
 constexpr float kRaise = 8.f;        // log2 units by which logits may pass the maximum in use
+constexpr float kRaiseFp8 = 4.f, kShiftFp8 = 11.f;   // f16 P: 2^11 2^{w - m} <= 2^15
 
 struct PreSmem {
   uint64_t q_full[2], k_full[2], v_full[2], k_free[2], v_free[2], s_full[2], p_full[2][2], o_full[2], drain;
@@ -45,6 +46,8 @@ struct PreSmem {
   uint32_t tmem_base;
   int abort_flag;
   int missing[4];                    // step n's page is missing: [n % 4]
+  // fp8, step n's keys: softmax scale x log2(e) x key scale; log2 of the value scale; its inverse
+  alignas(16) float scales[4][3][kKeys];
 };
 
 // MN-major operand (as in attn_tc.cu): 64-element rows along N, 8-row groups
@@ -129,6 +132,31 @@ __device__ __forceinline__ float2 add2(float2 x, float2 y) {
   return *reinterpret_cast<float2*>(&r);
 }
 
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+// Four e4m3 codes as bf16, exactly: the code's bits in place of a bf16's, with
+// the exponent biased by 127 instead of 7, times 2^120 (subnormal codes too).
+__device__ __forceinline__ uint2 bf16_of(uint32_t w) {
+  const uint32_t a = __byte_perm(w, 0u, 0x1404), b = __byte_perm(w, 0u, 0x3424);
+  const uint32_t ma = ((a >> 4) & 0x07F007F0u) | (a & 0x80008000u), mb = ((b >> 4) & 0x07F007F0u) | (b & 0x80008000u);
+  uint2 r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r.x) : "r"(ma), "r"(0x7B807B80u));
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r.y) : "r"(mb), "r"(0x7B807B80u));
+  return r;
+}
+// ... and as f16.
+__device__ __forceinline__ uint2 f16_of(uint32_t w) {
+  uint2 r;
+  asm("{\n.reg .b16 l, h;\nmov.b32 {l, h}, %2;\ncvt.rn.f16x2.e4m3x2 %0, l;\ncvt.rn.f16x2.e4m3x2 %1, h;\n}\n"
+      : "=r"(r.x), "=r"(r.y) : "r"(w));
+  return r;
+}
+__device__ __forceinline__ void st_shared16(uint32_t dst, uint2 lo, uint2 hi) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(lo.x), "r"(lo.y), "r"(hi.x), "r"(hi.y) : "memory");
+}
+
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -145,7 +173,7 @@ __device__ __forceinline__ uint32_t chunk_at(int r, int ch) {
   return uint32_t((ch >> 3) * (128 * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4));
 }
 
-template <int D>
+template <int D, bool kFp8>
 __global__ void __launch_bounds__(kThreads, 1) dense_prefill_kernel(const DenseAttnDev a, const SplitDev p) {
   constexpr int kTileBytes = 128 * D * 2;      // a Q tile, a step's keys or its values
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -222,6 +250,16 @@ __global__ void __launch_bounds__(kThreads, 1) dense_prefill_kernel(const DenseA
           float z[128];
           tc::tmem_ld64(s_at, z);
           tc::tmem_ld64(s_at + 64, z + 64);
+          const auto& sc = s.scales[(n0 + i) & 3];
+          if constexpr (kFp8) {          // logits in log2 units plus log2 of the value's scale
+#pragma unroll
+            for (int c = 0; c < 128; c += 4) {
+              const float4 k = *reinterpret_cast<const float4*>(&sc[0][c]), v = *reinterpret_cast<const float4*>(&sc[1][c]);
+              const float2 lo = fma2(make_float2(z[c], z[c + 1]), make_float2(k.x, k.y), make_float2(v.x, v.y));
+              const float2 hi = fma2(make_float2(z[c + 2], z[c + 3]), make_float2(k.z, k.w), make_float2(v.z, v.w));
+              z[c] = lo.x; z[c + 1] = lo.y; z[c + 2] = hi.x; z[c + 3] = hi.y;
+            }
+          }
           const int j0 = un.tr.at(pc.tile + i) * kKeys;
           const bool gone = s.missing[(n0 + i) & 3] != 0;
           if (gone || !all_visible(a, un.m_lo, un.m_hi, j0, kKeys)) {
@@ -241,8 +279,8 @@ __global__ void __launch_bounds__(kThreads, 1) dense_prefill_kernel(const DenseA
           for (int c = 4; c < 124; c += 8)
 #pragma unroll
             for (int k = 0; k < 4; ++k) mx[k] = max3(mx[k], z[c + k], z[c + k + 4]);
-          top = fmaxf(top, max3(max3(mx[0], mx[1], mx[2]), mx[3], fmaxf(max3(z[124], z[125], z[126]), z[127])) * f);
-          const bool raise = top > -INFINITY && (!any || top > ref + kRaise);
+          top = fmaxf(top, max3(max3(mx[0], mx[1], mx[2]), mx[3], fmaxf(max3(z[124], z[125], z[126]), z[127])) * (kFp8 ? 1.f : f));
+          const bool raise = top > -INFINITY && (!any || top > ref + (kFp8 ? kRaiseFp8 : kRaise));
           if (__any_sync(0xffffffffu, raise && any)) {   // the step before has left the accumulator: its MMAs precede S
             const float w = raise && any ? exp2f(ref - top) : 1.f;
             l *= w;
@@ -261,17 +299,23 @@ __global__ void __launch_bounds__(kThreads, 1) dense_prefill_kernel(const DenseA
             any = true;
           }
           float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-          const float2 f2 = make_float2(f, f), r2 = make_float2(-ref, -ref);
+          const float2 f2 = make_float2(f, f), r2 = kFp8 ? make_float2(kShiftFp8 - ref, kShiftFp8 - ref) : make_float2(-ref, -ref);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {          // the first 64 keys' product runs while the other 64 are exponentiated
             uint32_t pk[32];
 #pragma unroll
             for (int c = 0; c < 64; c += 2) {
-              float2 y = fma2(make_float2(z[64 * h + c], z[64 * h + c + 1]), f2, r2);
+              const float2 x2 = make_float2(z[64 * h + c], z[64 * h + c + 1]);
+              float2 y = kFp8 ? add2(x2, r2) : fma2(x2, f2, r2);
               y.x = exp2f(y.x);
               y.y = exp2f(y.y);
-              sum[(c >> 1) & 1] = add2(sum[(c >> 1) & 1], y);
-              pk[c >> 1] = pack_bf16(y.x, y.y);
+              if (kFp8) {
+                sum[(c >> 1) & 1] = fma2(y, *reinterpret_cast<const float2*>(&sc[2][64 * h + c]), sum[(c >> 1) & 1]);
+                pk[c >> 1] = pack_f16(y.x, y.y);
+              } else {
+                sum[(c >> 1) & 1] = add2(sum[(c >> 1) & 1], y);
+                pk[c >> 1] = pack_bf16(y.x, y.y);
+              }
             }
             tmem_st32(s_at + 32 * h, pk);
             tmem_wait_st();
@@ -310,9 +354,9 @@ __global__ void __launch_bounds__(kThreads, 1) dense_prefill_kernel(const DenseA
           }
           if (row < un.rows) {
             if (whole) {
-              if (a.lse) a.lse[at] = any ? (ref + log2f(l)) * 0.6931471805599453f : l == 0.f ? -INFINITY : l;
+              if (a.lse) a.lse[at] = any ? (ref - (kFp8 ? kShiftFp8 : 0.f) + log2f(l)) * 0.6931471805599453f : l == 0.f ? -INFINITY : l;
             } else {       // a piece without a key leaves nothing; one whose logits are all NaN is passed on
-              p.part_ml[part * 2] = any || l != 0.f ? ref : -INFINITY;
+              p.part_ml[part * 2] = any || l != 0.f ? ref - (kFp8 ? kShiftFp8 : 0.f) : -INFINITY;
               p.part_ml[part * 2 + 1] = l;
             }
           }
@@ -327,7 +371,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_prefill_kernel(const DenseA
     // in its softmax (with an issuer per tile the two ran in step: 4100 against 3100 clocks a step) ----
     if (lane == 0) {
       const uint32_t idesc_s = tc::make_idesc(1, 1, kRows, kKeys);
-      const uint32_t idesc_o = tc::make_idesc(1, 1, kRows, D) | (1u << 16);       // B is MN-major
+      const uint32_t idesc_o = tc::make_idesc(kFp8 ? 0 : 1, kFp8 ? 0 : 1, kRows, D) | (1u << 16);       // f16 or bf16; B is MN-major
       auto scores = [&](int t, int n) {
         const uint32_t st = tmem + 128 * t, qa = q0 + t * kTileBytes, kb = k0 + (n & 1) * kTileBytes;
 #pragma unroll
@@ -414,35 +458,78 @@ __global__ void __launch_bounds__(kThreads, 1) dense_prefill_kernel(const DenseA
           page = -1;
         }
         const int j0 = un.tr.at(pc.tile + i) * kKeys;
-        const uint8_t* rows_k =
-            a.pool + (page < 0 ? 0 : page * a.block_bytes + (int64_t(pc.hk) * kBlockPositions + j0 % kBlockPositions) * (2 * D));
-        const bool whole = page >= 0 && j0 + kKeys - 1 <= un.m_hi && (a.window == 0 || j0 > un.m_lo - a.window);
         if (lt == 0) s.missing[n & 3] = page < 0;
-#pragma unroll 1
-        for (int half = 0; half < 2; ++half) {
-          ok = wait_for(half ? &s.v_free[n & 1] : &s.k_free[n & 1], ((n >> 1) & 1) ^ 1, a.status, abort_flag);
-          if (!ok) break;
-          const uint8_t* src = rows_k + (page < 0 ? 0 : half * (int64_t(a.K) * kBlockPositions * (2 * D)));
-          const uint32_t dst = (half ? v0 : k0) + (n & 1) * kTileBytes;
-          // thread lt: chunk lt % (dim / 8) of rows lt / (dim / 8) + k * (96 / (dim / 8))
-          constexpr int kChunks = kKeys * (D / 8), kPasses = (kChunks + kLoaders - 1) / kLoaders;
-          if (whole) {
+        // rows up to hi, and of those the ones behind lo or before sk, are copied; the others are zeros
+        const int hi = page < 0 ? -1 : un.m_hi - j0, lo = a.window ? un.m_lo - a.window - j0 : -1, sk = a.window ? a.sinks - j0 : 0;
+        constexpr int kRow = kFp8 ? D : 2 * D;
+        const uint8_t* block = a.pool + (page < 0 ? 0 : page * a.block_bytes);
+        const int at = page < 0 ? 0 : pc.hk * kBlockPositions + j0 % kBlockPositions;       // first row of the step
+        if constexpr (kFp8) {
+          // codes are loaded ahead of their buffer, converted and stored into it; the step's scales with its keys
+          constexpr int kChunks = kKeys * (D / 16), kPasses = (kChunks + kLoaders - 1) / kLoaders;
+          const float* row_scale = reinterpret_cast<const float*>(block + int64_t(2 * a.K) * kBlockPositions * D) + at;
 #pragma unroll
-            for (int k = 0; k < kPasses; ++k) {
-              const int c = lt + k * kLoaders;
-              if (c < kChunks) copy16(dst + chunk_at(c / (D / 8), c % (D / 8)), src + c * 16, true);
-            }
-          } else {
-            const int hi = page < 0 ? -1 : un.m_hi - j0, lo = a.window ? un.m_lo - a.window - j0 : -1, sk = a.window ? a.sinks - j0 : 0;
-            const int step = page < 0 ? 0 : kLoaders * 16;
-            src += page < 0 ? 0 : lt * 16;
-#pragma unroll
-            for (int k = 0; k < kPasses; ++k) {
-              const int c = lt + k * kLoaders, r = c / (D / 8);
-              if (c < kChunks) copy16(dst + chunk_at(r, c % (D / 8)), src + k * step, r <= hi && (r > lo || r < sk));
+          for (int c0 = 0; c0 < kKeys; c0 += kLoaders) {
+            const int c = c0 + lt;
+            if (c < kKeys) {
+              const bool live = c <= hi && (c > lo || c < sk);
+              const float ks = live ? row_scale[c] : 0.f, vs = live ? row_scale[a.K * kBlockPositions + c] : 1.f;
+              const float l = vs > 0x1p-100f ? log2f(vs) : vs <= 0x1p-100f ? -100.f : vs;
+              s.scales[n & 3][0][c] = ks * a.scale_log2;
+              s.scales[n & 3][1][c] = l;
+              s.scales[n & 3][2][c] = exp2f(-l);
             }
           }
-          arrive_copies(half ? &s.v_full[n & 1] : &s.k_full[n & 1]);
+#pragma unroll 1
+          for (int half = 0; half < 2; ++half) {
+            const uint8_t* src = block + (int64_t(half * a.K) * kBlockPositions + at) * D;
+            uint4 raw[kPasses];
+#pragma unroll
+            for (int k = 0; k < kPasses; ++k) {
+              const int c = lt + k * kLoaders, r = c / (D / 16);
+              raw[k] = make_uint4(0, 0, 0, 0);
+              if (c < kChunks && r <= hi && (r > lo || r < sk)) raw[k] = __ldg(reinterpret_cast<const uint4*>(src + c * 16));
+            }
+            ok = wait_for(half ? &s.v_free[n & 1] : &s.k_free[n & 1], ((n >> 1) & 1) ^ 1, a.status, abort_flag);
+            if (!ok) break;
+            const uint32_t dst = (half ? v0 : k0) + (n & 1) * kTileBytes;
+#pragma unroll
+            for (int k = 0; k < kPasses; ++k) {
+              const int c = lt + k * kLoaders, r = c / (D / 16), ch = 2 * (c % (D / 16));
+              if (c < kChunks) {
+                st_shared16(dst + chunk_at(r, ch), half ? f16_of(raw[k].x) : bf16_of(raw[k].x), half ? f16_of(raw[k].y) : bf16_of(raw[k].y));
+                st_shared16(dst + chunk_at(r, ch + 1), half ? f16_of(raw[k].z) : bf16_of(raw[k].z), half ? f16_of(raw[k].w) : bf16_of(raw[k].w));
+              }
+            }
+            tc::fence_proxy_async();
+            tc::mbar_arrive(half ? &s.v_full[n & 1] : &s.k_full[n & 1]);
+          }
+        } else {
+          const bool whole = hi >= kKeys - 1 && lo < 0;
+#pragma unroll 1
+          for (int half = 0; half < 2; ++half) {
+            ok = wait_for(half ? &s.v_free[n & 1] : &s.k_free[n & 1], ((n >> 1) & 1) ^ 1, a.status, abort_flag);
+            if (!ok) break;
+            const uint8_t* src = block + (int64_t(half * a.K) * kBlockPositions + at) * kRow;
+            const uint32_t dst = (half ? v0 : k0) + (n & 1) * kTileBytes;
+            // thread lt: chunk lt % (dim / 8) of rows lt / (dim / 8) + k * (96 / (dim / 8))
+            constexpr int kChunks = kKeys * (D / 8), kPasses = (kChunks + kLoaders - 1) / kLoaders;
+            if (whole) {
+#pragma unroll
+              for (int k = 0; k < kPasses; ++k) {
+                const int c = lt + k * kLoaders;
+                if (c < kChunks) copy16(dst + chunk_at(c / (D / 8), c % (D / 8)), src + c * 16, true);
+              }
+            } else {
+#pragma unroll
+              for (int k = 0; k < kPasses; ++k) {
+                const int c = lt + k * kLoaders, r = c / (D / 8);
+                const bool live = r <= hi && (r > lo || r < sk);
+                if (c < kChunks) copy16(dst + chunk_at(r, c % (D / 8)), live ? src + c * 16 : a.pool, live);
+              }
+            }
+            arrive_copies(half ? &s.v_full[n & 1] : &s.k_full[n & 1]);
+          }
         }
       }
     }
@@ -461,13 +548,13 @@ __global__ void __launch_bounds__(kThreads, 1) dense_prefill_kernel(const DenseA
   pdl_trigger();
 }
 
-template <int D>
+template <int D, bool kFp8>
 int launch(const DenseAttnDev& d, const SplitDev& p, cudaStream_t stream) {
   // at least 116 KB: no two CTAs that allocate TMEM share an SM
   size_t bytes = 1024 + 6 * 128 * D * 2 + sizeof(PreSmem) + split_smem(p.split, p.U, d.B);
   if (bytes < 116 * 1024) bytes = 116 * 1024;
   if (bytes > 227 * 1024) return V4A_ERR_UNSUPPORTED;
-  auto kern = dense_prefill_kernel<D>;
+  auto kern = dense_prefill_kernel<D, kFp8>;
   static std::atomic<uint64_t> done{0};
   if (!raise_smem(kern, 227 * 1024, &done)) return V4A_ERR_CUDA;
   cudaFuncAttributes attr;
@@ -488,7 +575,7 @@ int64_t row_blocks(const v4a_dense_attn_args* a) {
 
 bool dense_prefill_takes(const v4a_dense_attn_args* a) {
   const int64_t rows = int64_t(a->max_new_per_seq) * (a->num_heads / a->kv.num_kv_heads);
-  return a->kv.format == V4A_KV_BF16 && (a->kv.dim == 64 || a->kv.dim == 128) && rows > 64;
+  return (a->kv.dim == 64 || a->kv.dim == 128) && rows > 64;
 }
 
 size_t dense_prefill_workspace(const v4a_dense_attn_args* a) { return split_workspace(kUnit, a->kv.dim, kSms); }
@@ -499,7 +586,8 @@ int dense_prefill(const v4a_dense_attn_args* a, const DenseAttnDev& d, void* ws,
   p.U = d.B * p.RG;
   p.split = p.U <= kMaxSplitUnits;
   split_carve(&p, ws, kUnit, a->kv.dim, kSms, kUnitCost);
-  return a->kv.dim == 64 ? launch<64>(d, p, stream) : launch<128>(d, p, stream);
+  if (a->kv.format == V4A_KV_FP8_TOKEN) return a->kv.dim == 64 ? launch<64, true>(d, p, stream) : launch<128, true>(d, p, stream);
+  return a->kv.dim == 64 ? launch<64, false>(d, p, stream) : launch<128, false>(d, p, stream);
 }
 
 }  // namespace v4a
