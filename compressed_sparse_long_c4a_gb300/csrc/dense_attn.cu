@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(Shape<D, NT, kFp8>::kThreads, Shape<D, NT, kFp
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_wait();
   Line<R, kKeys, kThreads> line(a, p, &s + 1);
-  if (!line.init(s.scan, kWarps)) return;          // a tile per warp at least
+  if (!line.init(s.scan, smem, kWarps)) return;          // a tile per warp at least
   const int64_t x0 = line.x0, x1 = line.x1;
 
   // ---- this warp's stream: tiles x0 + warp + j kWarps, j = 0, 1, ... ----
@@ -615,26 +615,39 @@ __global__ void __launch_bounds__(256) dense_join_rows(const DenseAttnDev a, con
   if (blockIdx.y == 0 && a.lse) a.lse[at] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
 }
 
-int rows_of(const v4a_dense_attn_args* a) {
-  const int64_t rows = int64_t(a->max_new_per_seq) * (a->num_heads / a->kv.num_kv_heads);
-  return rows > 8 && a->kv.dim <= 192 ? 16 : 8;      // 16 rows of dim 256 would not fit the registers
+// A call whose sequences all bring many rows runs dense_prefill.cu's form, one
+// whose sequences all bring few rows this file's, and a mixed one both, each
+// launch taking its sequences: it is mixed when the token count leaves room
+// for short sequences beside the longest.
+bool mixed(const v4a_dense_attn_args* a) {
+  return dense_prefill_takes(a) && a->num_tokens < int64_t(a->num_seqs) * a->max_new_per_seq;
 }
 
-int64_t row_groups(const v4a_dense_attn_args* a) {
+// The most rows a sequence brings to the form for few rows.
+int64_t most_rows(const v4a_dense_attn_args* a) {
   const int64_t rows = int64_t(a->max_new_per_seq) * (a->num_heads / a->kv.num_kv_heads);
-  return (rows + rows_of(a) - 1) / rows_of(a);
+  return dense_prefill_takes(a) ? few_rows(a->kv.format != V4A_KV_BF16) : rows;
 }
+
+int rows_of(const v4a_dense_attn_args* a) {
+  return most_rows(a) > 8 && a->kv.dim <= 192 ? 16 : 8;      // 16 rows of dim 256 would not fit the registers
+}
+
+int64_t row_groups(const v4a_dense_attn_args* a) { return (most_rows(a) + rows_of(a) - 1) / rows_of(a); }
 
 int ctas_of(const v4a_dense_attn_args* a) { return a->kv.dim <= 128 ? 2 * kSms : kSms; }
 
+size_t few_workspace(const v4a_dense_attn_args* a) { return split_workspace(rows_of(a), a->kv.dim, ctas_of(a)); }
+
+// Of every call of the shape, mixed or not.
 size_t workspace_of(const v4a_dense_attn_args* a) {
-  return dense_prefill_takes(a) ? dense_prefill_workspace(a) : split_workspace(rows_of(a), a->kv.dim, ctas_of(a));
+  return few_workspace(a) + (dense_prefill_takes(a) ? dense_prefill_workspace(a) : 0);
 }
 
 template <int D, int NT, bool kFp8>
 int launch(const DenseAttnDev& a, const SplitDev& p, cudaStream_t stream) {
   using S = Shape<D, NT, kFp8>;
-  const size_t smem = S::kWarps * S::kStages * S::kStage + sizeof(typename S::Tail) + split_smem(p.split, p.U, a.B);
+  const size_t smem = S::kWarps * S::kStages * S::kStage + sizeof(typename S::Tail) + split_smem(p.split, p.U);
   if (smem > 227 * 1024) return V4A_ERR_UNSUPPORTED;
   auto kern = dense_attn_mma<D, NT, kFp8>;
   static std::atomic<uint64_t> done{0};
@@ -666,7 +679,7 @@ int check_shape(const v4a_dense_attn_args* a) {
   if (c.dim != 64 && c.dim != 128 && c.dim != 192 && c.dim != 256) return V4A_ERR_UNSUPPORTED;
   if (c.format != V4A_KV_BF16 && c.format != V4A_KV_FP8_TOKEN) return V4A_ERR_UNSUPPORTED;
   if (a->num_heads > 1024 || a->max_new_per_seq > (1 << 22) || c.max_blocks > (1 << 22)) return V4A_ERR_UNSUPPORTED;
-  if (int64_t(a->num_seqs) * row_groups(a) > INT32_MAX) return V4A_ERR_UNSUPPORTED;
+  if (int64_t(a->max_new_per_seq) * (a->num_heads / c.num_kv_heads) > INT32_MAX / 2) return V4A_ERR_UNSUPPORTED;   // rows are counted in 32 bits
   return V4A_OK;
 }
 
@@ -676,7 +689,7 @@ int dense_join(const DenseAttnDev& a, const SplitDev& p, int dim, cudaStream_t s
   const bool many = p.rows > 16;
   auto kern = many ? (dim == 64 ? dense_join_rows<64> : dense_join_rows<128>)
                    : (dim == 64 ? dense_join_kernel<64> : dim == 128 ? dense_join_kernel<128> : dim == 192 ? dense_join_kernel<192> : dense_join_kernel<256>);
-  const int y = many ? dim / 16 : p.rows;
+  const int y = many ? dim / 16 : int(std::min<int64_t>(p.rows, std::min<int64_t>(int64_t(a.max_new) * a.G, p.rows_to)));   // rows that a unit can have
   const cudaError_t e = launch_pdl(kern, dim3(unsigned(p.grid), unsigned(y)), dim3(256), 0, stream, a, p);
   return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? V4A_OK : V4A_ERR_CUDA;
 }
@@ -689,7 +702,7 @@ int dense_attn(const v4a_dense_attn_args* a, void* ws, size_t ws_bytes, cudaStre
   DenseAttnDev d{};
   rc = dense_cache_check(a->kv, &d.block_bytes);
   if (rc) return rc;
-  if (!(a->softmax_scale > 0.f) || !std::isfinite(a->softmax_scale) || a->kv.max_blocks < 1) return V4A_ERR_INVALID_ARG;
+  if (!(a->softmax_scale > 0.f) || !std::isfinite(a->softmax_scale * 1.4426950408889634f) || a->kv.max_blocks < 1) return V4A_ERR_INVALID_ARG;
   if (a->num_tokens == 0 || a->num_seqs == 0) return V4A_OK;
   if (!a->positions || !a->token_starts || !a->kv.block_table || !a->q || !a->out) return V4A_ERR_INVALID_ARG;
   if ((reinterpret_cast<uintptr_t>(a->q) & 15) || (reinterpret_cast<uintptr_t>(a->out) & 15) ||
@@ -697,21 +710,32 @@ int dense_attn(const v4a_dense_attn_args* a, void* ws, size_t ws_bytes, cudaStre
     return V4A_ERR_INVALID_ARG;
   if (!ws || (reinterpret_cast<uintptr_t>(ws) & 15) || ws_bytes < workspace_of(a)) return V4A_ERR_WORKSPACE;
   d.T = a->num_tokens; d.B = a->num_seqs; d.H = a->num_heads; d.K = a->kv.num_kv_heads; d.G = d.H / d.K;
-  d.max_new = a->max_new_per_seq; d.max_blocks = a->kv.max_blocks; d.window = a->window; d.sinks = a->sinks;
+  d.max_new = a->max_new_per_seq; d.max_blocks = a->kv.max_blocks; d.sinks = a->sinks;
+  // a window as long as a sequence can be hides nothing (and the kernels' differences stay in 32 bits)
+  d.window = a->window < int64_t(a->kv.max_blocks) * kBlockPositions ? a->window : 0;
   d.num_blocks = a->kv.num_blocks;
   d.positions = a->positions; d.starts = a->token_starts; d.bt = a->kv.block_table;
   d.pool = static_cast<const uint8_t*>(a->kv.pool);
   d.q = a->q; d.out = a->out; d.lse = a->lse; d.status = a->status;
   d.scale_log2 = a->softmax_scale * 1.4426950408889634f;
-  if (dense_prefill_takes(a)) return dense_prefill(a, d, ws, stream);
   SplitDev p{};
+  p.rows_to = INT32_MAX;
+  if (dense_prefill_takes(a)) {
+    const bool both = mixed(a);
+    const int few = few_rows(a->kv.format != V4A_KV_BF16);
+    rc = dense_prefill(a, d, both ? few + 1 : 0, static_cast<uint8_t*>(ws) + few_workspace(a), stream);
+    if (rc || !both) return rc;
+    p.rows_to = few;
+  }
   p.RG = int(row_groups(a));
-  p.U = d.B * p.RG;
+  const int64_t units = units_bound(d, p.rows_from, p.RG, rows_of(a));
+  if (units > INT32_MAX) return V4A_ERR_UNSUPPORTED;
+  p.U = int(units);
   // One CTA per unit and KV head when there are enough of them and a window bounds their lengths (64
   // sequences x 8 heads x 1024 positions: 29 us, the even split 34); an even split otherwise, since the
   // lengths are the device's (200 sequences of 1 to 600 x 8: 47 us unsplit, 50 split; but one long
   // sequence among short ones would run alone).
-  p.split = p.U <= kMaxSplitUnits && (a->window == 0 || int64_t(p.U) * d.K < 256);
+  p.split = std::max(p.U, d.B) <= kMaxSplitUnits && (d.window == 0 || int64_t(p.U) * d.K < 256);
   split_carve(&p, ws, rows_of(a), a->kv.dim, ctas_of(a), kUnitCost);
   return a->kv.format == V4A_KV_FP8_TOKEN ? launch_dim<true>(d, p, a->kv.dim, stream) : launch_dim<false>(d, p, a->kv.dim, stream);
 }

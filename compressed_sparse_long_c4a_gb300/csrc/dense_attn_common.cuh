@@ -1,6 +1,7 @@
 // What the dense attention kernels share: the arguments on the device, which
 // keys a group of rows sees, and the tiles that cover them.
 #pragma once
+#include <algorithm>
 #include <atomic>
 
 #include "tc_common.cuh"
@@ -21,11 +22,20 @@ struct DenseAttnDev {
   float scale_log2;               // softmax_scale * log2(e): logits in log2 units
 };
 
+// Sequences of at most this many rows (tokens x heads of a group) go to the
+// form for few rows, which reads the cache once per 16 rows; the form for many
+// reads it once but converts fp8 codes on the way.  Few / many, 32 + 8 heads
+// of 128, us: bf16, 8 sequences at 8k: 32 rows 69 / 62, 64 rows 123 / 64; one
+// at 8k: 32 rows 22 / 32, 64 rows 28 / 32; 16 at 1k (dim 64): 24 / 26 and
+// 35 / 26; fp8, 8 at 8k: 32 rows 63 / 130, 64 rows 111 / 131, 128 rows 203 / 132.
+constexpr int few_rows(bool fp8) { return fp8 ? 64 : 32; }
+
 // One sequence's tokens of the call: first row, count and first position;
-// n = 0 when there are none or the entries are inconsistent (reported).
+// n = 0 when there are none, the entries are inconsistent (reported) or the
+// sequence belongs to the call's other launch.
 struct SeqRun { int s0, n, p0; };
 
-__device__ __forceinline__ SeqRun seq_run(const DenseAttnDev& a, int b, int32_t* status) {
+__device__ __forceinline__ SeqRun seq_run(const DenseAttnDev& a, int64_t rows_from, int64_t rows_to, int b, int32_t* status) {
   const int s0 = a.starts[b], s1 = a.starts[b + 1];
   SeqRun r{s0, 0, 0};
   if (s0 == s1 && s0 >= 0 && s1 <= a.T) return r;
@@ -35,8 +45,9 @@ __device__ __forceinline__ SeqRun seq_run(const DenseAttnDev& a, int b, int32_t*
     ok = p0 >= 0 && int64_t(p1) == int64_t(p0) + (s1 - s0) - 1 && p1 < int64_t(a.max_blocks) * kBlockPositions;
     r.p0 = p0;
   }
-  if (ok) r.n = s1 - s0;
-  else report(status, V4A_DEV_BAD_BATCH);
+  const int64_t rows = int64_t(s1 - s0) * a.G;
+  if (!ok) report(status, V4A_DEV_BAD_BATCH);
+  else if (rows >= rows_from && rows <= rows_to) r.n = s1 - s0;
   return r;
 }
 
@@ -75,18 +86,17 @@ __device__ __forceinline__ bool all_visible(const DenseAttnDev& a, int m_lo, int
 template <int kTile>
 struct Unit { int b, row0, rows, s0, m_lo, m_hi; TileRange<kTile> tr; };
 
+// What a unit is kept as: its last row gives the first (a multiple of R); -1: no rows.
+struct alignas(16) UnitRef { int b, s0, p0, last; };
+
 template <int R, int kTile>
-__device__ __forceinline__ Unit<kTile> make_unit(const DenseAttnDev& a, int b, int rg, const SeqRun& s) {
-  Unit<kTile> u;
-  u.b = b;
-  u.row0 = rg * R;
-  u.rows = int(min(int64_t(R), int64_t(s.n) * a.G - u.row0));
-  u.s0 = s.s0;
-  u.m_lo = u.m_hi = 0;
-  u.tr = TileRange<kTile>{0, 0, 0};
-  if (u.rows <= 0) return u;
-  u.m_lo = s.p0 + u.row0 / a.G;
-  u.m_hi = s.p0 + (u.row0 + u.rows - 1) / a.G;
+__device__ __forceinline__ Unit<kTile> make_unit(const DenseAttnDev& a, const UnitRef& f) {
+  Unit<kTile> u{f.b, 0, 0, f.s0, 0, 0, {0, 0, 0}};
+  if (f.last < 0) return u;
+  u.row0 = f.last & ~(R - 1);
+  u.rows = f.last - u.row0 + 1;
+  u.m_lo = f.p0 + u.row0 / a.G;
+  u.m_hi = f.p0 + f.last / a.G;
   u.tr = tile_range<kTile>(a, u.m_lo, u.m_hi);
   return u;
 }
@@ -97,15 +107,17 @@ __device__ __forceinline__ int64_t row_of(const DenseAttnDev& a, const Unit<kTil
   return int64_t(u.s0 + (u.row0 + r) / a.G) * a.H + hk * a.G + (u.row0 + r) % a.G;
 }
 
-// How a launch divides the units: split = 1: the tiles of all units and KV
-// heads form one line (unit by unit, KV head by KV head) that the CTAs divide
+// How a launch divides the units, which are numbered over the sequences' row
+// groups (sequences without tokens in this launch have none): split = 1: the
+// tiles of all units and KV heads form one line (unit by unit, KV head by KV head) that the CTAs divide
 // evenly, each unit counted with `cost` tiles more than it has (its set-up and
 // its end take about that long); split = 0: one CTA per unit and KV head.
 struct SplitDev {
-  int RG, U, split;               // row groups per sequence, units (sequences x row groups)
+  int RG, U, split;               // row groups of the longest sequence; units at most
   int rows, grid, cost;           // R; CTAs of the launch and a unit's extra tiles (split)
   struct JoinDesc* join;          // [CTA]
   float *part_o, *part_ml;        // [CTA][2][R][dim], [CTA][2][R][2] (maximum in log2 units, sum)
+  int rows_from, rows_to;         // the launch takes sequences of this many rows (tokens x group)
 };
 
 // A unit that starts in a CTA's range and goes on in the next CTAs' up to `last`:
@@ -115,11 +127,17 @@ struct alignas(32) JoinDesc { int rows, row0, s0, hk, last, pad[3]; };
 constexpr int kMaxSplitUnits = 512;   // more units than these fill the machine one by one
 constexpr int kSms = 152;
 
-__host__ __device__ constexpr size_t split_smem(int split, int U, int B) {
-  return split ? (U + 1) * sizeof(int64_t) + B * sizeof(SeqRun) : sizeof(SeqRun);
+// Units of R rows that a consistent batch has at most: a sequence of n rows has
+// n / R and one more, and only sequences of rows_from rows or more count.
+inline int64_t units_bound(const DenseAttnDev& a, int rows_from, int64_t RG, int R) {
+  const int64_t rows = int64_t(a.T) * a.G, seqs = std::min<int64_t>(a.B, rows_from > 0 ? rows / rows_from : a.T);
+  return RG == 1 ? a.B : std::min(a.B * RG, rows / R + seqs);
+}
+__host__ __device__ constexpr size_t split_smem(int split, int U) {
+  return split ? U * sizeof(UnitRef) + (U + 1) * sizeof(int64_t) : sizeof(UnitRef);
 }
 __host__ __device__ constexpr size_t split_workspace(int R, int dim, int ctas) {
-  return 16 + ctas * (sizeof(JoinDesc) + size_t(2) * R * (dim + 2) * sizeof(float));
+  return ctas * (sizeof(JoinDesc) + size_t(2) * R * (dim + 2) * sizeof(float));      // (a multiple of 16)
 }
 // Raises a kernel's dynamic shared memory limit, once per device (`done`: the devices it is done on).
 template <typename K>
@@ -146,61 +164,92 @@ template <int R, int kTile, int kThreads>
 struct Line {
   const DenseAttnDev& a;
   const SplitDev& p;
+  UnitRef* refs;                  // [U], or the one
   int64_t* pre;                   // [U + 1] tiles before unit u, over its KV heads
-  SeqRun* runs;                   // [B], or the one
   int64_t x0, x1, total, weight;
   int ctas, u_direct, hk_direct;
 
   struct Piece { int u, hk, tile; };
+  struct Seq { SeqRun r; int first; };      // a sequence and the units before it
 
-  // `scan`: kThreads / 32 words of shared memory.  At least min_tiles tiles per
-  // CTA.  Called by the whole CTA; false when it has no tiles.
   __device__ __forceinline__ Line(const DenseAttnDev& a_, const SplitDev& p_, void* mem) : a(a_), p(p_) {
-    pre = static_cast<int64_t*>(mem);
-    runs = reinterpret_cast<SeqRun*>(pre + (p.split ? p.U + 1 : 0));
+    refs = static_cast<UnitRef*>(mem);
+    pre = reinterpret_cast<int64_t*>(refs + p.U);
   }
-  __device__ __forceinline__ bool init(int64_t* scan, int min_tiles) {
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // `scan`: kThreads / 32 words of shared memory; `scratch`: kMaxSplitUnits Seq
+  // of it, free again on return.  At least min_tiles tiles (or units' costs)
+  // per CTA.  Called by the whole CTA; false when it has no tiles.
+  __device__ __forceinline__ bool init(int64_t* scan, void* scratch, int min_tiles) {
+    const int tid = threadIdx.x;
+    int32_t* st = blockIdx.x == 0 ? a.status : nullptr;     // one CTA reports the batch's faults
     u_direct = hk_direct = ctas = 0;
     total = 0;
     if (!p.split) {
       u_direct = int(blockIdx.x / unsigned(a.K));
       hk_direct = int(blockIdx.x % unsigned(a.K));
-      if (tid == 0) runs[0] = seq_run(a, u_direct / p.RG, hk_direct == 0 && u_direct % p.RG == 0 ? a.status : nullptr);
+      if (p.RG == 1) {
+        if (tid == 0) refs[0] = ref(u_direct, 0, run(u_direct, hk_direct == 0 ? a.status : nullptr));
+      } else {
+        // units counted by the starts alone, each thread a run of sequences; the one found is checked then
+        const int per = (a.B + kThreads - 1) / kThreads, b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
+        if (tid == 0) refs[0] = UnitRef{0, 0, 0, -1};
+        int64_t n = 0, all;
+        for (int b = b0; b < b1; ++b) {
+          n += groups(a.starts[b], a.starts[b + 1]);
+          if (st) run(b, st);
+        }
+        int64_t at = before(n, scan, &all);
+        if (u_direct >= at && u_direct < at + n) {
+          int b = b0;
+          for (int64_t g; at + (g = groups(a.starts[b], a.starts[b + 1])) <= u_direct; ++b) at += g;
+          refs[0] = ref(b, int(u_direct - at), run(b, nullptr));
+        }
+        if (st && tid == 0 && all > p.U) report(st, V4A_DEV_BAD_BATCH);       // sequences that share tokens
+      }
       __syncthreads();
       x0 = 0;
       x1 = unit(u_direct).tr.tiles;
       return x1 > 0;
     }
-    int32_t* st = blockIdx.x == 0 ? a.status : nullptr;     // one CTA reports the batch's faults
-    for (int b = tid; b < a.B; b += kThreads) runs[b] = seq_run(a, b, st);
+    Seq* const seqs = static_cast<Seq*>(scratch);
+    for (int b = tid; b < a.B; b += kThreads) seqs[b] = Seq{run(b, st), b};
     __syncthreads();
+    int units = p.U;
+    if (p.RG > 1) {
+      const int per = (a.B + kThreads - 1) / kThreads, b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
+      int64_t n = 0, all;
+      for (int b = b0; b < b1; ++b) n += groups(seqs[b].r.s0, seqs[b].r.s0 + seqs[b].r.n);
+      int64_t at = before(n, scan, &all);
+      units = int(min(all, int64_t(p.U)));
+      for (int b = b0; b < b1; ++b) {
+        seqs[b].first = int(min(at, int64_t(units)));
+        at += groups(seqs[b].r.s0, seqs[b].r.s0 + seqs[b].r.n);
+      }
+      if (st && tid == 0 && all > p.U) report(st, V4A_DEV_BAD_BATCH);         // sequences that share tokens
+      __syncthreads();
+    }
     // exclusive sums over the units: each thread a run of units, then the threads' totals
     const int per = (p.U + kThreads - 1) / kThreads, u0 = min(p.U, tid * per), u1 = min(p.U, u0 + per);
     int64_t sum = 0;
     for (int u = u0; u < u1; ++u) {
+      int lo = u;                                 // the unit's sequence: the last whose first <= u
+      if (p.RG > 1) {
+        lo = 0;
+        for (int hi = a.B; hi - lo > 1;) {
+          const int mid = (lo + hi) >> 1;
+          if (seqs[mid].first <= u) lo = mid; else hi = mid;
+        }
+      }
+      refs[u] = u < units ? ref(lo, u - seqs[lo].first, seqs[lo].r) : UnitRef{0, 0, 0, -1};
       pre[u] = sum;
       sum += int64_t(unit(u).tr.tiles) * a.K;
     }
-    int64_t v = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t w = __shfl_up_sync(0xffffffffu, v, o);
-      if (lane >= o) v += w;
-    }
-    if (lane == 31) scan[warp] = v;
-    __syncthreads();
-    int64_t before = v - sum;
-#pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) {
-      if (w < warp) before += scan[w];
-      total += scan[w];
-    }
-    for (int u = u0; u < u1; ++u) pre[u] += before;
+    const int64_t ahead = before(sum, scan, &total);
+    for (int u = u0; u < u1; ++u) pre[u] += ahead;
     if (tid == 0) pre[p.U] = total;
     __syncthreads();
-    weight = total + int64_t(p.cost) * a.K * p.U;
-    ctas = int(min(int64_t(gridDim.x), (total + min_tiles - 1) / min_tiles));
+    weight = total + int64_t(p.cost) * a.K * units;
+    ctas = int(min(int64_t(gridDim.x), (weight + min_tiles - 1) / min_tiles));
     x0 = x1 = 0;
     if (int(blockIdx.x) < ctas) {
       x0 = place(int64_t(blockIdx.x) * weight / ctas);
@@ -208,6 +257,35 @@ struct Line {
     }
     if (x0 == x1 && tid == 0) p.join[blockIdx.x].rows = 0;
     return x0 < x1;
+  }
+  __device__ __forceinline__ UnitRef ref(int b, int rg, const SeqRun& r) const {
+    return UnitRef{b, r.s0, r.p0, int(min(int64_t(r.n) * a.G, (int64_t(rg) + 1) * R)) - 1};
+  }
+  __device__ __forceinline__ SeqRun run(int b, int32_t* st) const { return seq_run(a, p.rows_from, p.rows_to, b, st); }
+  // Row groups of a sequence of tokens [s0, s1) in this launch.
+  __device__ __forceinline__ int64_t groups(int s0, int s1) const {
+    const int64_t n = int64_t(s1) - s0, rows = n * a.G;
+    return n > 0 && n <= a.max_new && rows >= p.rows_from && rows <= p.rows_to ? (rows + R - 1) / R : 0;
+  }
+  // The sum of the earlier threads' v, and of all (whole CTA; `scan` is free again behind a barrier).
+  __device__ __forceinline__ int64_t before(int64_t v, int64_t* scan, int64_t* all) const {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int64_t x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t w = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += w;
+    }
+    if (lane == 31) scan[warp] = x;
+    __syncthreads();
+    int64_t ahead = x - v;
+    *all = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) ahead += scan[w];
+      *all += scan[w];
+    }
+    return ahead;
   }
   // The first tile at or behind position w of the line with the units' costs,
   // which are in front of their tiles.
@@ -223,9 +301,7 @@ struct Line {
     const int64_t rem = w - pre[lo] - each * lo, hk = rem / (tiles + p.cost);
     return pre[lo] + hk * tiles + max(int64_t(0), rem - hk * (tiles + p.cost) - p.cost);
   }
-  __device__ __forceinline__ Unit<kTile> unit(int u) const {
-    return make_unit<R, kTile>(a, u / p.RG, u % p.RG, runs[p.split ? u / p.RG : 0]);
-  }
+  __device__ __forceinline__ Unit<kTile> unit(int u) const { return make_unit<R, kTile>(a, refs[p.split ? u : 0]); }
   // Where tile x of the line lies.
   __device__ __forceinline__ Piece locate(int64_t x, Unit<kTile>* un) const {
     if (!p.split) {
@@ -255,6 +331,6 @@ int dense_join(const DenseAttnDev& a, const SplitDev& p, int dim, cudaStream_t s
 // The tensor-core form for many rows (dense_prefill.cu): whether it takes the shape, and its launch.
 bool dense_prefill_takes(const v4a_dense_attn_args* a);
 size_t dense_prefill_workspace(const v4a_dense_attn_args* a);
-int dense_prefill(const v4a_dense_attn_args* a, const DenseAttnDev& d, void* ws, cudaStream_t stream);
+int dense_prefill(const v4a_dense_attn_args* a, const DenseAttnDev& d, int rows_from, void* ws, cudaStream_t stream);
 
 }  // namespace v4a

@@ -17,11 +17,12 @@
 //   O_t += P_t V    M = 128, N = dim, K = 128 keys      [256 + 128 t, +dim)
 //                   (P from TMEM, V as an MN-major operand)
 //
-// Roles (12 warps): 0-3 and 4-7 the two tiles' softmax (a thread owns a row),
-// 8 issues the MMAs, 9 to 11 copy keys and values (16-byte
-// cp.async into the 128-byte swizzle; rows that no row of the CTA sees are
-// filled with zeros, so what they hold cannot reach a product).  Keys and
-// values have two buffers each.
+// Roles: warps 0-3 and 4-7 the two tiles' softmax (a thread owns a row), 8
+// issues the MMAs, the others copy keys and values into the 128-byte swizzle
+// (bf16: 16-byte cp.async; fp8: through registers, the codes becoming bf16 keys
+// and f16 values exactly, their scales applied to the logits and to P).  Rows
+// that no row of the CTA sees are filled with zeros, so what they hold cannot
+// reach a product.  Keys and values have two buffers each.
 //
 // Bound: the tensor cores (4 dim flops per visible pair), and beside them the
 // exponentials: 128 x 128 per tile and step.
@@ -32,9 +33,19 @@ namespace {
 
 constexpr int kRows = 128;           // rows of a tile (MMA M)
 constexpr int kKeys = 128;           // keys per step
-constexpr int kThreads = 384;
 constexpr int kUnit = 2 * kRows;     // rows of a unit
-constexpr int kLoaders = 96;
+// Threads and registers of the two forms.  bf16 rows are copied as they are:
+// three warps (four: 306 us against 258 for 2k tokens over 10k, since the
+// softmax then has fewer registers).  fp8 rows go through the registers of
+// their copying warps, which convert them: seven warps (three: 583 us against
+// 488).  softmax x 256 + rest x (threads - 256) = launch x threads.
+template <bool kFp8>
+struct Roles {
+  static constexpr int kThreads = kFp8 ? 512 : 384;
+  static constexpr int kLoaders = kThreads - 9 * 32;
+  static constexpr int kSoftmaxRegs = kFp8 ? 192 : 200, kRestRegs = kFp8 ? 64 : 104, kLaunchRegs = kFp8 ? 128 : 168;
+  static_assert(kSoftmaxRegs * 256 + kRestRegs * (kThreads - 256) == kLaunchRegs * kThreads, "the split of the registers");
+};
 constexpr int kUnitCost = 3;         // steps that a unit's set-up and output take the time of
 constexpr int kMinSteps = 4;         // steps a CTA of an even split has at least
 constexpr float kRaise = 8.f;        // log2 units by which logits may pass the maximum in use
@@ -42,7 +53,7 @@ constexpr float kRaiseFp8 = 4.f, kShiftFp8 = 11.f;   // f16 P: 2^11 2^{w - m} <=
 
 struct PreSmem {
   uint64_t q_full[2], k_full[2], v_full[2], k_free[2], v_free[2], s_full[2], p_full[2][2], o_full[2], drain;
-  int64_t scan[kThreads / 32];
+  int64_t scan[16];
   uint32_t tmem_base;
   int abort_flag;
   int missing[4];                    // step n's page is missing: [n % 4]
@@ -174,7 +185,8 @@ __device__ __forceinline__ uint32_t chunk_at(int r, int ch) {
 }
 
 template <int D, bool kFp8>
-__global__ void __launch_bounds__(kThreads, 1) dense_prefill_kernel(const DenseAttnDev a, const SplitDev p) {
+__global__ void __launch_bounds__(Roles<kFp8>::kThreads, 1) dense_prefill_kernel(const DenseAttnDev a, const SplitDev p) {
+  constexpr int kThreads = Roles<kFp8>::kThreads, kLoaders = Roles<kFp8>::kLoaders;
   constexpr int kTileBytes = 128 * D * 2;      // a Q tile, a step's keys or its values
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -185,7 +197,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_prefill_kernel(const DenseA
 
   pdl_wait();
   Line<kUnit, kKeys, kThreads> line(a, p, &s + 1);
-  if (!line.init(s.scan, kMinSteps)) return;
+  if (!line.init(s.scan, base, kMinSteps)) return;
   const int64_t x0 = line.x0, x1 = line.x1;
 
   if (tid == 0) {
@@ -214,9 +226,8 @@ __global__ void __launch_bounds__(kThreads, 1) dense_prefill_kernel(const DenseA
   // Every role walks the CTA's segments (the parts of units in [x0, x1)) by
   // itself.  Counters: n = steps of the CTA (key and value buffers), e = steps
   // of a tile (its S and P), g = segments of a tile (its Q and O).
-  // registers: 256 threads x 200 + 128 x 104 = the launch's 384 x 168 (checked by the host)
-  if (warp < 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
-  else asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+  if (warp < 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Roles<kFp8>::kSoftmaxRegs));
+  else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Roles<kFp8>::kRestRegs));
   if (warp < 8) {
     // ---- a tile's queries, softmax and output ----
     const int t = warp >> 2, r = tid & 127;
@@ -551,7 +562,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_prefill_kernel(const DenseA
 template <int D, bool kFp8>
 int launch(const DenseAttnDev& d, const SplitDev& p, cudaStream_t stream) {
   // at least 116 KB: no two CTAs that allocate TMEM share an SM
-  size_t bytes = 1024 + 6 * 128 * D * 2 + sizeof(PreSmem) + split_smem(p.split, p.U, d.B);
+  size_t bytes = 1024 + 6 * 128 * D * 2 + sizeof(PreSmem) + split_smem(p.split, p.U);
   if (bytes < 116 * 1024) bytes = 116 * 1024;
   if (bytes > 227 * 1024) return V4A_ERR_UNSUPPORTED;
   auto kern = dense_prefill_kernel<D, kFp8>;
@@ -559,10 +570,10 @@ int launch(const DenseAttnDev& d, const SplitDev& p, cudaStream_t stream) {
   if (!raise_smem(kern, 227 * 1024, &done)) return V4A_ERR_CUDA;
   cudaFuncAttributes attr;
   if (cudaFuncGetAttributes(&attr, kern) != cudaSuccess) return V4A_ERR_CUDA;
-  if (attr.numRegs != 168) return V4A_ERR_UNSUPPORTED;     // the register split would not add up
+  if (attr.numRegs != Roles<kFp8>::kLaunchRegs) return V4A_ERR_UNSUPPORTED;     // the split of the registers would not add up
   const int64_t grid = p.split ? p.grid : int64_t(p.U) * d.K;
   if (grid > INT32_MAX) return V4A_ERR_UNSUPPORTED;
-  const cudaError_t e = launch_pdl(kern, dim3(unsigned(grid)), dim3(kThreads), bytes, stream, d, p);
+  const cudaError_t e = launch_pdl(kern, dim3(unsigned(grid)), dim3(Roles<kFp8>::kThreads), bytes, stream, d, p);
   if (e != cudaSuccess || cudaGetLastError() != cudaSuccess) return V4A_ERR_CUDA;
   return p.split ? dense_join(d, p, D, stream) : V4A_OK;
 }
@@ -575,16 +586,21 @@ int64_t row_blocks(const v4a_dense_attn_args* a) {
 
 bool dense_prefill_takes(const v4a_dense_attn_args* a) {
   const int64_t rows = int64_t(a->max_new_per_seq) * (a->num_heads / a->kv.num_kv_heads);
-  return (a->kv.dim == 64 || a->kv.dim == 128) && rows > 64;
+  return (a->kv.dim == 64 || a->kv.dim == 128) && rows > few_rows(a->kv.format != V4A_KV_BF16);
 }
 
 size_t dense_prefill_workspace(const v4a_dense_attn_args* a) { return split_workspace(kUnit, a->kv.dim, kSms); }
 
-int dense_prefill(const v4a_dense_attn_args* a, const DenseAttnDev& d, void* ws, cudaStream_t stream) {
+int dense_prefill(const v4a_dense_attn_args* a, const DenseAttnDev& d, int rows_from, void* ws, cudaStream_t stream) {
   SplitDev p{};
   p.RG = int(row_blocks(a));
-  p.U = d.B * p.RG;
-  p.split = p.U <= kMaxSplitUnits;
+  p.rows_from = rows_from;
+  p.rows_to = INT32_MAX;
+  if (rows_from > 0) p.RG = std::max(p.RG, 2);      // sequences of the other launch are not units
+  const int64_t units = units_bound(d, rows_from, p.RG, kUnit);
+  if (units > INT32_MAX) return V4A_ERR_UNSUPPORTED;
+  p.U = int(units);
+  p.split = std::max(p.U, d.B) <= kMaxSplitUnits;
   split_carve(&p, ws, kUnit, a->kv.dim, kSms, kUnitCost);
   if (a->kv.format == V4A_KV_FP8_TOKEN) return a->kv.dim == 64 ? launch<64, true>(d, p, stream) : launch<128, true>(d, p, stream);
   return a->kv.dim == 64 ? launch<64, false>(d, p, stream) : launch<128, false>(d, p, stream);

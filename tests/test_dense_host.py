@@ -145,7 +145,8 @@ def test_attention_refuses_caches(lib, kw, code):
     (dict(num_heads=7), INVALID), (dict(num_heads=1026), UNSUPPORTED), (dict(positions=None), INVALID), (dict(token_starts=None), INVALID),
     (dict(q=None), INVALID), (dict(out=None), INVALID), (dict(q=0x108), INVALID), (dict(out=0x208), INVALID), (dict(out=0x100), INVALID),
     (dict(window=-1), INVALID), (dict(sinks=-1), INVALID), (dict(softmax_scale=0.0), INVALID), (dict(softmax_scale=math.nan), INVALID),
-    (dict(softmax_scale=math.inf), INVALID), (dict(max_new_per_seq=(1 << 22) + 1), UNSUPPORTED)])
+    (dict(softmax_scale=math.inf), INVALID), (dict(softmax_scale=3e38), INVALID), (dict(max_new_per_seq=(1 << 22) + 1), UNSUPPORTED),
+    (dict(num_heads=1024, max_new_per_seq=1 << 22), UNSUPPORTED)])
 def test_attention_refuses_arguments(lib, kw, code):
     assert lib.v4a_dense_attn(C.byref(_attn(**kw)), 0x1000, 1 << 30, None) == code
 

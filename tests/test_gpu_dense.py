@@ -487,6 +487,117 @@ def test_chunks(cached, new, H, K, dim, fp8, window, sinks):
     _attend(layer, pos, starts, window, sinks, pad=2, tokens=some)
 
 
+MIXED = [
+    # (cached, new) per sequence, H, K, dim, fp8, window, sinks, room in max_new
+    ([(700, 1), (0, 300), (90, 1), (256, 8), (10, 9), (0, 33)], 8, 2, 128, False, 0, 0, 0),
+    ([(700, 1), (0, 300), (90, 1), (256, 16), (10, 17), (0, 33)], 8, 2, 64, True, 0, 0, 0),
+    ([(700, 1), (300, 200), (0, 0), (256, 3), (0, 0)], 16, 1, 128, True, 100, 5, 0),
+    ([(30, 1), (60, 2), (7, 5)], 8, 8, 128, False, 0, 0, 1000),              # the longest allowed is not there
+    ([(300, 70), (60, 64), (7, 65)], 4, 4, 64, False, 40, 0, 2000),
+    ([(i % 300, 1) for i in range(60)] + [(100, 700)] + [(i, 2) for i in range(60)], 4, 2, 64, False, 0, 0, 0),
+    ([(i % 90, 1 + 40 * (i % 61 == 0)) for i in range(700)], 2, 1, 64, False, 0, 0, 0),   # more sequences than are split evenly
+    ([(i % 90, 40 * (i % 61 == 0) + (i % 3 > 0)) for i in range(700)], 2, 1, 64, True, 20, 2, 0),
+    ([(i % 50, 1 + i % 120) for i in range(40)], 8, 1, 192, False, 0, 0, 0),
+    ([(i % 50, 1 + 30 * (i % 5 == 0)) for i in range(600)], 2, 1, 256, False, 0, 0, 0),
+]
+
+
+@pytest.mark.parametrize("runs,H,K,dim,fp8,window,sinks,room", MIXED)
+def test_mixed_batches(runs, H, K, dim, fp8, window, sinks, room):
+    """Decoding sequences beside chunks, with and without limits far above what the batch brings."""
+    cached, new = zip(*runs)
+    layer = Layer([c + n for c, n in runs], H, K, dim, fp8, seed=len(runs) + dim)
+    pos, starts = _runs(cached, new)
+    some = {t for b in range(len(new)) for t in (starts[b], starts[b + 1] - 1, (starts[b] + starts[b + 1]) // 2)
+            if starts[b] <= t < starts[b + 1] and (len(new) < 100 or b % 61 == 0 or b % 29 == 0)}
+    _attend(layer, pos, starts, window, sinks, max_new=max(new) + room, pad=3, tokens=some)
+
+
+@pytest.mark.parametrize("B", [41, 601])
+@pytest.mark.parametrize("dim", [64, 192])
+def test_sequences_that_share_tokens_are_reported(B, dim):
+    """Every other sequence claims all tokens: more rows than the call has."""
+    layer = Layer((100,) * B, 8, 2, dim, False, seed=2)
+    op = _dense().DenseAttention(layer.cache, 8, 100, 100)
+    q = layer.query(100)
+    buf = torch.full((300, 8, dim), 7.0, device=DEV, dtype=torch.bfloat16)
+    op.run(q, buf[100:200], torch.arange(100, dtype=torch.int32, device=DEV), torch.tensor(([0, 100] * B)[:B + 1], dtype=torch.int32, device=DEV))
+    torch.cuda.synchronize()
+    assert int(op.status.item()) & 2
+    assert (buf[:100] == 7.0).all() and (buf[200:] == 7.0).all()
+
+
+@pytest.mark.parametrize("cached,new,H,K,dim,fp8", [((9000, 100), (700, 500), 8, 2, 128, False), ((9000, 100), (700, 500), 8, 2, 128, True),
+                                                    ((0, 0, 5000), (3000, 1, 64), 4, 1, 64, False), ((20000,), (90,), 8, 2, 64, True),
+                                                    ((0,), (6000,), 8, 8, 128, False), ((3000,), (1000,), 4, 2, 192, True)])
+def test_long_chunks(cached, new, H, K, dim, fp8):
+    """Many steps per CTA, units over several CTAs, ranges over several units; every row against fp64."""
+    D = _dense()
+    g = torch.Generator(device=DEV).manual_seed(H + dim)
+    lengths = [c + n for c, n in zip(cached, new)]
+    held = [-(-n // 256) for n in lengths]
+    ids = torch.randperm(sum(held) + 2, generator=g, device=DEV).to(torch.int32)
+    table = torch.full((len(lengths), max(held)), -1, dtype=torch.int32, device=DEV)
+    for b, n in enumerate(held):
+        table[b, :n] = ids[sum(held[:b]):sum(held[:b]) + n]
+    body = 2 * K * 256 * dim
+    x = torch.randn((len(ids), body), generator=g, device=DEV)
+    if fp8:
+        sc = (torch.rand((len(ids), 2 * K * 256), generator=g, device=DEV) + 0.5) / 100
+        pool = torch.cat([(x * 100).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8), sc.view(torch.uint8)], 1)
+    else:
+        pool = x.to(torch.bfloat16).view(torch.uint8)
+    pos, starts = _runs(cached, new)
+    T = starts[-1]
+    q = torch.randn((T, H, dim), generator=g, device=DEV).mul_(2).to(torch.bfloat16)
+    out, lse = torch.empty_like(q), torch.empty((T, H), device=DEV)
+    op = D.DenseAttention(D.DenseCache(pool, table, K, dim, D.KV_FP8_TOKEN if fp8 else D.KV_BF16), H, T, max(new))
+    args = (torch.tensor(pos, dtype=torch.int32, device=DEV), torch.tensor(starts, dtype=torch.int32, device=DEV))
+    op.run(q, out, *args, lse)
+    torch.cuda.synchronize()
+    assert int(op.status.item()) == 0
+    G = H // K
+    for b, n in enumerate(lengths):
+        s, m = slice(starts[b], starts[b + 1]), torch.arange(cached[b], n, device=DEV)
+        for h in range(H):
+            page = table[b, :held[b]].long()
+            if fp8:
+                blk = pool[page]
+                rows = blk[:, :body].contiguous().view(torch.float8_e4m3fn).view(-1, 2, K, 256, dim)[:, :, h // G].double()
+                rows = rows * blk[:, body:body + 8 * K * 256].contiguous().view(torch.float32).view(-1, 2, K, 256, 1)[:, :, h // G].double()
+            else:
+                rows = pool[page][:, :2 * body].contiguous().view(torch.bfloat16).view(-1, 2, K, 256, dim)[:, :, h // G].double()
+            k, v = (rows[:, i].reshape(-1, dim)[:n] for i in (0, 1))
+            qd = q[s, h].double()
+            z = (qd @ k.T / math.sqrt(dim)).masked_fill_(torch.arange(n, device=DEV) > m[:, None], -math.inf)
+            amp = ((qd.abs() @ k.abs().T) / math.sqrt(dim)).amax(-1)
+            pr, l = torch.softmax(z, -1), torch.logsumexp(z, -1)
+            o, av = pr @ v, pr @ v.abs()
+            dz, dn = (dim + 8) * 2.0 ** -24 * amp[:, None], (n + 32) * 2.0 ** -24
+            assert ((out[s, h].double() - o).abs() <= (2.0 ** -8 + 2 * dz + 2 * dn) * av + 2.0 ** -8 * o.abs()).all(), (b, h)
+            assert ((lse[s, h].double() - l).abs() <= dz[:, 0] + dn + 2.0 ** -22 * l.abs() + 2.0 ** -20).all(), (b, h)
+    again, lse2 = torch.empty_like(out), torch.empty_like(lse)      # the same call gives the same bytes, on another stream too
+    op.run(q, again, *args, lse2, stream=torch.cuda.Stream())
+    torch.cuda.synchronize()
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_chunk_missing_blocks_and_nan(fp8):
+    """Chunk form: missing blocks are left out and reported; a NaN query row reaches its own output row alone."""
+    layer = Layer((900, 300), 8, 2, 128, fp8, seed=12, holes=[(0, 1), (0, 2), (1, 0)])
+    pos, starts = _runs((700, 100), (200, 150))
+    op, q, out, lse = _attend(layer, pos, starts, check=False)
+    assert int(op.status.item()) == 1
+    layer.check(q, out, lse, pos, starts, 0, 0, op.args.softmax_scale, tokens=set(range(0, 350, 23)))
+    q2, out2, lse2 = q.clone(), torch.empty_like(out), torch.empty_like(lse)
+    q2[130, 5, 7] = math.nan
+    op.run(q2, out2, torch.tensor(pos, dtype=torch.int32, device=DEV), torch.tensor(starts, dtype=torch.int32, device=DEV), lse2)
+    assert out2[130, 5].isnan().all() and lse2[130, 5].isnan()
+    out2[130, 5], lse2[130, 5] = out[130, 5], lse[130, 5]
+    assert torch.equal(out, out2) and torch.equal(lse, lse2)
+
+
 def test_many_units_take_the_unsplit_form():
     """More (sequence, row group) units than are split evenly: one CTA each."""
     n = 1100
@@ -569,6 +680,63 @@ def test_nan_query_gives_nan():
     op.run(q, out, torch.tensor([299, 89], dtype=torch.int32, device=DEV), torch.arange(3, dtype=torch.int32, device=DEV), lse)
     assert out[0, 3].isnan().all() and lse[0, 3].isnan()
     assert int(out.isnan().sum()) == 64 and int(lse.isnan().sum()) == 1
+
+
+@pytest.mark.parametrize("new", [1, 100])
+def test_huge_windows_and_sinks(new):
+    """Limits near the ends of their type: a window longer than the sequence hides nothing, as many sinks show everything."""
+    layer = Layer((500,), 8, 2, 64, False, seed=31)
+    pos, starts = _runs((500 - new,), (new,))
+    q = layer.query(new)
+    outs = []
+    for window, sinks in ((0, 0), (2 ** 31 - 1, 0), (2 ** 31 - 1, 2 ** 31 - 1), (512, 0), (2 ** 30, 3), (7, 2 ** 31 - 1), (0, 2 ** 31 - 1)):
+        op = _dense().DenseAttention(layer.cache, 8, new, new, window, sinks)
+        out = torch.empty_like(q)
+        op.run(q, out, torch.tensor(pos, dtype=torch.int32, device=DEV), torch.tensor(starts, dtype=torch.int32, device=DEV))
+        assert int(op.status.item()) == 0
+        outs.append(out)
+    for o in outs[:5] + outs[6:]:
+        assert torch.equal(outs[0], o)
+    lse = torch.empty((new, 8), device=DEV)
+    _dense().DenseAttention(layer.cache, 8, new, new, 7, 2 ** 31 - 1).run(q, outs[5], torch.tensor(pos, dtype=torch.int32, device=DEV),
+                                                                       torch.tensor(starts, dtype=torch.int32, device=DEV), lse)
+    layer.check(q, outs[5], lse, pos, starts, 0, 0, 1 / 8, tokens=set(range(0, new, 13)))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_pools_past_four_gigabytes(fp8):
+    """Insert and attention (decode and a chunk) in blocks whose offsets pass 32 bits."""
+    D = _dense()
+    H, K, dim = 32, 32, 128
+    stride = D.block_bytes(K, dim, D.KV_FP8_TOKEN if fp8 else D.KV_BF16)
+    blocks = (5 << 30) // stride
+    pool = torch.empty((blocks, stride), dtype=torch.uint8, device=DEV)
+    high = [blocks - 1, (1 << 32) // stride + 1, blocks - 2, 1]
+    table = torch.tensor([high], dtype=torch.int32, device=DEV)
+    cache = D.DenseCache(pool, table, K, dim, D.KV_FP8_TOKEN if fp8 else D.KV_BF16)
+    n = 4 * 256 - 30
+    g = torch.Generator(device=DEV).manual_seed(3)
+    k, v = (torch.randn((n, K, dim), generator=g, device=DEV).to(torch.bfloat16) for _ in range(2))
+    pos = torch.arange(n, dtype=torch.int32, device=DEV)
+    ins = D.DenseInsert(cache, 0, None)
+    ins.run(None, k, v, None, pos, table[0].long()[(pos // 256).long()] * 256 + pos % 256)
+    for new in (1, 90):
+        q = torch.randn((new, H, dim), generator=g, device=DEV).to(torch.bfloat16)
+        out, lse = torch.empty_like(q), torch.empty((new, H), device=DEV)
+        att = D.DenseAttention(cache, H, new, new)
+        att.run(q, out, pos[n - new:], torch.tensor([0, new], dtype=torch.int32, device=DEV), lse)
+        torch.cuda.synchronize()
+        assert int(att.status.item()) == 0 and int(ins.status.item()) == 0
+        for t in {0, new - 1}:
+            for h in (0, 31):
+                o, l, av, amp = _reference(pool, table, 0, n - new + t, q[t, h:h + 1], K, dim, fp8, h)
+                dz, dn = (dim + 8) * 2.0 ** -24 * amp[:, None], (n + 32) * 2.0 ** -24
+                assert ((out[t, h:h + 1].double() - o).abs() <= (2.0 ** -8 + 2 * dz + 2 * dn) * av + 2.0 ** -8 * o.abs()).all()
+                assert ((lse[t, h:h + 1].double() - l).abs() <= dz[:, 0] + dn + 2.0 ** -22 * l.abs() + 2.0 ** -20).all()
+    rows = (pool[high[1]][:2 * K * 256 * dim * (1 if fp8 else 2)].view(torch.float8_e4m3fn if fp8 else torch.bfloat16)
+            .view(2, K, 256, dim)[0].float())
+    if not fp8:
+        assert torch.equal(rows.transpose(0, 1), k[256:512].float())
 
 
 def test_same_call_same_bytes():
