@@ -1,6 +1,6 @@
 // Attention of chunks over the dense paged cache on the tensor cores
-// (v4a_dense_attn with many query rows per KV head; bf16 caches, dim 64 and
-// 128): tcgen05 kind::f16 with the accumulators in TMEM.
+// (v4a_dense_attn with many query rows per KV head; dim 64 and 128): tcgen05
+// kind::f16 with the accumulators in TMEM.
 //
 // Mathematics: as dense_attn.cu, one pass over the keys with a running
 // maximum and sum per row.  The rows of a CTA are 256 consecutive (token,
@@ -13,7 +13,7 @@
 // same maximum.
 //
 //   S_t = Q_t K^T   M = 128, N = 128 keys, K = dim     TMEM columns [128 t, +128)
-//   P_t = 2^{S f - m} in bf16, over S_t's columns       [128 t, +64)
+//   P_t = 2^{S f - m} in bf16 (fp8: f16), over S_t's columns  [128 t, +64)
 //   O_t += P_t V    M = 128, N = dim, K = 128 keys      [256 + 128 t, +dim)
 //                   (P from TMEM, V as an MN-major operand)
 //
@@ -24,8 +24,16 @@
 // that no row of the CTA sees are filled with zeros, so what they hold cannot
 // reach a product.  Keys and values have two buffers each.
 //
+// P is rounded to bf16: by at most 2^-8 of each weight, so by at most 2^-8
+// sum_j p_j |v_j| in the output, as much as the output's own rounding may be
+// where nothing cancels; the two-operand P of dense_attn.cu would double
+// the second product here, where the tensor cores set the time.
+//
 // Bound: the tensor cores (4 dim flops per visible pair), and beside them the
-// exponentials: 128 x 128 per tile and step.
+// exponentials: 128 x 128 per tile and step.  Measured, 32 + 8 heads of 128,
+// 2048 tokens over 10240 positions: bf16 258 us (1196 TFLOP/s), fp8 495 us (625:
+// the conversions of the codes); dim 64 bf16 212 us (727: the exponentials,
+// twice as many per flop); a window of 1024 with 1500 tokens 62 us.
 #include "dense_attn_common.cuh"
 
 namespace v4a {
@@ -34,22 +42,32 @@ namespace {
 constexpr int kRows = 128;           // rows of a tile (MMA M)
 constexpr int kKeys = 128;           // keys per step
 constexpr int kUnit = 2 * kRows;     // rows of a unit
-// Threads and registers of the two forms.  bf16 rows are copied as they are:
-// three warps (four: 306 us against 258 for 2k tokens over 10k, since the
-// softmax then has fewer registers).  fp8 rows go through the registers of
-// their copying warps, which convert them: seven warps (three: 583 us against
-// 488).  softmax x 256 + rest x (threads - 256) = launch x threads.
+// Threads and registers of the two forms (2k tokens over 10k, 32 + 8 heads of
+// 128).  bf16 rows are copied as they are: three warps and 200 registers for
+// the softmax, 258 us; four warps among 512 threads, whose softmax has 192, 314
+// us.  fp8 rows go through the registers of their copying warps, which convert
+// them: four warps and 184 + 72 registers, 495 us (192 + 64: 545; seven warps:
+// 546; three among 384 threads: 587).  The registers of a thread at launch come
+// in steps that four warps share, so 512 threads carry three warps that only
+// wait.  softmax x 256 + rest x (threads - 256) = launch x threads.
 template <bool kFp8>
 struct Roles {
   static constexpr int kThreads = kFp8 ? 512 : 384;
-  static constexpr int kLoaders = kThreads - 9 * 32;
-  static constexpr int kSoftmaxRegs = kFp8 ? 192 : 200, kRestRegs = kFp8 ? 64 : 104, kLaunchRegs = kFp8 ? 128 : 168;
+  static constexpr int kLoaders = kFp8 ? 128 : 96;
+  static constexpr int kSoftmaxRegs = kFp8 ? 184 : 200, kRestRegs = kFp8 ? 72 : 104, kLaunchRegs = kFp8 ? 128 : 168;
   static_assert(kSoftmaxRegs * 256 + kRestRegs * (kThreads - 256) == kLaunchRegs * kThreads, "the split of the registers");
 };
 constexpr int kUnitCost = 3;         // steps that a unit's set-up and output take the time of
 constexpr int kMinSteps = 4;         // steps a CTA of an even split has at least
-constexpr float kRaise = 8.f;        // log2 units by which logits may pass the maximum in use
-constexpr float kRaiseFp8 = 4.f, kShiftFp8 = 11.f;   // f16 P: 2^11 2^{w - m} <= 2^15
+// Log2 units by which logits may pass the maximum in use before it is raised:
+// with 0 the accumulator is rescaled whenever a maximum grows (269 us instead
+// of 258; mean relative error 0.0020 instead of 0.0024, since the largest
+// weight is then exactly one).  The bound is the same half step of each weight:
+// a float's relative step does not depend on its size.
+constexpr float kRaise = 8.f;
+// f16 P has 2^-14 as its smallest normal value, so it is held at 2^11 2^{w - m}
+// <= 2^15: weights down to 2^-25 of the largest are rounded to 11 bits.
+constexpr float kRaiseFp8 = 4.f, kShiftFp8 = 11.f;
 
 struct PreSmem {
   uint64_t q_full[2], k_full[2], v_full[2], k_free[2], v_free[2], s_full[2], p_full[2][2], o_full[2], drain;
@@ -379,7 +397,7 @@ __global__ void __launch_bounds__(Roles<kFp8>::kThreads, 1) dense_prefill_kernel
     }
   } else if (warp == 8) {
     // ---- the MMA issuer: tile 0's products, then tile 1's, so that one tile's run while the other is
-    // in its softmax (with an issuer per tile the two ran in step: 4100 against 3100 clocks a step) ----
+    // in its softmax (with an issuer per tile the two ran in step: 4100 clocks a step instead of 3760) ----
     if (lane == 0) {
       const uint32_t idesc_s = tc::make_idesc(1, 1, kRows, kKeys);
       const uint32_t idesc_o = tc::make_idesc(kFp8 ? 0 : 1, kFp8 ? 0 : 1, kRows, D) | (1u << 16);       // f16 or bf16; B is MN-major
@@ -446,7 +464,7 @@ __global__ void __launch_bounds__(Roles<kFp8>::kThreads, 1) dense_prefill_kernel
       }
     }
     __syncwarp();
-  } else {
+  } else if (tid < 9 * 32 + kLoaders) {
     // ---- the copying warps: each step's keys, then its values, as soon as a buffer is free; a
     // buffer's barrier completes when every thread's copies into it have landed ----
     const int lt = tid - 9 * 32;
@@ -477,40 +495,38 @@ __global__ void __launch_bounds__(Roles<kFp8>::kThreads, 1) dense_prefill_kernel
         const int at = page < 0 ? 0 : pc.hk * kBlockPositions + j0 % kBlockPositions;       // first row of the step
         if constexpr (kFp8) {
           // codes are loaded ahead of their buffer, converted and stored into it; the step's scales with its keys
-          constexpr int kChunks = kKeys * (D / 16), kPasses = (kChunks + kLoaders - 1) / kLoaders;
-          const float* row_scale = reinterpret_cast<const float*>(block + int64_t(2 * a.K) * kBlockPositions * D) + at;
-#pragma unroll
-          for (int c0 = 0; c0 < kKeys; c0 += kLoaders) {
-            const int c = c0 + lt;
-            if (c < kKeys) {
-              const bool live = c <= hi && (c > lo || c < sk);
-              const float ks = live ? row_scale[c] : 0.f, vs = live ? row_scale[a.K * kBlockPositions + c] : 1.f;
-              const float l = vs > 0x1p-100f ? log2f(vs) : vs <= 0x1p-100f ? -100.f : vs;
-              s.scales[n & 3][0][c] = ks * a.scale_log2;
-              s.scales[n & 3][1][c] = l;
-              s.scales[n & 3][2][c] = exp2f(-l);
-            }
+          // (a thread has one chunk of every kStep-th row, at the same place of the swizzle)
+          constexpr int kPerRow = D / 16, kStep = kLoaders / kPerRow, kPasses = kKeys / kStep;
+          static_assert(kStep % 8 == 0 && kLoaders % kPerRow == 0 && kKeys % kStep == 0 && kLoaders >= kKeys, "rows per pass");
+          const int r0 = lt / kPerRow, ch = lt % kPerRow;
+          if (lt < kKeys) {
+            const float* row_scale = reinterpret_cast<const float*>(block + int64_t(2 * a.K) * kBlockPositions * D) + at + lt;
+            const bool live = lt <= hi && (lt > lo || lt < sk);
+            const float ks = live ? row_scale[0] : 0.f, vs = live ? row_scale[a.K * kBlockPositions] : 1.f;
+            const float l = vs > 0x1p-100f ? log2f(vs) : vs <= 0x1p-100f ? -100.f : vs;
+            float* const sc = &s.scales[n & 3][0][lt];
+            sc[0] = ks * a.scale_log2;
+            sc[kKeys] = l;
+            sc[2 * kKeys] = exp2f(-l);
           }
 #pragma unroll 1
           for (int half = 0; half < 2; ++half) {
-            const uint8_t* src = block + (int64_t(half * a.K) * kBlockPositions + at) * D;
+            const uint8_t* src = block + (int64_t(half * a.K) * kBlockPositions + at) * D + lt * 16;
             uint4 raw[kPasses];
 #pragma unroll
             for (int k = 0; k < kPasses; ++k) {
-              const int c = lt + k * kLoaders, r = c / (D / 16);
+              const int r = r0 + k * kStep;
               raw[k] = make_uint4(0, 0, 0, 0);
-              if (c < kChunks && r <= hi && (r > lo || r < sk)) raw[k] = __ldg(reinterpret_cast<const uint4*>(src + c * 16));
+              if (r <= hi && (r > lo || r < sk)) raw[k] = __ldg(reinterpret_cast<const uint4*>(src + k * (kStep * D)));
             }
             ok = wait_for(half ? &s.v_free[n & 1] : &s.k_free[n & 1], ((n >> 1) & 1) ^ 1, a.status, abort_flag);
             if (!ok) break;
             const uint32_t dst = (half ? v0 : k0) + (n & 1) * kTileBytes;
+            const uint32_t even = dst + chunk_at(r0, 2 * ch), odd = dst + chunk_at(r0, 2 * ch + 1);
 #pragma unroll
             for (int k = 0; k < kPasses; ++k) {
-              const int c = lt + k * kLoaders, r = c / (D / 16), ch = 2 * (c % (D / 16));
-              if (c < kChunks) {
-                st_shared16(dst + chunk_at(r, ch), half ? f16_of(raw[k].x) : bf16_of(raw[k].x), half ? f16_of(raw[k].y) : bf16_of(raw[k].y));
-                st_shared16(dst + chunk_at(r, ch + 1), half ? f16_of(raw[k].z) : bf16_of(raw[k].z), half ? f16_of(raw[k].w) : bf16_of(raw[k].w));
-              }
+              st_shared16(even + k * (kStep * 128), half ? f16_of(raw[k].x) : bf16_of(raw[k].x), half ? f16_of(raw[k].y) : bf16_of(raw[k].y));
+              st_shared16(odd + k * (kStep * 128), half ? f16_of(raw[k].z) : bf16_of(raw[k].z), half ? f16_of(raw[k].w) : bf16_of(raw[k].w));
             }
             tc::fence_proxy_async();
             tc::mbar_arrive(half ? &s.v_full[n & 1] : &s.k_full[n & 1]);
