@@ -26,13 +26,21 @@
 // leaves a (sequence, KV head, row group): each leaves o in the stage that it
 // has just read.  Pieces of a unit that several CTAs hold go to the workspace
 // and are joined by a second kernel in CTA order.
+//
+// bf16 caches: P is taken as the sum of two bf16 operands (16 bits), since the
+// tensor cores have the time; fp8 caches: P in f16, with the values' scales in
+// its exponent.  Measured with 32 + 8 heads of 128: 8 sequences at 8k 48 us
+// (268 MB: 5.6 TB/s), a call of 6.6 GB 6.9 TB/s, one sequence at 1000
+// positions 10.2 us (the two launches and the loads one after the other).
 #include "dense_attn_common.cuh"
 
 namespace v4a {
 namespace {
 
 constexpr int kRingBytes = 192 * 1024;
-constexpr int kUnitCost = 16;        // tiles that a unit's set-up and merge take the time of
+// Tiles that a unit's set-up and merge take the time of (200 sequences of 1 to
+// 600: 0 tiles 76 us, 16 54, 48 57; one of 30000 among 60 of 100: 46, 34, 38).
+constexpr int kUnitCost = 16;
 
 template <int D, int NT, bool kFp8>
 struct Shape {

@@ -17,6 +17,9 @@
 // and the fp8 row maximum are shuffles inside the row's lanes.  A CTA takes one
 // token (or part of its rows when tokens are few): its angles are computed once
 // and shared by all its heads, and all its loads are issued before the first use.
+// Measured, 64 + 8 + 8 heads of 128: 16384 tokens, bf16 120 us (671 MB: 5.6
+// TB/s of the 6.8 that a copy reaches), fp8 143 us (the row maxima and the
+// codes); one token 2.1 us.
 #include "tc_common.cuh"
 #include "v4a_dense.h"
 #include "v4a_dense_internal.h"
@@ -25,7 +28,7 @@ namespace v4a {
 namespace {
 
 constexpr int kThreads = 128;     // eight CTAs an SM: 121 us for 16384 tokens of 64 + 8 + 8 heads; four of 256 threads took 124
-constexpr int kPasses = 5;        // rows per lane group held in registers (16 bytes a lane each)
+constexpr int kPasses = 5;        // rows per lane group held in registers (16 bytes a lane each; 3: 142 us, 10: 147 us)
 
 struct InsertDev {
   uint64_t turn[128];             // F_j: turns per position as a 64-bit fraction
@@ -263,7 +266,8 @@ int dense_insert(const v4a_dense_insert_args* a, cudaStream_t stream) {
   d.status = a->status;
   const int lanes = D == 64 ? 8 : D == 128 ? 16 : 32;
   const int rows = kThreads / lanes, need = (d.NR + rows - 1) / rows;
-  // few tokens: one pass per CTA, so that a token's rows spread over more SMs
+  // few tokens: one pass per CTA, so that a token's rows spread over more SMs (64 + 8 + 8 heads of 128: 4 tokens
+  // 2.2 us, five passes a CTA 3.4; 128 tokens 3.7 and 4.1; 256 tokens 5.2 and 5.4; 512 tokens 8.5 and 5.7)
   int y = (need + kPasses - 1) / kPasses;
   if (int64_t(a->num_tokens) * y < 2 * 152) y = need;
   d.passes = (need + y - 1) / y;

@@ -12,6 +12,11 @@
 // One CTA forms the sums (they are the only serial part).  Small steps are
 // filled by the same CTA; larger ones by a second, wide kernel that starts
 // while the first drains (programmatic dependent launch).
+//
+// Bound: latency.  The output of the largest steps is under a megabyte (4
+// sequences x 1024 tokens x 60 tables: 2 MB, 0.3 us of the memory's rate), and
+// the two launches, the loads and the scan one after the other take 5.5 us on
+// the device whatever the size; 64 decoding sequences with one table 3.4 us.
 #include "tc_common.cuh"
 #include "v4a_dense.h"
 #include "v4a_dense_internal.h"
@@ -24,8 +29,9 @@ constexpr int kFillThreads = 256;
 constexpr int kTablesPerItem = 4;     // tables one thread writes for its token
 constexpr int kMaxSeqs = 8192;
 // Steps of at most this many (token, table group) items are filled by the
-// scanning CTA.
-constexpr int64_t kInlineItems = 4096;
+// scanning CTA: a second launch costs more than they take (64 items: 3.4 us
+// inline, 4.6 wide; 960: 5.9 and 5.3; 2048: 6.5 and 5.5; 4096: 10.1 and 5.5).
+constexpr int64_t kInlineItems = 512;
 
 struct PlanHeader {                   // in the workspace, before the sums
   int32_t ok, tokens, fresh_blocks, back_blocks, first, count, pad[2];

@@ -57,7 +57,9 @@ struct Roles {
   static constexpr int kSoftmaxRegs = kFp8 ? 184 : 200, kRestRegs = kFp8 ? 72 : 104, kLaunchRegs = kFp8 ? 128 : 168;
   static_assert(kSoftmaxRegs * 256 + kRestRegs * (kThreads - 256) == kLaunchRegs * kThreads, "the split of the registers");
 };
-constexpr int kUnitCost = 3;         // steps that a unit's set-up and output take the time of
+// Steps that a unit's set-up and output take the time of (one chunk of 4096
+// tokens, 32 + 8 heads: 0 steps 320 us, 1 223, 3 147, 6 151, 12 163).
+constexpr int kUnitCost = 3;
 constexpr int kMinSteps = 4;         // steps a CTA of an even split has at least
 // Log2 units by which logits may pass the maximum in use before it is raised:
 // with 0 the accumulator is rescaled whenever a maximum grows (269 us instead

@@ -18,7 +18,8 @@
  * workspaces, no allocation, no synchronisation, the given stream only; a
  * nonzero return code launched nothing (except V4A_ERR_CUDA); problems only
  * the device can see set V4A_DEV_* bits in *status and skip the access.
- * Each call can be captured into a CUDA graph; two calls that may run at the
+ * Each call can be captured into a CUDA graph (a shape's first call on a
+ * device may load its kernels: make it before the capture); two calls that may run at the
  * same time need workspaces of their own.  A sequence's compressed layers and
  * dense layers can use one page allocator (v4a_pages.h): a dense cache is a
  * V4A_PAGES_BLOCK kind of v4a_dense_block_bytes bytes.
@@ -67,7 +68,8 @@ extern "C" {
  * too few pages (V4A_DEV_OUT_OF_PAGES), then every token is -1, token_starts
  * is 0 throughout, free_out = free_in and no table or ring entry changes, so
  * the step's other calls do nothing.  A page id outside [0, num_blocks) sets
- * V4A_DEV_BAD_BLOCK and gives the slot -1.
+ * V4A_DEV_BAD_BLOCK and gives the slot -1; it goes into the table, and back
+ * behind the free pages when its sequence ends, as it is.
  */
 typedef struct {
   int32_t num_seqs;            /* B: 0..8192 */
@@ -207,9 +209,18 @@ V4A_API int v4a_dense_insert(const v4a_dense_insert_args* args, void* stream);
  * behind the last sequence.  Cache rows that no query of the call sees do not
  * reach the outputs whatever they hold; a NaN or infinity in a row that one
  * query sees may reach the same sequence's other queries of the same call.
- * Dot products and sums are fp32; the probabilities are rounded to bf16 (bf16
- * caches) or f16 (fp8 caches) as an operand of the tensor cores.  fp8 value
- * scales below 2^-100 are read as 2^-100.
+ * Dot products and sums are fp32; the probabilities are rounded as an operand
+ * of the tensor cores: to f16 for fp8 caches, to 16 bits for bf16 caches, and
+ * to bf16 for the sequences of a bf16 cache of dim 64 or 128 that bring more
+ * than 32 rows (tokens x heads per KV head).  fp8 value scales below 2^-100
+ * are read as 2^-100.  Sequences that share tokens (entries not increasing)
+ * set V4A_DEV_BAD_BATCH once they are more than the call has room for, and
+ * what their rows hold then is not defined.
+ *
+ * A batch may mix decoding sequences and chunks; a call where every sequence
+ * brings max_new_per_seq tokens (num_tokens = num_seqs * max_new_per_seq)
+ * saves the launches for the other kind.  V4A_ERR_UNSUPPORTED: max_new_per_seq
+ * * num_heads / num_kv_heads of 2^30 rows or more.
  */
 typedef struct {
   int32_t num_tokens;          /* T >= 0: rows of q and out */
@@ -220,7 +231,7 @@ typedef struct {
   v4a_dense_cache kv;
   int32_t num_heads;           /* a multiple of kv.num_kv_heads, <= 1024 */
   const uint16_t* q;           /* [T][H][dim] bf16, 16-byte aligned */
-  float softmax_scale;         /* > 0 */
+  float softmax_scale;         /* > 0, and finite times log2(e) */
   int32_t window;              /* 0 = every earlier position; else >= 1 */
   int32_t sinks;               /* first positions that stay visible (>= 0; no effect without a window) */
   uint16_t* out;               /* [T][H][dim] bf16, 16-byte aligned; not q */
