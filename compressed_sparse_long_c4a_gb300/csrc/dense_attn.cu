@@ -578,7 +578,7 @@ __global__ void __launch_bounds__(256) dense_join_kernel(const DenseAttnDev a, c
   if (l == 0 && a.lse) a.lse[at] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
 }
 
-// The same for units of 256 rows (dense_prefill.cu), whose pieces are few and
+// The same for units of 128 or 256 rows (dense_prefill*.cu), whose pieces are few and
 // lie as [slot][dim / 4][row][4]: a thread takes a row's 16 dims (grid.y =
 // dim / 16) through the pieces in order.
 template <int D>
@@ -589,7 +589,7 @@ __global__ void __launch_bounds__(256) dense_join_rows(const DenseAttnDev a, con
   const JoinDesc j = p.join[c];
   if (r >= j.rows) return;
   auto slot = [&](int k) { return int64_t(c + k) * 2 + (k == 0 ? 1 : 0); };
-  auto ml = [&](int k) { return *reinterpret_cast<const float2*>(p.part_ml + (slot(k) * 256 + r) * 2); };
+  auto ml = [&](int k) { return *reinterpret_cast<const float2*>(p.part_ml + (slot(k) * p.rows + r) * 2); };
   const int pieces = j.last - c + 1;
   float top = -INFINITY, sum = 0.f;
 #pragma unroll 4
@@ -602,7 +602,7 @@ __global__ void __launch_bounds__(256) dense_join_rows(const DenseAttnDev a, con
     const float2 t = ml(k);
     float4 o[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] = reinterpret_cast<const float4*>(p.part_o)[(slot(k) * (D / 4) + d0 + i) * 256 + r];
+    for (int i = 0; i < 4; ++i) o[i] = reinterpret_cast<const float4*>(p.part_o)[(slot(k) * (D / 4) + d0 + i) * p.rows + r];
     if (t.x == -INFINITY) continue;
     const float w = exp2f(t.x - top);
     sum = fmaf(w, t.y, sum);
@@ -634,7 +634,7 @@ bool mixed(const v4a_dense_attn_args* a) {
 // The most rows a sequence brings to the form for few rows.
 int64_t most_rows(const v4a_dense_attn_args* a) {
   const int64_t rows = int64_t(a->max_new_per_seq) * (a->num_heads / a->kv.num_kv_heads);
-  return dense_prefill_takes(a) ? few_rows(a->kv.format != V4A_KV_BF16) : rows;
+  return dense_prefill_takes(a) ? few_rows(a->kv.dim, a->kv.format != V4A_KV_BF16) : rows;
 }
 
 int rows_of(const v4a_dense_attn_args* a) {
@@ -695,10 +695,10 @@ int check_shape(const v4a_dense_attn_args* a) {
 
 int dense_join(const DenseAttnDev& a, const SplitDev& p, int dim, cudaStream_t stream) {
   const bool many = p.rows > 16;
-  auto kern = many ? (dim == 64 ? dense_join_rows<64> : dense_join_rows<128>)
+  auto kern = many ? (dim == 64 ? dense_join_rows<64> : dim == 128 ? dense_join_rows<128> : dim == 192 ? dense_join_rows<192> : dense_join_rows<256>)
                    : (dim == 64 ? dense_join_kernel<64> : dim == 128 ? dense_join_kernel<128> : dim == 192 ? dense_join_kernel<192> : dense_join_kernel<256>);
   const int y = many ? dim / 16 : int(std::min<int64_t>(p.rows, std::min<int64_t>(int64_t(a.max_new) * a.G, p.rows_to)));   // rows that a unit can have
-  const cudaError_t e = launch_pdl(kern, dim3(unsigned(p.grid), unsigned(y)), dim3(256), 0, stream, a, p);
+  const cudaError_t e = launch_pdl(kern, dim3(unsigned(p.grid), unsigned(y)), dim3(many ? p.rows : 256), 0, stream, a, p);
   return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? V4A_OK : V4A_ERR_CUDA;
 }
 
@@ -730,7 +730,7 @@ int dense_attn(const v4a_dense_attn_args* a, void* ws, size_t ws_bytes, cudaStre
   p.rows_to = INT32_MAX;
   if (dense_prefill_takes(a)) {
     const bool both = mixed(a);
-    const int few = few_rows(a->kv.format != V4A_KV_BF16);
+    const int few = few_rows(a->kv.dim, a->kv.format != V4A_KV_BF16);
     rc = dense_prefill(a, d, both ? few + 1 : 0, static_cast<uint8_t*>(ws) + few_workspace(a), stream);
     if (rc || !both) return rc;
     p.rows_to = few;

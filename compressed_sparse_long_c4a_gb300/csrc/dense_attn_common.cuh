@@ -23,12 +23,15 @@ struct DenseAttnDev {
 };
 
 // Sequences of at most this many rows (tokens x heads of a group) go to the
-// form for few rows, which reads the cache once per 16 rows; the form for many
-// reads it once but converts fp8 codes on the way.  Few / many, 32 + 8 heads
+// form for few rows, which reads the cache once per 16 rows (8 of dim 256), so
+// up to twice for bf16 and four times for fp8; the form for many reads it once
+// but converts fp8 codes on the way.  Few / many, 32 + 8 heads
 // of 128, us: bf16, 8 sequences at 8k: 32 rows 69 / 62, 64 rows 123 / 64; one
 // at 8k: 32 rows 22 / 32, 64 rows 28 / 32; 16 at 1k (dim 64): 24 / 26 and
-// 35 / 26; fp8, 8 at 8k: 32 rows 63 / 130, 64 rows 111 / 131, 128 rows 203 / 132.
-constexpr int few_rows(bool fp8) { return fp8 ? 64 : 32; }
+// 35 / 26; fp8, 8 at 8k: 32 rows 63 / 130, 64 rows 111 / 131, 128 rows 203 / 132;
+// dim 256, 8 at 8k: bf16 16 rows 163 / 107, 32 rows 311 / 107, one at 8k 16 rows
+// 24 / 33; fp8 32 rows 186 / 187, 64 rows 355 / 186.
+constexpr int few_rows(int dim, bool fp8) { return (dim == 256 ? 8 : 16) * (fp8 ? 4 : 2); }
 
 // One sequence's tokens of the call: first row, count and first position;
 // n = 0 when there are none, the entries are inconsistent (reported) or the

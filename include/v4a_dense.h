@@ -211,8 +211,8 @@ V4A_API int v4a_dense_insert(const v4a_dense_insert_args* args, void* stream);
  * query sees may reach the same sequence's other queries of the same call.
  * Dot products and sums are fp32; the probabilities are rounded as an operand
  * of the tensor cores: to f16 for fp8 caches, to 16 bits for bf16 caches, and
- * to bf16 for the sequences of a bf16 cache of dim 64 or 128 that bring more
- * than 32 rows (tokens x heads per KV head).  fp8 value scales below 2^-100
+ * to bf16 for the sequences of a bf16 cache that bring more than 32 rows
+ * (tokens x heads per KV head; 16 of dim 256).  fp8 value scales below 2^-100
  * are read as 2^-100.  Sequences that share tokens (entries not increasing)
  * set V4A_DEV_BAD_BATCH once they are more than the call has room for, and
  * what their rows hold then is not defined.

@@ -498,6 +498,8 @@ MIXED = [
     ([(i % 90, 1 + 40 * (i % 61 == 0)) for i in range(700)], 2, 1, 64, False, 0, 0, 0),   # more sequences than are split evenly
     ([(i % 90, 40 * (i % 61 == 0) + (i % 3 > 0)) for i in range(700)], 2, 1, 64, True, 20, 2, 0),
     ([(i % 50, 1 + i % 120) for i in range(40)], 8, 1, 192, False, 0, 0, 0),
+    ([(600, 150), (0, 1), (0, 300), (90, 40)], 8, 2, 256, True, 100, 5, 0),
+    ([(600, 150), (0, 9), (0, 300), (90, 5)], 4, 2, 192, False, 64, 70, 100),
     ([(i % 50, 1 + 30 * (i % 5 == 0)) for i in range(600)], 2, 1, 256, False, 0, 0, 0),
 ]
 
@@ -529,7 +531,9 @@ def test_sequences_that_share_tokens_are_reported(B, dim):
 
 @pytest.mark.parametrize("cached,new,H,K,dim,fp8", [((9000, 100), (700, 500), 8, 2, 128, False), ((9000, 100), (700, 500), 8, 2, 128, True),
                                                     ((0, 0, 5000), (3000, 1, 64), 4, 1, 64, False), ((20000,), (90,), 8, 2, 64, True),
-                                                    ((0,), (6000,), 8, 8, 128, False), ((3000,), (1000,), 4, 2, 192, True)])
+                                                    ((0,), (6000,), 8, 8, 128, False), ((3000,), (1000,), 4, 2, 192, True),
+                                                    ((7000, 300), (900, 257), 4, 2, 256, False), ((5000, 0, 20), (600, 200, 1), 8, 2, 256, True),
+                                                    ((100,), (2500,), 3, 1, 192, False)])
 def test_long_chunks(cached, new, H, K, dim, fp8):
     """Many steps per CTA, units over several CTAs, ranges over several units; every row against fp64."""
     D = _dense()
