@@ -116,9 +116,12 @@ __global__ void __launch_bounds__(Shape<D, NT, kFp8>::kThreads, Shape<D, NT, kFp
   extern __shared__ __align__(128) uint8_t smem[];
   typename S::Tail& s = *reinterpret_cast<typename S::Tail*>(smem + kWarps * S::kStages * S::kStage);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  pdl_wait();
+  if (!p.late) pdl_wait();
   Line<R, kKeys, kThreads> line(a, p, &s + 1);
-  if (!line.init(s.scan, smem, kWarps)) return;          // a tile per warp at least
+  if (!line.init(s.scan, smem, kWarps)) {                // a tile per warp at least
+    if (p.late) pdl_wait();
+    return;
+  }
   const int64_t x0 = line.x0, x1 = line.x1;
 
   // ---- this warp's stream: tiles x0 + warp + j kWarps, j = 0, 1, ... ----
@@ -518,6 +521,7 @@ __global__ void __launch_bounds__(Shape<D, NT, kFp8>::kThreads, Shape<D, NT, kFp
     x += count;
   }
   if (p.split && tid == 0) p.join[blockIdx.x] = desc;
+  if (p.late) pdl_wait();
 }
 
 // Joins the pieces of a unit that several CTAs hold: piece c's slot 1, then
@@ -626,7 +630,9 @@ __global__ void __launch_bounds__(256) dense_join_rows(const DenseAttnDev a, con
 // A call whose sequences all bring many rows runs dense_prefill.cu's form, one
 // whose sequences all bring few rows this file's, and a mixed one both, each
 // launch taking its sequences: it is mixed when the token count leaves room
-// for short sequences beside the longest.
+// for short sequences beside the longest.  256 decoding sequences beside a
+// chunk of 4096 (32 + 8 heads of 128): 304 us, 147 and 147 alone; the launches
+// for short sequences that are not there cost two chunks of 1024 8 us of 54.
 bool mixed(const v4a_dense_attn_args* a) {
   return dense_prefill_takes(a) && a->num_tokens < int64_t(a->num_seqs) * a->max_new_per_seq;
 }
@@ -663,8 +669,7 @@ int launch(const DenseAttnDev& a, const SplitDev& p, cudaStream_t stream) {
   const int64_t grid = p.split ? p.grid : int64_t(p.U) * a.K;
   if (grid > INT32_MAX) return V4A_ERR_UNSUPPORTED;
   const cudaError_t e = launch_pdl(kern, dim3(unsigned(grid)), dim3(S::kThreads), smem, stream, a, p);
-  if (e != cudaSuccess || cudaGetLastError() != cudaSuccess) return V4A_ERR_CUDA;
-  return p.split ? dense_join(a, p, D, stream) : V4A_OK;
+  return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? V4A_OK : V4A_ERR_CUDA;
 }
 
 template <bool kFp8>
@@ -726,14 +731,16 @@ int dense_attn(const v4a_dense_attn_args* a, void* ws, size_t ws_bytes, cudaStre
   d.pool = static_cast<const uint8_t*>(a->kv.pool);
   d.q = a->q; d.out = a->out; d.lse = a->lse; d.status = a->status;
   d.scale_log2 = a->softmax_scale * 1.4426950408889634f;
-  SplitDev p{};
+  SplitDev p{}, many{};
   p.rows_to = INT32_MAX;
   if (dense_prefill_takes(a)) {
     const bool both = mixed(a);
     const int few = few_rows(a->kv.dim, a->kv.format != V4A_KV_BF16);
-    rc = dense_prefill(a, d, both ? few + 1 : 0, static_cast<uint8_t*>(ws) + few_workspace(a), stream);
-    if (rc || !both) return rc;
+    rc = dense_prefill(a, d, both ? few + 1 : 0, static_cast<uint8_t*>(ws) + few_workspace(a), &many, stream);
+    if (rc) return rc;
+    if (!both) return many.split ? dense_join(d, many, a->kv.dim, stream) : V4A_OK;
     p.rows_to = few;
+    p.late = many.U > 0;
   }
   p.RG = int(row_groups(a));
   const int64_t units = units_bound(d, p.rows_from, p.RG, rows_of(a));
@@ -745,7 +752,9 @@ int dense_attn(const v4a_dense_attn_args* a, void* ws, size_t ws_bytes, cudaStre
   // sequence among short ones would run alone).
   p.split = std::max(p.U, d.B) <= kMaxSplitUnits && (d.window == 0 || int64_t(p.U) * d.K < 256);
   split_carve(&p, ws, rows_of(a), a->kv.dim, ctas_of(a), kUnitCost);
-  return a->kv.format == V4A_KV_FP8_TOKEN ? launch_dim<true>(d, p, a->kv.dim, stream) : launch_dim<false>(d, p, a->kv.dim, stream);
+  rc = a->kv.format == V4A_KV_FP8_TOKEN ? launch_dim<true>(d, p, a->kv.dim, stream) : launch_dim<false>(d, p, a->kv.dim, stream);
+  if (rc == V4A_OK && many.split && many.U > 0) rc = dense_join(d, many, a->kv.dim, stream);
+  return rc == V4A_OK && p.split ? dense_join(d, p, a->kv.dim, stream) : rc;
 }
 
 }  // namespace v4a

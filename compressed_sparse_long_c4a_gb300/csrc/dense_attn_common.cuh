@@ -121,6 +121,9 @@ struct SplitDev {
   struct JoinDesc* join;          // [CTA]
   float *part_o, *part_ml;        // [CTA][2][R][dim], [CTA][2][R][2] (maximum in log2 units, sum)
   int rows_from, rows_to;         // the launch takes sequences of this many rows (tokens x group)
+  // A call's two launches need nothing of each other: the first lets the second
+  // start as its CTAs leave (early), which waits for it at its end (late).
+  int early, late;
 };
 
 // A unit that starts in a CTA's range and goes on in the next CTAs' up to `last`:
@@ -331,9 +334,10 @@ struct Line {
 // Joins the pieces of every split unit (dense_attn.cu).
 int dense_join(const DenseAttnDev& a, const SplitDev& p, int dim, cudaStream_t stream);
 
-// The tensor-core form for many rows (dense_prefill.cu): whether it takes the shape, and its launch.
+// The tensor-core form for many rows (dense_prefill.cu): whether it takes the
+// shape, and its launch, which leaves in *p what is to be joined (p->split).
 bool dense_prefill_takes(const v4a_dense_attn_args* a);
 size_t dense_prefill_workspace(const v4a_dense_attn_args* a);
-int dense_prefill(const v4a_dense_attn_args* a, const DenseAttnDev& d, int rows_from, void* ws, cudaStream_t stream);
+int dense_prefill(const v4a_dense_attn_args* a, const DenseAttnDev& d, int rows_from, void* ws, SplitDev* p, cudaStream_t stream);
 
 }  // namespace v4a

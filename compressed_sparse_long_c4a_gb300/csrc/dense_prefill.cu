@@ -89,6 +89,7 @@ __global__ void __launch_bounds__(Roles<kFp8>::kThreads, 1) dense_prefill_kernel
   volatile int* abort_flag = &s.abort_flag;
 
   pdl_wait();
+  if (p.early) pdl_trigger();
   Line<kUnit, kKeys, kThreads> line(a, p, &s + 1);
   if (!line.init(s.scan, base, kMinSteps)) return;
   const int64_t x0 = line.x0, x1 = line.x1;
@@ -465,8 +466,7 @@ int launch(const DenseAttnDev& d, const SplitDev& p, cudaStream_t stream) {
   const int64_t grid = p.split ? p.grid : int64_t(p.U) * d.K;
   if (grid > INT32_MAX) return V4A_ERR_UNSUPPORTED;
   const cudaError_t e = launch_pdl(kern, dim3(unsigned(grid)), dim3(Roles<kFp8>::kThreads), bytes, stream, d, p);
-  if (e != cudaSuccess || cudaGetLastError() != cudaSuccess) return V4A_ERR_CUDA;
-  return p.split ? dense_join(d, p, D, stream) : V4A_OK;
+  return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? V4A_OK : V4A_ERR_CUDA;
 }
 
 }  // namespace
@@ -480,20 +480,23 @@ size_t dense_prefill_workspace(const v4a_dense_attn_args* a) {
   return split_workspace(a->kv.dim > 128 ? kWideUnit : kUnit, a->kv.dim, kSms);
 }
 
-int dense_prefill(const v4a_dense_attn_args* a, const DenseAttnDev& d, int rows_from, void* ws, cudaStream_t stream) {
+int dense_prefill(const v4a_dense_attn_args* a, const DenseAttnDev& d, int rows_from, void* ws, SplitDev* out, cudaStream_t stream) {
   const bool wide = a->kv.dim > 128;
   const int unit = wide ? kWideUnit : kUnit;
   SplitDev p{};
   p.RG = int((int64_t(a->max_new_per_seq) * d.G + unit - 1) / unit);
   p.rows_from = rows_from;
   p.rows_to = INT32_MAX;
+  p.early = rows_from > 0;
   if (rows_from > 0) p.RG = std::max(p.RG, 2);      // sequences of the other launch are not units
   const int64_t units = units_bound(d, rows_from, p.RG, unit);
   if (units > INT32_MAX) return V4A_ERR_UNSUPPORTED;
   p.U = int(units);
   p.split = std::max(p.U, d.B) <= kMaxSplitUnits;
   split_carve(&p, ws, unit, a->kv.dim, kSms, wide ? kWideUnitCost : kUnitCost);
+  *out = p;
   const bool fp8 = a->kv.format == V4A_KV_FP8_TOKEN;
+  if (units == 0) return V4A_OK;                    // too few tokens for a sequence of this form
   if (wide) return dense_prefill_wide(a->kv.dim, fp8, d, p, stream);
   if (fp8) return a->kv.dim == 64 ? launch<64, true>(d, p, stream) : launch<128, true>(d, p, stream);
   return a->kv.dim == 64 ? launch<64, false>(d, p, stream) : launch<128, false>(d, p, stream);

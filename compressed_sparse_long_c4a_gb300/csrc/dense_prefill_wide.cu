@@ -71,6 +71,7 @@ __global__ void __launch_bounds__(Wide<D, kFp8>::kThreads, 1) dense_prefill_wide
   volatile int* abort_flag = &s.abort_flag;
 
   pdl_wait();
+  if (p.early) pdl_trigger();
   Line<kRows, kKeys, W::kThreads> line(a, p, &s + 1);
   if (!line.init(s.scan, base, kMinSteps)) return;
   const int64_t x0 = line.x0, x1 = line.x1;
@@ -394,8 +395,7 @@ int launch(const DenseAttnDev& d, const SplitDev& p, cudaStream_t stream) {
   const int64_t grid = p.split ? p.grid : int64_t(p.U) * d.K;
   if (grid > INT32_MAX) return V4A_ERR_UNSUPPORTED;
   const cudaError_t e = launch_pdl(kern, dim3(unsigned(grid)), dim3(Wide<D, kFp8>::kThreads), bytes, stream, d, p);
-  if (e != cudaSuccess || cudaGetLastError() != cudaSuccess) return V4A_ERR_CUDA;
-  return p.split ? dense_join(d, p, D, stream) : V4A_OK;
+  return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? V4A_OK : V4A_ERR_CUDA;
 }
 
 }  // namespace

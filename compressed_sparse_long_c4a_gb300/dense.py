@@ -98,15 +98,19 @@ class _Op:
     def _launch(self, stream):
         """Calls the C entry on the kept argument struct."""
         dev = self.device
+        if dev.type != "cuda":
+            raise ValueError(f"{self._where}: the tensors are on {dev}")
         if stream is None:
-            stream = torch.cuda.current_stream(dev)
+            raw = torch._C._cuda_getCurrentRawStream(dev.index)      # (a stream object takes 2 us)
         elif stream.device != dev:
             raise ValueError(f"{self._where}: the stream is on {stream.device}, the tensors on {dev}")
+        else:
+            raw = stream.cuda_stream
         if torch.cuda.current_device() == dev.index:
-            rc = self._fn(*self._call, stream.cuda_stream)
+            rc = self._fn(*self._call, raw)
         else:
             with torch.cuda.device(dev):
-                rc = self._fn(*self._call, stream.cuda_stream)
+                rc = self._fn(*self._call, raw)
         if rc:
             v4a._check(self._where, rc)
 
@@ -150,7 +154,7 @@ class StepPlan(_Op):
         a, dev = self.args, self.device
         free_out = free_in if free_out is None else free_out
         for n, t, k in (("cached", cached, a.num_seqs), ("fresh", fresh, a.num_seqs), ("free_in", free_in, 2), ("free_out", free_out, 2)):
-            if not (t.dtype is torch.int32 and t.device == dev and t.shape == (k,) and t.is_contiguous()):
+            if not (isinstance(t, torch.Tensor) and t.dtype is torch.int32 and t.device == dev and t.shape == (k,) and t.is_contiguous()):
                 _want(t, n, torch.int32, dev, (k,))
         a.cached, a.fresh, a.free_in, a.free_out = cached.data_ptr(), fresh.data_ptr(), free_in.data_ptr(), free_out.data_ptr()
         self._launch(stream)
@@ -235,7 +239,7 @@ class DenseInsert(_Op):
         stride of a multiple of 8; q and q_out None with num_heads = 0);
         positions int32 [T], slots int64 [T]."""
         a, c, dev = self.args, self.cache, self.device
-        n = k.shape[0]
+        n = k.shape[0] if isinstance(k, torch.Tensor) and k.dim() else 0
         a.num_tokens = n
         if a.num_heads:
             a.q_stride = _rows(q, "q", dev, a.num_heads, c.dim, n)
@@ -245,7 +249,7 @@ class DenseInsert(_Op):
         a.v_stride = _rows(v, "v", dev, c.num_kv_heads, c.dim, n)
         a.k, a.v = k.data_ptr(), v.data_ptr()
         for name, t, dtype in (("positions", positions, torch.int32), ("slots", slots, torch.int64)):
-            if not (t.dtype is dtype and t.device == dev and t.shape == (n,) and t.is_contiguous()):
+            if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.device == dev and t.shape == (n,) and t.is_contiguous()):
                 _want(t, name, dtype, dev, (n,))
         a.positions, a.slots = positions.data_ptr(), slots.data_ptr()
         self._launch(stream)
@@ -277,7 +281,7 @@ class DenseAttention(_Op):
         """q, out [T][heads][dim] bf16, T <= max_tokens; positions int32 [T];
         token_starts int32 [sequences + 1]; lse fp32 [T][heads] or None."""
         a, dev = self.args, self.device
-        n = q.shape[0]
+        n = q.shape[0] if isinstance(q, torch.Tensor) and q.dim() else 0
         if n > self.max_tokens:
             raise ValueError(f"q: {n} tokens, at most {self.max_tokens}")
         for name, t, dtype, shape in (("q", q, torch.bfloat16, (n, a.num_heads, self.cache.dim)),

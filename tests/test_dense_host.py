@@ -184,5 +184,23 @@ def test_binding_refuses_tensors(lib):
     for q, k in ((x[:, :4].float(), x[:, 4:6]), (x[:, :3], x[:, 4:6]), (x[:4, :4], x[:, 4:6]), (x[:, ::2], x[:, 4:6])):
         with pytest.raises(ValueError):
             op.run(q, k, x[:, 6:], torch.zeros((5, 4, 64), dtype=torch.bfloat16), pos, slots)
+    for pos2, slots2 in ((None, slots), (pos, None), (pos.long(), slots), (pos, slots[:4])):
+        with pytest.raises(ValueError):
+            op.run(x[:, :4], x[:, 4:6], x[:, 6:], torch.zeros((5, 4, 64), dtype=torch.bfloat16), pos2, slots2)
+    with pytest.raises(ValueError):
+        op.run(x[:, :4], None, x[:, 6:], None, pos, slots)
+    with pytest.raises(ValueError):                                # no CPU path
+        op.run(x[:, :4], x[:, 4:6], x[:, 6:], torch.zeros((5, 4, 64), dtype=torch.bfloat16), pos, slots)
     with pytest.raises(ValueError):
         D.StepPlan(torch.zeros((1, 2, 3), dtype=torch.int32), torch.zeros(4, dtype=torch.int64), 4)
+    plan = D.StepPlan(torch.zeros((1, 2, 3), dtype=torch.int32), torch.zeros(4, dtype=torch.int32), 4)
+    two = torch.zeros(2, dtype=torch.int32)
+    for args in ((two, two, None), (two, None, two), (two[:1], two, two), (two.long(), two, two), (two, two, two)):
+        with pytest.raises(ValueError):
+            plan.run(*args)
+    att = D.DenseAttention(D.DenseCache(pool, torch.zeros((1, 3), dtype=torch.int32), 2, 64), 4, 8, 8)
+    q = torch.zeros((5, 4, 64), dtype=torch.bfloat16)
+    for args in ((None, q, pos, two), (q, None, pos, two), (q, q[:4], pos, two), (q, q.clone(), pos, pos), (q, q.clone(), pos, two, q),
+                 (torch.zeros((9, 4, 64), dtype=torch.bfloat16), q, pos, two), (q, q.clone(), pos, two)):
+        with pytest.raises(ValueError):
+            att.run(*args)
