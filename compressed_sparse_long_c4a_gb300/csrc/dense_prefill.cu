@@ -492,7 +492,12 @@ int dense_prefill(const v4a_dense_attn_args* a, const DenseAttnDev& d, int rows_
   const int64_t units = units_bound(d, rows_from, p.RG, unit);
   if (units > INT32_MAX) return V4A_ERR_UNSUPPORTED;
   p.U = int(units);
-  p.split = std::max(p.U, d.B) <= kMaxSplitUnits;
+  // Under a window the units are about equally long, and one CTA each saves the cut units' pieces and their
+  // join, unless the last wave of CTAs is so empty that more than nine steps of 128 keys go to waste on the
+  // average SM (window 1024, 32 + 8 heads of 128: 6000 tokens 146 us unsplit, 169 split; 2048 tokens 58 and 71;
+  // 1500 tokens, 1.2 waves, 57 both; 2 KV heads, 5000 tokens, 1.03 waves: 57 and 51).
+  const int64_t ctas = int64_t(p.U) * d.K, idle = (ctas + kSms - 1) / kSms * kSms - ctas;
+  p.split = std::max(p.U, d.B) <= kMaxSplitUnits && (d.window == 0 || idle * (d.window / 128 + 5) > 9 * kSms);
   split_carve(&p, ws, unit, a->kv.dim, kSms, wide ? kWideUnitCost : kUnitCost);
   *out = p;
   const bool fp8 = a->kv.format == V4A_KV_FP8_TOKEN;

@@ -472,6 +472,7 @@ CHUNKS = [
     ((30,), (100,), 4, 2, 192, False, 0, 0), ((30,), (60,), 4, 2, 256, False, 50, 3), ((0, 90), (65, 64), 2, 2, 64, True, 30, 2),
     ((400,), (150,), 32, 2, 128, True, 0, 0), ((0,), (513,), 5, 1, 128, False, 0, 0), ((255, 256, 511), (2, 256, 130), 8, 8, 64, False, 0, 0),
     ((0,), (300,), 128, 1, 64, False, 0, 0), ((0, 0, 0), (1, 260, 2), 64, 4, 128, False, 1, 0),
+    ((1500,), (300,), 8, 2, 128, False, 1100, 3), ((1500, 20), (140, 200), 4, 1, 256, True, 1300, 0), ((2000,), (90,), 4, 2, 64, True, 1025, 300),
 ]
 
 
