@@ -20,6 +20,8 @@
 // Measured, 64 + 8 + 8 heads of 128: 16384 tokens, bf16 120 us (671 MB: 5.6
 // TB/s of the 6.8 that a copy reaches), fp8 143 us (the row maxima and the
 // codes); one token 2.1 us.
+#include <type_traits>
+
 #include "tc_common.cuh"
 #include "v4a_dense.h"
 #include "v4a_dense_internal.h"
@@ -28,6 +30,7 @@ namespace v4a {
 namespace {
 
 constexpr int kThreads = 128;     // eight CTAs an SM: 121 us for 16384 tokens of 64 + 8 + 8 heads; four of 256 threads took 124
+static_assert(kThreads == 1 << 7, "threads of a token");
 constexpr int kPasses = 5;        // rows per lane group held in registers (16 bytes a lane each; 3: 142 us, 10: 147 us)
 
 struct InsertDev {
@@ -35,6 +38,7 @@ struct InsertDev {
   float magnitude;
   int R, first, half;
   int D, H, K, NR, passes;        // NR = H + 2K rows a token
+  int tokens, share;              // T; tokens per CTA, log2
   float eps;
   const int32_t* positions;
   const int64_t* slots;
@@ -59,12 +63,17 @@ __device__ __forceinline__ uint2 pack4(const float* x) {
 }
 
 // kLanes: lanes of one row (dim / 8, or 32 with the last eight idle at dim 192).
-template <int kLanes, bool kFp8>
+// kShare: several tokens of few rows in a CTA (the division costs the others 5%: 121 us against 127).
+template <int kLanes, bool kFp8, bool kShare>
 __global__ void __launch_bounds__(kThreads, 8) dense_insert_kernel(const __grid_constant__ InsertDev p) {
   constexpr int kRows = kThreads / kLanes;      // rows per pass
-  __shared__ alignas(16) float cs[256];         // cos [0, R/2), sin [R/2, R)
-  const int t = blockIdx.x, tid = threadIdx.x;
-  const int l = tid % kLanes, r0 = blockIdx.y * (kRows * p.passes) + tid / kLanes;
+  __shared__ alignas(16) float angles[kShare ? 4 : 1][256];      // of a token: cos [0, R/2), sin [R/2, R)
+  // a CTA's threads are divided among its tokens
+  const int share = kShare ? p.share : 0, threads = kThreads >> share, rows = kRows >> share;
+  const int part = kShare ? threadIdx.x >> (7 - share) : 0, tid = kShare ? threadIdx.x & (threads - 1) : threadIdx.x;
+  const int t = (blockIdx.x << share) + part;
+  float* const cs = angles[part];
+  const int l = tid % kLanes, r0 = blockIdx.y * (rows * p.passes) + tid / kLanes;
   const int D = p.D;
   const bool live = 8 * l < D;
   // this lane's dims: d0 .. d0 + 3 and d1 .. d1 + 3; with `rot` their pairs' cosines start at cs[j]
@@ -88,14 +97,15 @@ __global__ void __launch_bounds__(kThreads, 8) dense_insert_kernel(const __grid_
   rot = rot && live;
   pdl_trigger();
   pdl_wait();
-  const int64_t slot = p.slots[t];
-  const int P = p.positions[t];
+  const bool some = !kShare || t < p.tokens;
+  const int64_t slot = some ? p.slots[t] : -1;
+  const int P = some ? p.positions[t] : 0;
   uint2 lo[kPasses], hi[kPasses];
 #pragma unroll
   for (int i = 0; i < kPasses; ++i) {
-    const int r = r0 + i * kRows;
+    const int r = r0 + i * rows;
     lo[i] = hi[i] = make_uint2(0, 0);
-    if (i < p.passes && r < p.NR && live) {
+    if (i < p.passes && r < p.NR && live && some) {
       const uint16_t* src = r < p.H ? p.q + int64_t(t) * p.qs + r * D
                             : r < p.H + p.K ? p.k + int64_t(t) * p.ks + (r - p.H) * D
                                             : p.v + int64_t(t) * p.vs + (r - p.H - p.K) * D;
@@ -103,11 +113,10 @@ __global__ void __launch_bounds__(kThreads, 8) dense_insert_kernel(const __grid_
       hi[i] = *reinterpret_cast<const uint2*>(src + d1);
     }
   }
-  if (slot < 0 || slot >= p.num_slots || P < 0) {   // the whole CTA
-    if (tid == 0 && slot != -1) report(p.status, slot < 0 || slot >= p.num_slots ? V4A_DEV_BAD_BLOCK : V4A_DEV_BAD_BATCH);
-    return;
-  }
-  for (int i = tid; i < p.R / 2; i += kThreads) {
+  const bool skip = slot < 0 || slot >= p.num_slots || P < 0;      // all threads of the token
+  if (skip && tid == 0 && slot != -1) report(p.status, slot < 0 || slot >= p.num_slots ? V4A_DEV_BAD_BLOCK : V4A_DEV_BAD_BATCH);
+  if (!kShare && skip) return;
+  for (int i = kShare && skip ? p.R : tid; i < p.R / 2; i += threads) {
     const int32_t frac = int32_t((uint64_t(uint32_t(P)) * p.turn[i]) >> 32);
     float sn, co;
     sincospif(float(frac) * 0x1p-31f, &sn, &co);
@@ -115,6 +124,7 @@ __global__ void __launch_bounds__(kThreads, 8) dense_insert_kernel(const __grid_
     cs[p.R / 2 + i] = sn * p.magnitude;
   }
   __syncthreads();
+  if (kShare && skip) return;
   float co[4] = {1.f, 1.f, 1.f, 1.f}, sn[4] = {0.f, 0.f, 0.f, 0.f};
   if (rot) {
     const float4 c = *reinterpret_cast<const float4*>(cs + j), s = *reinterpret_cast<const float4*>(cs + p.R / 2 + j);
@@ -125,7 +135,7 @@ __global__ void __launch_bounds__(kThreads, 8) dense_insert_kernel(const __grid_
   const int at = int(slot % kBlockPositions);
 #pragma unroll
   for (int i = 0; i < kPasses; ++i) {
-    const int r = r0 + i * kRows;
+    const int r = r0 + i * rows;
     if (i >= p.passes) break;                    // the same for the whole CTA
     const bool is_q = r < p.H, is_v = r >= p.H + p.K;
     float x[8];
@@ -137,7 +147,7 @@ __global__ void __launch_bounds__(kThreads, 8) dense_insert_kernel(const __grid_
 #pragma unroll
       for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
       // a group of lanes that shares a row is here together
-      const uint32_t group = kLanes == 32 ? 0xffffffffu : ((1u << (kLanes & 31)) - 1u) << ((tid & 31) / kLanes * kLanes);
+      const uint32_t group = kLanes == 32 ? 0xffffffffu : ((1u << (kLanes & 31)) - 1u) << ((threadIdx.x & 31) / kLanes * kLanes);
 #pragma unroll
       for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(group, ss, o);
       const float inv = rsqrtf(ss / float(D) + p.eps);
@@ -170,7 +180,7 @@ __global__ void __launch_bounds__(kThreads, 8) dense_insert_kernel(const __grid_
     } else {
       // row maximum of |x| as bits: a NaN is the largest of them, and makes the
       // row's scale NaN (readers may decode the code itself as a number)
-      const uint32_t group = kLanes == 32 ? 0xffffffffu : ((1u << (kLanes & 31)) - 1u) << ((tid & 31) / kLanes * kLanes);
+      const uint32_t group = kLanes == 32 ? 0xffffffffu : ((1u << (kLanes & 31)) - 1u) << ((threadIdx.x & 31) / kLanes * kLanes);
       uint32_t top = 0;
 #pragma unroll
       for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(x[e]) & 0x7fffffffu);
@@ -272,11 +282,20 @@ int dense_insert(const v4a_dense_insert_args* a, cudaStream_t stream) {
   if (int64_t(a->num_tokens) * y < 2 * 152) y = need;
   d.passes = (need + y - 1) / y;
   y = (need + d.passes - 1) / d.passes;
+  // many tokens of few rows: two or four a CTA while the machine stays full (16384
+  // tokens of 4 + 1 + 1 heads of 64: one 20 us, two 13, four 12; 2500 tokens 4.7, 3.9, 4.2)
+  d.tokens = a->num_tokens;
+  auto passes = [&](int share) { return (d.NR + (rows >> share) - 1) / (rows >> share); };
+  while (y == 1 && d.share < 2 && passes(d.share + 1) <= kPasses && a->num_tokens >> (d.share + 1) >= 152 * 8) d.passes = passes(++d.share);
   const bool fp8 = a->kv.format == V4A_KV_FP8_TOKEN;
-  auto kern = lanes == 8    ? (fp8 ? dense_insert_kernel<8, true> : dense_insert_kernel<8, false>)
-              : lanes == 16 ? (fp8 ? dense_insert_kernel<16, true> : dense_insert_kernel<16, false>)
-                            : (fp8 ? dense_insert_kernel<32, true> : dense_insert_kernel<32, false>);
-  const cudaError_t e = launch_pdl(kern, dim3(a->num_tokens, y), dim3(kThreads), 0, stream, d);
+  auto pick = [&](auto share) {
+    constexpr bool kShare = decltype(share)::value;
+    return lanes == 8    ? (fp8 ? dense_insert_kernel<8, true, kShare> : dense_insert_kernel<8, false, kShare>)
+           : lanes == 16 ? (fp8 ? dense_insert_kernel<16, true, kShare> : dense_insert_kernel<16, false, kShare>)
+                         : (fp8 ? dense_insert_kernel<32, true, kShare> : dense_insert_kernel<32, false, kShare>);
+  };
+  auto kern = d.share ? pick(std::true_type{}) : pick(std::false_type{});
+  const cudaError_t e = launch_pdl(kern, dim3(unsigned(a->num_tokens + (int64_t(1) << d.share) - 1) >> d.share, y), dim3(kThreads), 0, stream, d);
   return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? V4A_OK : V4A_ERR_CUDA;
 }
 

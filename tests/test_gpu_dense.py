@@ -226,6 +226,41 @@ def test_insert(dim, H, K, fp8, rope, norm, T):
     assert np.array_equal(after[~mask], was[~mask])
 
 
+@pytest.mark.parametrize("dim,H,K", [(64, 4, 1), (64, 1, 1), (128, 2, 1), (128, 4, 2), (256, 1, 1), (192, 1, 1), (64, 0, 2), (128, 64, 8)])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_insert_of_many_tokens(dim, H, K, fp8):
+    """A long call writes what calls of few tokens write, byte for byte (tokens share a CTA when their rows are few)."""
+    D = _dense()
+    T = 5003
+    g = torch.Generator(device=DEV).manual_seed(dim + H)
+    x = torch.randn((T, (H + 2 * K) * dim), generator=g, device=DEV).to(torch.bfloat16)
+    q, k, v = (x[:, a * dim:b * dim].unflatten(1, (b - a, dim)) for a, b in ((0, H), (H, H + K), (H + K, H + 2 * K)))
+    gam = torch.rand(dim, generator=g, device=DEV) + 0.5
+    pos = torch.randint(0, 1 << 20, (T,), generator=g, device=DEV, dtype=torch.int32)
+    slots = torch.randperm(8192, generator=g, device=DEV)[:T].contiguous()
+    slots[::97] = -1
+    outs, ops = [], []
+    for parts in ([T], [700] * 7 + [T - 4900], [1, T - 2, 1]):
+        pool = torch.zeros((32, D.block_bytes(K, dim, D.KV_FP8_TOKEN if fp8 else D.KV_BF16)), dtype=torch.uint8, device=DEV)
+        qo = torch.full((T, H, dim), 7.0, dtype=torch.bfloat16, device=DEV)
+        op = D.DenseInsert(D.DenseCache(pool, None, K, dim, D.KV_FP8_TOKEN if fp8 else D.KV_BF16), H, D.Rope(64, first=0, layout=1), gam, gam)
+        at = 0
+        for n in parts:
+            s = slice(at, at + n)
+            op.run(q[s] if H else None, k[s], v[s], qo[s] if H else None, pos[s], slots[s])
+            at += n
+        torch.cuda.synchronize()
+        assert int(op.status.item()) == 0
+        outs.append((pool, qo))
+    for pool, qo in outs[1:]:
+        assert torch.equal(outs[0][0], pool) and torch.equal(outs[0][1], qo)
+    assert (outs[0][1][::97] == 7.0).all()
+    bad = slots.clone()
+    bad[2500], bad[4000] = 32 * 256, -5
+    op.run(q if H else None, k, v, qo if H else None, pos, bad)
+    assert int(op.status.item()) == 1
+
+
 def test_insert_in_place_and_contiguous():
     """q rotated in place equals q rotated into another tensor, byte for byte."""
     D = _dense()
