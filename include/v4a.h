@@ -11,7 +11,8 @@
  * k, why the short window).  Byte layouts of the fp8 indexer entry follow the
  * SGLang KV-pool article, section "DSA", and the DeepSeek-V4 584-byte cache
  * row its section "DeepSeek-V4".  The host page allocator (page-size
- * buckets) is declared in v4a_pages.h.
+ * buckets) is declared in v4a_pages.h, the operators of layers with a full
+ * cache per KV head in v4a_dense.h.
  *
  * General rules for every entry point:
  *  - All pointers inside the argument structs are DEVICE pointers unless a
