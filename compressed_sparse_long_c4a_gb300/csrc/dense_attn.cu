@@ -667,7 +667,6 @@ int launch(const DenseAttnDev& a, const SplitDev& p, cudaStream_t stream) {
   static std::atomic<uint64_t> done{0};
   if (!raise_smem(kern, 227 * 1024, &done)) return V4A_ERR_CUDA;
   const int64_t grid = p.split ? p.grid : int64_t(p.U) * a.K;
-  if (grid > INT32_MAX) return V4A_ERR_UNSUPPORTED;
   const cudaError_t e = launch_pdl(kern, dim3(unsigned(grid)), dim3(S::kThreads), smem, stream, a, p);
   return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? V4A_OK : V4A_ERR_CUDA;
 }
@@ -731,28 +730,31 @@ int dense_attn(const v4a_dense_attn_args* a, void* ws, size_t ws_bytes, cudaStre
   d.pool = static_cast<const uint8_t*>(a->kv.pool);
   d.q = a->q; d.out = a->out; d.lse = a->lse; d.status = a->status;
   d.scale_log2 = a->softmax_scale * 1.4426950408889634f;
+  const bool fp8 = a->kv.format == V4A_KV_FP8_TOKEN, takes = dense_prefill_takes(a), both = takes && mixed(a);
+  const int few = few_rows(a->kv.dim, fp8);
   SplitDev p{}, many{};
-  p.rows_to = INT32_MAX;
-  if (dense_prefill_takes(a)) {
-    const bool both = mixed(a);
-    const int few = few_rows(a->kv.dim, a->kv.format != V4A_KV_BF16);
+  p.RG = int(row_groups(a));
+  p.rows_to = both ? few : INT32_MAX;
+  const int64_t units = units_bound(d, p.rows_from, p.RG, rows_of(a));
+  // all refusals come before the first launch
+  if (!takes || both)
+    if (units > INT32_MAX || units * d.K > INT32_MAX) return V4A_ERR_UNSUPPORTED;
+  if (takes) {
     rc = dense_prefill(a, d, both ? few + 1 : 0, static_cast<uint8_t*>(ws) + few_workspace(a), &many, stream);
     if (rc) return rc;
     if (!both) return many.split ? dense_join(d, many, a->kv.dim, stream) : V4A_OK;
-    p.rows_to = few;
     p.late = many.U > 0;
   }
-  p.RG = int(row_groups(a));
-  const int64_t units = units_bound(d, p.rows_from, p.RG, rows_of(a));
-  if (units > INT32_MAX) return V4A_ERR_UNSUPPORTED;
   p.U = int(units);
-  // One CTA per unit and KV head when there are enough of them and a window bounds their lengths (64
-  // sequences x 8 heads x 1024 positions: 29 us, the even split 34); an even split otherwise, since the
-  // lengths are the device's (200 sequences of 1 to 600 x 8: 47 us unsplit, 50 split; but one long
-  // sequence among short ones would run alone).
-  p.split = std::max(p.U, d.B) <= kMaxSplitUnits && (d.window == 0 || int64_t(p.U) * d.K < 256);
+  // One CTA per unit and KV head under a window of up to 4096 when there are enough of them to keep the memory
+  // busy (one streams 50 GB/s of bf16 rows, 25 of fp8 ones), or it is short; an even split otherwise.  Unsplit /
+  // split, us: 64 sequences x 8 heads of 64, window 1024: 29 / 34; heads of 128, 4096: 153 / 172; 64 x 2 heads,
+  // 1024: 15 / 19; 20 x 2, 1024: 15 / 13, 4096: 45 / 18, 256: 8 / 12; fp8, 20 x 8, 4096: 50 / 41.  Longer windows
+  // gain less (16384: 579 / 619) and would leave one long sequence among short ones to run alone.
+  p.split = std::max(p.U, d.B) <= kMaxSplitUnits &&
+            (d.window == 0 || d.window > 4096 || (units * d.K < (fp8 ? 256 : 128) && d.window > 512));
   split_carve(&p, ws, rows_of(a), a->kv.dim, ctas_of(a), kUnitCost);
-  rc = a->kv.format == V4A_KV_FP8_TOKEN ? launch_dim<true>(d, p, a->kv.dim, stream) : launch_dim<false>(d, p, a->kv.dim, stream);
+  rc = fp8 ? launch_dim<true>(d, p, a->kv.dim, stream) : launch_dim<false>(d, p, a->kv.dim, stream);
   if (rc == V4A_OK && many.split && many.U > 0) rc = dense_join(d, many, a->kv.dim, stream);
   return rc == V4A_OK && p.split ? dense_join(d, p, a->kv.dim, stream) : rc;
 }

@@ -464,7 +464,6 @@ int launch(const DenseAttnDev& d, const SplitDev& p, cudaStream_t stream) {
   if (cudaFuncGetAttributes(&attr, kern) != cudaSuccess) return V4A_ERR_CUDA;
   if (attr.numRegs != Roles<kFp8>::kLaunchRegs) return V4A_ERR_UNSUPPORTED;     // the split of the registers would not add up
   const int64_t grid = p.split ? p.grid : int64_t(p.U) * d.K;
-  if (grid > INT32_MAX) return V4A_ERR_UNSUPPORTED;
   const cudaError_t e = launch_pdl(kern, dim3(unsigned(grid)), dim3(Roles<kFp8>::kThreads), bytes, stream, d, p);
   return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? V4A_OK : V4A_ERR_CUDA;
 }
@@ -490,7 +489,7 @@ int dense_prefill(const v4a_dense_attn_args* a, const DenseAttnDev& d, int rows_
   p.early = rows_from > 0;
   if (rows_from > 0) p.RG = std::max(p.RG, 2);      // sequences of the other launch are not units
   const int64_t units = units_bound(d, rows_from, p.RG, unit);
-  if (units > INT32_MAX) return V4A_ERR_UNSUPPORTED;
+  if (units > INT32_MAX || units * d.K > INT32_MAX) return V4A_ERR_UNSUPPORTED;
   p.U = int(units);
   // Under a window the units are about equally long, and one CTA each saves the cut units' pieces and their
   // join, unless the last wave of CTAs is so empty that more than nine steps of 128 keys go to waste on the

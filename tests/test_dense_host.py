@@ -151,6 +151,13 @@ def test_attention_refuses_arguments(lib, kw, code):
     assert lib.v4a_dense_attn(C.byref(_attn(**kw)), 0x1000, 1 << 30, None) == code
 
 
+@pytest.mark.parametrize("num_seqs,num_tokens", [(1 << 22, 1 << 22), (1 << 21, 100 << 21), (1 << 21, 99 << 21)])
+def test_attention_refuses_grids_before_any_launch(lib, num_seqs, num_tokens):
+    """More (unit, KV head) pairs than a grid holds, in the first, the only and the second launch of the call."""
+    a = _attn(_cache(num_kv_heads=1024), num_heads=1024, num_seqs=num_seqs, num_tokens=num_tokens, max_new_per_seq=100)
+    assert lib.v4a_dense_attn(C.byref(a), 0x1000, 1 << 40, None) == UNSUPPORTED
+
+
 def test_attention_refuses_workspaces(lib):
     a = _attn()
     need = lib.v4a_dense_attn_workspace_size(C.byref(a))
