@@ -116,12 +116,10 @@ __global__ void __launch_bounds__(Shape<D, NT, kFp8>::kThreads, Shape<D, NT, kFp
   extern __shared__ __align__(128) uint8_t smem[];
   typename S::Tail& s = *reinterpret_cast<typename S::Tail*>(smem + kWarps * S::kStages * S::kStage);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (!p.late) pdl_wait();
+  pdl_wait();
+  if (p.early) pdl_trigger();
   Line<R, kKeys, kThreads> line(a, p, &s + 1);
-  if (!line.init(s.scan, smem, kWarps)) {                // a tile per warp at least
-    if (p.late) pdl_wait();
-    return;
-  }
+  if (!line.init(s.scan, smem, kWarps)) return;          // a tile per warp at least
   const int64_t x0 = line.x0, x1 = line.x1;
 
   // ---- this warp's stream: tiles x0 + warp + j kWarps, j = 0, 1, ... ----
@@ -521,7 +519,6 @@ __global__ void __launch_bounds__(Shape<D, NT, kFp8>::kThreads, Shape<D, NT, kFp
     x += count;
   }
   if (p.split && tid == 0) p.join[blockIdx.x] = desc;
-  if (p.late) pdl_wait();
 }
 
 // Joins the pieces of a unit that several CTAs hold: piece c's slot 1, then
@@ -627,12 +624,15 @@ __global__ void __launch_bounds__(256) dense_join_rows(const DenseAttnDev a, con
   if (blockIdx.y == 0 && a.lse) a.lse[at] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
 }
 
-// A call whose sequences all bring many rows runs dense_prefill.cu's form, one
+// A call whose sequences all bring many rows runs the form of dense_prefill*.cu, one
 // whose sequences all bring few rows this file's, and a mixed one both, each
 // launch taking its sequences: it is mixed when the token count leaves room
-// for short sequences beside the longest.  256 decoding sequences beside a
-// chunk of 4096 (32 + 8 heads of 128): 304 us, 147 and 147 alone; the launches
-// for short sequences that are not there cost two chunks of 1024 8 us of 54.
+// for short sequences beside the longest.  The short ones go first, so that
+// the few CTAs of a small chunk do not hold back an even share of theirs: 64
+// decoding sequences (32 + 8 heads of 128) beside a chunk of 9 tokens 63 us (75
+// in the other order), of 4096 295 (306), 256 beside 4096 312 (304; 146 and 147
+// alone).  The launches for short sequences that are not there cost two chunks
+// of 1024 9 us of 54.
 bool mixed(const v4a_dense_attn_args* a) {
   return dense_prefill_takes(a) && a->num_tokens < int64_t(a->num_seqs) * a->max_new_per_seq;
 }
@@ -740,10 +740,13 @@ int dense_attn(const v4a_dense_attn_args* a, void* ws, size_t ws_bytes, cudaStre
   if (!takes || both)
     if (units > INT32_MAX || units * d.K > INT32_MAX) return V4A_ERR_UNSUPPORTED;
   if (takes) {
-    rc = dense_prefill(a, d, both ? few + 1 : 0, static_cast<uint8_t*>(ws) + few_workspace(a), &many, stream);
+    rc = dense_prefill_plan(a, d, both ? few + 1 : 0, static_cast<uint8_t*>(ws) + few_workspace(a), &many);
     if (rc) return rc;
-    if (!both) return many.split ? dense_join(d, many, a->kv.dim, stream) : V4A_OK;
-    p.late = many.U > 0;
+    if (!both) {
+      rc = dense_prefill(a, d, many, stream);
+      return rc == V4A_OK && many.split ? dense_join(d, many, a->kv.dim, stream) : rc;
+    }
+    p.early = many.late = many.U > 0;               // (no room for a sequence of the other form: no launch for it)
   }
   p.U = int(units);
   // One CTA per unit and KV head under a window of up to 4096 when there are enough of them to keep the memory
@@ -755,8 +758,9 @@ int dense_attn(const v4a_dense_attn_args* a, void* ws, size_t ws_bytes, cudaStre
             (d.window == 0 || d.window > 4096 || (units * d.K < (fp8 ? 256 : 128) && d.window > 512));
   split_carve(&p, ws, rows_of(a), a->kv.dim, ctas_of(a), kUnitCost);
   rc = fp8 ? launch_dim<true>(d, p, a->kv.dim, stream) : launch_dim<false>(d, p, a->kv.dim, stream);
-  if (rc == V4A_OK && many.split && many.U > 0) rc = dense_join(d, many, a->kv.dim, stream);
-  return rc == V4A_OK && p.split ? dense_join(d, p, a->kv.dim, stream) : rc;
+  if (rc == V4A_OK && many.U > 0) rc = dense_prefill(a, d, many, stream);
+  if (rc == V4A_OK && p.split) rc = dense_join(d, p, a->kv.dim, stream);
+  return rc == V4A_OK && many.U > 0 && many.split ? dense_join(d, many, a->kv.dim, stream) : rc;
 }
 
 }  // namespace v4a

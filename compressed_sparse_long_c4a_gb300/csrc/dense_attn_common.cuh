@@ -121,8 +121,8 @@ struct SplitDev {
   struct JoinDesc* join;          // [CTA]
   float *part_o, *part_ml;        // [CTA][2][R][dim], [CTA][2][R][2] (maximum in log2 units, sum)
   int rows_from, rows_to;         // the launch takes sequences of this many rows (tokens x group)
-  // A call's two launches need nothing of each other: the first lets the second
-  // start as its CTAs leave (early), which waits for it at its end (late).
+  // A call's two launches need nothing of each other: the one for few rows lets
+  // the other start as its CTAs leave (early), which waits for it at its end (late).
   int early, late;
 };
 
@@ -335,9 +335,11 @@ struct Line {
 int dense_join(const DenseAttnDev& a, const SplitDev& p, int dim, cudaStream_t stream);
 
 // The tensor-core form for many rows (dense_prefill.cu): whether it takes the
-// shape, and its launch, which leaves in *p what is to be joined (p->split).
+// shape, its division (U = 0: no sequence of the call can have so many rows)
+// and its launch, whose pieces are then to be joined (p.split).
 bool dense_prefill_takes(const v4a_dense_attn_args* a);
 size_t dense_prefill_workspace(const v4a_dense_attn_args* a);
-int dense_prefill(const v4a_dense_attn_args* a, const DenseAttnDev& d, int rows_from, void* ws, SplitDev* p, cudaStream_t stream);
+int dense_prefill_plan(const v4a_dense_attn_args* a, const DenseAttnDev& d, int rows_from, void* ws, SplitDev* p);
+int dense_prefill(const v4a_dense_attn_args* a, const DenseAttnDev& d, const SplitDev& p, cudaStream_t stream);
 
 }  // namespace v4a

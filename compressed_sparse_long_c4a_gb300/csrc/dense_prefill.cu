@@ -88,10 +88,12 @@ __global__ void __launch_bounds__(Roles<kFp8>::kThreads, 1) dense_prefill_kernel
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   volatile int* abort_flag = &s.abort_flag;
 
-  pdl_wait();
-  if (p.early) pdl_trigger();
+  if (!p.late) pdl_wait();
   Line<kUnit, kKeys, kThreads> line(a, p, &s + 1);
-  if (!line.init(s.scan, base, kMinSteps)) return;
+  if (!line.init(s.scan, base, kMinSteps)) {
+    if (p.late) pdl_wait();
+    return;
+  }
   const int64_t x0 = line.x0, x1 = line.x1;
 
   if (tid == 0) {
@@ -448,6 +450,7 @@ __global__ void __launch_bounds__(Roles<kFp8>::kThreads, 1) dense_prefill_kernel
     const bool tail = pc.tile + 1 < un.tr.tiles && x1 - 1 - pc.tile >= x0;
     p.join[blockIdx.x] = tail ? line.describe(pc, un) : JoinDesc{};
   }
+  if (p.late) pdl_wait();
   pdl_trigger();
 }
 
@@ -479,14 +482,13 @@ size_t dense_prefill_workspace(const v4a_dense_attn_args* a) {
   return split_workspace(a->kv.dim > 128 ? kWideUnit : kUnit, a->kv.dim, kSms);
 }
 
-int dense_prefill(const v4a_dense_attn_args* a, const DenseAttnDev& d, int rows_from, void* ws, SplitDev* out, cudaStream_t stream) {
+int dense_prefill_plan(const v4a_dense_attn_args* a, const DenseAttnDev& d, int rows_from, void* ws, SplitDev* out) {
   const bool wide = a->kv.dim > 128;
   const int unit = wide ? kWideUnit : kUnit;
   SplitDev p{};
   p.RG = int((int64_t(a->max_new_per_seq) * d.G + unit - 1) / unit);
   p.rows_from = rows_from;
   p.rows_to = INT32_MAX;
-  p.early = rows_from > 0;
   if (rows_from > 0) p.RG = std::max(p.RG, 2);      // sequences of the other launch are not units
   const int64_t units = units_bound(d, rows_from, p.RG, unit);
   if (units > INT32_MAX || units * d.K > INT32_MAX) return V4A_ERR_UNSUPPORTED;
@@ -499,8 +501,11 @@ int dense_prefill(const v4a_dense_attn_args* a, const DenseAttnDev& d, int rows_
   p.split = std::max(p.U, d.B) <= kMaxSplitUnits && (d.window == 0 || idle * (d.window / 128 + 5) > 9 * kSms);
   split_carve(&p, ws, unit, a->kv.dim, kSms, wide ? kWideUnitCost : kUnitCost);
   *out = p;
-  const bool fp8 = a->kv.format == V4A_KV_FP8_TOKEN;
-  if (units == 0) return V4A_OK;                    // too few tokens for a sequence of this form
+  return V4A_OK;
+}
+
+int dense_prefill(const v4a_dense_attn_args* a, const DenseAttnDev& d, const SplitDev& p, cudaStream_t stream) {
+  const bool wide = a->kv.dim > 128, fp8 = a->kv.format == V4A_KV_FP8_TOKEN;
   if (wide) return dense_prefill_wide(a->kv.dim, fp8, d, p, stream);
   if (fp8) return a->kv.dim == 64 ? launch<64, true>(d, p, stream) : launch<128, true>(d, p, stream);
   return a->kv.dim == 64 ? launch<64, false>(d, p, stream) : launch<128, false>(d, p, stream);

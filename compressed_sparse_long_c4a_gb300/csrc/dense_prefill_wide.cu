@@ -70,10 +70,12 @@ __global__ void __launch_bounds__(Wide<D, kFp8>::kThreads, 1) dense_prefill_wide
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   volatile int* abort_flag = &s.abort_flag;
 
-  pdl_wait();
-  if (p.early) pdl_trigger();
+  if (!p.late) pdl_wait();
   Line<kRows, kKeys, W::kThreads> line(a, p, &s + 1);
-  if (!line.init(s.scan, base, kMinSteps)) return;
+  if (!line.init(s.scan, base, kMinSteps)) {
+    if (p.late) pdl_wait();
+    return;
+  }
   const int64_t x0 = line.x0, x1 = line.x1;
 
   if (tid == 0) {
@@ -381,6 +383,7 @@ __global__ void __launch_bounds__(Wide<D, kFp8>::kThreads, 1) dense_prefill_wide
     const bool tail = pc.tile + 1 < un.tr.tiles && x1 - 1 - pc.tile >= x0;
     p.join[blockIdx.x] = tail ? line.describe(pc, un) : JoinDesc{};
   }
+  if (p.late) pdl_wait();
   pdl_trigger();
 }
 
