@@ -38,13 +38,17 @@ constexpr int few_rows(int dim, bool fp8) { return (dim == 256 ? 8 : 16) * (fp8 
 // sequence belongs to the call's other launch.
 struct SeqRun { int s0, n, p0; };
 
-__device__ __forceinline__ SeqRun seq_run(const DenseAttnDev& a, int64_t rows_from, int64_t rows_to, int b, int32_t* status) {
-  const int s0 = a.starts[b], s1 = a.starts[b + 1];
+// Past the L1 in a launch that does not wait for the writers (SplitDev::late).  Many CTAs that look
+// through the same starts want it (1000 decoding sequences beside a chunk of 4096: 849 us, past it 973).
+__device__ __forceinline__ int32_t load(const int32_t* x, bool late) { return late ? __ldcg(x) : *x; }
+
+__device__ __forceinline__ SeqRun seq_run(const DenseAttnDev& a, int64_t rows_from, int64_t rows_to, bool late, int b, int32_t* status) {
+  const int s0 = load(a.starts + b, late), s1 = load(a.starts + b + 1, late);
   SeqRun r{s0, 0, 0};
   if (s0 == s1 && s0 >= 0 && s1 <= a.T) return r;
   bool ok = s0 >= 0 && s1 > s0 && s1 <= a.T && s1 - s0 <= a.max_new;
   if (ok) {
-    const int p0 = a.positions[s0], p1 = a.positions[s1 - 1];
+    const int p0 = load(a.positions + s0, late), p1 = load(a.positions + s1 - 1, late);
     ok = p0 >= 0 && int64_t(p1) == int64_t(p0) + (s1 - s0) - 1 && p1 < int64_t(a.max_blocks) * kBlockPositions;
     r.p0 = p0;
   }
@@ -122,7 +126,9 @@ struct SplitDev {
   float *part_o, *part_ml;        // [CTA][2][R][dim], [CTA][2][R][2] (maximum in log2 units, sum)
   int rows_from, rows_to;         // the launch takes sequences of this many rows (tokens x group)
   // A call's two launches need nothing of each other: the one for few rows lets
-  // the other start as its CTAs leave (early), which waits for it at its end (late).
+  // the other start as its CTAs leave (early), which waits for it at its end (late)
+  // and reads memory past the L1 throughout, since it does not wait for the writers
+  // before (which had ended when the first of the two began its work).
   int early, late;
 };
 
@@ -201,13 +207,13 @@ struct Line {
         if (tid == 0) refs[0] = UnitRef{0, 0, 0, -1};
         int64_t n = 0, all;
         for (int b = b0; b < b1; ++b) {
-          n += groups(a.starts[b], a.starts[b + 1]);
+          n += groups(load(a.starts + b, p.late), load(a.starts + b + 1, p.late));
           if (st) run(b, st);
         }
         int64_t at = before(n, scan, &all);
         if (u_direct >= at && u_direct < at + n) {
           int b = b0;
-          for (int64_t g; at + (g = groups(a.starts[b], a.starts[b + 1])) <= u_direct; ++b) at += g;
+          for (int64_t g; at + (g = groups(load(a.starts + b, p.late), load(a.starts + b + 1, p.late))) <= u_direct; ++b) at += g;
           refs[0] = ref(b, int(u_direct - at), run(b, nullptr));
         }
         if (st && tid == 0 && all > p.U) report(st, V4A_DEV_BAD_BATCH);       // sequences that share tokens
@@ -267,7 +273,7 @@ struct Line {
   __device__ __forceinline__ UnitRef ref(int b, int rg, const SeqRun& r) const {
     return UnitRef{b, r.s0, r.p0, int(min(int64_t(r.n) * a.G, (int64_t(rg) + 1) * R)) - 1};
   }
-  __device__ __forceinline__ SeqRun run(int b, int32_t* st) const { return seq_run(a, p.rows_from, p.rows_to, b, st); }
+  __device__ __forceinline__ SeqRun run(int b, int32_t* st) const { return seq_run(a, p.rows_from, p.rows_to, p.late, b, st); }
   // Row groups of a sequence of tokens [s0, s1) in this launch.
   __device__ __forceinline__ int64_t groups(int s0, int s1) const {
     const int64_t n = int64_t(s1) - s0, rows = n * a.G;

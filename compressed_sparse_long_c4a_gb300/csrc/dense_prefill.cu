@@ -31,7 +31,7 @@
 //
 // Bound: the tensor cores (4 dim flops per visible pair), and beside them the
 // exponentials: 128 x 128 per tile and step.  Measured, 32 + 8 heads of 128,
-// 2048 tokens over 10240 positions: bf16 258 us (1196 TFLOP/s), fp8 495 us (625:
+// 2048 tokens over 10240 positions: bf16 258 us (1200 TFLOP/s), fp8 480 us (645:
 // the conversions of the codes); dim 64 bf16 212 us (727: the exponentials,
 // twice as many per flop); a window of 1024 with 1500 tokens 62 us.
 #include "dense_prefill_common.cuh"
@@ -46,7 +46,8 @@ constexpr int kUnit = 2 * kRows;     // rows of a unit
 // 128).  bf16 rows are copied as they are: three warps and 200 registers for
 // the softmax, 258 us; four warps among 512 threads, whose softmax has 192, 314
 // us.  fp8 rows go through the registers of their copying warps, which convert
-// them: four warps and 184 + 72 registers, 495 us (192 + 64: 545; seven warps:
+// them: four warps and 184 + 72 registers, 495 us, and 480 since their
+// loads go past the L1 (192 + 64: 545; seven warps:
 // 546; three among 384 threads: 587).  The registers of a thread at launch come
 // in steps that four warps share, so 512 threads carry three warps that only
 // wait.  softmax x 256 + rest x (threads - 256) = launch x threads.
@@ -354,7 +355,7 @@ __global__ void __launch_bounds__(Roles<kFp8>::kThreads, 1) dense_prefill_kernel
       const int count = int(min(int64_t(un.tr.tiles - pc.tile), x1 - x));
       x += count;
       auto entry = [&](int i) {      // step i's table entry, read a step ahead of its use
-        return i < count ? a.bt[int64_t(un.b) * a.max_blocks + un.tr.at(pc.tile + i) / (kBlockPositions / kKeys)] : -1;
+        return i < count ? __ldcg(a.bt + int64_t(un.b) * a.max_blocks + un.tr.at(pc.tile + i) / (kBlockPositions / kKeys)) : -1;
       };
       int32_t next = entry(0);
       for (int i = 0; i < count && ok; ++i, ++n) {
@@ -380,7 +381,7 @@ __global__ void __launch_bounds__(Roles<kFp8>::kThreads, 1) dense_prefill_kernel
           if (lt < kKeys) {
             const float* row_scale = reinterpret_cast<const float*>(block + int64_t(2 * a.K) * kBlockPositions * D) + at + lt;
             const bool live = lt <= hi && (lt > lo || lt < sk);
-            const float ks = live ? row_scale[0] : 0.f, vs = live ? row_scale[a.K * kBlockPositions] : 1.f;
+            const float ks = live ? __ldcg(row_scale) : 0.f, vs = live ? __ldcg(row_scale + a.K * kBlockPositions) : 1.f;
             const float l = vs > 0x1p-100f ? log2f(vs) : vs <= 0x1p-100f ? -100.f : vs;
             float* const sc = &s.scales[n & 3][0][lt];
             sc[0] = ks * a.scale_log2;
@@ -395,7 +396,7 @@ __global__ void __launch_bounds__(Roles<kFp8>::kThreads, 1) dense_prefill_kernel
             for (int k = 0; k < kPasses; ++k) {
               const int r = r0 + k * kStep;
               raw[k] = make_uint4(0, 0, 0, 0);
-              if (r <= hi && (r > lo || r < sk)) raw[k] = __ldg(reinterpret_cast<const uint4*>(src + k * (kStep * D)));
+              if (r <= hi && (r > lo || r < sk)) raw[k] = __ldcg(reinterpret_cast<const uint4*>(src + k * (kStep * D)));
             }
             ok = wait_for(half ? &s.v_free[n & 1] : &s.k_free[n & 1], ((n >> 1) & 1) ^ 1, a.status, abort_flag);
             if (!ok) break;

@@ -22,9 +22,9 @@
 //
 // Bound: the tensor cores (4 dim flops per visible pair); a step's keys and
 // values (4 dim bytes a key from the L2) serve 128 rows only.  Measured, 2048
-// tokens over 10240 positions, 16 + 4 heads: dim 256 bf16 321 us (963 TFLOP/s;
+// tokens over 10240 positions, 16 + 4 heads: dim 256 bf16 320 us (966 TFLOP/s;
 // the form for few rows, which had them before, re-reads the cache per 8 rows),
-// fp8 519 us (596: the conversions); dim 192 bf16 274 us (847), fp8 467 (497).
+// fp8 505 us (613: the conversions); dim 192 bf16 274 us (847), fp8 467 (497).
 #include "dense_prefill_common.cuh"
 
 namespace v4a {
@@ -304,7 +304,7 @@ __global__ void __launch_bounds__(Wide<D, kFp8>::kThreads, 1) dense_prefill_wide
       const int count = int(min(int64_t(un.tr.tiles - pc.tile), x1 - x));
       x += count;
       auto entry = [&](int i) {      // step i's table entry, read a step ahead of its use
-        return i < count ? a.bt[int64_t(un.b) * a.max_blocks + un.tr.at(pc.tile + i) / (kBlockPositions / kKeys)] : -1;
+        return i < count ? __ldcg(a.bt + int64_t(un.b) * a.max_blocks + un.tr.at(pc.tile + i) / (kBlockPositions / kKeys)) : -1;
       };
       int32_t next = entry(0);
       for (int i = 0; i < count && ok; ++i, ++n) {
@@ -324,7 +324,7 @@ __global__ void __launch_bounds__(Wide<D, kFp8>::kThreads, 1) dense_prefill_wide
         if (kFp8 && lt < kKeys) {
           const float* row_scale = reinterpret_cast<const float*>(block + int64_t(2 * a.K) * kBlockPositions * D) + at + lt;
           const bool live = lt <= hi && (lt > lo || lt < sk);
-          const float ks = live ? row_scale[0] : 0.f, vs = live ? row_scale[a.K * kBlockPositions] : 1.f;
+          const float ks = live ? __ldcg(row_scale) : 0.f, vs = live ? __ldcg(row_scale + a.K * kBlockPositions) : 1.f;
           const float l = vs > 0x1p-100f ? log2f(vs) : vs <= 0x1p-100f ? -100.f : vs;
           s.scales[n & 3][0][lt] = ks * a.scale_log2;
           s.scales[n & 3][1][lt] = l;
@@ -344,7 +344,7 @@ __global__ void __launch_bounds__(Wide<D, kFp8>::kThreads, 1) dense_prefill_wide
             for (int k = 0; k < kKeys / W::kStep; ++k) {
               const int r = r0 + W::kStep * k;
               raw[k] = make_uint4(0, 0, 0, 0);
-              if (r <= hi && (r > lo || r < sk)) raw[k] = __ldg(reinterpret_cast<const uint4*>(src + k * (W::kStep * D)));
+              if (r <= hi && (r > lo || r < sk)) raw[k] = __ldcg(reinterpret_cast<const uint4*>(src + k * (W::kStep * D)));
             }
             ok = wait_for(free, ((n >> 1) & 1) ^ 1, a.status, abort_flag);
             if (!ok) break;
