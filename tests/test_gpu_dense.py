@@ -809,6 +809,67 @@ def test_two_streams_with_their_own_workspaces():
         assert torch.equal(alone[i], both[i])
 
 
+@pytest.mark.parametrize("dim", [128, 256])
+def test_two_streams_of_mixed_batches(dim):
+    """Both forms of two calls in flight at once."""
+    runs = [[(900, 1), (200, 150), (40, 3), (0, 300)], [(10, 90), (1500, 2), (0, 0), (33, 200)]]
+    layers = [Layer([c + n for c, n in r], 8, 2, dim, i == 1, seed=40 + i) for i, r in enumerate(runs)]
+    ops, args, alone = [], [], []
+    for L, r in zip(layers, runs):
+        pos, starts = _runs(*zip(*r))
+        op = _dense().DenseAttention(L.cache, 8, len(pos), max(n for _, n in r))
+        q = L.query(len(pos))
+        out = torch.empty_like(q)
+        args.append((q, torch.tensor(pos, dtype=torch.int32, device=DEV), torch.tensor(starts, dtype=torch.int32, device=DEV)))
+        op.run(q, out, *args[-1][1:])
+        torch.cuda.synchronize()
+        ops.append(op)
+        alone.append(out)
+    both = [torch.empty_like(o) for o in alone]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(20):
+        for i in range(2):
+            ops[i].run(args[i][0], both[i], *args[i][1:], stream=streams[i])
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert torch.equal(alone[i], both[i]) and int(ops[i].status.item()) == 0
+
+
+@pytest.mark.parametrize("dim,fp8", [(64, True), (128, True), (128, False), (256, True)])
+def test_mixed_steps_see_what_was_just_inserted(dim, fp8):
+    """Insert and attention without a pause: rows beside each other, and the scales in one line with older ones, are
+    new at every step; a call after a synchronisation gives the same bytes."""
+    D = _dense()
+    H, K, steps, chunk = 8, 2, 24, 37
+    fmt = D.KV_FP8_TOKEN if fp8 else D.KV_BF16
+    g = torch.Generator(device=DEV).manual_seed(dim)
+    table = torch.randperm(12, generator=g, device=DEV).to(torch.int32).view(3, 4)
+    pool = torch.full((12, D.block_bytes(K, dim, fmt)), 0xff, dtype=torch.uint8, device=DEV)      # NaN everywhere
+    cache = D.DenseCache(pool, table, K, dim, fmt)
+    T = 2 + chunk
+    ins, att = D.DenseInsert(cache, H, D.Rope(dim, layout=1)), D.DenseAttention(cache, H, T, chunk)
+    xs = torch.randn((steps, T, H + 2 * K, dim), generator=g, device=DEV).to(torch.bfloat16)
+    starts = torch.tensor([0, 1, 1 + chunk, T], dtype=torch.int32, device=DEV)
+    pos, slots, qr, out = [], [], torch.empty((steps, T, H, dim), dtype=torch.bfloat16, device=DEV), None
+    for s in range(steps):
+        p = torch.tensor([s, *range(s * chunk, (s + 1) * chunk), s], dtype=torch.int32, device=DEV)
+        b = torch.tensor([0] + [1] * chunk + [2], device=DEV)
+        pos.append(p)
+        slots.append(table[b, (p // 256).long()].long() * 256 + p % 256)
+    out = torch.zeros_like(qr)
+    torch.cuda.synchronize()
+    for s in range(steps):
+        ins.run(xs[s, :, :H], xs[s, :, H:H + K], xs[s, :, H + K:], qr[s], pos[s], slots[s])
+        att.run(qr[s], out[s], pos[s], starts)
+    torch.cuda.synchronize()
+    assert int(ins.status.item()) == 0 and int(att.status.item()) == 0 and bool(out.isfinite().all())
+    again = torch.zeros_like(out)
+    for s in range(steps):                      # later rows are hidden from earlier steps' queries
+        att.run(qr[s], again[s], pos[s], starts)
+        torch.cuda.synchronize()
+    assert torch.equal(out, again)
+
+
 # --------------------------------------------------------------------------
 # The three together
 # --------------------------------------------------------------------------
