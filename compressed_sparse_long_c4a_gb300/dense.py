@@ -93,7 +93,9 @@ def _want(t, name, dtype, device, shape=None, contiguous=True):
 
 
 class _Op:
-    """Launches on the tensors' device, whatever the current one is."""
+    """Launches on the tensors' device, whatever the current one is.  A handle
+    keeps one argument struct and one workspace: calls that may run at the same
+    time (streams, threads, graphs replayed side by side) need handles of their own."""
 
     def _launch(self, stream):
         """Calls the C entry on the kept argument struct."""
