@@ -632,7 +632,9 @@ __global__ void __launch_bounds__(256) dense_join_rows(const DenseAttnDev a, con
 // decoding sequences (32 + 8 heads of 128) beside a chunk of 9 tokens 63 us (75
 // in the other order), of 4096 295 (306), 256 beside 4096 312 (304; 146 and 147
 // alone).  The launches for short sequences that are not there cost two chunks
-// of 1024 9 us of 54.
+// of 1024 9 us of 54.  (Choosing the order by the batch's mean rows saved 8 us
+// there and cost every small decode call 4%: the form for few rows would have to
+// read past the L1 as well.)
 bool mixed(const v4a_dense_attn_args* a) {
   return dense_prefill_takes(a) && a->num_tokens < int64_t(a->num_seqs) * a->max_new_per_seq;
 }
@@ -662,7 +664,7 @@ template <int D, int NT, bool kFp8>
 int launch(const DenseAttnDev& a, const SplitDev& p, cudaStream_t stream) {
   using S = Shape<D, NT, kFp8>;
   const size_t smem = S::kWarps * S::kStages * S::kStage + sizeof(typename S::Tail) + split_smem(p.split, p.U);
-  if (smem > 227 * 1024) return V4A_ERR_UNSUPPORTED;
+  static_assert(S::kWarps * S::kStages * S::kStage + sizeof(typename S::Tail) + split_smem(1, kMaxSplitUnits) <= 227 * 1024, "shared memory of a CTA");
   auto kern = dense_attn_mma<D, NT, kFp8>;
   static std::atomic<uint64_t> done{0};
   if (!raise_smem(kern, 227 * 1024, &done)) return V4A_ERR_CUDA;

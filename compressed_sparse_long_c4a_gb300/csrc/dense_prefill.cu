@@ -460,13 +460,13 @@ int launch(const DenseAttnDev& d, const SplitDev& p, cudaStream_t stream) {
   // at least 116 KB: no two CTAs that allocate TMEM share an SM
   size_t bytes = 1024 + 6 * 128 * D * 2 + sizeof(PreSmem) + split_smem(p.split, p.U);
   if (bytes < 116 * 1024) bytes = 116 * 1024;
-  if (bytes > 227 * 1024) return V4A_ERR_UNSUPPORTED;
+  static_assert(1024 + 6 * 128 * D * 2 + sizeof(PreSmem) + split_smem(1, kMaxSplitUnits) <= 227 * 1024, "shared memory of a CTA");
   auto kern = dense_prefill_kernel<D, kFp8>;
   static std::atomic<uint64_t> done{0};
   if (!raise_smem(kern, 227 * 1024, &done)) return V4A_ERR_CUDA;
   cudaFuncAttributes attr;
   if (cudaFuncGetAttributes(&attr, kern) != cudaSuccess) return V4A_ERR_CUDA;
-  if (attr.numRegs != Roles<kFp8>::kLaunchRegs) return V4A_ERR_UNSUPPORTED;     // the split of the registers would not add up
+  if (attr.numRegs != Roles<kFp8>::kLaunchRegs) return V4A_ERR_CUDA;     // built otherwise: the split of the registers would not add up
   const int64_t grid = p.split ? p.grid : int64_t(p.U) * d.K;
   const cudaError_t e = launch_pdl(kern, dim3(unsigned(grid)), dim3(Roles<kFp8>::kThreads), bytes, stream, d, p);
   return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? V4A_OK : V4A_ERR_CUDA;

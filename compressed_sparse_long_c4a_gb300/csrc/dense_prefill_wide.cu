@@ -391,7 +391,7 @@ template <int D, bool kFp8>
 int launch(const DenseAttnDev& d, const SplitDev& p, cudaStream_t stream) {
   // more than 116 KB: no two CTAs that allocate TMEM share an SM
   const size_t bytes = 1024 + Wide<D, kFp8>::kQBytes + 4 * Wide<D, kFp8>::kStepBytes + sizeof(WideSmem) + split_smem(p.split, p.U);
-  if (bytes > 227 * 1024) return V4A_ERR_UNSUPPORTED;
+  static_assert(1024 + Wide<D, kFp8>::kQBytes + 4 * Wide<D, kFp8>::kStepBytes + sizeof(WideSmem) + split_smem(1, kMaxSplitUnits) <= 227 * 1024, "shared memory of a CTA");
   auto kern = dense_prefill_wide_kernel<D, kFp8>;
   static std::atomic<uint64_t> done{0};
   if (!raise_smem(kern, 227 * 1024, &done)) return V4A_ERR_CUDA;
