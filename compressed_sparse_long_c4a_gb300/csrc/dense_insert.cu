@@ -187,8 +187,10 @@ __global__ void __launch_bounds__(kThreads, 8) dense_insert_kernel(const __grid_
 #pragma unroll
       for (int o = kLanes / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(group, top, o));
       if (r < p.NR && live) {
-        // exact divisions: the codes are those of the definition in fp32
-        const float s = top ? __fdiv_rn(__uint_as_float(top), 448.f) : 1.f;
+        // exact divisions: the codes are those of the definition in fp32, but for subnormals, which the
+        // library's fast math flushes: a quotient below the smallest normal number would be a scale of zero and
+        // the row's zeros 0 / 0, so it is raised to that number (as bits: a NaN and an infinity stay what they are)
+        const float s = top ? __uint_as_float(max(__float_as_uint(__fdiv_rn(__uint_as_float(top), 448.f)), 0x00800000u)) : 1.f;
         uint32_t w[2] = {0, 0};
 #pragma unroll
         for (int e = 0; e < 8; ++e) w[e >> 2] |= uint32_t(f32_to_e4m3(__fdiv_rn(x[e], s))) << (8 * (e & 3));

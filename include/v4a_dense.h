@@ -102,7 +102,8 @@ V4A_API int v4a_step_plan(const v4a_plan_args* args, void* workspace, size_t wor
  * [256 n, 256 n + 256): first the keys [num_kv_heads][256][dim], then the
  * values in the same layout, then for V4A_KV_FP8_TOKEN the fp32 scales of the
  * key rows [num_kv_heads][256] and of the value rows.  Formats: V4A_KV_BF16
- * and V4A_KV_FP8_TOKEN (e4m3 codes, one scale amax/448 per row).
+ * and V4A_KV_FP8_TOKEN (e4m3 codes, one scale amax/448 per row: 1 for a row of
+ * zeros, at least 2^-126, and elements below 2^-126 may count as zeros).
  */
 typedef struct {
   int32_t num_kv_heads;        /* >= 1, <= 1024 */

@@ -1,0 +1,81 @@
+"""fp8 rows whose largest element is near the smallest fp32 numbers: the
+library is built with fast math, which flushes subnormals, so amax / 448 must
+not become a zero scale (its row's zeros would be 0 / 0)."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import dense as OD
+from oracle import formats as F
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+TINY = 2.0 ** -126          # smallest normal fp32
+EDGE = 448 * TINY           # largest elements below it have a subnormal quotient
+
+
+def _rows(dim):
+    """Rows of `dim` bf16 values, each with zeros: one element, several of several sizes, around the edge, subnormal."""
+    x = torch.zeros((9, dim), dtype=torch.float64)
+    x[0, 3] = 1e-37
+    x[1, 0], x[1, 7], x[1, dim - 1] = 1e-36, -3e-37, 2e-38
+    x[2, 5] = 1e-40                               # bf16 subnormals
+    x[3, :8] = torch.tensor([2.0 ** -133, -2.0 ** -127, 2.0 ** -130, 0, 2.0 ** -128, 0, 0, 2.0 ** -132], dtype=torch.float64)
+    x[4, 1] = EDGE * (1 - 2.0 ** -7)              # just below and just above the edge
+    x[5, 1] = EDGE * (1 + 2.0 ** -7)
+    x[6, 2], x[6, 4] = -EDGE, 2.0 ** -125
+    x[7, :4] = torch.tensor([1e-30, 0, -3e-31, 1e-33], dtype=torch.float64)
+    return x.to(torch.bfloat16)                   # row 8: zeros
+
+
+def _check(codes, scale, row, where):
+    """The scale is amax / 448, at least the smallest normal number; each element within half a step of its code,
+    and of what arithmetic without subnormals loses."""
+    amax = np.abs(row).max()
+    if amax == 0:
+        assert scale == 1.0 and not (codes & 0x7f).any(), where
+        return
+    assert not ((codes & 0x7f) == 0x7f).any(), where
+    if amax < TINY:                               # flushed before the maximum, or not: both are rows of (almost) nothing
+        assert scale in (1.0, TINY), where
+        scale = TINY if scale == TINY else 0.0
+    else:
+        want = max(amax / 448, TINY)
+        assert abs(scale - want) <= 2.0 ** -22 * want, where
+    got = F.e4m3_decode(codes) * scale
+    assert (np.abs(got - row) <= 2.0 ** -4 * np.abs(row) + 2.0 ** -10 * scale + TINY).all(), where
+
+
+@pytest.mark.parametrize("dim", [64, 128, 192, 256])
+@pytest.mark.parametrize("many", [False, True])
+def test_dense_insert_and_attention(dim, many):
+    from compressed_sparse_long_c4a_gb300 import dense as D
+    x = _rows(dim)
+    reps = 300 if many else 1                     # several tokens of few rows share a CTA
+    n = len(x) * reps
+    pos = torch.arange(n, dtype=torch.int32, device=DEV)
+    table = torch.randperm(-(-n // 256) + 1, dtype=torch.int32, device=DEV)[None, :-(-n // 256)].contiguous()
+    pool = torch.full((table.shape[1] + 1, D.block_bytes(1, dim, D.KV_FP8_TOKEN)), 0xff, dtype=torch.uint8, device=DEV)
+    cache = D.DenseCache(pool, table, 1, dim, D.KV_FP8_TOKEN)
+    kv = x.repeat(reps, 1)[:, None].to(DEV)
+    ins = D.DenseInsert(cache, 0, None)
+    ins.run(None, kv, kv, None, pos, table[0].long()[(pos // 256).long()] * 256 + pos % 256)
+    torch.cuda.synchronize()
+    assert int(ins.status.item()) == 0
+    host, rows = pool.cpu().numpy(), x.double().numpy()
+    for t in range(n):
+        for which in (0, 1):
+            codes, scale = OD.raw_row(host, 1, dim, int(table[0, t // 256]), which, 0, t % 256)
+            _check(codes, float(scale), rows[t % len(x)], (t, which))
+    # every value is within 448 * 2^-100 of zero as attention reads it, in the few-row form and in the form for chunks
+    for new in (1, min(n, 200)):
+        q = torch.ones((new, 1, dim), dtype=torch.bfloat16, device=DEV)
+        out, lse = torch.full_like(q, 7.0), torch.zeros((new, 1), device=DEV)
+        D.DenseAttention(cache, 1, new, new).run(q, out, pos[n - new:].contiguous(), torch.tensor([0, new], dtype=torch.int32, device=DEV), lse)
+        assert (out.abs() <= 448 * 2.0 ** -100).all()
+        # equal logits.  The running maximum carries log2 of the value scale (down to -100), so lse is the sum of two
+        # numbers of up to 112 in log2 units: a logarithm to 2^-22 of its value and three roundings to 2^-24 make
+        # 112 ln 2 (2^-22 + 3 * 2^-24) < 2^-14.8
+        want = torch.log(torch.arange(n - new + 1, n + 1, device=DEV).double())
+        assert (lse[:, 0].double() - want).abs().max() <= 2.0 ** -14.8
+
