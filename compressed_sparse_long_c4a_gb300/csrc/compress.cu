@@ -128,7 +128,7 @@ __device__ void store_kv_row(int format, int dim, int p, bool own, float v0, flo
   // fp8 e4m3 with one fp32 scale per row: amax / 448
   float a = own ? fmaxf(fabsf(v0), fabsf(v1)) : 0.f;
   const float amax = block_reduce<true>(a, red);
-  const float s = amax > 0.f ? amax / 448.f : 1.f;
+  const float s = quant_scale(amax, 448.f);
   if (own) {
     const uint16_t c = uint16_t(f32_to_e4m3(v0 / s)) | (uint16_t(f32_to_e4m3(v1 / s)) << 8);
     reinterpret_cast<uint16_t*>(row)[p] = c;
@@ -153,7 +153,7 @@ __device__ void store_ix_row(int format, int dim, int p, bool own, float v0, flo
     for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     float s;
     if (format == V4A_IX_FP4_B32) {
-      s = m > 0.f ? m / 6.f : 1.f;
+      s = quant_scale(m, 6.f);
     } else {
       // OCP MX shared scale: 2^(floor(log2 amax) - 2), 2 = the largest power
       // of two of e2m1; exponent clamped to the normal fp32 range
@@ -175,7 +175,7 @@ __device__ void store_ix_row(int format, int dim, int p, bool own, float v0, flo
   if (lane == 0) red[warp] = wm;
   __syncthreads();
   const float m = fmaxf(red[(warp & ~1)], red[(warp & ~1) + 1]);
-  const float s = m > 0.f ? m / 448.f : 1.f;
+  const float s = quant_scale(m, 448.f);
   if (own) {
     const uint16_t c = uint16_t(f32_to_e4m3(v0 / s)) | (uint16_t(f32_to_e4m3(v1 / s)) << 8);
     reinterpret_cast<uint16_t*>(row)[p] = c;
@@ -396,7 +396,7 @@ __device__ void index_query_head(const IndexQuerySide& q, int t, int P, int h, i
     }
   }
   amax = warp_max(amax);
-  const float s = amax > 0.f ? amax / 448.f : 1.f;
+  const float s = quant_scale(amax, 448.f);
   uint16_t* out = reinterpret_cast<uint16_t*>(q.q_out + row);
 #pragma unroll
   for (int i = 0; i < kWarpPairsMax; ++i)

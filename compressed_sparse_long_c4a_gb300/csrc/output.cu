@@ -128,7 +128,7 @@ inv_rope_quant_kernel(const OutDev a) {
   }
   cluster.sync();   // no CTA leaves while others may still read its slice_amax
   const float tok = red[0];
-  const float s = tok > 0.f ? tok / 448.f : 1.f;
+  const float s = quant_scale(tok, 448.f);
   if (!landed) return;
   uint2* out = reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.out) + int64_t(t) * a.H * a.D) + c0;
   for (int c = threadIdx.x; c < nchunks; c += kThreads) {
@@ -343,7 +343,7 @@ __global__ void __launch_bounds__(256) encode_rows_kernel(const EncDev a) {
     float m = 0.f;
     for (int h = threadIdx.x; h < a.H; h += 32) m = fmaxf(m, __ldcg(ml + int64_t(h) * 2));
     m = warp_max(m);
-    if (threadIdx.x == 0) tok_s = m > 0.f ? m / 448.f : 1.f;
+    if (threadIdx.x == 0) tok_s = quant_scale(m, 448.f);
   }
   __syncthreads();
   const float sc = tok_s;

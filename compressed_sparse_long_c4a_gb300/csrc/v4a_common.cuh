@@ -63,6 +63,13 @@ __device__ __forceinline__ uint8_t f32_to_e4m3(float f) {
   return static_cast<uint8_t>(__nv_cvt_float_to_fp8(f, __NV_SATFINITE, __NV_E4M3));
 }
 
+// The scale amax / most of a row or block: 1 for zeros, and at least the smallest
+// normal number, since fast math flushes a smaller quotient to zero (the row's
+// zeros would then be 0 / 0).
+__device__ __forceinline__ float quant_scale(float amax, float most) {
+  return amax > 0.f ? fmaxf(amax / most, 0x1p-126f) : 1.f;
+}
+
 // ---- fp4 e2m1 ------------------------------------------------------------------
 // Magnitudes of the OCP e2m1 codes 0..7 (sign in bit 3).
 __device__ __forceinline__ float e2m1_to_f32(uint32_t nib) {

@@ -1,6 +1,9 @@
 """fp8 rows whose largest element is near the smallest fp32 numbers: the
 library is built with fast math, which flushes subnormals, so amax / 448 must
 not become a zero scale (its row's zeros would be 0 / 0)."""
+import ctypes as C
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -79,3 +82,48 @@ def test_dense_insert_and_attention(dim, many):
         want = torch.log(torch.arange(n - new + 1, n + 1, device=DEV).double())
         assert (lse[:, 0].double() - want).abs().max() <= 2.0 ** -14.8
 
+def test_index_query():
+    from compressed_sparse_long_c4a_gb300 import v4a
+    x = _rows(128)
+    T = len(x)
+    q = x[:, None].contiguous().to(DEV)
+    codes = torch.empty((T, 1, 128), dtype=torch.uint8, device=DEV)
+    scales, w = torch.empty((T, 1), device=DEV), torch.ones((T, 1), device=DEV)
+    ids, status = torch.arange(T, dtype=torch.int32, device=DEV), torch.zeros(1, dtype=torch.int32, device=DEV)
+    iq = v4a.IndexQuery(q.data_ptr(), codes.data_ptr(), scales.data_ptr(), w.data_ptr(), w.data_ptr(), 1.0, 1, 128, 0, 10000.0)
+    a = v4a.CompressArgs(v4a.Batch(T, ids.data_ptr(), ids.data_ptr(), T, 1), None, None, None, status.data_ptr(), None, C.pointer(iq))
+    assert v4a.lib().v4a_compress_insert(C.byref(a), None) == 0
+    torch.cuda.synchronize()
+    for t in range(T):
+        _check(codes[t, 0].cpu().numpy(), float(scales[t, 0]), x[t].double().numpy(), t)
+
+
+def test_window_key():
+    from compressed_sparse_long_c4a_gb300 import v4a
+    x = _rows(128)
+    T = len(x)
+    k = x.contiguous().to(DEV)
+    ring = torch.full((T, 4, 128), 0xff, dtype=torch.uint8, device=DEV)
+    scales = torch.full((T, 4), math.nan, device=DEV)
+    ids, pos = torch.arange(T, dtype=torch.int32, device=DEV), torch.zeros(T, dtype=torch.int32, device=DEV)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    win = v4a.Window(k.data_ptr(), 128, 0, 10000.0, F.KV_FP8_TOKEN, ring.data_ptr(), scales.data_ptr(), 4, 4)
+    a = v4a.CompressArgs(v4a.Batch(T, ids.data_ptr(), pos.data_ptr(), T, 1), None, None, C.pointer(win), status.data_ptr(), None, None)
+    assert v4a.lib().v4a_compress_insert(C.byref(a), None) == 0
+    torch.cuda.synchronize()
+    assert int(status.item()) == 0
+    for t in range(T):
+        _check(ring[t, 0].cpu().numpy(), float(scales[t, 0]), x[t].double().numpy(), t)
+
+
+def test_inv_rope_quant():
+    from compressed_sparse_long_c4a_gb300 import v4a
+    x = _rows(512)
+    T = len(x)
+    o, pos = x[:, None].contiguous().to(DEV), torch.zeros(T, dtype=torch.int32, device=DEV)
+    out, scales = torch.empty((T, 1, 512), dtype=torch.uint8, device=DEV), torch.empty(T, device=DEV)
+    a = v4a.OutputArgs(T, pos.data_ptr(), 1, 512, 0, 10000.0, o.data_ptr(), 1, out.data_ptr(), scales.data_ptr())
+    assert v4a.lib().v4a_inv_rope_quant(C.byref(a), None) == 0
+    torch.cuda.synchronize()
+    for t in range(T):
+        _check(out[t, 0].cpu().numpy(), float(scales[t]), x[t].double().numpy(), t)
