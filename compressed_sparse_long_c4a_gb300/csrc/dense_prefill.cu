@@ -100,7 +100,7 @@ __global__ void __launch_bounds__(Roles<kFp8>::kThreads, 1) dense_prefill_kernel
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(&s.q_full[i], kRows);
-      tc::mbar_init(&s.k_full[i], kLoaders);
+      tc::mbar_init(&s.k_full[i], kLoaders + (kFp8 ? 0 : 1));
       tc::mbar_init(&s.v_full[i], kLoaders);
       tc::mbar_init(&s.k_free[i], 1);
       tc::mbar_init(&s.v_free[i], 1);
@@ -416,6 +416,8 @@ __global__ void __launch_bounds__(Roles<kFp8>::kThreads, 1) dense_prefill_kernel
           for (int half = 0; half < 2; ++half) {
             ok = wait_for(half ? &s.v_free[n & 1] : &s.k_free[n & 1], ((n >> 1) & 1) ^ 1, a.status, abort_flag);
             if (!ok) break;
+            // the copies' own arrivals release no plain store: s.missing has one of its own
+            if (half == 0 && lt == 0) tc::mbar_arrive(&s.k_full[n & 1]);
             const uint8_t* src = block + (int64_t(half * a.K) * kBlockPositions + at) * kRow;
             const uint32_t dst = (half ? v0 : k0) + (n & 1) * kTileBytes;
             // thread lt: chunk lt % (dim / 8) of rows lt / (dim / 8) + k * (96 / (dim / 8))

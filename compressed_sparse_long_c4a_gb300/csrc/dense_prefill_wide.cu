@@ -81,7 +81,7 @@ __global__ void __launch_bounds__(Wide<D, kFp8>::kThreads, 1) dense_prefill_wide
   if (tid == 0) {
     tc::mbar_init(&s.q_full, kRows);
     for (int i = 0; i < 2; ++i) {
-      tc::mbar_init(&s.k_full[i], W::kLoaders);
+      tc::mbar_init(&s.k_full[i], W::kLoaders + (kFp8 ? 0 : 1));
       tc::mbar_init(&s.v_full[i], W::kLoaders);
       tc::mbar_init(&s.k_free[i], 1);
       tc::mbar_init(&s.v_free[i], 1);
@@ -359,6 +359,8 @@ __global__ void __launch_bounds__(Wide<D, kFp8>::kThreads, 1) dense_prefill_wide
           } else {
             ok = wait_for(free, ((n >> 1) & 1) ^ 1, a.status, abort_flag);
             if (!ok) break;
+            // the copies' own arrivals release no plain store: s.missing has one of its own
+            if (half == 0 && lt == 0) tc::mbar_arrive(full);
             const int r0 = lt / (D / 8), ch = lt % (D / 8);      // four rows a pass
 #pragma unroll
             for (int k = 0; k < kKeys / 4; ++k) {
