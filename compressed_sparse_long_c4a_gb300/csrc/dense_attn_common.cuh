@@ -134,7 +134,8 @@ struct SplitDev {
 
 // A unit that starts in a CTA's range and goes on in the next CTAs' up to `last`:
 // its pieces are this CTA's slot 1 and slot 0 of the others.  rows = 0: none.
-struct alignas(32) JoinDesc { int rows, row0, s0, hk, last, pad[3]; };
+struct alignas(16) JoinDesc { int rows, row0, s0, hk, last, pad[3]; };
+static_assert(alignof(JoinDesc) <= 16 && sizeof(JoinDesc) == 32, "lies at the front of a workspace, which the caller aligns to 16 bytes");
 
 constexpr int kMaxSplitUnits = 512;   // more units than these fill the machine one by one
 constexpr int kSms = 152;

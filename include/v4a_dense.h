@@ -92,8 +92,8 @@ typedef struct {
   int32_t* status;             /* optional device word */
 } v4a_plan_args;
 
-/* Bytes of device workspace v4a_step_plan needs (0 on bad arguments); its
- * contents need no initialisation. */
+/* Bytes of device workspace v4a_step_plan needs (0 on bad arguments); it is
+ * 16-byte aligned and its contents need no initialisation. */
 V4A_API size_t v4a_plan_workspace_size(const v4a_plan_args* args);
 V4A_API int v4a_step_plan(const v4a_plan_args* args, void* workspace, size_t workspace_bytes, void* stream);
 
@@ -240,8 +240,8 @@ typedef struct {
   int32_t* status;             /* optional device word */
 } v4a_dense_attn_args;
 
-/* Bytes of device workspace v4a_dense_attn needs (0 on a bad shape); its
- * contents need no initialisation. */
+/* Bytes of device workspace v4a_dense_attn needs (0 on a bad shape); it is
+ * 16-byte aligned and its contents need no initialisation. */
 V4A_API size_t v4a_dense_attn_workspace_size(const v4a_dense_attn_args* args);
 V4A_API int v4a_dense_attn(const v4a_dense_attn_args* args, void* workspace, size_t workspace_bytes, void* stream);
 
