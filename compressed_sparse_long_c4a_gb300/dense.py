@@ -95,7 +95,14 @@ def _want(t, name, dtype, device, shape=None, contiguous=True):
 class _Op:
     """Launches on the tensors' device, whatever the current one is.  A handle
     keeps one argument struct and one workspace: calls that may run at the same
-    time (streams, threads, graphs replayed side by side) need handles of their own."""
+    time (streams, threads, graphs replayed side by side) need handles of their own.
+
+    The handle's own tensors are made on the stream that is current at its
+    construction.  Its first call on another stream waits for that, and the
+    handle may be dropped while calls are queued; neither holds for a capture:
+    construct the handle before it (torch.cuda.graph synchronises when it
+    begins) and keep the handle as long as the graph.  The caller's tensors are
+    the caller's to order and to keep."""
 
     def _launch(self, stream):
         """Calls the C entry on the kept argument struct."""
@@ -108,6 +115,8 @@ class _Op:
             raise ValueError(f"{self._where}: the stream is on {stream.device}, the tensors on {dev}")
         else:
             raw = stream.cuda_stream
+        if raw not in self._streams:
+            self._enter(raw, torch.cuda.current_stream(dev) if stream is None else stream)
         if torch.cuda.current_device() == dev.index:
             rc = self._fn(*self._call, raw)
         else:
@@ -116,10 +125,30 @@ class _Op:
         if rc:
             v4a._check(self._where, rc)
 
-    def _bind(self, where, fn, workspace=None):
+    def _enter(self, raw, stream):
+        """The first call on a stream: behind the construction, whose memory the stream uses from now on."""
+        with torch.cuda.stream(stream):
+            if torch.cuda.is_current_stream_capturing():
+                return
+        if self._made is not None:
+            stream.wait_event(self._made)
+        for t in self._own:
+            t.record_stream(stream)
+        self._streams.add(raw)
+
+    def _bind(self, where, fn, workspace=None, outputs=()):
+        """The C entry, and the tensors that the handle has made for it."""
         self._where, self._fn, self.workspace = where, fn, workspace
         ws = () if workspace is None else (workspace.data_ptr(), workspace.numel())
         self._call = (C.byref(self.args), *ws)
+        self._own = [t for t in (self.status, workspace, *outputs) if t is not None]
+        self._streams, self._made = set(), None
+        if self.device.type == "cuda":
+            with torch.cuda.device(self.device):
+                self._streams.add(torch._C._cuda_getCurrentRawStream(self.device.index))
+                if not torch.cuda.is_current_stream_capturing():
+                    self._made = torch.cuda.Event()
+                    self._made.record()
 
 
 class StepPlan(_Op):
@@ -148,7 +177,8 @@ class StepPlan(_Op):
         need = lib().v4a_plan_workspace_size(C.byref(self.args))
         if need == 0:
             raise ValueError("StepPlan: sizes outside v4a_step_plan's limits")
-        self._bind("v4a_step_plan", lib().v4a_step_plan, torch.empty(need, dtype=torch.uint8, device=dev))
+        self._bind("v4a_step_plan", lib().v4a_step_plan, torch.empty(need, dtype=torch.uint8, device=dev),
+                   (self.seq_ids, self.positions, self.slots, self.token_starts))
 
     def run(self, cached: torch.Tensor, fresh: torch.Tensor, free_in: torch.Tensor, free_out: torch.Tensor | None = None,
             stream=None):

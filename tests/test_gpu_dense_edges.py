@@ -69,3 +69,79 @@ def test_plan_workspaces_on_sixteen_bytes():
     for name in ("seq_ids", "positions", "slots", "token_starts", "block_table", "free_ring"):
         assert torch.equal(getattr(want, name), getattr(got, name)), name
     assert (whole[:at] == 0xa5).all() and (whole[at + need:] == 0xa5).all()
+
+
+def test_plan_on_another_stream_than_its_construction():
+    """What the constructor queues (here behind a fifth of a second of other work) comes before a first run elsewhere."""
+    _run_plan([10], [1], np.array([[[3]]], np.int32), np.arange(8, dtype=np.int32), 0, 8, 1)      # loads the kernels
+    tables = torch.tensor([[[3, -1], [4, -1]]], dtype=torch.int32, device=DEV)
+    ring, args = torch.arange(8, dtype=torch.int32, device=DEV), [torch.tensor(x, dtype=torch.int32, device=DEV) for x in ([10, 250], [1, 10], [5, 3])]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(400_000_000)
+    plan = _dense().StepPlan(tables, ring, 11)
+    plan.run(*args, stream=side)
+    torch.cuda.synchronize()
+    assert plan.positions.tolist() == [10, *range(250, 260)] and plan.seq_ids.tolist() == [0] + [1] * 10
+    assert plan.slots[0].tolist() == [3 * 256 + 10, *(4 * 256 + i for i in range(250, 256)), *(5 * 256 + i for i in range(4))]
+    assert plan.token_starts.tolist() == [0, 1, 11] and args[2].tolist() == [6, 2]
+
+
+def test_insert_and_attention_on_another_stream_than_their_construction():
+    """Status words are cleared before the first run, wherever it is."""
+    layer = Layer((300, 200), 4, 2, 64, False, seed=2, holes=[(0, 0)])
+    q, x = layer.query(2), torch.ones((2, 2, 64), dtype=torch.bfloat16, device=DEV)
+    out, pos, starts = torch.empty_like(q), torch.tensor([299, 199], dtype=torch.int32, device=DEV), torch.arange(3, dtype=torch.int32, device=DEV)
+    slots = torch.tensor([-2, -1], device=DEV)
+    for warm in (True, False):
+        side = torch.cuda.Stream()
+        torch.cuda.synchronize()
+        if not warm:
+            torch.cuda._sleep(400_000_000)
+        att, ins = _dense().DenseAttention(layer.cache, 4, 2), _dense().DenseInsert(layer.cache, 0, None)
+        att.run(q, out, pos, starts, stream=side)
+        with torch.cuda.stream(side):
+            ins.run(None, x, x, None, pos, slots)
+        torch.cuda.synchronize()
+        assert int(att.status.item()) == 1 and int(ins.status.item()) == 1
+
+
+def test_handles_dropped_while_their_calls_are_queued():
+    """The memory of a dropped handle is not another tensor's before its calls on a side stream are done."""
+    layer = Layer((5000, 300), 8, 2, 128, False, seed=3)
+    pos, starts = _runs((4999, 170), (1, 130))
+    op, q, want, _ = _attend(layer, pos, starts, tokens={0, 1, 130})
+    args = (torch.tensor(pos, dtype=torch.int32, device=DEV), torch.tensor(starts, dtype=torch.int32, device=DEV))
+    size, side = op.workspace.numel(), torch.cuda.Stream()
+    out = torch.zeros_like(want)
+    torch.cuda.synchronize()
+    op = _dense().DenseAttention(layer.cache, 8, len(pos), 130)
+    at = op.workspace.data_ptr()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(400_000_000)
+    op.run(q, out, *args, stream=side)
+    del op
+    taken = [torch.empty(size, dtype=torch.uint8, device=DEV) for _ in range(4)]
+    assert all(t.data_ptr() != at for t in taken)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+
+
+def test_first_call_of_a_stream_inside_a_capture():
+    """A handle made before the capture may have its first call in it, and is used eagerly on that stream after it."""
+    layer = Layer((700, 90), 8, 2, 64, False, seed=4)
+    pos, starts = torch.tensor([699, 89], dtype=torch.int32, device=DEV), torch.arange(3, dtype=torch.int32, device=DEV)
+    op, q, want, _ = _attend(layer, [699, 89], [0, 1, 2])
+    fresh = _dense().DenseAttention(layer.cache, 8, 2)
+    out, stream = torch.zeros_like(want), torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        fresh.run(q, out, pos, starts)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+    out.zero_()
+    torch.cuda.synchronize()
+    fresh.run(q, out, pos, starts, stream=stream)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and int(fresh.status.item()) == 0
