@@ -13,10 +13,15 @@
 // filled by the same CTA; larger ones by a second, wide kernel that starts
 // while the first drains (programmatic dependent launch).
 //
-// Bound: latency.  The output of the largest steps is under a megabyte (4
-// sequences x 1024 tokens x 60 tables: 2 MB, 0.3 us of the memory's rate), and
-// the two launches, the loads and the scan one after the other take 5.5 us on
-// the device whatever the size; 64 decoding sequences with one table 3.4 us.
+// Bound: latency.  The loads, the scan and the two launches one after the other
+// take 5 to 6 us on the device (64 decoding sequences with 60 tables 5.2, 4 x
+// 1024 tokens with 60 tables, whose slots are 2 MB, 5.8, 1000 sequences 6 to 7,
+// 8000 19: the scan's eight rounds); 64 decoding sequences with one table 3.3.
+// A step that ends long sequences moves their pages too: table rows lie far
+// apart, so each page is a sector of its own (one sequence of 1M positions, 61
+// tables, 250k pages: 8.9 us over 152 SMs, 156 in a step that one CTA fills).
+#include <algorithm>
+
 #include "tc_common.cuh"
 #include "v4a_dense.h"
 #include "v4a_dense_internal.h"
@@ -28,9 +33,14 @@ constexpr int kScanThreads = 1024;
 constexpr int kFillThreads = 256;
 constexpr int kTablesPerItem = 4;     // tables one thread writes for its token
 constexpr int kMaxSeqs = 8192;
+constexpr uint32_t kBackBatch = 8;    // given-back pages a thread has under way
 // Steps of at most this many (token, table group) items are filled by the
 // scanning CTA: a second launch costs more than they take (64 items: 3.4 us
 // inline, 4.6 wide; 960: 5.9 and 5.3; 2048: 6.5 and 5.5; 4096: 10.1 and 5.5).
+// Given-back pages are not counted, since only the device knows them: a small
+// step that ends a sequence of 4096 pages takes 5.7 us, of 31k 22, of 250k 156
+// (wide 8.9), once in a sequence's life, and the second launch in every small
+// step would cost more (8 sequences, 61 tables: 3.6 us inline, 5 wide).
 constexpr int64_t kInlineItems = 512;
 
 struct PlanHeader {                   // in the workspace, before the sums
@@ -115,24 +125,37 @@ __device__ void fill(const PlanDev& p, const PlanHeader& h, const int32_t* st, c
       a.slots[int64_t(l) * T + t] = slot;
     }
   }
-  // new table entries: (block, table) pairs, tables fastest (the ring's order)
-  const int64_t fresh = int64_t(h.fresh_blocks) * L;
-  for (int64_t it = tid; it < fresh; it += n) {
-    const int j = int(it / L), l = int(it - int64_t(j) * L);
+  // new table entries: (block, table) pairs, tables fastest (the ring's order); at most 2^30, as the ring has
+  const uint32_t fresh = uint32_t(h.fresh_blocks) * uint32_t(L), step = uint32_t(n);
+  for (uint32_t it = uint32_t(tid); it < fresh; it += step) {
+    const int j = int(it / uint32_t(L)), l = int(it - uint32_t(j) * uint32_t(L));
     const int b = find_row(nb, B, j);
     const int k = blocks_for(a.cached[b]) + (j - nb[b]);
     const int32_t page = a.free_ring[ring_at(a, h.first, it)];
     if (page < 0 || page >= a.num_blocks) report(a.status, V4A_DEV_BAD_BLOCK);
     a.block_table[int64_t(l) * a.table_stride + int64_t(b) * a.max_blocks + k] = page;
   }
-  // given-back pages, behind the last free one
-  const int64_t back = int64_t(h.back_blocks) * L;
-  for (int64_t it = tid; it < back; it += n) {
-    const int j = int(it / L), l = int(it - int64_t(j) * L);
-    const int b = find_row(bb, B, j);
-    const int32_t page = a.block_table[int64_t(l) * a.table_stride + int64_t(b) * a.max_blocks + (j - bb[b])];
-    if (page < 0 || page >= a.num_blocks) report(a.status, V4A_DEV_BAD_BLOCK);
-    a.free_ring[ring_at(a, h.first, int64_t(h.count) + it)] = page;
+  // given-back pages, behind the last free one; a thread's loads of several are under way together
+  const uint32_t back = uint32_t(h.back_blocks) * uint32_t(L);
+  for (uint32_t i0 = uint32_t(tid); i0 < back; i0 += kBackBatch * step) {
+    int32_t page[kBackBatch];
+#pragma unroll
+    for (uint32_t u = 0; u < kBackBatch; ++u) {
+      const uint32_t it = i0 + u * step;
+      page[u] = 0;
+      if (it < back) {
+        const int j = int(it / uint32_t(L)), l = int(it - uint32_t(j) * uint32_t(L));
+        const int b = find_row(bb, B, j);
+        page[u] = a.block_table[int64_t(l) * a.table_stride + int64_t(b) * a.max_blocks + (j - bb[b])];
+      }
+    }
+#pragma unroll
+    for (uint32_t u = 0; u < kBackBatch; ++u) {
+      const uint32_t it = i0 + u * step;
+      if (it >= back) break;
+      if (page[u] < 0 || page[u] >= a.num_blocks) report(a.status, V4A_DEV_BAD_BLOCK);
+      a.free_ring[ring_at(a, h.first, int64_t(h.count) + it)] = page[u];
+    }
   }
 }
 
@@ -236,6 +259,8 @@ __global__ void __launch_bounds__(kFillThreads) plan_fill(const PlanDev p) {
   pdl_trigger();
   pdl_wait();
   const PlanHeader h = *p.hdr;
+  const int64_t most = max(p.items, int64_t(max(h.fresh_blocks, h.back_blocks)) * p.a.num_tables);
+  if (int64_t(blockIdx.x) * kFillThreads >= most) return;
   for (int b = tid; b <= B; b += kFillThreads) {
     st[b] = p.a.token_starts[b];
     nb[b] = p.sums[b];
@@ -284,7 +309,10 @@ int step_plan(const v4a_plan_args* a, void* ws, size_t ws_bytes, cudaStream_t st
   }
   cudaError_t e = launch_pdl(plan_scan, dim3(1), dim3(kScanThreads), smem, stream, p);
   if (e == cudaSuccess && !p.inline_fill) {
-    const int64_t want = (p.items + kFillThreads - 1) / kFillThreads;
+    // enough CTAs for the tokens, and one an SM for the pages that a step may give back (how many only the device
+    // knows; CTAs that find nothing leave)
+    const int64_t pages = std::min(int64_t(a->ring_cap), int64_t(a->num_seqs) * a->max_blocks * a->num_tables);
+    const int64_t want = std::max((p.items + kFillThreads - 1) / kFillThreads, std::min((pages + kFillThreads - 1) / kFillThreads, int64_t(152)));
     const int grid = int(want < 152 * 8 ? want : 152 * 8);
     e = launch_pdl(plan_fill, dim3(grid), dim3(kFillThreads), smem, stream, p);
   }

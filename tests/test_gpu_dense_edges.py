@@ -5,6 +5,8 @@ import numpy as np
 import pytest
 import torch
 
+from oracle import dense as OD
+
 from .test_gpu_dense import DEV, Layer, _attend, _dense, _plan_case, _run_plan, _runs
 
 pytestmark = pytest.mark.gpu
@@ -145,3 +147,17 @@ def test_first_call_of_a_stream_inside_a_capture():
     fresh.run(q, out, pos, starts, stream=stream)
     torch.cuda.synchronize()
     assert torch.equal(out, want) and int(fresh.status.item()) == 0
+
+
+@pytest.mark.parametrize("B,L,cached_hi,ended,new", [(3, 61, 120000, 0.7, 1), (40, 61, 60000, 0.5, 1), (9, 7, 300000, 1.0, 1), (600, 3, 9000, 0.6, 2),
+                                                     (2, 300, 70000, 1.0, 1), (5, 1, 400000, 0.6, 3000)])
+def test_steps_that_end_long_sequences(B, L, cached_hi, ended, new):
+    """Far more given-back pages than tokens, in steps of few tokens (one CTA) and of more; the ring wraps."""
+    case = _plan_case(np.random.default_rng(B * 1000 + L), B, L, cached_hi, new, ended, 1)
+    cached, fresh, tables, ring, first, count, T = case
+    plan, free = _run_plan(cached, fresh, tables.copy(), ring.copy(), first, count, T)
+    sid, pos, slots, starts, first2, count2 = OD.step_plan(cached, fresh, tables, ring, first, count, T)
+    assert int(plan.status.item()) == 0 and free.tolist() == [first2, count2]
+    assert plan.seq_ids.tolist() == sid and plan.positions.tolist() == pos and plan.token_starts.tolist() == starts
+    assert np.array_equal(plan.slots.cpu().numpy(), np.array(slots).reshape(L, T))
+    assert np.array_equal(plan.block_table.cpu().numpy(), tables) and np.array_equal(plan.free_ring.cpu().numpy(), ring)
