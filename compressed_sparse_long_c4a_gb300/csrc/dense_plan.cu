@@ -39,8 +39,8 @@ constexpr uint32_t kBackBatch = 8;    // given-back pages a thread has under way
 // inline, 4.6 wide; 960: 5.9 and 5.3; 2048: 6.5 and 5.5; 4096: 10.1 and 5.5).
 // Given-back pages are not counted, since only the device knows them: a small
 // step that ends a sequence of 4096 pages takes 5.7 us, of 31k 22, of 250k 156
-// (wide 8.9), once in a sequence's life, and the second launch in every small
-// step would cost more (8 sequences, 61 tables: 3.6 us inline, 5 wide).
+// (wide 8.9), once in a sequence's life; the second launch would cost every
+// small step 1.2 us.
 constexpr int64_t kInlineItems = 512;
 
 struct PlanHeader {                   // in the workspace, before the sums

@@ -157,6 +157,10 @@ class StepPlan(_Op):
     slots [tables][max_tokens], token_starts), the status word and the workspace.
 
     num_blocks: pages of the pool (default: the ring's length).
+
+    A sequence ends with all blocks of its row.  Blocks behind a window are the
+    caller's to give back, between two calls and behind the ring's last free
+    page, and so is the end of a sequence whose row has such holes.
     """
 
     def __init__(self, block_table: torch.Tensor, free_ring: torch.Tensor, max_tokens: int, num_blocks: int | None = None):

@@ -70,6 +70,15 @@ extern "C" {
  * the step's other calls do nothing.  A page id outside [0, num_blocks) sets
  * V4A_DEV_BAD_BLOCK and gives the slot -1; it goes into the table, and back
  * behind the free pages when its sequence ends, as it is.
+ *
+ * The plan gives back whole sequences: all blocks that `cached` counts.  It
+ * takes no part in giving back blocks behind a window, and a row with holes
+ * must not be ended with fresh = -1 (its -1 entries would be counted as free
+ * pages; V4A_DEV_BAD_BLOCK is set).  A caller that gives such blocks back does
+ * so between two calls, behind the last free page: free_ring[(first + count) %
+ * ring_cap] and so on, count grown by as many, the table's entries set to -1.
+ * It ends the sequence in the same way, with the pages that are left; the row
+ * then starts anew at cached = 0.
  */
 typedef struct {
   int32_t num_seqs;            /* B: 0..8192 */
@@ -201,9 +210,9 @@ V4A_API int v4a_dense_insert(const v4a_dense_insert_args* args, void* stream);
  *   out[t][h] = sum_j softmax(z)_j value_j over the visible j,
  *   lse[t][h] = ln sum_j exp(z_j).
  * Positions in a block that is unallocated or out of range are left out and
- * set V4A_DEV_BAD_BLOCK (blocks that no query sees are never looked up, so a
- * window layer may give them back); a query with nothing left gets 0 and
- * lse = -inf.  A sequence whose entries are inconsistent (starts not
+ * set V4A_DEV_BAD_BLOCK (blocks that no query sees are never looked up, so the
+ * caller of a window layer may give them back, see v4a_step_plan); a query
+ * with nothing left gets 0 and lse = -inf.  A sequence whose entries are inconsistent (starts not
  * increasing or past num_tokens, more than max_new_per_seq tokens, first
  * position negative, last position not first + tokens - 1 or past max_blocks)
  * sets V4A_DEV_BAD_BATCH and its rows are left as they were, as are the rows

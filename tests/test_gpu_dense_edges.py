@@ -161,3 +161,69 @@ def test_steps_that_end_long_sequences(B, L, cached_hi, ended, new):
     assert plan.seq_ids.tolist() == sid and plan.positions.tolist() == pos and plan.token_starts.tolist() == starts
     assert np.array_equal(plan.slots.cpu().numpy(), np.array(slots).reshape(L, T))
     assert np.array_equal(plan.block_table.cpu().numpy(), tables) and np.array_equal(plan.free_ring.cpu().numpy(), ring)
+
+
+@pytest.mark.parametrize("layers", [1, 2])
+def test_window_layers_whose_caller_gives_blocks_back(layers):
+    """A window layer's sequence far longer than its pages: between two plans the caller puts blocks that no later
+    query sees behind the last free page, and ends the sequence so; the pages serve the next one.  With two layers the
+    second keeps every block."""
+    D = _dense()
+    H, K, dim, window, sinks, cols = 4, 2, 64, 300, 4, 9
+    pages = 7 if layers == 1 else 7 + cols
+    i32 = dict(dtype=torch.int32, device=DEV)
+    tables, ring = torch.full((layers, 1, cols), -1, **i32), torch.randperm(pages, device=DEV).to(torch.int32)
+    free, cached, fresh = torch.tensor([3, pages], **i32), torch.zeros(1, **i32), torch.zeros(1, **i32)
+    pool = torch.full((pages, OD.block_bytes(K, dim, False)), 0xff, dtype=torch.uint8, device=DEV)
+    caches = [D.DenseCache(pool, tables[l], K, dim) for l in range(layers)]
+    plan = D.StepPlan(tables, ring, 256)
+    ins = [D.DenseInsert(c, 0, None) for c in caches]
+    att = [D.DenseAttention(c, H, 256, 256, window if l == 0 else 0, sinks if l == 0 else 0) for l, c in enumerate(caches)]
+    g = torch.Generator().manual_seed(1)
+
+    def give_back(l, blocks):
+        first, count = free.tolist()
+        held = [n for n in blocks if int(tables[l, 0, n]) >= 0]
+        for i, n in enumerate(held):
+            ring[(first + count + i) % pages] = tables[l, 0, n]
+            tables[l, 0, n] = -1
+        free[1] += len(held)
+
+    for life in range(2):
+        history = torch.zeros((2, 0, K, dim))
+        at = 0
+        for new in (250, 256, 1, 200, 256, 256, 17, 256, 256, 1, 100, 256):
+            kv = torch.randn((2, 256, K, dim), generator=g).to(torch.bfloat16)
+            q = torch.randn((256, H, dim), generator=g).to(torch.bfloat16).to(DEV)
+            cached.fill_(at)
+            fresh.fill_(new)
+            plan.run(cached, fresh, free)
+            assert int(plan.status.item()) == 0 and plan.token_starts.tolist() == [0, new]
+            held = tables[tables >= 0].tolist()
+            assert len(set(held)) == len(held) == pages - int(free[1])
+            history = torch.cat([history, kv[:, :new].float()], 1)
+            for l in range(layers):
+                out, lse = torch.empty_like(q), torch.zeros((256, H), device=DEV)
+                ins[l].run(None, kv[0].to(DEV), kv[1].to(DEV), None, plan.positions, plan.slots[l])
+                att[l].run(q, out, plan.positions, plan.token_starts, lse)
+                assert int(ins[l].status.item()) == 0 and int(att[l].status.item()) == 0
+                for t in (0, new // 2, new - 1):
+                    seen = OD.visible(at + t, *((window, sinks) if l == 0 else (0, 0)))
+                    for h in range(K):
+                        k, v = (history[i, seen, h].double().numpy() for i in (0, 1))
+                        o, _, av, amp = OD.attention(q[t, 2 * h:2 * h + 2].double().cpu().numpy(), k, v, dim ** -0.5)
+                        tol = (2.0 ** -8 + 2 * (dim + 8) * 2.0 ** -24 * amp[:, None] + 2 * (len(seen) + 32) * 2.0 ** -24) * av + 2.0 ** -8 * np.abs(o)
+                        assert (np.abs(out[t, 2 * h:2 * h + 2].double().cpu().numpy() - o) <= tol).all(), (life, l, at, t)
+            at += new
+            # a query from `at` on sees j > at - window and j < sinks
+            give_back(0, [n for n in range(1, cols) if 256 * n + 255 <= at - window])
+        assert at > 2000
+        for l in range(layers):
+            give_back(l, range(cols))
+        assert int(free[1]) == pages and sorted(ring.tolist()) == list(range(pages))
+
+
+def test_ending_a_row_with_holes_is_reported():
+    plan, free = _run_plan([300, 10], [-1, 1], np.array([[[3, -1], [4, -1]]], np.int32), np.arange(8, dtype=np.int32), 6, 2, 1)
+    assert int(plan.status.item()) == 1 and free.tolist() == [6, 4] and plan.slots.tolist() == [[4 * 256 + 10]]
+    assert plan.free_ring.tolist() == [3, -1, 2, 3, 4, 5, 6, 7]
