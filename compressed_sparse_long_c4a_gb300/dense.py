@@ -294,7 +294,9 @@ class DenseInsert(_Op):
 class DenseAttention(_Op):
     """v4a_dense_attn over `cache` (its block table's rows are the sequences).
 
-    max_new_per_seq: the most tokens one sequence brings in a call.
+    max_new_per_seq: the most tokens one sequence brings in a call.  A run of
+    T >= sequences x max_new_per_seq tokens is taken as one where each brings
+    that many, padded or not: shorter sequences then take the chunks' form.
     window: 0 for every earlier position, else the last `window` ones (own
     included) and the first `sinks`.  scale defaults to 1 / sqrt(dim).
     """

@@ -222,14 +222,18 @@ V4A_API int v4a_dense_insert(const v4a_dense_insert_args* args, void* stream);
  * Dot products and sums are fp32; the probabilities are rounded as an operand
  * of the tensor cores: to f16 for fp8 caches, to 16 bits for bf16 caches, and
  * to bf16 for the sequences of a bf16 cache that bring more than 32 rows
- * (tokens x heads per KV head; 16 of dim 256).  fp8 value scales below 2^-100
+ * (tokens x heads per KV head; 16 of dim 256) and in the full calls below.  fp8 value scales below 2^-100
  * are read as 2^-100.  Sequences that share tokens (entries not increasing)
  * set V4A_DEV_BAD_BATCH once they are more than the call has room for, and
  * what their rows hold then is not defined.
  *
- * A batch may mix decoding sequences and chunks; a call where every sequence
- * brings max_new_per_seq tokens (num_tokens = num_seqs * max_new_per_seq)
- * saves the launches for the other kind.  V4A_ERR_UNSUPPORTED: max_new_per_seq
+ * A batch may mix decoding sequences and chunks.  A call whose num_tokens
+ * reaches num_seqs * max_new_per_seq is taken as one where every sequence
+ * brings max_new_per_seq tokens and saves the launches for the other kind:
+ * in a batch padded that far, sequences of few rows are attended to in the
+ * form for chunks (probabilities in bf16 over bf16 caches, about twice the
+ * time); a num_tokens below that, by one token of padding less for instance,
+ * keeps each kind its own.  V4A_ERR_UNSUPPORTED: max_new_per_seq
  * * num_heads / num_kv_heads of 2^30 rows or more.
  */
 typedef struct {

@@ -7,8 +7,6 @@ output almost cancels: its own rounding (2^-8 of it) is small beside
 sum p|v|, and what is left of the tolerance is the probabilities' rounding.
 Half steps of a value: bf16 2^-8, f16 2^-11, and two bf16 operands 2^-16 (the
 second holds what the first left, at most 2^-8 of it, to 2^-8)."""
-import math
-
 import numpy as np
 import pytest
 import torch
