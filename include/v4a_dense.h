@@ -169,8 +169,9 @@ typedef struct {
  * encoded into slot slots[t] (block slots[t] / 256, row slots[t] % 256) of
  * every KV head.  A token with slot -1 is skipped and its q_out row is left as
  * it was; a slot below -1 or past the pool sets V4A_DEV_BAD_BLOCK, a negative
- * position with a valid slot V4A_DEV_BAD_BATCH, and the token is skipped.  Two
- * tokens with one slot leave one of them there (which one is not defined).
+ * position with a valid slot V4A_DEV_BAD_BATCH, and the token is skipped.  The
+ * rows of a slot that two tokens of a call share hold pieces of either (an fp8
+ * row perhaps one's codes with the other's scale): nothing is to be read there.
  * q, k and v are rows of bf16 with a stride between tokens (three views of one
  * projection's output, for instance); heads are contiguous.  All row pointers
  * must be 16-byte aligned, the token strides multiples of 8 elements, the

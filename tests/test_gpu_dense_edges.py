@@ -227,3 +227,25 @@ def test_ending_a_row_with_holes_is_reported():
     plan, free = _run_plan([300, 10], [-1, 1], np.array([[[3, -1], [4, -1]]], np.int32), np.arange(8, dtype=np.int32), 6, 2, 1)
     assert int(plan.status.item()) == 1 and free.tolist() == [6, 4] and plan.slots.tolist() == [[4 * 256 + 10]]
     assert plan.free_ring.tolist() == [3, -1, 2, 3, 4, 5, 6, 7]
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_insert_of_two_tokens_with_one_slot(fp8):
+    """Pieces of either there, and every other slot and every query as without the clash."""
+    D = _dense()
+    K, dim, T, fmt = 2, 128, 400, D.KV_FP8_TOKEN if fp8 else D.KV_BF16
+    g = torch.Generator(device=DEV).manual_seed(1)
+    x = torch.randn((T, 4 + 2 * K, dim), generator=g, device=DEV).to(torch.bfloat16)
+    pos, slots = torch.arange(T, dtype=torch.int32, device=DEV), torch.arange(T, device=DEV)
+    got = []
+    for s in (slots, torch.where(slots >= 300, slots - 300, slots)):          # slots 0..99 twice
+        pool, qo = torch.zeros((2, D.block_bytes(K, dim, fmt)), dtype=torch.uint8, device=DEV), torch.zeros((T, 4, dim), dtype=torch.bfloat16, device=DEV)
+        op = D.DenseInsert(D.DenseCache(pool, None, K, dim, fmt), 4, D.Rope(dim, layout=1))
+        op.run(x[:, :4], x[:, 4:4 + K], x[:, 4 + K:], qo, pos, s.contiguous())
+        torch.cuda.synchronize()
+        assert int(op.status.item()) == 0
+        body = pool[:, :2 * K * 256 * dim * (1 if fp8 else 2)].contiguous().view(torch.uint8 if fp8 else torch.int16)
+        got.append((qo, body.view(2, 2 * K, 256, dim).transpose(0, 1).reshape(2 * K, 512, dim)))
+    (q0, alone), (q1, both) = got
+    assert torch.equal(q0, q1) and torch.equal(alone[:, 100:300], both[:, 100:300]) and not both[:, 300:].any()
+    assert ((both[:, :100] == alone[:, :100]) | (both[:, :100] == alone[:, 300:400])).all()
