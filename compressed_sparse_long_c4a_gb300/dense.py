@@ -198,7 +198,11 @@ class StepPlan(_Op):
 
 @dataclass
 class Rope:
-    """The position rotation of v4a_rope; table: inverse frequencies (ROPE_TABLE)."""
+    """The position rotation of v4a_rope; table: inverse frequencies (ROPE_TABLE).
+
+    ROPE_YARN blends frequencies by a ramp that is linear in their turns over
+    the original context, as the YaRN paper has it.  Many models' own code has
+    a ramp linear in the pair index instead: their frequencies are a table."""
     dims: int
     first: int = 0
     layout: int = ROPE_INTERLEAVED

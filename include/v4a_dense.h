@@ -137,7 +137,10 @@ V4A_API int64_t v4a_dense_block_bytes(int32_t num_kv_heads, int32_t dim, int32_t
 #define V4A_ROPE_LINEAR 1  /* f_j / factor (positions interpolated) */
 #define V4A_ROPE_YARN   2  /* with r_j = original f_j / (2 pi) turns over the original context and
                               g_j = clamp((r_j - beta_slow) / (beta_fast - beta_slow), 0, 1):
-                              f_j (g_j + (1 - g_j) / factor)  (YaRN, Peng et al. 2023) */
+                              f_j (g_j + (1 - g_j) / factor)  (YaRN, Peng et al. 2023).  The ramp g is
+                              linear in the turns, as in the paper; a model whose ramp is linear in the
+                              pair index j, between the (rounded) indices whose r is beta_fast and
+                              beta_slow, has other frequencies there and takes V4A_ROPE_TABLE */
 #define V4A_ROPE_TABLE  3  /* f_j = inv_freq[j], for any other rule */
 
 /*

@@ -211,3 +211,21 @@ def test_binding_refuses_tensors(lib):
                  (torch.zeros((9, 4, 64), dtype=torch.bfloat16), q, pos, two), (q, q.clone(), pos, two)):
         with pytest.raises(ValueError):
             att.run(*args)
+
+
+def test_yarn_ramp_over_pair_indices_is_a_table(lib):
+    """The ramp that is linear in the pair index agrees with ROPE_YARN at both ends and not between; it goes in as a table."""
+    from oracle import dense as OD
+    dims, theta, factor, original, fast, slow = 128, 1e4, 16.0, 4096.0, 32.0, 1.0
+    index = lambda turns: dims * math.log(original / (turns * 2 * math.pi)) / (2 * math.log(theta))  # noqa: E731
+    lo, hi = math.floor(index(fast)), math.ceil(index(slow))
+    table = []
+    for j in range(dims // 2):
+        f, keep = theta ** (-2.0 * j / dims), 1 - min(max((j - lo) / (hi - lo), 0.0), 1.0)
+        table.append(f * keep + f / factor * (1 - keep))
+    yarn = OD.frequencies(dims, theta, "yarn", factor, original, fast, slow)
+    assert table[:lo] == pytest.approx(yarn[:lo], rel=1e-14) and table[hi:] == pytest.approx(yarn[hi:], rel=1e-14)
+    assert max(abs(t / y - 1) for t, y in zip(table[lo:hi], yarn[lo:hi])) > 0.3
+    for rope in (D.Rope(dims, scaling=D.ROPE_TABLE, table=table),
+                 D.Rope(dims, scaling=D.ROPE_YARN, factor=factor, original=original, beta_fast=fast, beta_slow=slow)):
+        assert lib.v4a_dense_insert(C.byref(_insert(rope=rope, num_tokens=0)), None) == 0
