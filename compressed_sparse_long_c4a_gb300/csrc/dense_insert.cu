@@ -217,7 +217,7 @@ int fill_rope(const v4a_rope& r, int dim, InsertDev* d) {
   }
   if (r.layout != V4A_ROPE_INTERLEAVED && r.layout != V4A_ROPE_HALF) return V4A_ERR_INVALID_ARG;
   if (r.scaling < V4A_ROPE_PLAIN || r.scaling > V4A_ROPE_TABLE) return V4A_ERR_INVALID_ARG;
-  if (!std::isfinite(r.magnitude)) return V4A_ERR_INVALID_ARG;
+  if (!std::isfinite(d->magnitude)) return V4A_ERR_INVALID_ARG;     // (as the kernel takes it, in fp32)
   if (r.scaling == V4A_ROPE_TABLE ? !r.inv_freq : !(r.theta > 0)) return V4A_ERR_INVALID_ARG;
   if ((r.scaling == V4A_ROPE_LINEAR || r.scaling == V4A_ROPE_YARN) && !(r.factor > 0)) return V4A_ERR_INVALID_ARG;
   if (r.scaling == V4A_ROPE_YARN && (!(r.original > 0) || !(r.beta_fast > r.beta_slow))) return V4A_ERR_INVALID_ARG;

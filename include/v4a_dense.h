@@ -158,7 +158,7 @@ typedef struct {
   double factor;               /* LINEAR, YARN: > 0 */
   double original;             /* YARN: original context length, > 0 */
   double beta_fast, beta_slow; /* YARN: beta_fast > beta_slow */
-  double magnitude;            /* factor on cos and sin (1 for none; YaRN uses 0.1 ln(factor) + 1) */
+  double magnitude;            /* factor on cos and sin, finite in fp32 (1 for none; YaRN uses 0.1 ln(factor) + 1) */
   const double* inv_freq;      /* TABLE: HOST array [dims / 2], read during the call, each in [0, pi] */
 } v4a_rope;
 

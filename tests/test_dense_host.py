@@ -229,3 +229,8 @@ def test_yarn_ramp_over_pair_indices_is_a_table(lib):
     for rope in (D.Rope(dims, scaling=D.ROPE_TABLE, table=table),
                  D.Rope(dims, scaling=D.ROPE_YARN, factor=factor, original=original, beta_fast=fast, beta_slow=slow)):
         assert lib.v4a_dense_insert(C.byref(_insert(rope=rope, num_tokens=0)), None) == 0
+
+
+@pytest.mark.parametrize("magnitude,code", [(1e39, INVALID), (-1e300, INVALID), (math.nan, INVALID), (3.4e38, 0), (-1.0, 0), (0.0, 0)])
+def test_rotation_magnitude_is_finite_in_fp32(lib, magnitude, code):
+    assert lib.v4a_dense_insert(C.byref(_insert(rope=D.Rope(64, magnitude=magnitude), num_tokens=0)), None) == code
