@@ -254,7 +254,7 @@ def _rows(t, name, device, heads, dim, tokens):
     st = t.stride()
     if st[2] != 1 or st[1] != dim and heads > 1:
         raise ValueError(f"{name}: heads and dims must be contiguous")
-    return st[0] if tokens > 1 else max(st[0], heads * dim)
+    return st[0] if tokens > 1 else heads * dim      # (one token's stride may be anything, and is not used)
 
 
 class DenseInsert(_Op):

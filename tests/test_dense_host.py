@@ -234,3 +234,11 @@ def test_yarn_ramp_over_pair_indices_is_a_table(lib):
 @pytest.mark.parametrize("magnitude,code", [(1e39, INVALID), (-1e300, INVALID), (math.nan, INVALID), (3.4e38, 0), (-1.0, 0), (0.0, 0)])
 def test_rotation_magnitude_is_finite_in_fp32(lib, magnitude, code):
     assert lib.v4a_dense_insert(C.byref(_insert(rope=D.Rope(64, magnitude=magnitude), num_tokens=0)), None) == code
+
+
+def test_binding_takes_one_token_of_any_stride():
+    """A single token's rows out of a wide tensor of odd width: its stride means nothing."""
+    x = torch.zeros((3, 1001), dtype=torch.bfloat16)
+    for rows, tokens in ((x[:1, :256], 1), (x[:0, :256], 0), (x[:, :256], 3)):
+        stride = D._rows(rows.unflatten(1, (4, 64)), "q", x.device, 4, 64, tokens)
+        assert stride == (1001 if tokens == 3 else 256)
