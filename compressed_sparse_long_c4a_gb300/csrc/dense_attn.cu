@@ -667,7 +667,7 @@ int launch(const DenseAttnDev& a, const SplitDev& p, cudaStream_t stream) {
   static_assert(S::kWarps * S::kStages * S::kStage + sizeof(typename S::Tail) + split_smem(1, kMaxSplitUnits) <= 227 * 1024, "shared memory of a CTA");
   auto kern = dense_attn_mma<D, NT, kFp8>;
   static std::atomic<uint64_t> done{0};
-  if (!raise_smem(kern, 227 * 1024, &done)) return V4A_ERR_CUDA;
+  if (!once_per_device(&done, [=] { return raise_smem(kern, 227 * 1024); })) return V4A_ERR_CUDA;
   const int64_t grid = p.split ? p.grid : int64_t(p.U) * a.K;
   const cudaError_t e = launch_pdl(kern, dim3(unsigned(grid)), dim3(S::kThreads), smem, stream, a, p);
   return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? V4A_OK : V4A_ERR_CUDA;
@@ -744,6 +744,7 @@ int dense_attn(const v4a_dense_attn_args* a, void* ws, size_t ws_bytes, cudaStre
   if (takes) {
     rc = dense_prefill_plan(a, d, both ? few + 1 : 0, static_cast<uint8_t*>(ws) + few_workspace(a), &many);
     if (rc) return rc;
+    if (many.U > 0 && !dense_prefill_ready(a)) return V4A_ERR_CUDA;
     if (!both) {
       rc = dense_prefill(a, d, many, stream);
       return rc == V4A_OK && many.split ? dense_join(d, many, a->kv.dim, stream) : rc;

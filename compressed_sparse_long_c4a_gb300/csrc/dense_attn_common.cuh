@@ -152,15 +152,20 @@ __host__ __device__ constexpr size_t split_smem(int split, int U) {
 __host__ __device__ constexpr size_t split_workspace(int R, int dim, int ctas) {
   return ctas * (sizeof(JoinDesc) + size_t(2) * R * (dim + 2) * sizeof(float));      // (a multiple of 16)
 }
-// Raises a kernel's dynamic shared memory limit, once per device (`done`: the devices it is done on).
-template <typename K>
-inline bool raise_smem(K kern, int bytes, std::atomic<uint64_t>* done) {
+// f() where it has not been true on the current device yet (`done`: the devices where it was).
+template <typename F>
+inline bool once_per_device(std::atomic<uint64_t>* done, F f) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return false;
   if (dev < 64 && (done->load() >> dev & 1)) return true;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
+  if (!f()) return false;
   if (dev < 64) done->fetch_or(uint64_t(1) << dev);
   return true;
+}
+// Raises a kernel's dynamic shared memory limit on the current device.
+template <typename K>
+inline bool raise_smem(K kern, int bytes) {
+  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess;
 }
 
 inline void split_carve(SplitDev* p, void* ws, int R, int dim, int ctas, int cost) {
@@ -342,11 +347,13 @@ struct Line {
 int dense_join(const DenseAttnDev& a, const SplitDev& p, int dim, cudaStream_t stream);
 
 // The tensor-core form for many rows (dense_prefill.cu): whether it takes the
-// shape, its division (U = 0: no sequence of the call can have so many rows)
-// and its launch, whose pieces are then to be joined (p.split).
+// shape, its division (U = 0: no sequence of the call can have so many rows),
+// its kernel's readiness on the current device (ahead of the call's first
+// launch) and its launch, whose pieces are then to be joined (p.split).
 bool dense_prefill_takes(const v4a_dense_attn_args* a);
 size_t dense_prefill_workspace(const v4a_dense_attn_args* a);
 int dense_prefill_plan(const v4a_dense_attn_args* a, const DenseAttnDev& d, int rows_from, void* ws, SplitDev* p);
+bool dense_prefill_ready(const v4a_dense_attn_args* a);
 int dense_prefill(const v4a_dense_attn_args* a, const DenseAttnDev& d, const SplitDev& p, cudaStream_t stream);
 
 }  // namespace v4a

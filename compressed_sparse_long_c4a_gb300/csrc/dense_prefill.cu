@@ -457,6 +457,18 @@ __global__ void __launch_bounds__(Roles<kFp8>::kThreads, 1) dense_prefill_kernel
   pdl_trigger();
 }
 
+// The split of the registers adds up only with those that the kernel was to be built with: setmaxnreg would wait
+// for ever with fewer.  (The build's tests read them from the compiler; this is what a library built otherwise meets.)
+template <int D, bool kFp8>
+bool ready() {
+  static std::atomic<uint64_t> done{0};
+  return once_per_device(&done, [] {
+    auto kern = dense_prefill_kernel<D, kFp8>;
+    cudaFuncAttributes attr;
+    return cudaFuncGetAttributes(&attr, kern) == cudaSuccess && attr.numRegs == Roles<kFp8>::kLaunchRegs && raise_smem(kern, 227 * 1024);
+  });
+}
+
 template <int D, bool kFp8>
 int launch(const DenseAttnDev& d, const SplitDev& p, cudaStream_t stream) {
   // at least 116 KB: no two CTAs that allocate TMEM share an SM
@@ -464,11 +476,6 @@ int launch(const DenseAttnDev& d, const SplitDev& p, cudaStream_t stream) {
   if (bytes < 116 * 1024) bytes = 116 * 1024;
   static_assert(1024 + 6 * 128 * D * 2 + sizeof(PreSmem) + split_smem(1, kMaxSplitUnits) <= 227 * 1024, "shared memory of a CTA");
   auto kern = dense_prefill_kernel<D, kFp8>;
-  static std::atomic<uint64_t> done{0};
-  if (!raise_smem(kern, 227 * 1024, &done)) return V4A_ERR_CUDA;
-  cudaFuncAttributes attr;
-  if (cudaFuncGetAttributes(&attr, kern) != cudaSuccess) return V4A_ERR_CUDA;
-  if (attr.numRegs != Roles<kFp8>::kLaunchRegs) return V4A_ERR_CUDA;     // built otherwise: the split of the registers would not add up
   const int64_t grid = p.split ? p.grid : int64_t(p.U) * d.K;
   const cudaError_t e = launch_pdl(kern, dim3(unsigned(grid)), dim3(Roles<kFp8>::kThreads), bytes, stream, d, p);
   return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? V4A_OK : V4A_ERR_CUDA;
@@ -505,6 +512,13 @@ int dense_prefill_plan(const v4a_dense_attn_args* a, const DenseAttnDev& d, int 
   split_carve(&p, ws, unit, a->kv.dim, kSms, wide ? kWideUnitCost : kUnitCost);
   *out = p;
   return V4A_OK;
+}
+
+bool dense_prefill_ready(const v4a_dense_attn_args* a) {
+  const bool fp8 = a->kv.format == V4A_KV_FP8_TOKEN;
+  if (a->kv.dim > 128) return dense_prefill_wide_ready(a->kv.dim, fp8);
+  if (fp8) return a->kv.dim == 64 ? ready<64, true>() : ready<128, true>();
+  return a->kv.dim == 64 ? ready<64, false>() : ready<128, false>();
 }
 
 int dense_prefill(const v4a_dense_attn_args* a, const DenseAttnDev& d, const SplitDev& p, cudaStream_t stream) {

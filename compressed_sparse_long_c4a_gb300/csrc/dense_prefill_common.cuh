@@ -138,6 +138,7 @@ constexpr int kWideUnit = 128;       // rows of a unit
 // Steps that a unit's set-up and output take the time of (a chunk of 4096 tokens, 16 + 4 heads of 256: 3 steps 233
 // us, 6 175, 12 183).
 constexpr int kWideUnitCost = 6;
+bool dense_prefill_wide_ready(int dim, bool fp8);
 int dense_prefill_wide(int dim, bool fp8, const DenseAttnDev& d, const SplitDev& p, cudaStream_t stream);
 
 }  // namespace v4a

@@ -390,19 +390,28 @@ __global__ void __launch_bounds__(Wide<D, kFp8>::kThreads, 1) dense_prefill_wide
 }
 
 template <int D, bool kFp8>
+bool ready() {
+  static std::atomic<uint64_t> done{0};
+  return once_per_device(&done, [] { return raise_smem(dense_prefill_wide_kernel<D, kFp8>, 227 * 1024); });
+}
+
+template <int D, bool kFp8>
 int launch(const DenseAttnDev& d, const SplitDev& p, cudaStream_t stream) {
   // more than 116 KB: no two CTAs that allocate TMEM share an SM
   const size_t bytes = 1024 + Wide<D, kFp8>::kQBytes + 4 * Wide<D, kFp8>::kStepBytes + sizeof(WideSmem) + split_smem(p.split, p.U);
   static_assert(1024 + Wide<D, kFp8>::kQBytes + 4 * Wide<D, kFp8>::kStepBytes + sizeof(WideSmem) + split_smem(1, kMaxSplitUnits) <= 227 * 1024, "shared memory of a CTA");
   auto kern = dense_prefill_wide_kernel<D, kFp8>;
-  static std::atomic<uint64_t> done{0};
-  if (!raise_smem(kern, 227 * 1024, &done)) return V4A_ERR_CUDA;
   const int64_t grid = p.split ? p.grid : int64_t(p.U) * d.K;
   const cudaError_t e = launch_pdl(kern, dim3(unsigned(grid)), dim3(Wide<D, kFp8>::kThreads), bytes, stream, d, p);
   return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? V4A_OK : V4A_ERR_CUDA;
 }
 
 }  // namespace
+
+bool dense_prefill_wide_ready(int dim, bool fp8) {
+  if (dim == 192) return fp8 ? ready<192, true>() : ready<192, false>();
+  return fp8 ? ready<256, true>() : ready<256, false>();
+}
 
 int dense_prefill_wide(int dim, bool fp8, const DenseAttnDev& d, const SplitDev& p, cudaStream_t stream) {
   if (dim == 192) return fp8 ? launch<192, true>(d, p, stream) : launch<192, false>(d, p, stream);
