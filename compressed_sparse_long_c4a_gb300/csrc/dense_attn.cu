@@ -226,8 +226,9 @@ __global__ void __launch_bounds__(Shape<D, NT, kFp8>::kThreads, Shape<D, NT, kFp
             const uint32_t w = qf[ks][nt][i];
             qf[ks][nt][i] = pack_f16(__uint_as_float(w << 16) * up, __uint_as_float(w & 0xffff0000u) * up);
           }
-        fq[nt][0] = f * __shfl_sync(0xffffffffu, down, 4 * c2);
-        fq[nt][1] = f * __shfl_sync(0xffffffffu, down, 4 * c2 + 4);
+        // at least the smallest normal number: flushed to zero, it would make NaNs of hidden keys' -inf
+        fq[nt][0] = fmaxf(f * __shfl_sync(0xffffffffu, down, 4 * c2), 0x1p-126f);
+        fq[nt][1] = fmaxf(f * __shfl_sync(0xffffffffu, down, 4 * c2 + 4), 0x1p-126f);
       }
     }
   };
@@ -731,7 +732,7 @@ int dense_attn(const v4a_dense_attn_args* a, void* ws, size_t ws_bytes, cudaStre
   d.positions = a->positions; d.starts = a->token_starts; d.bt = a->kv.block_table;
   d.pool = static_cast<const uint8_t*>(a->kv.pool);
   d.q = a->q; d.out = a->out; d.lse = a->lse; d.status = a->status;
-  d.scale_log2 = a->softmax_scale * 1.4426950408889634f;
+  d.scale_log2 = std::max(a->softmax_scale * 1.4426950408889634f, 0x1p-126f);      // (a subnormal one would be flushed)
   const bool fp8 = a->kv.format == V4A_KV_FP8_TOKEN, takes = dense_prefill_takes(a), both = takes && mixed(a);
   const int few = few_rows(a->kv.dim, fp8);
   SplitDev p{}, many{};

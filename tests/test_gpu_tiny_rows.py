@@ -127,3 +127,35 @@ def test_inv_rope_quant():
     torch.cuda.synchronize()
     for t in range(T):
         _check(out[t, 0].cpu().numpy(), float(scales[t]), x[t].double().numpy(), t)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("dim", [64, 128, 192, 256])
+@pytest.mark.parametrize("new", [1, 3, 90])
+def test_tiny_queries_and_scales(dim, new, fp8):
+    """Queries of 1e-40 to 1e-25, and a softmax scale below the smallest normal number: all logits are (almost) zero, so
+    the rows are the visible values' means, whatever the power of two that a query is brought to."""
+    from compressed_sparse_long_c4a_gb300 import dense as D
+
+    from .test_gpu_dense import Layer
+    layer = Layer((333,), 4, 2, dim, fp8, seed=dim + new)
+    sizes = (1e-40, 1e-38, 1e-36, 1e-34, 3e-33, 1e-30, 1e-25)
+    q = torch.randn((new, 4, dim), generator=layer.gen) * torch.tensor(sizes).repeat(4 * new // 7 + 1)[:4 * new].view(new, 4, 1)
+    q = q.to(torch.bfloat16)
+    q[-1, 3] = 0
+    pos = torch.arange(333 - new, 333, dtype=torch.int32, device=DEV)
+    for scale, queries in ((None, q), (1e-40, q / q.abs().amax(-1, keepdim=True).clamp_min(1e-45)), (1.2e-38, q * 0 + 1), (1e-30, q * 1e20)):
+        queries = torch.nan_to_num(queries).to(torch.bfloat16).to(DEV)
+        out, lse = torch.full_like(queries, 7.0), torch.full((new, 4), 7.0, device=DEV)
+        op = D.DenseAttention(layer.cache, 4, new, new, scale=scale)
+        op.run(queries, out, pos, torch.tensor([0, new], dtype=torch.int32, device=DEV), lse)
+        torch.cuda.synchronize()
+        got, got_l = out.double().cpu().numpy(), lse.double().cpu().numpy()
+        for t in {0, new // 2, new - 1}:
+            n = 333 - new + t + 1
+            for h in range(4):
+                v = layer.rows(0, 1, h // 2, n)
+                # the probabilities are 1 / n, a power of two before the division (fp8: with the values' scales, f16)
+                tol = ((2.0 ** -11 if fp8 else 2.0 ** -16) + 2 * (n + 32) * 2.0 ** -24) * np.abs(v).mean(0) + 2.0 ** -8 * np.abs(v.mean(0))
+                assert (np.abs(got[t, h] - v.mean(0)) <= tol).all(), (scale, t, h)
+                assert abs(got_l[t, h] - math.log(n)) <= 2.0 ** -17, (scale, t, h)
