@@ -150,7 +150,8 @@ __global__ void __launch_bounds__(kThreads, 8) dense_insert_kernel(const __grid_
       const uint32_t group = kLanes == 32 ? 0xffffffffu : ((1u << (kLanes & 31)) - 1u) << ((threadIdx.x & 31) / kLanes * kLanes);
 #pragma unroll
       for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(group, ss, o);
-      const float inv = rsqrtf(ss / float(D) + p.eps);
+      const float mean = ss / float(D) + p.eps;
+      const float inv = rsqrtf(mean < 0x1p-126f ? 0x1p-126f : mean);     // (squares that small are flushed; a NaN stays one)
       const int at0 = live ? d0 : 0, at1 = live ? d1 : 0;
       const float4 g0 = __ldg(reinterpret_cast<const float4*>(gamma + at0)), g1 = __ldg(reinterpret_cast<const float4*>(gamma + at1));
       x[0] *= inv * g0.x; x[1] *= inv * g0.y; x[2] *= inv * g0.z; x[3] *= inv * g0.w;

@@ -167,10 +167,10 @@ typedef struct {
  *   q_out[t][h] = rope_P(norm(q[t][h]; q_gamma)),   h < num_heads
  *   key         = rope_P(norm(k[t][h]; k_gamma)),   h < num_kv_heads
  *   value       = v[t][h]
- * norm(x; g) = x / sqrt(mean(x^2) + eps) * g over the head's dims (x itself
- * when the gamma pointer is NULL), in fp32 and rounded once.  Key and value are
- * encoded into slot slots[t] (block slots[t] / 256, row slots[t] % 256) of
- * every KV head.  A token with slot -1 is skipped and its q_out row is left as
+ * norm(x; g) = x / sqrt(max(mean(x^2) + eps, 2^-126)) * g over the head's dims
+ * (x itself when the gamma pointer is NULL), in fp32, where squares below
+ * 2^-126 count as zeros, and rounded once.  Key and value are encoded into
+ * slot slots[t] (block slots[t] / 256, row slots[t] % 256) of every KV head.  A token with slot -1 is skipped and its q_out row is left as
  * it was; a slot below -1 or past the pool sets V4A_DEV_BAD_BLOCK, a negative
  * position with a valid slot V4A_DEV_BAD_BATCH, and the token is skipped.  The
  * rows of a slot that two tokens of a call share hold pieces of either (an fp8

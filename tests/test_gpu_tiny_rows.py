@@ -155,7 +155,36 @@ def test_tiny_queries_and_scales(dim, new, fp8):
             n = 333 - new + t + 1
             for h in range(4):
                 v = layer.rows(0, 1, h // 2, n)
-                # the probabilities are 1 / n, a power of two before the division (fp8: with the values' scales, f16)
+                # bf16 caches: every weight is exactly one before the division; fp8: the values' scales, in f16
                 tol = ((2.0 ** -11 if fp8 else 2.0 ** -16) + 2 * (n + 32) * 2.0 ** -24) * np.abs(v).mean(0) + 2.0 ** -8 * np.abs(v.mean(0))
                 assert (np.abs(got[t, h] - v.mean(0)) <= tol).all(), (scale, t, h)
                 assert abs(got_l[t, h] - math.log(n)) <= 2.0 ** -17, (scale, t, h)
+
+
+def test_norm_without_eps():
+    """eps = 0 is allowed: a mean square below the smallest normal number is taken as that number."""
+    from compressed_sparse_long_c4a_gb300 import dense as D
+    dim = 64
+    x = torch.zeros((8, 1, dim), dtype=torch.bfloat16)
+    x[0, 0, 3] = 1e-30
+    x[1, 0, :] = 1e-21
+    x[2, 0, ::2] = -1e-19                         # squares just below 2^-126
+    x[3, 0, :40], x[3, 0, 40:] = 2e-19, 1e-19     # some below, some above
+    x[4, 0, 5] = 1e-17
+    x[5, 0, 5], x[5, 0, 6] = 1e-3, 1e-25
+    x[6, 0, 5] = 1e5                              # row 7: zeros
+    pool = torch.zeros((1, D.block_bytes(1, dim, 0)), dtype=torch.uint8, device=DEV)
+    g = torch.ones(dim, device=DEV)
+    op = D.DenseInsert(D.DenseCache(pool, None, 1, dim), 1, None, g, g, eps=0.0)
+    q = x.to(DEV)
+    out, at = torch.empty_like(q), torch.arange(8, dtype=torch.int32, device=DEV)
+    op.run(q, q, q, out, at, at.long())
+    torch.cuda.synchronize()
+    squares = x.double() ** 2
+    mean = squares.mean(-1, keepdim=True)
+    want = x.double() / torch.sqrt(mean.clamp_min(TINY))
+    got, keys = out.double().cpu(), pool.view(torch.bfloat16).view(2, 256, dim)[0, :8].double().cpu()[:, None]
+    # a mean of at least 2^-126 lacks the squares that count as zeros; a smaller one is raised with or without them
+    lost = torch.where(squares < TINY, squares, 0.0).mean(-1, keepdim=True)
+    rel = 2.0 ** -8 + 2.0 ** -16 + torch.where(mean >= TINY, lost / mean, 0.0)
+    assert torch.equal(got, keys) and ((got - want).abs() <= rel * want.abs()).all()
