@@ -249,3 +249,42 @@ def test_insert_of_two_tokens_with_one_slot(fp8):
     (q0, alone), (q1, both) = got
     assert torch.equal(q0, q1) and torch.equal(alone[:, 100:300], both[:, 100:300]) and not both[:, 300:].any()
     assert ((both[:, :100] == alone[:, :100]) | (both[:, :100] == alone[:, 300:400])).all()
+
+
+@pytest.mark.parametrize("T", [40, 3000])
+def test_plan_without_slots_or_status_and_with_wide_tables(T):
+    """What only the C entry takes: no slot maps, no status word, tables further apart than they are long."""
+    L, B, cols, apart = 3, 9, 5, 77
+    rng = np.random.default_rng(T)
+    cached, fresh = [int(x) for x in rng.integers(0, 1000, B)], [int(x) for x in rng.integers(0, 5, B)]
+    fresh[4] = -1
+    whole = torch.full((L, apart), 1000, dtype=torch.int32, device=DEV)
+    tables, at = np.full((L, B, cols), -1, np.int32), 0
+    for l in range(L):
+        for b, c in enumerate(cached):
+            tables[l, b, :-(-c // 256)] = np.arange(at, at - (-c // 256))
+            at += -(-c // 256)
+    whole[:, :B * cols] = torch.from_numpy(tables).to(DEV).view(L, -1)
+    ring = np.arange(200, dtype=np.int32) + 300
+    plan = _dense().StepPlan(torch.from_numpy(tables).to(DEV), torch.from_numpy(ring).to(DEV), T, num_blocks=500)
+    plan.args.block_table, plan.args.table_stride, plan.args.slots, plan.args.status = whole.data_ptr(), apart, None, None
+    free = torch.tensor([190, 100], dtype=torch.int32, device=DEV)
+    plan.run(torch.tensor(cached, dtype=torch.int32, device=DEV), torch.tensor(fresh, dtype=torch.int32, device=DEV), free)
+    torch.cuda.synchronize()
+    sid, pos, _, starts, first, count = OD.step_plan(cached, fresh, tables, ring, 190, 100, T)
+    assert plan.seq_ids.tolist() == sid and plan.positions.tolist() == pos and plan.token_starts.tolist() == starts
+    assert np.array_equal(whole[:, :B * cols].cpu().numpy().reshape(L, B, cols), tables) and (whole[:, B * cols:] == 1000).all()
+    assert plan.free_ring.tolist() == ring.tolist() and free.tolist() == [first, count]
+    assert (plan.slots == -1).all()
+
+
+def test_attention_of_default_block_bytes_without_lse_and_status():
+    """block_bytes = 0 is the shape's own size; lse and status may be NULL, in both forms."""
+    for new in (1, 150):
+        layer = Layer((400, 290), 8, 2, 64, False, seed=6, extra=0)
+        pos, starts = _runs((400 - new, 290 - new), (new, new))
+        op, q, out, _ = _attend(layer, pos, starts, pad=0, tokens={0, len(pos) - 1})
+        op.args.kv.block_bytes, op.args.status = 0, None
+        again = torch.empty_like(out)
+        op.run(q, again, torch.tensor(pos, dtype=torch.int32, device=DEV), torch.tensor(starts, dtype=torch.int32, device=DEV))
+        assert torch.equal(out, again)
