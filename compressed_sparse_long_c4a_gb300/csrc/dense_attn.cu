@@ -29,9 +29,11 @@
 //
 // bf16 caches: P is taken as the sum of two bf16 operands (16 bits), since the
 // tensor cores have the time; fp8 caches: P in f16, with the values' scales in
-// its exponent.  Measured with 32 + 8 heads of 128: 8 sequences at 8k 48 us
-// (268 MB: 5.6 TB/s), a call of 6.6 GB 6.9 TB/s, one sequence at 1000
-// positions 10.2 us (the two launches and the loads one after the other).
+// its exponent.  Measured with 32 + 8 heads of 128: 8 sequences at 8k 49 us
+// (268 MB: 5.4 TB/s) and fp8 34 (4.1), a call of 6.6 GB 6.9 TB/s, one sequence at
+// 1000 positions 10.7 us (the two launches and the loads one after the other).
+// Dim 192 and 256: 8 sequences at 8k 73 and 87 us (5.5 and 6.2 TB/s), fp8 49 and 58
+// (4.2 and 4.7); 16 at 32k at the copy rate, fp8 at 85% and 94% of it.
 #include "dense_attn_common.cuh"
 
 namespace v4a {

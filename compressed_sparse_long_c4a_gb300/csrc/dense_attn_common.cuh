@@ -30,7 +30,9 @@ struct DenseAttnDev {
 // at 8k: 32 rows 22 / 32, 64 rows 28 / 32; 16 at 1k (dim 64): 24 / 26 and
 // 35 / 26; fp8, 8 at 8k: 32 rows 63 / 130, 64 rows 111 / 131, 128 rows 203 / 132;
 // dim 256, 8 at 8k: bf16 16 rows 163 / 107, 32 rows 311 / 107, one at 8k 16 rows
-// 24 / 33; fp8 32 rows 186 / 187, 64 rows 355 / 186.
+// 24 / 33; fp8 32 rows 186 / 187, 64 rows 355 / 186.  The limits are those of
+// one sequence, where the second pass costs nothing; with more sequences 9 to
+// 16 rows of dim 256 (bf16) would be faster in the form for many.
 constexpr int few_rows(int dim, bool fp8) { return (dim == 256 ? 8 : 16) * (fp8 ? 4 : 2); }
 
 // One sequence's tokens of the call: first row, count and first position;
@@ -137,7 +139,12 @@ struct SplitDev {
 struct alignas(16) JoinDesc { int rows, row0, s0, hk, last, pad[3]; };
 static_assert(alignof(JoinDesc) <= 16 && sizeof(JoinDesc) == 32, "lies at the front of a workspace, which the caller aligns to 16 bytes");
 
-constexpr int kMaxSplitUnits = 512;   // more units than these fill the machine one by one
+// The most units (and sequences) of an even split: their table lies in shared
+// memory.  More run one CTA each, which is as fast where they are about equally
+// long (600 sequences at 1k, 32 + 8 heads of 128: 350 us, 7.2 TB/s) and not where
+// one is far longer: 256k among 600 at 1k 2.8 ms (among 500, split: 475 us), 512
+// tokens over 32k beside 600 decoding at 1k 870 us (beside 500: 560).
+constexpr int kMaxSplitUnits = 512;
 constexpr int kSms = 152;
 
 // Units of R rows that a consistent batch has at most: a sequence of n rows has

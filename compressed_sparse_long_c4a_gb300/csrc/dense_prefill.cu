@@ -29,11 +29,14 @@
 // where nothing cancels; the two-operand P of dense_attn.cu would double
 // the second product here, where the tensor cores set the time.
 //
-// Bound: the tensor cores (4 dim flops per visible pair), and beside them the
-// exponentials: 128 x 128 per tile and step.  Measured, 32 + 8 heads of 128,
-// 2048 tokens over 10240 positions: bf16 258 us (1200 TFLOP/s), fp8 480 us (645:
-// the conversions of the codes); dim 64 bf16 212 us (727: the exponentials,
-// twice as many per flop); a window of 1024 with 1500 tokens 62 us.
+// Bound: no one unit.  A step is a chain of product, softmax and product for
+// each of two row tiles, and two softmax warps a scheduler do not cover its
+// waits: dim 128 bf16 keeps the tensor pipe 50% busy, the issue slots 40% and the
+// exponential unit 25%; dim 64, with half of the flops for the same softmax,
+// 30%, 44% and 30%.  Measured, 32 + 8 heads of 128, 2048 tokens over 10240
+// positions: bf16 258 us (1200 TFLOP/s), fp8 480 us (645: the conversions of the
+// codes); dim 64 bf16 211 us (733), fp8 396 (390); a window of 1024 with 1500
+// tokens 61 us.
 #include "dense_prefill_common.cuh"
 
 namespace v4a {
