@@ -14,9 +14,9 @@
 // while the first drains (programmatic dependent launch).
 //
 // Bound: latency.  The loads, the scan and the two launches one after the other
-// take 5 to 6 us on the device (64 decoding sequences with 60 tables 5.2, 4 x
-// 1024 tokens with 60 tables, whose slots are 2 MB, 5.8, 1000 sequences 6 to 7,
-// 8000 19: the scan's eight rounds); 64 decoding sequences with one table 3.3.
+// take 5 to 6 us on the device (64 decoding sequences with 60 tables 5.6, 4 x
+// 1024 tokens with 60 tables, whose slots are 2 MB, 5.7, 1000 sequences 6 to 7,
+// 8000 19: the scan's eight rounds); 64 decoding sequences with one table 3.4.
 // A step that ends long sequences moves their pages too: table rows lie far
 // apart, so each page is a sector of its own (one sequence of 1M positions, 61
 // tables, 250k pages: 8.9 us over 152 SMs, 156 in a step that one CTA fills).
@@ -259,8 +259,9 @@ __global__ void __launch_bounds__(kFillThreads) plan_fill(const PlanDev p) {
   pdl_trigger();
   pdl_wait();
   const PlanHeader h = *p.hdr;
-  const int64_t most = max(p.items, int64_t(max(h.fresh_blocks, h.back_blocks)) * p.a.num_tables);
-  if (int64_t(blockIdx.x) * kFillThreads >= most) return;
+  // (the CTAs that have tokens do not wait for the header before they load the sums)
+  const int64_t first = int64_t(blockIdx.x) * kFillThreads;
+  if (first >= p.items && first >= int64_t(max(h.fresh_blocks, h.back_blocks)) * p.a.num_tables) return;
   for (int b = tid; b <= B; b += kFillThreads) {
     st[b] = p.a.token_starts[b];
     nb[b] = p.sums[b];
