@@ -75,9 +75,10 @@ extern "C" {
                                  outputs are incomplete (never expected; reported, never hung) */
 
 /* ---- formats ---------------------------------------------------------------- */
+/* fp32 scales that the library writes (amax / 448, fp4 amax / 6) are 1 where amax is 0 and at least 2^-126. */
 /* Shared-K=V cache and window ring rows. */
 #define V4A_KV_BF16       0  /* row = dim bf16 */
-#define V4A_KV_FP8_TOKEN  1  /* row = dim e4m3 codes; one fp32 scale per row (amax/448, at least 2^-126, 1 for zeros) */
+#define V4A_KV_FP8_TOKEN  1  /* row = dim e4m3 codes; one fp32 scale per row (amax/448) */
 #define V4A_KV_FP8_DSV4   2  /* compressed cache only, dim 512 with 64 rope dims: the DeepSeek-V4
                                 row of the SGLang KV-pool article ("DeepSeek-V4"), 584 B =
                                 448 e4m3 codes of the non-rope dims, the 64 rope dims in bf16,
