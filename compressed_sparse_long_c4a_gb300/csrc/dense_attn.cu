@@ -44,13 +44,15 @@ constexpr int kRingBytes = 192 * 1024;
 // 600: 0 tiles 76 us, 16 54, 48 57; one of 30000 among 60 of 100: 46, 34, 38).
 constexpr int kUnitCost = 16;
 
-template <int D, int NT, bool kFp8>
+// kFmt: the cache's format, V4A_KV_BF16, V4A_KV_FP8_TOKEN or V4A_KV_FP8_GROUP.
+template <int D, int NT, int kFmt>
 struct Shape {
+  static constexpr bool kFp8 = kFmt != V4A_KV_BF16;
   static constexpr int R = 8 * NT;                               // query rows of a unit
   static constexpr int kKeys = (kFp8 ? 32 : 16) * (D == 64 ? 2 : 1);   // positions per tile
   static constexpr int kRow = kFp8 ? D : 2 * D;                  // bytes of a row
   static constexpr int kHalf = kKeys * kRow;                     // keys (or values) of a tile: 32 D bytes (64 D at dim 64)
-  static constexpr int kScales = kFp8 ? 2 * kKeys * 4 : 0;
+  static constexpr int kScales = kFmt == V4A_KV_FP8_GROUP ? 16 : kFp8 ? 2 * kKeys * 4 : 0;      // a tile lies in one group
   static constexpr int kStage = 2 * kHalf + kScales;             // holds R x D fp32 for the merge as well
   static constexpr int kWarps = 4;
   static constexpr int kThreads = 32 * kWarps;
@@ -111,9 +113,10 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&b);
 }
-template <int D, int NT, bool kFp8>
-__global__ void __launch_bounds__(Shape<D, NT, kFp8>::kThreads, Shape<D, NT, kFp8>::kPerSm) dense_attn_mma(const DenseAttnDev a, const SplitDev p) {
-  using S = Shape<D, NT, kFp8>;
+template <int D, int NT, int kFmt>
+__global__ void __launch_bounds__(Shape<D, NT, kFmt>::kThreads, Shape<D, NT, kFmt>::kPerSm) dense_attn_mma(const DenseAttnDev a, const SplitDev p) {
+  using S = Shape<D, NT, kFmt>;
+  constexpr bool kFp8 = S::kFp8, kGroup = kFmt == V4A_KV_FP8_GROUP;
   constexpr int R = S::R, kWarps = S::kWarps, kThreads = S::kThreads, kKeys = S::kKeys, MT = kKeys / 16;
   extern __shared__ __align__(128) uint8_t smem[];
   typename S::Tail& s = *reinterpret_cast<typename S::Tail*>(smem + kWarps * S::kStages * S::kStage);
@@ -162,7 +165,9 @@ __global__ void __launch_bounds__(Shape<D, NT, kFp8>::kThreads, Shape<D, NT, kFp
           tc::cp_async16(dst + to, src + c * 16);
           tc::cp_async16(dst + S::kHalf + to, src + to_values + c * 16);
         }
-        if (kFp8 && lane < kKeys / 2) {          // the rows' scales: keys' from the first half of these lanes, values' from the rest
+        if (kGroup && lane < 2)                  // the group's scales
+          tc::cp_async4(dst + 2 * S::kHalf + lane * 4, block + 2 * to_values + (lane * a.K * kGroupsPerBlock + row / kGroupPositions) * 4);
+        if (kFp8 && !kGroup && lane < kKeys / 2) {          // the rows' scales: keys' from the first half of these lanes, values' from the rest
           const int which = lane / (kKeys / 4), q = lane % (kKeys / 4);
           const uint8_t* sc = block + 2 * to_values + (row + int64_t(which) * a.K * kBlockPositions) * 4;
           tc::cp_async16(dst + 2 * S::kHalf + which * kKeys * 4 + q * 16, sc + q * 16);
@@ -306,11 +311,13 @@ __global__ void __launch_bounds__(Shape<D, NT, kFp8>::kThreads, Shape<D, NT, kFp
               for (int nt = 0; nt < NT; ++nt) mma16816_f16(z[mt][nt], k, qf[2 * c + h][nt]);
             }
           }
-          const float k0 = scale[mt * 16 + g4], k1 = scale[mt * 16 + g4 + 8];
+          if constexpr (!kGroup) {
+            const float k0 = scale[mt * 16 + g4], k1 = scale[mt * 16 + g4 + 8];
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            z[mt][nt][0] *= k0; z[mt][nt][1] *= k0;
-            z[mt][nt][2] *= k1; z[mt][nt][3] *= k1;
+            for (int nt = 0; nt < NT; ++nt) {
+              z[mt][nt][0] *= k0; z[mt][nt][1] *= k0;
+              z[mt][nt][2] *= k1; z[mt][nt][3] *= k1;
+            }
           }
         }
       }
@@ -330,9 +337,17 @@ __global__ void __launch_bounds__(Shape<D, NT, kFp8>::kThreads, Shape<D, NT, kFp
       // scales are and fits f16, whose 11 bits keep the single dominating key exact to 2^-12 (a bf16
       // product p sv lost up to 2^-9 there); 2^15 P uses f16's upper range, so that keys down to
       // 2^-39 of the largest count.  l sums 2^{z - m} itself: at most 2^100 a key.
-      float ls[MT][2];
+      float ls[MT][2], fz[NT][2];                // fz: the scores' factors (a group's key scale among them)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) fz[nt][e] = kGroup ? fmaxf(fq[nt][e] * scale[0], 0x1p-126f) : fq[nt][e];
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
+        if constexpr (kGroup) {
+          ls[mt][0] = ls[mt][1] = scale_log2(scale[1]);
+          continue;
+        }
         ls[mt][0] = kFp8 ? scale_log2(scale[kKeys + mt * 16 + g4]) : 0.f;
         ls[mt][1] = kFp8 ? scale_log2(scale[kKeys + mt * 16 + g4 + 8]) : 0.f;
       }
@@ -345,7 +360,7 @@ __global__ void __launch_bounds__(Shape<D, NT, kFp8>::kThreads, Shape<D, NT, kFp
           float t = -INFINITY;
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt)
-            t = kFp8 ? fmaxf(t, fmaxf(fmaf(z[mt][nt][e], fq[nt][e], ls[mt][0]), fmaf(z[mt][nt][e + 2], fq[nt][e], ls[mt][1])))
+            t = kFp8 ? fmaxf(t, fmaxf(fmaf(z[mt][nt][e], fz[nt][e], ls[mt][0]), fmaf(z[mt][nt][e + 2], fz[nt][e], ls[mt][1])))
                      : fmaxf(t, fmaxf(z[mt][nt][e], z[mt][nt][e + 2]));
           t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
           t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
@@ -375,8 +390,8 @@ __global__ void __launch_bounds__(Shape<D, NT, kFp8>::kThreads, Shape<D, NT, kFp
         const float b0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0], b1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
-          const float y0 = fmaf(z[mt][nt][0], fq[nt][0], -b0), y1 = fmaf(z[mt][nt][1], fq[nt][1], -b1);
-          const float y2 = fmaf(z[mt][nt][2], fq[nt][0], -b0), y3 = fmaf(z[mt][nt][3], fq[nt][1], -b1);
+          const float y0 = fmaf(z[mt][nt][0], fz[nt][0], -b0), y1 = fmaf(z[mt][nt][1], fz[nt][1], -b1);
+          const float y2 = fmaf(z[mt][nt][2], fz[nt][0], -b0), y3 = fmaf(z[mt][nt][3], fz[nt][1], -b1);
           const float p0 = exp2f(y0), p1 = exp2f(y1), p2 = exp2f(y2), p3 = exp2f(y3);
           l[nt][0] += p0 + p2;
           l[nt][1] += p1 + p3;
@@ -645,7 +660,7 @@ bool mixed(const v4a_dense_attn_args* a) {
 // The most rows a sequence brings to the form for few rows.
 int64_t most_rows(const v4a_dense_attn_args* a) {
   const int64_t rows = int64_t(a->max_new_per_seq) * (a->num_heads / a->kv.num_kv_heads);
-  return dense_prefill_takes(a) ? few_rows(a->kv.dim, a->kv.format != V4A_KV_BF16) : rows;
+  return dense_prefill_takes(a) ? few_rows(a->kv.dim, a->kv.format) : rows;
 }
 
 int rows_of(const v4a_dense_attn_args* a) {
@@ -663,12 +678,12 @@ size_t workspace_of(const v4a_dense_attn_args* a) {
   return few_workspace(a) + (dense_prefill_takes(a) ? dense_prefill_workspace(a) : 0);
 }
 
-template <int D, int NT, bool kFp8>
+template <int D, int NT, int kFmt>
 int launch(const DenseAttnDev& a, const SplitDev& p, cudaStream_t stream) {
-  using S = Shape<D, NT, kFp8>;
+  using S = Shape<D, NT, kFmt>;
   const size_t smem = S::kWarps * S::kStages * S::kStage + sizeof(typename S::Tail) + split_smem(p.split, p.U);
   static_assert(S::kWarps * S::kStages * S::kStage + sizeof(typename S::Tail) + split_smem(1, kMaxSplitUnits) <= 227 * 1024, "shared memory of a CTA");
-  auto kern = dense_attn_mma<D, NT, kFp8>;
+  auto kern = dense_attn_mma<D, NT, kFmt>;
   static std::atomic<uint64_t> done{0};
   if (!once_per_device(&done, [=] { return raise_smem(kern, 227 * 1024); })) return V4A_ERR_CUDA;
   const int64_t grid = p.split ? p.grid : int64_t(p.U) * a.K;
@@ -676,14 +691,14 @@ int launch(const DenseAttnDev& a, const SplitDev& p, cudaStream_t stream) {
   return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? V4A_OK : V4A_ERR_CUDA;
 }
 
-template <bool kFp8>
+template <int kFmt>
 int launch_dim(const DenseAttnDev& a, const SplitDev& p, int dim, cudaStream_t stream) {
   const bool two = p.rows == 16;
   switch (dim) {
-    case 64: return two ? launch<64, 2, kFp8>(a, p, stream) : launch<64, 1, kFp8>(a, p, stream);
-    case 128: return two ? launch<128, 2, kFp8>(a, p, stream) : launch<128, 1, kFp8>(a, p, stream);
-    case 192: return two ? launch<192, 2, kFp8>(a, p, stream) : launch<192, 1, kFp8>(a, p, stream);
-    default: return launch<256, 1, kFp8>(a, p, stream);
+    case 64: return two ? launch<64, 2, kFmt>(a, p, stream) : launch<64, 1, kFmt>(a, p, stream);
+    case 128: return two ? launch<128, 2, kFmt>(a, p, stream) : launch<128, 1, kFmt>(a, p, stream);
+    case 192: return two ? launch<192, 2, kFmt>(a, p, stream) : launch<192, 1, kFmt>(a, p, stream);
+    default: return launch<256, 1, kFmt>(a, p, stream);
   }
 }
 
@@ -694,7 +709,7 @@ int check_shape(const v4a_dense_attn_args* a) {
   const v4a_dense_cache& c = a->kv;
   if (c.num_kv_heads < 1 || c.num_kv_heads > 1024 || a->num_heads % c.num_kv_heads) return V4A_ERR_INVALID_ARG;
   if (c.dim != 64 && c.dim != 128 && c.dim != 192 && c.dim != 256) return V4A_ERR_UNSUPPORTED;
-  if (c.format != V4A_KV_BF16 && c.format != V4A_KV_FP8_TOKEN) return V4A_ERR_UNSUPPORTED;
+  if (c.format != V4A_KV_BF16 && c.format != V4A_KV_FP8_TOKEN && c.format != V4A_KV_FP8_GROUP) return V4A_ERR_UNSUPPORTED;
   if (a->num_heads > 1024 || a->max_new_per_seq > (1 << 22) || c.max_blocks > (1 << 22)) return V4A_ERR_UNSUPPORTED;
   if (int64_t(a->max_new_per_seq) * (a->num_heads / c.num_kv_heads) > INT32_MAX / 2) return V4A_ERR_UNSUPPORTED;   // rows are counted in 32 bits
   return V4A_OK;
@@ -735,8 +750,8 @@ int dense_attn(const v4a_dense_attn_args* a, void* ws, size_t ws_bytes, cudaStre
   d.pool = static_cast<const uint8_t*>(a->kv.pool);
   d.q = a->q; d.out = a->out; d.lse = a->lse; d.status = a->status;
   d.scale_log2 = std::max(a->softmax_scale * 1.4426950408889634f, 0x1p-126f);      // (a subnormal one would be flushed)
-  const bool fp8 = a->kv.format == V4A_KV_FP8_TOKEN, takes = dense_prefill_takes(a), both = takes && mixed(a);
-  const int few = few_rows(a->kv.dim, fp8);
+  const bool fp8 = a->kv.format != V4A_KV_BF16, takes = dense_prefill_takes(a), both = takes && mixed(a);
+  const int few = few_rows(a->kv.dim, a->kv.format);
   SplitDev p{}, many{};
   p.RG = int(row_groups(a));
   p.rows_to = both ? few : INT32_MAX;
@@ -763,7 +778,8 @@ int dense_attn(const v4a_dense_attn_args* a, void* ws, size_t ws_bytes, cudaStre
   p.split = std::max(p.U, d.B) <= kMaxSplitUnits &&
             (d.window == 0 || d.window > 4096 || (units * d.K < (fp8 ? 256 : 128) && d.window > 512));
   split_carve(&p, ws, rows_of(a), a->kv.dim, ctas_of(a), kUnitCost);
-  rc = fp8 ? launch_dim<true>(d, p, a->kv.dim, stream) : launch_dim<false>(d, p, a->kv.dim, stream);
+  rc = a->kv.format == V4A_KV_FP8_GROUP ? launch_dim<V4A_KV_FP8_GROUP>(d, p, a->kv.dim, stream)
+       : fp8 ? launch_dim<V4A_KV_FP8_TOKEN>(d, p, a->kv.dim, stream) : launch_dim<V4A_KV_BF16>(d, p, a->kv.dim, stream);
   if (rc == V4A_OK && many.U > 0) rc = dense_prefill(a, d, many, stream);
   if (rc == V4A_OK && p.split) rc = dense_join(d, p, a->kv.dim, stream);
   return rc == V4A_OK && many.U > 0 && many.split ? dense_join(d, many, a->kv.dim, stream) : rc;

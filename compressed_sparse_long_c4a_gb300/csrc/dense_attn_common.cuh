@@ -33,7 +33,7 @@ struct DenseAttnDev {
 // 24 / 33; fp8 32 rows 186 / 187, 64 rows 355 / 186.  The limits are those of
 // one sequence, where the second pass costs nothing; with more sequences 9 to
 // 16 rows of dim 256 (bf16) would be faster in the form for many.
-constexpr int few_rows(int dim, bool fp8) { return (dim == 256 ? 8 : 16) * (fp8 ? 4 : 2); }
+constexpr int few_rows(int dim, int format) { return (dim == 256 ? 8 : 16) * (format == V4A_KV_FP8_TOKEN ? 4 : 2); }
 
 // One sequence's tokens of the call: first row, count and first position;
 // n = 0 when there are none, the entries are inconsistent (reported) or the
@@ -185,9 +185,10 @@ inline void split_carve(SplitDev* p, void* ws, int R, int dim, int ctas, int cos
 }
 
 // The CTA's part of the line (or its unit), kept in shared memory behind `mem`.
-template <int R, int kTile, int kThreads>
+// Dev: the arguments, with a seq_run and a make_unit of their own.
+template <int R, int kTile, int kThreads, typename Dev = DenseAttnDev>
 struct Line {
-  const DenseAttnDev& a;
+  const Dev& a;
   const SplitDev& p;
   UnitRef* refs;                  // [U], or the one
   int64_t* pre;                   // [U + 1] tiles before unit u, over its KV heads
@@ -197,7 +198,7 @@ struct Line {
   struct Piece { int u, hk, tile; };
   struct Seq { SeqRun r; int first; };      // a sequence and the units before it
 
-  __device__ __forceinline__ Line(const DenseAttnDev& a_, const SplitDev& p_, void* mem) : a(a_), p(p_) {
+  __device__ __forceinline__ Line(const Dev& a_, const SplitDev& p_, void* mem) : a(a_), p(p_) {
     refs = static_cast<UnitRef*>(mem);
     pre = reinterpret_cast<int64_t*>(refs + p.U);
   }
@@ -362,5 +363,11 @@ size_t dense_prefill_workspace(const v4a_dense_attn_args* a);
 int dense_prefill_plan(const v4a_dense_attn_args* a, const DenseAttnDev& d, int rows_from, void* ws, SplitDev* p);
 bool dense_prefill_ready(const v4a_dense_attn_args* a);
 int dense_prefill(const v4a_dense_attn_args* a, const DenseAttnDev& d, const SplitDev& p, cudaStream_t stream);
+
+// The same for caches with a scale per group (dense_group.cu); the division is shared with whole prompts (prompt_attn.cu).
+size_t stream_workspace(int dim);
+int stream_plan(const DenseAttnDev& d, int dim, int rows_from, void* ws, SplitDev* p);
+bool dense_group_ready(int dim);
+int dense_group(int dim, const DenseAttnDev& d, const SplitDev& p, cudaStream_t stream);
 
 }  // namespace v4a

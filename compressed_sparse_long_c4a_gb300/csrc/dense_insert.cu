@@ -20,6 +20,10 @@
 // Measured, 64 + 8 + 8 heads of 128: 16384 tokens, bf16 120 us (671 MB: 5.6
 // TB/s of the 6.8 that a copy reaches), fp8 143 us (the row maxima and the
 // codes); one token 2.1 us.
+//
+// A cache with a scale per group takes two launches (v4a_dense_insert_rows): this
+// kernel for queries and keys as rows, then dense_quant.cu for the codes, which
+// needs all rows of a group at once.
 #include <type_traits>
 
 #include "tc_common.cuh"
@@ -43,8 +47,8 @@ struct InsertDev {
   const int32_t* positions;
   const int64_t* slots;
   const uint16_t *q, *k, *v;
-  uint16_t* q_out;
-  int64_t qs, qos, ks, vs;
+  uint16_t *q_out, *k_out;         // k_out: the keys as packed rows, or nullptr
+  int64_t qs, qos, ks, vs, kos;
   const float *qg, *kg;
   uint8_t* pool;
   int64_t num_slots, block_bytes;
@@ -63,9 +67,12 @@ __device__ __forceinline__ uint2 pack4(const float* x) {
 }
 
 // kLanes: lanes of one row (dim / 8, or 32 with the last eight idle at dim 192).
+// kMode: what the cache gets, bf16 rows, fp8 rows with a scale each, or nothing (keys go to k_out alone, values are not read).
 // kShare: several tokens of few rows in a CTA (the division costs the others 5%: 121 us against 127).
-template <int kLanes, bool kFp8, bool kShare>
+enum { kBf16, kFp8Rows, kRowsOnly };
+template <int kLanes, int kMode, bool kShare>
 __global__ void __launch_bounds__(kThreads, 8) dense_insert_kernel(const __grid_constant__ InsertDev p) {
+  constexpr bool kFp8 = kMode == kFp8Rows;
   constexpr int kRows = kThreads / kLanes;      // rows per pass
   __shared__ alignas(16) float angles[kShare ? 4 : 1][256];      // of a token: cos [0, R/2), sin [R/2, R)
   // a CTA's threads are divided among its tokens
@@ -171,6 +178,12 @@ __global__ void __launch_bounds__(kThreads, 8) dense_insert_kernel(const __grid_
         for (int e = 0; e < 4; ++e) turn(x[2 * e], x[2 * e + 1], co[e], sn[e]);
       }
     }
+    if (p.k_out && !is_q && !is_v && live) {
+      uint16_t* dst = p.k_out + int64_t(t) * p.kos + (r - p.H) * D;
+      *reinterpret_cast<uint2*>(dst + d0) = pack4(x);
+      *reinterpret_cast<uint2*>(dst + d1) = pack4(x + 4);
+    }
+    if (kMode == kRowsOnly && !is_q) continue;
     const int64_t row = int64_t(r - p.H) * kBlockPositions + at;     // keys' heads, then values'
     if (is_q || !kFp8) {
       if (r < p.NR && live) {
@@ -241,7 +254,7 @@ int fill_rope(const v4a_rope& r, int dim, InsertDev* d) {
 
 int dense_cache_check(const v4a_dense_cache& c, int64_t* block_bytes) {
   if (c.num_kv_heads < 1 || c.num_kv_heads > 1024 || c.num_blocks < 1 || !c.pool) return V4A_ERR_INVALID_ARG;
-  if (c.format != V4A_KV_BF16 && c.format != V4A_KV_FP8_TOKEN) return V4A_ERR_UNSUPPORTED;
+  if (c.format != V4A_KV_BF16 && c.format != V4A_KV_FP8_TOKEN && c.format != V4A_KV_FP8_GROUP) return V4A_ERR_UNSUPPORTED;
   if (c.dim != 64 && c.dim != 128 && c.dim != 192 && c.dim != 256) return V4A_ERR_UNSUPPORTED;
   const int64_t need = v4a_dense_block_bytes(c.num_kv_heads, c.dim, c.format);
   *block_bytes = c.block_bytes ? c.block_bytes : need;
@@ -250,12 +263,14 @@ int dense_cache_check(const v4a_dense_cache& c, int64_t* block_bytes) {
   return V4A_OK;
 }
 
-int dense_insert(const v4a_dense_insert_args* a, cudaStream_t stream) {
+int dense_insert(const v4a_dense_insert_args* a, bool with_rows, uint16_t* k_out, int64_t k_out_stride, cudaStream_t stream) {
   if (!a || a->num_tokens < 0 || a->num_heads < 0 || !(a->eps >= 0.f)) return V4A_ERR_INVALID_ARG;
   if (a->num_heads > 1024) return V4A_ERR_UNSUPPORTED;
   InsertDev d{};
   int rc = dense_cache_check(a->kv, &d.block_bytes);
   if (rc) return rc;
+  const bool group = a->kv.format == V4A_KV_FP8_GROUP;
+  if (group && !with_rows) return V4A_ERR_UNSUPPORTED;
   const int D = a->kv.dim, K = a->kv.num_kv_heads, H = a->num_heads;
   if (H % K) return V4A_ERR_INVALID_ARG;
   rc = fill_rope(a->rope, D, &d);
@@ -268,8 +283,14 @@ int dense_insert(const v4a_dense_insert_args* a, cudaStream_t stream) {
   if ((H > 0 && (a->q_stride < int64_t(H) * D || a->q_out_stride < int64_t(H) * D || a->q_stride % 8 || a->q_out_stride % 8)) ||
       a->k_stride < int64_t(K) * D || a->v_stride < int64_t(K) * D || a->k_stride % 8 || a->v_stride % 8)
     return V4A_ERR_INVALID_ARG;
+  if (with_rows) {
+    if (!k_out || !aligned(k_out, 16) || k_out_stride < int64_t(K) * D || k_out_stride % 8 || (k_out == a->k && k_out_stride != a->k_stride))
+      return V4A_ERR_INVALID_ARG;
+    d.k_out = k_out;
+    d.kos = k_out_stride;
+  }
   if (H > 0 && a->q == a->q_out && a->q_stride != a->q_out_stride) return V4A_ERR_INVALID_ARG;
-  d.D = D; d.H = H; d.K = K; d.NR = H + 2 * K; d.eps = a->eps;
+  d.D = D; d.H = H; d.K = K; d.NR = H + (group ? 1 : 2) * K; d.eps = a->eps;
   d.positions = a->positions; d.slots = a->slots;
   d.q = a->q; d.k = a->k; d.v = a->v; d.q_out = a->q_out;
   d.qs = a->q_stride; d.qos = a->q_out_stride; d.ks = a->k_stride; d.vs = a->v_stride;
@@ -290,16 +311,20 @@ int dense_insert(const v4a_dense_insert_args* a, cudaStream_t stream) {
   d.tokens = a->num_tokens;
   auto passes = [&](int share) { return (d.NR + (rows >> share) - 1) / (rows >> share); };
   while (y == 1 && d.share < 2 && passes(d.share + 1) <= kPasses && a->num_tokens >> (d.share + 1) >= 152 * 8) d.passes = passes(++d.share);
-  const bool fp8 = a->kv.format == V4A_KV_FP8_TOKEN;
-  auto pick = [&](auto share) {
+  auto pick = [&](auto mode, auto share) {
+    constexpr int kMode = decltype(mode)::value;
     constexpr bool kShare = decltype(share)::value;
-    return lanes == 8    ? (fp8 ? dense_insert_kernel<8, true, kShare> : dense_insert_kernel<8, false, kShare>)
-           : lanes == 16 ? (fp8 ? dense_insert_kernel<16, true, kShare> : dense_insert_kernel<16, false, kShare>)
-                         : (fp8 ? dense_insert_kernel<32, true, kShare> : dense_insert_kernel<32, false, kShare>);
+    return lanes == 8 ? dense_insert_kernel<8, kMode, kShare> : lanes == 16 ? dense_insert_kernel<16, kMode, kShare> : dense_insert_kernel<32, kMode, kShare>;
   };
-  auto kern = d.share ? pick(std::true_type{}) : pick(std::false_type{});
+  auto pick_mode = [&](auto share) {
+    return group ? pick(std::integral_constant<int, kRowsOnly>{}, share)
+           : a->kv.format == V4A_KV_FP8_TOKEN ? pick(std::integral_constant<int, kFp8Rows>{}, share)
+                                              : pick(std::integral_constant<int, kBf16>{}, share);
+  };
+  auto kern = d.share ? pick_mode(std::true_type{}) : pick_mode(std::false_type{});
   const cudaError_t e = launch_pdl(kern, dim3(unsigned(a->num_tokens + (int64_t(1) << d.share) - 1) >> d.share, y), dim3(kThreads), 0, stream, d);
-  return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? V4A_OK : V4A_ERR_CUDA;
+  rc = e == cudaSuccess && cudaGetLastError() == cudaSuccess ? V4A_OK : V4A_ERR_CUDA;
+  return rc == V4A_OK && group ? dense_quant(*a, k_out, k_out_stride, d.block_bytes, stream) : rc;
 }
 
 }  // namespace v4a

@@ -488,14 +488,16 @@ int launch(const DenseAttnDev& d, const SplitDev& p, cudaStream_t stream) {
 
 bool dense_prefill_takes(const v4a_dense_attn_args* a) {
   const int64_t rows = int64_t(a->max_new_per_seq) * (a->num_heads / a->kv.num_kv_heads);
-  return rows > few_rows(a->kv.dim, a->kv.format != V4A_KV_BF16);
+  return rows > few_rows(a->kv.dim, a->kv.format);
 }
 
 size_t dense_prefill_workspace(const v4a_dense_attn_args* a) {
+  if (a->kv.format == V4A_KV_FP8_GROUP) return stream_workspace(a->kv.dim);
   return split_workspace(a->kv.dim > 128 ? kWideUnit : kUnit, a->kv.dim, kSms);
 }
 
 int dense_prefill_plan(const v4a_dense_attn_args* a, const DenseAttnDev& d, int rows_from, void* ws, SplitDev* out) {
+  if (a->kv.format == V4A_KV_FP8_GROUP) return stream_plan(d, a->kv.dim, rows_from, ws, out);
   const bool wide = a->kv.dim > 128;
   const int unit = wide ? kWideUnit : kUnit;
   SplitDev p{};
@@ -518,6 +520,7 @@ int dense_prefill_plan(const v4a_dense_attn_args* a, const DenseAttnDev& d, int 
 }
 
 bool dense_prefill_ready(const v4a_dense_attn_args* a) {
+  if (a->kv.format == V4A_KV_FP8_GROUP) return dense_group_ready(a->kv.dim);
   const bool fp8 = a->kv.format == V4A_KV_FP8_TOKEN;
   if (a->kv.dim > 128) return dense_prefill_wide_ready(a->kv.dim, fp8);
   if (fp8) return a->kv.dim == 64 ? ready<64, true>() : ready<128, true>();
@@ -525,6 +528,7 @@ bool dense_prefill_ready(const v4a_dense_attn_args* a) {
 }
 
 int dense_prefill(const v4a_dense_attn_args* a, const DenseAttnDev& d, const SplitDev& p, cudaStream_t stream) {
+  if (a->kv.format == V4A_KV_FP8_GROUP) return dense_group(a->kv.dim, d, p, stream);
   const bool wide = a->kv.dim > 128, fp8 = a->kv.format == V4A_KV_FP8_TOKEN;
   if (wide) return dense_prefill_wide(a->kv.dim, fp8, d, p, stream);
   if (fp8) return a->kv.dim == 64 ? launch<64, true>(d, p, stream) : launch<128, true>(d, p, stream);

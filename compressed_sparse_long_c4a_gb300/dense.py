@@ -1,5 +1,6 @@
 """ctypes binding of the dense-layer operators (v4a_dense.h): the step plan,
-norm + rotation + cache insert, and attention over the dense paged cache.
+norm + rotation + cache insert, attention over the dense paged cache, the read
+back of cached rows, and attention of whole prompts over packed rows.
 
 Argument marshalling only: every object checks its tensors, keeps the C
 argument struct and the workspace, and calls the library on the current (or
@@ -19,6 +20,8 @@ from .v4a import KV_BF16, KV_FP8_TOKEN  # noqa: F401
 BLOCK_POSITIONS = 256
 ROPE_INTERLEAVED, ROPE_HALF = 0, 1
 ROPE_PLAIN, ROPE_LINEAR, ROPE_YARN, ROPE_TABLE = 0, 1, 2, 3
+KV_FP8_GROUP = 3           # e4m3 codes with one power-of-two scale per 64 positions and KV head
+GROUP_POSITIONS = 64
 DEV_OUT_OF_PAGES = 16
 
 _p = C.c_void_p
@@ -55,6 +58,19 @@ class AttnArgs(C.Structure):
                 ("window", C.c_int32), ("sinks", C.c_int32), ("out", _p), ("lse", _p), ("status", _p)]
 
 
+class ReadArgs(C.Structure):
+    _fields_ = [("num_rows", C.c_int32), ("num_seqs", C.c_int32), ("row_starts", _p), ("first", _p), ("kv", CacheArgs), ("k", _p),
+                ("k_stride", C.c_int64), ("v", _p), ("v_stride", C.c_int64), ("status", _p)]
+
+
+class PromptArgs(C.Structure):
+    _fields_ = [("num_tokens", C.c_int32), ("num_kv_tokens", C.c_int32), ("num_seqs", C.c_int32), ("max_new_per_seq", C.c_int32),
+                ("token_starts", _p), ("kv_starts", _p), ("num_heads", C.c_int32), ("num_kv_heads", C.c_int32), ("dim", C.c_int32),
+                ("causal", C.c_int32), ("window", C.c_int32), ("sinks", C.c_int32), ("softmax_scale", C.c_float), ("q", _p),
+                ("q_stride", C.c_int64), ("k", _p), ("k_stride", C.c_int64), ("v", _p), ("v_stride", C.c_int64), ("out", _p),
+                ("lse", _p), ("status", _p)]
+
+
 _sigs_done = False
 
 
@@ -69,6 +85,11 @@ def lib() -> C.CDLL:
         L.v4a_dense_block_bytes.argtypes = [C.c_int32, C.c_int32, C.c_int32]
         L.v4a_dense_block_bytes.restype = C.c_int64
         L.v4a_dense_insert.argtypes = [C.POINTER(InsertArgs), _p]
+        L.v4a_dense_insert_rows.argtypes = [C.POINTER(InsertArgs), _p, C.c_int64, _p]
+        L.v4a_dense_read.argtypes = [C.POINTER(ReadArgs), _p]
+        L.v4a_prompt_attn_workspace_size.argtypes = [C.POINTER(PromptArgs)]
+        L.v4a_prompt_attn_workspace_size.restype = C.c_size_t
+        L.v4a_prompt_attn.argtypes = [C.POINTER(PromptArgs), _p, C.c_size_t, _p]
         L.v4a_dense_attn_workspace_size.argtypes = [C.POINTER(AttnArgs)]
         L.v4a_dense_attn_workspace_size.restype = C.c_size_t
         L.v4a_dense_attn.argtypes = [C.POINTER(AttnArgs), _p, C.c_size_t, _p]
@@ -259,7 +280,9 @@ def _rows(t, name, device, heads, dim, tokens):
 
 class DenseInsert(_Op):
     """v4a_dense_insert into `cache`: the queries' and keys' norm (None gamma:
-    none) and rotation, and the keys' and values' insert."""
+    none) and rotation, and the keys' and values' insert.  With k_out a run also
+    leaves the keys as packed rows (v4a_dense_insert_rows), which a KV_FP8_GROUP
+    cache always needs: it holds those rows quantised."""
 
     def __init__(self, cache: DenseCache, num_heads: int, rope: Rope | None, q_gamma=None, k_gamma=None, eps: float = 1e-6):
         self.cache, self.device = cache, cache.device
@@ -273,11 +296,14 @@ class DenseInsert(_Op):
                                None if q_gamma is None else q_gamma.data_ptr(), None if k_gamma is None else k_gamma.data_ptr(),
                                eps, self._rope, cache.struct(), self.status.data_ptr())
         self._bind("v4a_dense_insert", lib().v4a_dense_insert)
+        self._plain = self._where, self._fn, self._call
+        if cache.fmt == KV_FP8_GROUP:
+            self._plain = None
 
-    def run(self, q, k, v, q_out, positions: torch.Tensor, slots: torch.Tensor, stream=None):
-        """q, q_out [T][heads][dim], k, v [T][KV heads][dim] bf16 (any token
-        stride of a multiple of 8; q and q_out None with num_heads = 0);
-        positions int32 [T], slots int64 [T]."""
+    def run(self, q, k, v, q_out, positions: torch.Tensor, slots: torch.Tensor, stream=None, k_out=None):
+        """q, q_out [T][heads][dim], k, v, k_out [T][KV heads][dim] bf16 (any
+        token stride of a multiple of 8; q and q_out None with num_heads = 0;
+        k_out may be k); positions int32 [T], slots int64 [T]."""
         a, c, dev = self.args, self.cache, self.device
         n = k.shape[0] if isinstance(k, torch.Tensor) and k.dim() else 0
         a.num_tokens = n
@@ -292,6 +318,42 @@ class DenseInsert(_Op):
             if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.device == dev and t.shape == (n,) and t.is_contiguous()):
                 _want(t, name, dtype, dev, (n,))
         a.positions, a.slots = positions.data_ptr(), slots.data_ptr()
+        if k_out is not None:
+            stride = _rows(k_out, "k_out", dev, c.num_kv_heads, c.dim, n)
+            self._where, self._fn, self._call = "v4a_dense_insert_rows", lib().v4a_dense_insert_rows, (C.byref(a), k_out.data_ptr(), stride)
+        elif self._plain is None:
+            raise ValueError("DenseInsert: a cache with a scale per group needs k_out")
+        else:
+            self._where, self._fn, self._call = self._plain
+        self._launch(stream)
+
+
+class DenseRead(_Op):
+    """v4a_dense_read from `cache` (its block table's rows are the sequences)."""
+
+    def __init__(self, cache: DenseCache):
+        if cache.block_table is None:
+            raise ValueError("DenseRead: the cache has no block table")
+        self.cache, self.device = cache, cache.device
+        self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
+        self.args = ReadArgs(0, cache.block_table.shape[0], None, None, cache.struct(), None, 0, None, 0, self.status.data_ptr())
+        self._bind("v4a_dense_read", lib().v4a_dense_read)
+
+    def run(self, row_starts: torch.Tensor, k: torch.Tensor, v: torch.Tensor, first: torch.Tensor | None = None, stream=None):
+        """k, v [N][KV heads][dim] bf16 (any row stride of a multiple of 8)
+        receive positions first[b] .. of sequence b (None: 0 ..) at rows
+        row_starts[b] ..; row_starts int32 [sequences + 1], first int32 [sequences]."""
+        a, c, dev = self.args, self.cache, self.device
+        n = k.shape[0] if isinstance(k, torch.Tensor) and k.dim() else 0
+        a.k_stride = _rows(k, "k", dev, c.num_kv_heads, c.dim, n)
+        a.v_stride = _rows(v, "v", dev, c.num_kv_heads, c.dim, n)
+        for name, t, shape in (("row_starts", row_starts, (a.num_seqs + 1,)), ("first", first, (a.num_seqs,))):
+            if t is None and name == "first":
+                continue
+            if not (isinstance(t, torch.Tensor) and t.dtype is torch.int32 and t.device == dev and t.shape == shape and t.is_contiguous()):
+                _want(t, name, torch.int32, dev, shape)
+        a.num_rows, a.k, a.v, a.row_starts = n, k.data_ptr(), v.data_ptr(), row_starts.data_ptr()
+        a.first = None if first is None else first.data_ptr()
         self._launch(stream)
 
 
@@ -337,5 +399,54 @@ class DenseAttention(_Op):
                 _want(t, name, dtype, dev, shape)
         a.num_tokens = n
         a.q, a.out, a.positions, a.token_starts = q.data_ptr(), out.data_ptr(), positions.data_ptr(), token_starts.data_ptr()
+        a.lse = None if lse is None else lse.data_ptr()
+        self._launch(stream)
+
+
+class PromptAttention(_Op):
+    """v4a_prompt_attn: attention of whole packed prompts over packed keys and
+    values, for num_seqs sequences of at most max_new_per_seq queries, max_tokens
+    queries in all.  A sequence's queries are its last positions.  causal=False:
+    every query sees every key; window, sinks and scale as DenseAttention has them.
+    """
+
+    def __init__(self, num_heads: int, num_kv_heads: int, dim: int, num_seqs: int, max_tokens: int, max_new_per_seq: int,
+                 causal: bool = True, window: int = 0, sinks: int = 0, scale: float | None = None, device="cuda"):
+        dev = torch.device(device)
+        if dev.type == "cuda" and dev.index is None:
+            dev = torch.device("cuda", torch.cuda.current_device())
+        self.device, self.max_tokens = dev, max_tokens
+        self.status = torch.zeros(1, dtype=torch.int32, device=dev)
+        self.args = PromptArgs(max_tokens, 0, num_seqs, max_new_per_seq, None, None, num_heads, num_kv_heads, dim, int(bool(causal)),
+                               window, sinks, 1.0 / math.sqrt(dim) if scale is None else scale, None, 0, None, 0, None, 0, None, None,
+                               self.status.data_ptr())
+        need = lib().v4a_prompt_attn_workspace_size(C.byref(self.args))
+        if need == 0:
+            raise ValueError("PromptAttention: sizes outside v4a_prompt_attn's limits")
+        self._bind("v4a_prompt_attn", lib().v4a_prompt_attn, torch.empty(need, dtype=torch.uint8, device=dev))
+
+    def run(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor, token_starts: torch.Tensor,
+            kv_starts: torch.Tensor | None = None, lse=None, stream=None):
+        """q [T][heads][dim], k, v [N][KV heads][dim] bf16 (any token stride of a
+        multiple of 8), out [T][heads][dim] bf16, T <= max_tokens; token_starts,
+        kv_starts int32 [sequences + 1] (None: token_starts); lse fp32 [T][heads] or None."""
+        a, dev = self.args, self.device
+        n, nk = (x.shape[0] if isinstance(x, torch.Tensor) and x.dim() else 0 for x in (q, k))
+        if n > self.max_tokens:
+            raise ValueError(f"q: {n} tokens, at most {self.max_tokens}")
+        a.q_stride = _rows(q, "q", dev, a.num_heads, a.dim, n)
+        a.k_stride = _rows(k, "k", dev, a.num_kv_heads, a.dim, nk)
+        a.v_stride = _rows(v, "v", dev, a.num_kv_heads, a.dim, nk)
+        for name, t, dtype, shape in (("out", out, torch.bfloat16, (n, a.num_heads, a.dim)),
+                                      ("token_starts", token_starts, torch.int32, (a.num_seqs + 1,)),
+                                      ("kv_starts", kv_starts, torch.int32, (a.num_seqs + 1,)),
+                                      ("lse", lse, torch.float32, (n, a.num_heads))):
+            if t is None and name in ("kv_starts", "lse"):
+                continue
+            if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.device == dev and t.shape == shape and t.is_contiguous()):
+                _want(t, name, dtype, dev, shape)
+        a.num_tokens, a.num_kv_tokens = n, nk
+        a.q, a.k, a.v, a.out, a.token_starts = q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), token_starts.data_ptr()
+        a.kv_starts = None if kv_starts is None else kv_starts.data_ptr()
         a.lse = None if lse is None else lse.data_ptr()
         self._launch(stream)

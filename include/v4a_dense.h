@@ -14,6 +14,15 @@
  *                     optional sliding window with sinks
  *
  * A step calls them in this order; the layers of one model share the plan.
+ * Beside them:
+ *
+ *   v4a_dense_insert_rows  the insert, which also gives the keys as packed rows;
+ *                          the one for caches with a scale per group
+ *   v4a_dense_read         cached keys and values as packed rows
+ *   v4a_prompt_attn        attention of whole prompts over packed keys and values
+ *                          (those that v4a_dense_insert_rows leaves, behind
+ *                          prefixes that v4a_dense_read gives), no cache
+ *
  * The general rules of v4a.h hold: device pointers, caller-owned buffers and
  * workspaces, no allocation, no synchronisation, the given stream only; a
  * nonzero return code launched nothing (except V4A_ERR_CUDA); problems only
@@ -35,6 +44,10 @@
 #ifdef __cplusplus
 extern "C" {
 #endif
+
+/* ---- a format of dense caches alone (the others are in v4a.h) ----------------- */
+#define V4A_KV_FP8_GROUP 3 /* e4m3 codes; one fp32 scale, a power of two, per KV head and group of 64
+                              positions (a quarter of a block) of the keys and of the values */
 
 /* ---- device status bit (the others are in v4a.h) ------------------------------ */
 #define V4A_DEV_OUT_OF_PAGES 16 /* v4a_step_plan: the free ring holds too few pages */
@@ -112,12 +125,14 @@ V4A_API int v4a_step_plan(const v4a_plan_args* args, void* workspace, size_t wor
  * values in the same layout, then for V4A_KV_FP8_TOKEN the fp32 scales of the
  * key rows [num_kv_heads][256] and of the value rows.  Formats: V4A_KV_BF16
  * and V4A_KV_FP8_TOKEN (e4m3 codes, one scale amax/448 per row: 1 for a row of
- * zeros, at least 2^-126, and elements below 2^-126 may count as zeros).
+ * zeros, at least 2^-126, and elements below 2^-126 may count as zeros), and
+ * V4A_KV_FP8_GROUP, whose codes are followed by the fp32 scales of the keys'
+ * groups [num_kv_heads][4] and of the values'.
  */
 typedef struct {
   int32_t num_kv_heads;        /* >= 1, <= 1024 */
   int32_t dim;                 /* 64, 128, 192 or 256 */
-  int32_t format;              /* V4A_KV_BF16 or V4A_KV_FP8_TOKEN */
+  int32_t format;              /* V4A_KV_BF16, V4A_KV_FP8_TOKEN or V4A_KV_FP8_GROUP */
   void* pool;                  /* block n starts at n * block_bytes; 16-byte aligned */
   int64_t num_blocks;
   int64_t block_bytes;         /* stride of blocks: a multiple of 16, at least v4a_dense_block_bytes;
@@ -205,6 +220,56 @@ typedef struct {
 V4A_API int v4a_dense_insert(const v4a_dense_insert_args* args, void* stream);
 
 /*
+ * The same call with the keys as packed rows too: k_out[t][h] = bf16(key), with
+ * k_out_stride elements between tokens (16-byte aligned, a multiple of 8, at
+ * least num_kv_heads * dim).  k_out may be k (in place, with equal strides) and
+ * must overlap nothing else; a skipped token's row is left as it was.  The
+ * cache receives what v4a_dense_insert writes.
+ *
+ * This is the call for V4A_KV_FP8_GROUP caches (v4a_dense_insert returns
+ * V4A_ERR_UNSUPPORTED for them), which hold the rows k_out and v quantised as
+ * they come, x standing for a row's elements:
+ *   pow2(a) = the smallest power of two s with a / s <= 448, at least 2^-126
+ *   for each group with rows W among the call's (keys and values and each KV head apart):
+ *     old   = 2^-126 if row 0 is in W, else the stored scale
+ *     scale = max(old, pow2(max |x| over the finite x of W))
+ *     codes of W    = e4m3(x / scale)   (nearest even; infinities become +-448, a NaN its code)
+ *     other codes c = e4m3(c * old / scale), if scale > old and row 0 is not in W
+ * A group begins anew with its row 0: what its other rows held before is lost
+ * then, unless the call writes them.  A stored scale is read by its exponent
+ * (0 counts as 2^-126).  The tokens of a group lie within 64 consecutive tokens
+ * of the call, as v4a_step_plan leaves them, with a slot each: of tokens farther
+ * apart the group holds pieces of any.
+ */
+V4A_API int v4a_dense_insert_rows(const v4a_dense_insert_args* args, uint16_t* k_out, int64_t k_out_stride, void* stream);
+
+/*
+ * Cached rows as packed bf16 rows, each code times its scale rounded once
+ * (V4A_KV_BF16 and V4A_KV_FP8_GROUP: exactly, above 2^-126).  Row r with
+ * row_starts[b] <= r < row_starts[b + 1] receives sequence b's position
+ * first[b] + r - row_starts[b].  A row whose block is unallocated or out of
+ * range (V4A_DEV_BAD_BLOCK) or whose position is negative or past max_blocks
+ * (V4A_DEV_BAD_BATCH) is left as it was, as are the rows before the first
+ * sequence and behind the last one.  row_starts must not decrease (otherwise
+ * which sequence a row is read from is not defined).  The outputs overlap
+ * nothing else.
+ */
+typedef struct {
+  int32_t num_rows;            /* N >= 0: rows of k and v */
+  int32_t num_seqs;            /* B >= 0 */
+  const int32_t* row_starts;   /* [B + 1] */
+  const int32_t* first;        /* [B] first positions, or NULL: 0 */
+  v4a_dense_cache kv;
+  uint16_t* k;                 /* [N] rows of [num_kv_heads][dim], 16-byte aligned */
+  int64_t k_stride;            /* elements between rows: a multiple of 8, at least num_kv_heads * dim */
+  uint16_t* v;
+  int64_t v_stride;
+  int32_t* status;             /* optional device word */
+} v4a_dense_read_args;
+
+V4A_API int v4a_dense_read(const v4a_dense_read_args* args, void* stream);
+
+/*
  * Attention.  Sequence b's tokens are t in [token_starts[b],
  * token_starts[b + 1]), at consecutive positions; their keys and values are in
  * the cache already.  For token t at position m and head h (its KV head is
@@ -261,6 +326,55 @@ typedef struct {
  * 16-byte aligned and its contents need no initialisation. */
 V4A_API size_t v4a_dense_attn_workspace_size(const v4a_dense_attn_args* args);
 V4A_API int v4a_dense_attn(const v4a_dense_attn_args* args, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Attention of whole prompts over packed rows.  Sequence b's queries are the
+ * tokens t in [token_starts[b], token_starts[b + 1]), n of them; its keys and
+ * values the rows [kv_starts[b], kv_starts[b + 1]), N of them.  The queries are
+ * the sequence's last positions: the i-th is at position m = N - n + i.
+ *   causal:      visible(j) = j <= m and (window == 0 or j > m - window or j < sinks)
+ *   not causal:  visible(j) = every j < N
+ * with z, out, lse and the KV head of a head as v4a_dense_attn has them.  A query
+ * that sees no key (N = 0, or m < 0 where n > N) gets 0 and lse = -inf.  A
+ * sequence whose entries are inconsistent (starts decreasing, negative or past
+ * num_tokens or num_kv_tokens, more than max_new_per_seq queries) sets
+ * V4A_DEV_BAD_BATCH and its rows are left as they were, as are the rows behind
+ * the last sequence.  Sequences may share keys, not queries (V4A_DEV_BAD_BATCH
+ * once they are more than the call has room for, and what their rows hold then
+ * is not defined).  Rows outside [kv_starts[b], kv_starts[b + 1]) do not reach
+ * sequence b's outputs whatever they hold; a NaN or infinity inside may reach
+ * any of them.  Dot products and sums are fp32; the probabilities are rounded
+ * to bf16, the output once.
+ */
+typedef struct {
+  int32_t num_tokens;          /* T >= 0: rows of q and out */
+  int32_t num_kv_tokens;       /* rows of k and v, 0..2^30 */
+  int32_t num_seqs;            /* B >= 0 */
+  int32_t max_new_per_seq;     /* host-side bound on one sequence's queries, 1..2^22 */
+  const int32_t* token_starts; /* [B + 1] */
+  const int32_t* kv_starts;    /* [B + 1], or NULL: token_starts */
+  int32_t num_heads;           /* H, a multiple of num_kv_heads, <= 1024 */
+  int32_t num_kv_heads;
+  int32_t dim;                 /* 64, 128, 192 or 256 */
+  int32_t causal;              /* 1 or 0 */
+  int32_t window;              /* 0 = every earlier position; else >= 1 (causal only) */
+  int32_t sinks;               /* first positions that stay visible (>= 0; no effect without a window) */
+  float softmax_scale;         /* > 0, and finite times log2(e) */
+  const uint16_t* q;           /* [T] rows of [H][dim] bf16; rows 16-byte aligned, strides multiples of 8 elements */
+  int64_t q_stride;            /* elements between tokens, >= H * dim */
+  const uint16_t* k;           /* [num_kv_tokens] rows of [num_kv_heads][dim] */
+  int64_t k_stride;
+  const uint16_t* v;
+  int64_t v_stride;
+  uint16_t* out;               /* [T][H][dim] bf16, 16-byte aligned; overlaps no input */
+  float* lse;                  /* [T][H] or NULL */
+  int32_t* status;             /* optional device word */
+} v4a_prompt_attn_args;
+
+/* Bytes of device workspace v4a_prompt_attn needs (0 on a bad shape); it is
+ * 16-byte aligned and its contents need no initialisation. */
+V4A_API size_t v4a_prompt_attn_workspace_size(const v4a_prompt_attn_args* args);
+V4A_API int v4a_prompt_attn(const v4a_prompt_attn_args* args, void* workspace, size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }
