@@ -762,7 +762,7 @@ int dense_attn(const v4a_dense_attn_args* a, void* ws, size_t ws_bytes, cudaStre
   if (takes) {
     rc = dense_prefill_plan(a, d, both ? few + 1 : 0, static_cast<uint8_t*>(ws) + few_workspace(a), &many);
     if (rc) return rc;
-    if (many.U > 0 && !dense_prefill_ready(a)) return V4A_ERR_CUDA;
+    if (many.U > 0 && !dense_prefill_ready(a, d)) return V4A_ERR_CUDA;
     if (!both) {
       rc = dense_prefill(a, d, many, stream);
       return rc == V4A_OK && many.split ? dense_join(d, many, a->kv.dim, stream) : rc;

@@ -361,13 +361,13 @@ int dense_join(const DenseAttnDev& a, const SplitDev& p, int dim, cudaStream_t s
 bool dense_prefill_takes(const v4a_dense_attn_args* a);
 size_t dense_prefill_workspace(const v4a_dense_attn_args* a);
 int dense_prefill_plan(const v4a_dense_attn_args* a, const DenseAttnDev& d, int rows_from, void* ws, SplitDev* p);
-bool dense_prefill_ready(const v4a_dense_attn_args* a);
+bool dense_prefill_ready(const v4a_dense_attn_args* a, const DenseAttnDev& d);
 int dense_prefill(const v4a_dense_attn_args* a, const DenseAttnDev& d, const SplitDev& p, cudaStream_t stream);
 
 // The same for caches with a scale per group (dense_group.cu); the division is shared with whole prompts (prompt_attn.cu).
 size_t stream_workspace(int dim);
 int stream_plan(const DenseAttnDev& d, int dim, int rows_from, void* ws, SplitDev* p);
-bool dense_group_ready(int dim);
+bool dense_group_ready(int dim, const DenseAttnDev& d);
 int dense_group(int dim, const DenseAttnDev& d, const SplitDev& p, cudaStream_t stream);
 
 }  // namespace v4a

@@ -2,36 +2,90 @@
 // per 64 positions and KV head (v4a_dense_attn, V4A_KV_FP8_GROUP, many query
 // rows per KV head): dense_stream.cuh over that cache.
 //
-// Mathematics: a step of 64 keys is one group, so its key scale is one factor of
-// the step's logits and its value scale one shift of their exponents: the softmax
-// costs what it does over bf16 rows.  Codes become f16 on their way into shared
-// memory, exactly; the query joins them there as f16 times the power of two that
-// brings its row's largest element to [2^14, 2^15), exact down to 2^-31 of that
-// element.  P is f16 and holds 2^11 2^{w - m}, w the logit plus log2 of the value
-// scale: weights down to 2^-25 of the largest are rounded to 11 bits.
+// Mathematics: the keys of a group share a scale, so a step's key scales are one
+// factor of the logits of each 64 keys and the value scales one shift of their
+// exponents: the softmax costs what it does over bf16 rows.  The scores are an
+// 8-bit product of the key codes as they lie in the cache: a query row times the
+// power of two that brings its largest element to [2^7, 2^8) is taken as the sum
+// of two e4m3 numbers, the nearest one and what that leaves, each multiplied with
+// the keys at twice the 16-bit rate.  A bf16 has 8 bits, a nearest e4m3 4 of them
+// and the rest at most 4, so the sum is exact down to 2^-9 of the row's largest
+// element and within 2^-17 of that element below.  Value codes become f16, exactly:
+// P in 8 bits would be too coarse.  P is f16 and holds 2^11 2^{w - m}, w the logit
+// plus log2 of the value scale: weights down to 2^-25 of the largest are rounded
+// to 11 bits.
+//
+// Copies: one lane has TMA bring the key codes into the swizzle that the MMA reads,
+// and the value codes as they are; two to four warps convert the latter from shared
+// memory.  Key rows that no row sees hold anything: their scores are replaced, not
+// multiplied; hidden value rows become zeros.
 #include "dense_stream.cuh"
 
 namespace v4a {
 namespace {
 
-struct GroupCache {
-  using Dev = DenseAttnDev;
-  static constexpr bool kScaled = true, kPaged = true;
-  // Threads that copy the keys (and as many the values): each has one 16-code chunk of every kStep-th row.
-  template <int D>
-  static constexpr int loaders() { return D == 64 ? 64 : D / 2; }
-  template <int D>
-  static constexpr int threads() { return Stream<D>::kSoftmax + 32 + 2 * loaders<D>(); }
-  template <int D>
-  static constexpr int arrivals() { return loaders<D>(); }
+struct GroupDev : DenseAttnDev {
+  CUtensorMap km;                   // [pages][2 K 256 rows][dim codes]
+};
 
-  static __device__ __forceinline__ int row_position(const Dev& a, const Unit<kStreamKeys>& un, int row) {
+// K-major operand of 64-byte rows with the 64-byte swizzle: 8-row groups 512 bytes apart.
+__device__ __forceinline__ uint64_t desc_sw64(uint32_t saddr) {
+  return uint64_t((saddr & 0x3FFFFu) >> 4) | (uint64_t(1) << 16) | (uint64_t(512 >> 4) << 32) | (uint64_t(1) << 46) | (uint64_t(4) << 61);
+}
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+  uint32_t r;
+  asm("{\n.reg .b16 c;\ncvt.rn.satfinite.e4m3x2.f32 c, %2, %1;\ncvt.u32.u16 %0, c;\n}\n" : "=r"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 e4m3x2_values(uint32_t codes) {
+  uint32_t r;
+  asm("{\n.reg .b16 c;\ncvt.u16.u32 c, %1;\ncvt.rn.f16x2.e4m3x2 %0, c;\n}\n" : "=r"(r) : "r"(codes));
+  return __half22float2(*reinterpret_cast<const __half2*>(&r));
+}
+
+struct GroupCache {
+  using Dev = GroupDev;
+  static constexpr bool kScaled = true, kPaged = true;
+  static constexpr int kLead = 2;                  // steps that copies are issued ahead
+  template <int D> static constexpr int copiers() { return D == 192 ? 96 : D == 256 ? 128 : 64; }
+  template <int D> static constexpr int key_stages() { return 3; }
+  template <int D> static constexpr int value_stages() { return 2; }
+  template <int D> static constexpr int key_bytes() { return Stream<D>::kKeys * D; }
+  template <int D> static constexpr int extra_bytes() { return 2 * key_bytes<D>(); }       // value codes
+  template <int D> static constexpr int value_arrivals() { return copiers<D>(); }
+  // Codes of an operand lie in blocks of this many bytes a row, the span of its swizzle.
+  template <int D> static constexpr int block() { return D % 128 ? 64 : 128; }
+
+  // Byte offset of 16-byte chunk `ch` of row r in an operand of [dim / block][kN rows][block].
+  template <int D, int kN>
+  static __device__ __forceinline__ uint32_t code_chunk(int r, int ch) {
+    constexpr int kPer = block<D>() / 16;
+    return uint32_t(ch / kPer * (kN * block<D>()) + r * block<D>() + (((ch % kPer) ^ (kPer == 8 ? r & 7 : (r >> 1) & 3)) << 4));
+  }
+
+  template <int kKeys>
+  static __device__ __forceinline__ int row_position(const Dev& a, const Unit<kKeys>& un, int row) {
     return un.m_lo + (un.row0 % a.G + row) / a.G;
   }
 
-  // Row r of tile t as f16 into the operand at q0; zeros behind the unit's last row.
   template <int D>
-  static __device__ __forceinline__ float load_q(const Dev& a, const Unit<kStreamKeys>& un, int hk, int t, int r, uint32_t q0) {
+  static __device__ __forceinline__ void scores(uint32_t st, uint32_t qa, uint32_t kb) {
+    constexpr int kKeys = Stream<D>::kKeys, kPer = block<D>() / 32;
+    constexpr uint32_t idesc = tc::make_idesc(0, 0, kTileRows, kKeys);
+    auto desc = [](uint32_t at) { return block<D>() == 128 ? tc::desc_sw128(at) : desc_sw64(at); };
+#pragma unroll
+    for (int k = 0; k < 2 * (D / 32); ++k) {       // the nearest e4m3, then the rest, against the same codes
+      const int j = k % (D / 32);
+      tc::mma_f8f6f4(st, desc(qa + (k / (D / 32)) * (kTileRows * D) + j / kPer * (kTileRows * block<D>())) + 2 * (j % kPer),
+                     desc(kb + j / kPer * (kKeys * block<D>())) + 2 * (j % kPer), idesc, k > 0);
+    }
+  }
+
+  static __device__ __forceinline__ bool q_copied(const Dev&) { return false; }
+
+  // Row r of tile t as two e4m3 operands at q0 and behind; zeros behind the unit's last row.
+  template <int D>
+  static __device__ __forceinline__ float load_q(const Dev& a, const Unit<Stream<D>::kKeys>& un, int hk, int t, int r, uint32_t q0) {
     const int row = t * kTileRows + r;
     const bool live = row < un.rows;
     const uint4* q = reinterpret_cast<const uint4*>(a.q + row_of(a, un, hk, live ? row : 0) * D);
@@ -42,93 +96,188 @@ struct GroupCache {
       top = __vmaxu2(top, __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu), __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu)));
     }
     top = max(top >> 16, top & 0xffffu);
-    const int e = top == 0 ? 127 : min(253, max(1, 268 - int(top >> 7)));      // the power's exponent field
-    const float up = __int_as_float(e << 23), down = __int_as_float((254 - e) << 23);
-    auto f16 = [&](uint32_t w) { return live ? pack_f16(__uint_as_float(w << 16) * up, __uint_as_float(w & 0xffff0000u) * up) : 0u; };
-#pragma unroll 8
-    for (int ch = 0; ch < D / 8; ++ch) {
-      const uint4 w = __ldcg(q + ch);
-      st_shared16(q0 + stream_chunk<kTileRows>(r, ch), make_uint2(f16(w.x), f16(w.y)), make_uint2(f16(w.z), f16(w.w)));
+    const int e = top == 0 ? 127 : min(253, max(1, 261 - int(top >> 7)));      // the power's exponent field
+    const float up = live ? __int_as_float(e << 23) : 0.f, down = __int_as_float((254 - e) << 23);
+#pragma unroll 4
+    for (int ch = 0; ch < D / 16; ++ch) {
+      const uint4 u = __ldcg(q + 2 * ch), w = __ldcg(q + 2 * ch + 1);
+      const uint32_t in[8] = {u.x, u.y, u.z, u.w, w.x, w.y, w.z, w.w};
+      uint32_t near[4], rest[4];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float x = __uint_as_float(in[k] << 16) * up, y = __uint_as_float(in[k] & 0xffff0000u) * up;
+        const uint32_t c = e4m3x2(x, y);
+        const float2 v = e4m3x2_values(c);
+        const uint32_t d = e4m3x2(x - v.x, y - v.y);
+        near[k >> 1] = k & 1 ? near[k >> 1] | c << 16 : c;
+        rest[k >> 1] = k & 1 ? rest[k >> 1] | d << 16 : d;
+      }
+      const uint32_t at = q0 + code_chunk<D, kTileRows>(r, ch);
+      st_shared16(at, make_uint2(near[0], near[1]), make_uint2(near[2], near[3]));
+      st_shared16(at + kTileRows * D, make_uint2(rest[0], rest[1]), make_uint2(rest[2], rest[3]));
     }
     return fmaxf(a.scale_log2 * down, 0x1p-126f);
   }
 
-  // Keys (half 0) or values of `count` steps from tile `tile` of the unit on, step n of the CTA first.
+  // The copies of a step's codes, issued by one lane kLead steps ahead.  Table entries are read two steps before they
+  // are used and the scales one step.
   template <int D>
-  static __device__ __forceinline__ bool copy(const Dev& a, const Unit<kStreamKeys>& un, int hk, int tile, int count, int n, int half, int lt,
-                                              uint8_t* buffers, StreamSmem& s) {
-    constexpr int S = Stream<D>::kStages, kPerRow = D / 16, kStep = loaders<D>() / kPerRow, kPasses = kStreamKeys / kStep;
-    static_assert(kStep % 8 == 0 && loaders<D>() % kPerRow == 0, "a thread's chunks lie at the same place of the swizzle");
+  struct Feed {
+    using W = Stream<D>;
+    using L = StreamLayout<D, GroupCache>;
+    static constexpr int kGroups = W::kKeys / kGroupPositions;
+    const Dev& a;
+    uint8_t* base;
+    StreamSmem& s;
+    const Unit<W::kKeys>* un = nullptr;
+    int hk = 0, tile = 0, count = 0, issued = 0;       // issued: steps of the CTA whose copies are on their way
+    int32_t entry = -1;                                // table entry of the step behind `page`'s
+    int32_t page = -1;                                 // of the step to be issued; -1: missing
+    float scale = 1.f;                                 // lanes 0..3: its groups' key scales, then value scales
+
+    __device__ __forceinline__ Feed(const Dev& a_, uint8_t* base_, StreamSmem& s_) : a(a_), base(base_), s(s_) {}
+    __device__ __forceinline__ int lane() const { return threadIdx.x & 31; }
+    __device__ __forceinline__ int32_t lookup(int i) const {
+      return i < count ? __ldcg(a.bt + int64_t(un->b) * a.max_blocks + un->tr.at(tile + i) / (kBlockPositions / W::kKeys)) : -1;
+    }
+    // Takes `entry`, of step i, for the next step to be issued, and reads its scales and the entry behind.
+    __device__ __forceinline__ void advance(int i) {
+      page = entry;
+      entry = lookup(i + 1);
+      if (i < count && (page < 0 || page >= a.num_blocks)) {
+        if (lane() == 0) report(a.status, V4A_DEV_BAD_BLOCK);
+        page = -1;
+      }
+      scale = 1.f;
+      if (page >= 0 && lane() < 2 * kGroups) {
+        const int which = lane() / kGroups, g = lane() % kGroups;
+        const int j = un->tr.at(tile + i) * W::kKeys + g * kGroupPositions;       // the group's first position
+        const float* at = reinterpret_cast<const float*>(a.pool + page * a.block_bytes + int64_t(2 * a.K) * kBlockPositions * D);
+        // (of a group that no row sees the scale may be anything)
+        if (j <= un->m_hi && (a.window == 0 || j + kGroupPositions - 1 > un->m_lo - a.window || j < a.sinks))
+          scale = __ldcg(at + (which * a.K + hk) * kGroupsPerBlock + j % kBlockPositions / kGroupPositions);
+      }
+    }
+    // Issues the copies of step i of the segment, step n of the CTA.
+    __device__ __forceinline__ bool issue(int i, int n) {
+      constexpr int SK = key_stages<D>();
+      bool ok = wait_for(&s.k_free[n % SK], ((n / SK) & 1) ^ 1, a.status, &s.abort_flag) &&
+                wait_for(&s.raw_free[n % 2], ((n / 2) & 1) ^ 1, a.status, &s.abort_flag);
+      if (!__all_sync(0xffffffffu, ok)) return false;
+      if (lane() < 2 * kGroups) {
+        const int which = lane() / kGroups, g = lane() % kGroups;
+        float* const to = s.scales[n & 7][g];
+        if (which == 0) {
+          to[0] = scale;
+        } else {
+          const float l = scale > 0x1p-100f ? log2f(scale) : scale <= 0x1p-100f ? -100.f : scale;
+          to[1] = l;
+          to[2] = exp2f(-l);
+        }
+      }
+      if (lane() == 0) s.missing[n & 7] = page < 0;
+      __syncwarp();
+      if (lane() == 0) {
+        if (page < 0) {
+          tc::mbar_arrive(&s.k_full[n % SK]);
+          tc::mbar_arrive(&s.raw_full[n % 2]);
+        } else {
+          const int at = hk * kBlockPositions + un->tr.at(tile + i) * W::kKeys % kBlockPositions;       // first row of the step
+          uint8_t* const keys = base + L::kKeys + (n % SK) * L::kKeyBytes;
+          tc::mbar_arrive_expect_tx(&s.k_full[n % SK], L::kKeyBytes);
+#pragma unroll
+          for (int c = 0; c < D / block<D>(); ++c)
+            tc::tma_load_3d(keys + c * (W::kKeys * block<D>()), &a.km, c * block<D>(), at, page, &s.k_full[n % SK]);
+          tc::mbar_arrive_expect_tx(&s.raw_full[n % 2], L::kKeyBytes);
+          tc::bulk_load(base + L::kExtra + (n % 2) * L::kKeyBytes,
+                        a.pool + page * a.block_bytes + (int64_t(a.K) * kBlockPositions + at) * D, L::kKeyBytes, &s.raw_full[n % 2]);
+        }
+      }
+      issued = n + 1;
+      advance(i + 1);
+      return true;
+    }
+    __device__ __forceinline__ bool begin(const Unit<W::kKeys>& un_, int hk_, int tile_, int count_, int n) {
+      un = &un_;
+      hk = hk_; tile = tile_; count = count_;
+      entry = lookup(0);
+      advance(0);
+      for (int i = 0; i < min(count, kLead); ++i)
+        if (!issue(i, n + i)) return false;
+      return true;
+    }
+    __device__ __forceinline__ bool step(int i, int n) { return i + kLead >= count || issue(i + kLead, n + kLead); }
+    __device__ __forceinline__ void drain() {
+      drain_copies(s.k_full, key_stages<D>(), issued);
+      drain_copies(s.raw_full, 2, issued);
+    }
+  };
+
+  // Value codes of `count` steps from tile `tile` of the unit on, step n of the CTA first, as f16.
+  template <int D>
+  static __device__ __forceinline__ bool copy(const Dev& a, const Unit<Stream<D>::kKeys>& un, int, int tile, int count, int n, int lt,
+                                              uint8_t* base, StreamSmem& s) {
+    using L = StreamLayout<D, GroupCache>;
+    constexpr int SV = value_stages<D>(), kKeys = Stream<D>::kKeys, kPerRow = D / 16, kStep = copiers<D>() / kPerRow, kPasses = kKeys / kStep;
+    static_assert(kStep % 8 == 0 && copiers<D>() % kPerRow == 0 && kKeys % kStep == 0, "a thread's chunks lie at the same place of the swizzle");
     const int r0 = lt / kPerRow, ch = lt % kPerRow;
-    const uint32_t even = tc::smem_u32(buffers) + stream_chunk<kStreamKeys>(r0, 2 * ch), odd = tc::smem_u32(buffers) + stream_chunk<kStreamKeys>(r0, 2 * ch + 1);
-    uint64_t* const full = half ? s.v_full : s.k_full;
-    uint64_t* const free = half ? s.v_free : s.k_free;
+    const uint32_t values = tc::smem_u32(base + L::kValues);
+    const uint32_t even = values + stream_chunk<kKeys>(r0, 2 * ch), odd = values + stream_chunk<kKeys>(r0, 2 * ch + 1);
     volatile int* abort_flag = &s.abort_flag;
-    auto entry = [&](int i) {        // step i's table entry, read ahead of its use
-      return i < count ? __ldcg(a.bt + int64_t(un.b) * a.max_blocks + un.tr.at(tile + i) / (kBlockPositions / kStreamKeys)) : -1;
-    };
-    // step i's rows and scales; rows up to hi, and of those the ones behind lo or before sk, are read, the others are zeros
-    struct Step { uint4 raw[kPasses]; float ks, vs; bool missing; };
-    auto read = [&](int i, int32_t page, Step& st) {
-      st.missing = page < 0 || page >= a.num_blocks;
-      if (st.missing && lt == 0 && half == 0) report(a.status, V4A_DEV_BAD_BLOCK);
-      const int j0 = un.tr.at(tile + i) * kStreamKeys;
-      const int hi = st.missing ? -1 : un.m_hi - j0, lo = a.window ? un.m_lo - a.window - j0 : -1, sk = a.window ? a.sinks - j0 : 0;
-      const uint8_t* block = a.pool + (st.missing ? 0 : page * a.block_bytes);
-      const int at = st.missing ? 0 : hk * kBlockPositions + j0 % kBlockPositions;       // first row of the step
-      const uint8_t* src = block + (int64_t(half * a.K) * kBlockPositions + at) * D + lt * 16;
+    for (int i = 0; i < count; ++i, ++n) {
+      if (!wait_for(&s.raw_full[n % 2], (n / 2) & 1, a.status, abort_flag)) return false;
+      const int j0 = un.tr.at(tile + i) * kKeys;
+      // rows up to hi, and of those the ones behind lo or before sk, are values, the others zeros
+      const int hi = s.missing[n & 7] ? -1 : un.m_hi - j0, lo = a.window ? un.m_lo - a.window - j0 : -1, sk = a.window ? a.sinks - j0 : 0;
+      const uint4* raw = reinterpret_cast<const uint4*>(base + L::kExtra + (n % 2) * L::kKeyBytes) + lt;
+      if (!wait_for(&s.v_free[n % SV], ((n / SV) & 1) ^ 1, a.status, abort_flag)) return false;
+      const uint32_t to = (n % SV) * Stream<D>::kStepBytes;
 #pragma unroll
       for (int k = 0; k < kPasses; ++k) {
         const int r = r0 + k * kStep;
-        st.raw[k] = make_uint4(0, 0, 0, 0);
-        if (r <= hi && (r > lo || r < sk)) st.raw[k] = __ldcg(reinterpret_cast<const uint4*>(src + k * (kStep * D)));
+        uint4 w = raw[k * copiers<D>()];
+        if (!(r <= hi && (r > lo || r < sk))) w = make_uint4(0, 0, 0, 0);
+        st_shared16(even + to + k * (kStep * 128), f16_of(w.x), f16_of(w.y));
+        st_shared16(odd + to + k * (kStep * 128), f16_of(w.z), f16_of(w.w));
       }
-      st.ks = st.vs = 1.f;
-      if (lt == 0 && half == 0 && !st.missing) {
-        const float* scale = reinterpret_cast<const float*>(block + int64_t(2 * a.K) * kBlockPositions * D) + at / kStreamKeys;
-        st.ks = __ldcg(scale);
-        st.vs = __ldcg(scale + a.K * (kBlockPositions / kStreamKeys));
-      }
-    };
-    Step cur, next;
-    read(0, entry(0), cur);
-    int32_t page = entry(1);
-    for (int i = 0; i < count; ++i, ++n) {
-      if (i + 1 < count) read(i + 1, page, next);
-      page = entry(i + 2);
-      if (!wait_for(&free[n % S], ((n / S) & 1) ^ 1, a.status, abort_flag)) return false;
-      if (lt == 0 && half == 0) {
-        const float l = cur.vs > 0x1p-100f ? log2f(cur.vs) : cur.vs <= 0x1p-100f ? -100.f : cur.vs;
-        s.missing[n & 7] = cur.missing;
-        *reinterpret_cast<float4*>(s.scales[n & 7]) = make_float4(cur.ks, l, exp2f(-l), 0.f);
-      }
-      const uint32_t to = (n % S) * Stream<D>::kStepBytes;
-#pragma unroll
-      for (int k = 0; k < kPasses; ++k) {
-        st_shared16(even + to + k * (kStep * 128), f16_of(cur.raw[k].x), f16_of(cur.raw[k].y));
-        st_shared16(odd + to + k * (kStep * 128), f16_of(cur.raw[k].z), f16_of(cur.raw[k].w));
-      }
+      tc::mbar_arrive(&s.raw_free[n % 2]);
       tc::fence_proxy_async();
-      tc::mbar_arrive(&full[n % S]);
-      cur = next;
+      tc::mbar_arrive(&s.v_full[n % SV]);
     }
     return true;
   }
 };
 
+bool make_map(CUtensorMap* map, const DenseAttnDev& d, int dim) {
+  auto fn = tc::encode_fn();
+  if (!fn) return false;
+  const int block = dim % 128 ? 64 : 128;
+  const cuuint64_t dims[3] = {cuuint64_t(dim), cuuint64_t(2 * d.K) * kBlockPositions, cuuint64_t(d.num_blocks)};
+  const cuuint64_t strides[2] = {cuuint64_t(dim), cuuint64_t(d.block_bytes)};
+  const cuuint32_t box[3] = {cuuint32_t(block), cuuint32_t(dim <= 128 ? 128 : 64), 1}, step[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t*>(d.pool), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            block == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace
 
-bool dense_group_ready(int dim) {
+bool dense_group_ready(int dim, const DenseAttnDev& d) {
+  CUtensorMap map;
+  if (!make_map(&map, d, dim)) return false;
   return dim == 64 ? stream_ready<64, GroupCache>() : dim == 128 ? stream_ready<128, GroupCache>()
        : dim == 192 ? stream_ready<192, GroupCache>() : stream_ready<256, GroupCache>();
 }
 
 int dense_group(int dim, const DenseAttnDev& d, const SplitDev& p, cudaStream_t stream) {
+  GroupDev g{};
+  static_cast<DenseAttnDev&>(g) = d;
+  if (!make_map(&g.km, d, dim)) return V4A_ERR_CUDA;
   switch (dim) {
-    case 64: return stream_launch<64, GroupCache>(d, p, stream);
-    case 128: return stream_launch<128, GroupCache>(d, p, stream);
-    case 192: return stream_launch<192, GroupCache>(d, p, stream);
-    default: return stream_launch<256, GroupCache>(d, p, stream);
+    case 64: return stream_launch<64, GroupCache>(g, p, stream);
+    case 128: return stream_launch<128, GroupCache>(g, p, stream);
+    case 192: return stream_launch<192, GroupCache>(g, p, stream);
+    default: return stream_launch<256, GroupCache>(g, p, stream);
   }
 }
 
@@ -147,7 +296,7 @@ int stream_plan(const DenseAttnDev& d, int dim, int rows_from, void* ws, SplitDe
   // under a window one CTA per unit and KV head, unless the last wave of CTAs is nearly empty (as dense_prefill_plan)
   const int64_t ctas = int64_t(p.U) * d.K, idle = (ctas + kSms - 1) / kSms * kSms - ctas;
   p.split = std::max(p.U, d.B) <= kMaxSplitUnits && (d.window == 0 || idle * (d.window / 128 + 5) > 9 * kSms);
-  split_carve(&p, ws, unit, dim, kSms, kStreamCost);
+  split_carve(&p, ws, unit, dim, kSms, dim <= 128 ? Stream<128>::kCost : Stream<256>::kCost);
   *out = p;
   return V4A_OK;
 }

@@ -519,8 +519,8 @@ int dense_prefill_plan(const v4a_dense_attn_args* a, const DenseAttnDev& d, int 
   return V4A_OK;
 }
 
-bool dense_prefill_ready(const v4a_dense_attn_args* a) {
-  if (a->kv.format == V4A_KV_FP8_GROUP) return dense_group_ready(a->kv.dim);
+bool dense_prefill_ready(const v4a_dense_attn_args* a, const DenseAttnDev& d) {
+  if (a->kv.format == V4A_KV_FP8_GROUP) return dense_group_ready(a->kv.dim, d);
   const bool fp8 = a->kv.format == V4A_KV_FP8_TOKEN;
   if (a->kv.dim > 128) return dense_prefill_wide_ready(a->kv.dim, fp8);
   if (fp8) return a->kv.dim == 64 ? ready<64, true>() : ready<128, true>();

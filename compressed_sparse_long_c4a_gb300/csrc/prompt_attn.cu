@@ -1,7 +1,7 @@
 // Attention of whole packed prompts over packed keys and values
 // (v4a_dense.h, v4a_prompt_attn): dense_stream.cuh over bf16 rows.
 //
-// Keys and values come by TMA (a box of 64 rows x 64 dims of one head lands in
+// Keys and values come by TMA (a box of a step's rows x 64 dims of one head lands in
 // the 128-byte swizzle that the MMA reads), but for a step that reaches past
 // its sequence: its rows behind the last are zeros, so that the next
 // sequence's cannot reach a product, and are copied by the warp.
@@ -16,6 +16,8 @@ struct PromptDev : DenseAttnDev {
   int64_t qs, ks, vs;               // elements between tokens
   const uint16_t *k, *v;
   CUtensorMap km, vm;               // [Tk][K][dim]
+  CUtensorMap qm;                   // [T][K][G][dim]
+  int q_copied;
 };
 
 // One sequence's rows: p0 is its first row's position among its keys (not causal: every row's, the last key's).
@@ -44,22 +46,80 @@ __device__ __forceinline__ Unit<kTile> make_unit(const PromptDev& a, const UnitR
   return u;
 }
 
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, int c0, int c1, int c2, int c3, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
+          tc::smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(tc::smem_u32(bar))
+      : "memory");
+}
+
 struct PackedRows {
   using Dev = PromptDev;
   static constexpr bool kScaled = false, kPaged = false;
-  template <int D>
-  static constexpr int loaders() { return 32; }
-  template <int D>
-  static constexpr int threads() { return Stream<D>::kSoftmax + 32 + 64; }
-  template <int D>
-  static constexpr int arrivals() { return 1; }
+  template <int D> static constexpr int copiers() { return 64; }       // a warp for the keys, one for the values
+  template <int D> static constexpr int key_stages() { return D == 64 ? 4 : D == 192 ? 3 : 2; }
+  template <int D> static constexpr int value_stages() { return key_stages<D>(); }
+  template <int D> static constexpr int key_bytes() { return Stream<D>::kStepBytes; }
+  template <int D> static constexpr int extra_bytes() { return 0; }
+  template <int D> static constexpr int value_arrivals() { return 1; }
 
-  static __device__ __forceinline__ int row_position(const Dev& a, const Unit<kStreamKeys>& un, int row) {
+  template <int kKeys>
+  static __device__ __forceinline__ int row_position(const Dev& a, const Unit<kKeys>& un, int row) {
     return un.m_lo + (a.causal ? (un.row0 % a.G + row) / a.G : 0);
   }
 
   template <int D>
-  static __device__ __forceinline__ float load_q(const Dev& a, const Unit<kStreamKeys>& un, int hk, int t, int r, uint32_t q0) {
+  static __device__ __forceinline__ void scores(uint32_t st, uint32_t qa, uint32_t kb) {
+    constexpr int kKeys = Stream<D>::kKeys;
+    constexpr uint32_t idesc = tc::make_idesc(1, 1, kTileRows, kKeys);
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k)
+      tc::mma_f16(st, tc::desc_sw128(qa + (k >> 2) * (kTileRows * 128)) + 2 * (k & 3),
+                  tc::desc_sw128(kb + (k >> 2) * (kKeys * 128)) + 2 * (k & 3), idesc, k > 0);
+  }
+
+  // Rows are (token, head of the group) pairs: where a group divides a tile, a tile's are a box.
+  static __device__ __forceinline__ bool q_copied(const Dev& a) { return a.q_copied != 0; }
+
+  template <int D>
+  struct Feed {
+    using W = Stream<D>;
+    const Dev& a;
+    uint8_t* base;
+    StreamSmem& s;
+    int tiles[2] = {0, 0};
+    __device__ __forceinline__ Feed(const Dev& a_, uint8_t* base_, StreamSmem& s_) : a(a_), base(base_), s(s_) {}
+    __device__ __forceinline__ bool begin(const Unit<W::kKeys>& un, int hk, int, int, int n) {
+      if (!a.q_copied) return true;
+      // Q is free when the unit before's last scores, the last to read its keys, are there
+      constexpr int SK = key_stages<D>();
+      const bool ok = n == 0 || wait_for(&s.k_free[(n - 1) % SK], ((n - 1) / SK) & 1, a.status, &s.abort_flag);
+      if (!__all_sync(0xffffffffu, ok)) return false;
+#pragma unroll
+      for (int t = 0; t < W::kTiles; ++t) {
+        if (un.rows <= t * kTileRows) continue;
+        if ((threadIdx.x & 31) == 0) {
+          tc::mbar_arrive_expect_tx(&s.q_full[t], W::kQBytes);
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c)
+            tma_load_4d(base + t * W::kQBytes + c * (kTileRows * 128), &a.qm, 64 * c, 0, hk, un.s0 + (un.row0 + t * kTileRows) / a.G, &s.q_full[t]);
+        }
+        ++tiles[t];
+      }
+      return true;
+    }
+    __device__ __forceinline__ bool step(int, int) { return true; }
+    __device__ __forceinline__ void drain() {
+      if (!a.q_copied) return;
+#pragma unroll
+      for (int t = 0; t < W::kTiles; ++t)
+        if (tiles[t]) drain_copies(&s.q_full[t], 1, tiles[t]);
+    }
+  };
+
+  template <int D>
+  static __device__ __forceinline__ float load_q(const Dev& a, const Unit<Stream<D>::kKeys>& un, int hk, int t, int r, uint32_t q0) {
 #pragma unroll 4
     for (int c = r; c < kTileRows * (D / 8); c += kTileRows) {
       const int qr = c / (D / 8), ch = c % (D / 8), row = t * kTileRows + qr, i = un.row0 + min(row, un.rows - 1);
@@ -70,10 +130,14 @@ struct PackedRows {
     return a.scale_log2;
   }
 
+  // Keys (the first warp) or values of `count` steps from tile `tile` of the unit on, step n of the CTA first.
   template <int D>
-  static __device__ __forceinline__ bool copy(const Dev& a, const Unit<kStreamKeys>& un, int hk, int tile, int count, int n, int half, int lane,
-                                              uint8_t* buffers, StreamSmem& s) {
-    constexpr int S = Stream<D>::kStages;
+  static __device__ __forceinline__ bool copy(const Dev& a, const Unit<Stream<D>::kKeys>& un, int hk, int tile, int count, int n, int lt,
+                                              uint8_t* base, StreamSmem& s) {
+    using L = StreamLayout<D, PackedRows>;
+    constexpr int S = key_stages<D>(), kKeys = Stream<D>::kKeys;
+    const int half = lt / 32, lane = lt % 32;
+    uint8_t* const buffers = base + (half ? L::kValues : L::kKeys);
     const int k0 = a.kv_starts[un.b], nk = a.kv_starts[un.b + 1] - k0;
     const CUtensorMap* map = half ? &a.vm : &a.km;
     const uint16_t* rows = half ? a.v : a.k;
@@ -82,22 +146,25 @@ struct PackedRows {
     uint64_t* const free = half ? s.v_free : s.k_free;
     volatile int* abort_flag = &s.abort_flag;
     for (int i = 0; i < count; ++i, ++n) {
-      if (!__all_sync(0xffffffffu, wait_for(&free[n % S], ((n / S) & 1) ^ 1, a.status, abort_flag))) return false;
+      if (!__all_sync(0xffffffffu, wait_for(&free[n % S], ((n / S) & 1) ^ 1, a.status, abort_flag))) {
+        drain_copies(full, S, n);
+        return false;
+      }
       uint8_t* const to = buffers + (n % S) * Stream<D>::kStepBytes;
-      const int j0 = un.tr.at(tile + i) * kStreamKeys;
-      if (j0 + kStreamKeys <= nk) {
+      const int j0 = un.tr.at(tile + i) * kKeys;
+      if (j0 + kKeys <= nk) {
         if (lane == 0) {
           tc::mbar_arrive_expect_tx(&full[n % S], Stream<D>::kStepBytes);
 #pragma unroll
-          for (int c = 0; c < D / 64; ++c) tc::tma_load_3d(to + c * (kStreamKeys * 128), map, 64 * c, hk, k0 + j0, &full[n % S]);
+          for (int c = 0; c < D / 64; ++c) tc::tma_load_3d(to + c * (kKeys * 128), map, 64 * c, hk, k0 + j0, &full[n % S]);
         }
       } else {
         const uint32_t dst = tc::smem_u32(to);
 #pragma unroll 4
-        for (int c = lane; c < kStreamKeys * (D / 8); c += 32) {
+        for (int c = lane; c < kKeys * (D / 8); c += 32) {
           const int r = c / (D / 8), ch = c % (D / 8);
           const bool live = j0 + r < nk;
-          copy16(dst + stream_chunk<kStreamKeys>(r, ch), rows + (live ? (int64_t(k0) + j0 + r) * stride + hk * D + ch * 8 : 0), live);
+          copy16(dst + stream_chunk<kKeys>(r, ch), rows + (live ? (int64_t(k0) + j0 + r) * stride + hk * D + ch * 8 : 0), live);
         }
         tc::cp_async_wait_all();
         tc::fence_proxy_async();
@@ -109,14 +176,25 @@ struct PackedRows {
   }
 };
 
-// A map of [rows][heads][dim] whose boxes are 64 rows x 64 dims of one head.
+// A map of [rows][heads][dim] whose boxes are a step's rows x 64 dims of one head.
 bool make_map(CUtensorMap* map, const uint16_t* rows, int64_t n, int heads, int dim, int64_t stride) {
   auto fn = tc::encode_fn();
   if (!fn) return false;
   const cuuint64_t dims[3] = {cuuint64_t(dim), cuuint64_t(heads), cuuint64_t(n)};
   const cuuint64_t strides[2] = {cuuint64_t(dim) * 2, cuuint64_t(stride) * 2};
-  const cuuint32_t box[3] = {64, 1, kStreamKeys}, step[3] = {1, 1, 1};
+  const cuuint32_t box[3] = {64, 1, cuuint32_t(dim <= 128 ? 128 : 64)}, step[3] = {1, 1, 1};
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t*>(rows), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// A map of queries [tokens][KV heads][group][dim] whose boxes are a tile's rows x 64 dims of one KV head.
+bool make_q_map(CUtensorMap* map, const PromptDev& d, int dim) {
+  auto fn = tc::encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[4] = {cuuint64_t(dim), cuuint64_t(d.G), cuuint64_t(d.K), cuuint64_t(d.T)};
+  const cuuint64_t strides[3] = {cuuint64_t(dim) * 2, cuuint64_t(d.G) * dim * 2, cuuint64_t(d.qs) * 2};
+  const cuuint32_t box[4] = {64, cuuint32_t(d.G), 1, cuuint32_t(kTileRows / d.G)}, step[4] = {1, 1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<uint16_t*>(d.q), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -171,6 +249,8 @@ int prompt_attn(const v4a_prompt_attn_args* a, void* ws, size_t ws_bytes, cudaSt
   rc = stream_plan(d, a->dim, 0, ws, &p);
   if (rc) return rc;
   if (a->num_kv_tokens > 0 && (!make_map(&d.km, a->k, d.Tk, d.K, a->dim, d.ks) || !make_map(&d.vm, a->v, d.Tk, d.K, a->dim, d.vs))) return V4A_ERR_CUDA;
+  d.q_copied = kTileRows % d.G == 0;
+  if (d.q_copied && !make_q_map(&d.qm, d, a->dim)) return V4A_ERR_CUDA;
   if (!ready(a->dim)) return V4A_ERR_CUDA;
   switch (a->dim) {
     case 64: rc = stream_launch<64, PackedRows>(d, p, stream); break;

@@ -8,7 +8,13 @@ off by at most 2^-8 of the value, a probability rounded to bf16 by 2^-8 of
 itself (prompts), one rounded to f16 by 2^-11 (caches; those below 2^-25 of the
 largest by 2^-36 of it); a logit's dot product of D terms is off by (D + 8)
 2^-24 of the largest sum |q||k| (as a relative error of p, twice: in p and in
-the sum); the sums over N keys by (N + 32) 2^-24.
+the sum); the sums over N keys by (N + 32) 2^-24.  Chunks over a cache take a
+query as two e4m3 numbers after a power of two that brings the row's largest
+element into [2^7, 2^8): a bf16 x of exponent e is a multiple of 2^(e - 7), the
+nearest e4m3 (half a step: 2^(e - 4)) leaves at most 8 such units, which four bits
+hold, so the sum is x unless the rest falls below e4m3's least step 2^-9: then it
+is off by half of that, 2^-10 <= 2^-17 of the largest element.  A logit is off by
+at most 2^-17 of that element times the largest sum |k|, times the scale.
 """
 from __future__ import annotations
 
@@ -316,10 +322,10 @@ class GroupLayer(Layer):
                 if tokens is None or t in tokens:
                     m = positions[t]
                     seen = [j for j in OD.visible(m, window, sinks) if self.table[b, j // 256] >= 0]
-                    _check_token(q[t], out[t], lse[t], lambda w, h: self.rows(b, w, h, m + 1)[seen], self.K, scale, 2.0 ** -11, (b, t))
+                    _check_token(q[t], out[t], lse[t], lambda w, h: self.rows(b, w, h, m + 1)[seen], self.K, scale, 2.0 ** -11, (b, t), 2.0 ** -17)
 
 
-def _check_token(q, out, lse, rows, K, scale, p_step, where):
+def _check_token(q, out, lse, rows, K, scale, p_step, where, q_step=0.0):
     """One token's heads against the oracle; p_step: half a step of a probability."""
     q, got, got_l = _f64(q), _f64(out), _f64(lse)
     G, dim = q.shape[0] // K, q.shape[1]
@@ -327,6 +333,8 @@ def _check_token(q, out, lse, rows, K, scale, p_step, where):
         k, v = rows(0, h), rows(1, h)
         o, l, av, amp = OD.attention(q[h * G:(h + 1) * G], k, v, scale)
         dz = (dim + 8) * 2.0 ** -24 * amp[:, None]
+        if len(k):
+            dz = dz + q_step * scale * np.abs(q[h * G:(h + 1) * G]).max(1, keepdims=True) * np.abs(k).sum(1).max()
         n = (len(k) + 32) * 2.0 ** -24
         small = len(k) * 2.0 ** -34 * np.abs(v).max() if len(k) else 0.0      # (weights that f16 holds as subnormals)
         tol = (p_step + 2 * dz + 2 * n) * av + 2.0 ** -8 * np.abs(o) + small + 1e-30
