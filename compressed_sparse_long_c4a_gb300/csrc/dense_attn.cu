@@ -765,7 +765,7 @@ int dense_attn(const v4a_dense_attn_args* a, void* ws, size_t ws_bytes, cudaStre
     if (many.U > 0 && !dense_prefill_ready(a, d)) return V4A_ERR_CUDA;
     if (!both) {
       rc = dense_prefill(a, d, many, stream);
-      return rc == V4A_OK && many.split ? dense_join(d, many, a->kv.dim, stream) : rc;
+      return rc == V4A_OK && many.split == 1 ? dense_join(d, many, a->kv.dim, stream) : rc;
     }
     p.early = many.late = many.U > 0;               // (no room for a sequence of the other form: no launch for it)
   }
@@ -782,7 +782,7 @@ int dense_attn(const v4a_dense_attn_args* a, void* ws, size_t ws_bytes, cudaStre
        : fp8 ? launch_dim<V4A_KV_FP8_TOKEN>(d, p, a->kv.dim, stream) : launch_dim<V4A_KV_BF16>(d, p, a->kv.dim, stream);
   if (rc == V4A_OK && many.U > 0) rc = dense_prefill(a, d, many, stream);
   if (rc == V4A_OK && p.split) rc = dense_join(d, p, a->kv.dim, stream);
-  return rc == V4A_OK && many.U > 0 && many.split ? dense_join(d, many, a->kv.dim, stream) : rc;
+  return rc == V4A_OK && many.U > 0 && many.split == 1 ? dense_join(d, many, a->kv.dim, stream) : rc;
 }
 
 }  // namespace v4a

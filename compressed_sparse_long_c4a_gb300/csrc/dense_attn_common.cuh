@@ -122,7 +122,7 @@ __device__ __forceinline__ int64_t row_of(const DenseAttnDev& a, const Unit<kTil
 // evenly, each unit counted with `cost` tiles more than it has (its set-up and
 // its end take about that long); split = 0: one CTA per unit and KV head.
 struct SplitDev {
-  int RG, U, split;               // row groups of the longest sequence; units at most
+  int RG, U, split;               // row groups of the longest sequence; units at most (split = 2: dense_stream.cuh)
   int rows, grid, cost;           // R; CTAs of the launch and a unit's extra tiles (split)
   struct JoinDesc* join;          // [CTA]
   float *part_o, *part_ml;        // [CTA][2][R][dim], [CTA][2][R][2] (maximum in log2 units, sum)
@@ -364,9 +364,10 @@ int dense_prefill_plan(const v4a_dense_attn_args* a, const DenseAttnDev& d, int 
 bool dense_prefill_ready(const v4a_dense_attn_args* a, const DenseAttnDev& d);
 int dense_prefill(const v4a_dense_attn_args* a, const DenseAttnDev& d, const SplitDev& p, cudaStream_t stream);
 
-// The same for caches with a scale per group (dense_group.cu); the division is shared with whole prompts (prompt_attn.cu).
+// The same for caches with a scale per group (dense_group.cu).  The division is shared with whole prompts
+// (prompt_attn.cu); keys: what a sequence has at most or on the average, causal_whole: its queries are all of them.
 size_t stream_workspace(int dim);
-int stream_plan(const DenseAttnDev& d, int dim, int rows_from, void* ws, SplitDev* p);
+int stream_plan(const DenseAttnDev& d, int dim, int rows_from, int64_t keys, bool causal_whole, void* ws, SplitDev* p);
 bool dense_group_ready(int dim, const DenseAttnDev& d);
 int dense_group(int dim, const DenseAttnDev& d, const SplitDev& p, cudaStream_t stream);
 

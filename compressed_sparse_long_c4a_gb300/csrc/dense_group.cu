@@ -283,7 +283,12 @@ int dense_group(int dim, const DenseAttnDev& d, const SplitDev& p, cudaStream_t 
 
 size_t stream_workspace(int dim) { return split_workspace(stream_unit(dim), dim, kSms); }
 
-int stream_plan(const DenseAttnDev& d, int dim, int rows_from, void* ws, SplitDev* out) {
+// Whole units are dealt out unless an even split of the steps should take less time: that has no idle CTAs, but cut units
+// leave pieces to be joined, which costs the time of about 11 steps of 128 keys.  Even split / dealt out, us, 32 + 8
+// heads of 128: prompts of 16384 tokens 1450 / 1372, 2048 61 / 43, 4 + 1 heads 8192 78 / 109, 4096 45 / 61, 16384 207 /
+// 205; 32 of 300 to 700 tokens 209 / 150; a window of 1024 over 16384 301 / 266; group caches, 4096 tokens over 28672
+// 1599 / 1776, 1000 over 4000 111 / 94.
+int stream_plan(const DenseAttnDev& d, int dim, int rows_from, int64_t keys, bool causal_whole, void* ws, SplitDev* out) {
   const int unit = stream_unit(dim);
   SplitDev p{};
   p.RG = int((int64_t(d.max_new) * d.G + unit - 1) / unit);
@@ -293,9 +298,12 @@ int stream_plan(const DenseAttnDev& d, int dim, int rows_from, void* ws, SplitDe
   const int64_t units = units_bound(d, rows_from, p.RG, unit);
   if (units > INT32_MAX || units * d.K > INT32_MAX) return V4A_ERR_UNSUPPORTED;
   p.U = int(units);
-  // under a window one CTA per unit and KV head, unless the last wave of CTAs is nearly empty (as dense_prefill_plan)
-  const int64_t ctas = int64_t(p.U) * d.K, idle = (ctas + kSms - 1) / kSms * kSms - ctas;
-  p.split = std::max(p.U, d.B) <= kMaxSplitUnits && (d.window == 0 || idle * (d.window / 128 + 5) > 9 * kSms);
+  // times in steps of 128 keys: of the longest unit, of an average one, of the call in either form
+  const double longest = double(d.window ? std::min<int64_t>(keys, d.window + 256) : keys) / 128;
+  const double mean = causal_whole && !d.window ? longest / 2 : longest, rounds = double(p.U) * d.K / kSms;
+  const double even = rounds * mean + 11, dealt = causal_whole && !d.window ? std::max(longest, rounds * mean) : std::ceil(rounds) * mean;
+  const bool can_split = std::max(p.U, d.B) <= kMaxSplitUnits, can_deal = d.B <= kMaxDealtSeqs;
+  p.split = can_split && (even < dealt || !can_deal) ? 1 : can_deal ? 2 : 0;
   split_carve(&p, ws, unit, dim, kSms, dim <= 128 ? Stream<128>::kCost : Stream<256>::kCost);
   *out = p;
   return V4A_OK;

@@ -67,6 +67,70 @@ __device__ __forceinline__ uint32_t stream_chunk(int r, int ch) {
   return uint32_t((ch >> 3) * (kN * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4));
 }
 
+// The CTA's segments (parts of units), one after the other.  SplitDev::split = 0 and 1 as in Line; 2: whole units, the
+// (unit, KV head) pairs dealt out to the CTAs and found through a table of the sequences.  One sequence's go from the
+// last on, forth and back, since a causal prompt's last units are its longest (a prompt of 16384 tokens, 32 + 8 heads
+// of 128: 1378 us, from the first on 1468); several sequences' in their order (16 of 1000 to 3000: 568 us, the other
+// way 604).
+template <int R, int kTile, int kThreads, typename Dev>
+struct Segments : Line<R, kTile, kThreads, Dev> {
+  using Base = Line<R, kTile, kThreads, Dev>;
+  using Base::a, Base::p, Base::x0, Base::x1;
+  struct Segment { int hk, tile, count; bool whole; };      // tile: the first of `count`; whole: the unit's all
+  typename Base::Seq* seqs;
+  unsigned pairs;
+
+  __device__ __forceinline__ Segments(const Dev& a_, const SplitDev& p_, void* mem) : Base(a_, p_, mem), seqs(static_cast<typename Base::Seq*>(mem)), pairs(0) {}
+  __device__ __forceinline__ bool init(int64_t* scan, void* scratch, int min_tiles) {
+    if (p.split != 2) return Base::init(scan, scratch, min_tiles);
+    const int tid = threadIdx.x;
+    int32_t* st = blockIdx.x == 0 ? a.status : nullptr;     // one CTA reports the batch's faults
+    for (int b = tid; b < a.B; b += kThreads) seqs[b] = typename Base::Seq{this->run(b, st), 0};
+    __syncthreads();
+    const int per = (a.B + kThreads - 1) / kThreads, b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
+    int64_t n = 0, all;
+    for (int b = b0; b < b1; ++b) n += this->groups(seqs[b].r.s0, seqs[b].r.s0 + seqs[b].r.n);
+    int64_t at = this->before(n, scan, &all);
+    const int units = int(min(all, int64_t(p.U)));
+    for (int b = b0; b < b1; ++b) {
+      seqs[b].first = int(min(at, int64_t(units)));
+      at += this->groups(seqs[b].r.s0, seqs[b].r.s0 + seqs[b].r.n);
+    }
+    if (st && tid == 0 && all > p.U) report(st, V4A_DEV_BAD_BATCH);         // sequences that share tokens
+    __syncthreads();
+    pairs = unsigned(units) * unsigned(a.K);        // (below 2^31: stream_plan)
+    const unsigned turns = pairs / gridDim.x, rest = pairs % gridDim.x;
+    x0 = 0;
+    x1 = turns + (seat(turns) < rest);
+    return x1 > 0;
+  }
+  __device__ __forceinline__ unsigned seat(unsigned turn) const { return a.B == 1 && turn & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x; }
+  // The segment at x, and x moved behind it.
+  __device__ __forceinline__ Segment next(int64_t* x, Unit<kTile>* un) const {
+    if (p.split != 2) {
+      const auto pc = this->locate(*x, un);
+      const int count = int(min(int64_t(un->tr.tiles - pc.tile), x1 - *x));
+      *x += count;
+      return Segment{pc.hk, pc.tile, count, pc.tile == 0 && count == un->tr.tiles};
+    }
+    const unsigned turn = unsigned(*x), place = turn * gridDim.x + seat(turn), pair = a.B == 1 ? pairs - 1 - place : place;
+    const int u = int(pair / unsigned(a.K));
+    int lo = 0;                                     // the unit's sequence: the last whose first <= u (empty ones precede)
+    for (int hi = a.B; hi - lo > 1;) {
+      const int mid = (lo + hi) >> 1;
+      if (seqs[mid].first <= u) lo = mid; else hi = mid;
+    }
+    *un = make_unit<R, kTile>(a, this->ref(lo, u - seqs[lo].first, seqs[lo].r));
+    ++*x;
+    return Segment{int(pair % unsigned(a.K)), 0, un->tr.tiles, true};
+  }
+  __device__ __forceinline__ JoinDesc tail() const {      // (split = 1) what the CTA leaves to the next ones
+    Unit<kTile> un;
+    const auto pc = this->locate(x1 - 1, &un);      // at most the last unit goes on: its first tile has to lie in the range, its last one behind it
+    return pc.tile + 1 < un.tr.tiles && x1 - 1 - pc.tile >= x0 ? this->describe(pc, un) : JoinDesc{};
+  }
+};
+
 // A value that a warp's lanes share, said so to the compiler: what an MMA takes from uniform registers need not be
 // moved there for each.
 template <typename T>
@@ -104,7 +168,7 @@ stream_attn_kernel(const __grid_constant__ typename Src::Dev a, const SplitDev p
   volatile int* abort_flag = &s.abort_flag;
 
   if (!p.late) pdl_wait();
-  Line<W::kUnit, kKeys, kThreads, typename Src::Dev> line(a, p, &s + 1);
+  Segments<W::kUnit, kKeys, kThreads, typename Src::Dev> line(a, p, &s + 1);
   if (!line.init(s.scan, base, W::kMinSteps)) {
     if (p.late) pdl_wait();
     return;
@@ -157,9 +221,8 @@ stream_attn_kernel(const __grid_constant__ typename Src::Dev a, const SplitDev p
     int n = 0, e = 0, g = 0;
     for (int64_t x = x0; x < x1 && ok;) {
       Unit<kKeys> un;
-      const auto pc = line.locate(x, &un);
-      const int count = int(min(int64_t(un.tr.tiles - pc.tile), x1 - x));
-      x += count;
+      const auto sg = line.next(&x, &un);
+      const int count = sg.count;
       if (un.rows <= t * kTileRows) {
         n += count;
         continue;
@@ -167,7 +230,7 @@ stream_attn_kernel(const __grid_constant__ typename Src::Dev a, const SplitDev p
       // a row's logits in log2 units: its scores times f (fp8: and the key scale)
       float f = a.scale_log2;
       if (!q_copied) {
-        f = Src::template load_q<D>(a, un, pc.hk, t, r, q0 + t * W::kQBytes);
+        f = Src::template load_q<D>(a, un, sg.hk, t, r, q0 + t * W::kQBytes);
         tc::fence_proxy_async();
         tc::mbar_arrive(&s.q_full[t]);
       }
@@ -192,7 +255,7 @@ stream_attn_kernel(const __grid_constant__ typename Src::Dev a, const SplitDev p
             inv_v[h] = sc.z;
           }
         }
-        const int j0 = un.tr.at(pc.tile + i) * kKeys;
+        const int j0 = un.tr.at(sg.tile + i) * kKeys;
         const bool gone = Src::kPaged && s.missing[n & 7] != 0;
         const bool hides = gone || !all_visible(a, un.m_lo, un.m_hi, j0, kKeys);
         // columns up to hi, and of those the ones behind lo or before sk; a warp whose rows see all skips each side
@@ -283,9 +346,9 @@ stream_attn_kernel(const __grid_constant__ typename Src::Dev a, const SplitDev p
       ++g;
       if (ok) {
         tc::tc_fence_after();
-        const bool begins = pc.tile == 0, whole = begins && pc.tile + count == un.tr.tiles;
+        const bool begins = sg.tile == 0, whole = sg.whole;
         const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;
-        const int64_t at = row_of(a, un, pc.hk, min(row, un.rows - 1));
+        const int64_t at = row_of(a, un, sg.hk, min(row, un.rows - 1));
         const int64_t slot = int64_t(blockIdx.x) * 2 + (begins ? 1 : 0), part = slot * W::kUnit + row;
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
@@ -331,9 +394,8 @@ stream_attn_kernel(const __grid_constant__ typename Src::Dev a, const SplitDev p
     int n = 0, e[2] = {0, 0}, g[2] = {0, 0};
     for (int64_t x = x0; x < x1 && ok;) {
       Unit<kKeys> un;
-      const auto pc = line.locate(x, &un);
-      const int count = uniform(int(min(int64_t(un.tr.tiles - pc.tile), x1 - x)));
-      x += count;
+      const auto sg = line.next(&x, &un);
+      const int count = uniform(sg.count);
       const int tiles = uniform(W::kTiles == 2 && un.rows > kTileRows ? 2 : 1);
       for (int j = 0; j < min(count, kBuffers) && ok; ++j) {
         ok = __all_sync(0xffffffffu, wait(&s.k_full[(n + j) % SK], ((n + j) / SK) & 1));
@@ -395,10 +457,9 @@ stream_attn_kernel(const __grid_constant__ typename Src::Dev a, const SplitDev p
     int n = 0, e = 0;
     for (int64_t x = x0; x < x1 && ok;) {
       Unit<kKeys> un;
-      const auto pc = line.locate(x, &un);
-      const int count = int(min(int64_t(un.tr.tiles - pc.tile), x1 - x));
-      x += count;
-      ok = feed.begin(un, pc.hk, pc.tile, count, n);
+      const auto sg = line.next(&x, &un);
+      const int count = sg.count;
+      ok = feed.begin(un, sg.hk, sg.tile, count, n);
       for (int j = 0; j < min(count, kBuffers) && ok; ++j)      // (a phase is asked for when the one before it has been)
         ok = __all_sync(0xffffffffu, wait(&s.k_full[(n + j) % SK], (n + j) / SK));
       for (int i = 0; i < count && ok; ++i, ++n, ++e) {
@@ -417,23 +478,16 @@ stream_attn_kernel(const __grid_constant__ typename Src::Dev a, const SplitDev p
     int n = 0;
     for (int64_t x = x0; x < x1 && ok;) {
       Unit<kKeys> un;
-      const auto pc = line.locate(x, &un);
-      const int count = int(min(int64_t(un.tr.tiles - pc.tile), x1 - x));
-      x += count;
-      ok = Src::template copy<D>(a, un, pc.hk, pc.tile, count, n, tid - W::kSoftmax - 64, base, s);
+      const auto sg = line.next(&x, &un);
+      const int count = sg.count;
+      ok = Src::template copy<D>(a, un, sg.hk, sg.tile, count, n, tid - W::kSoftmax - 64, base, s);
       n += count;
     }
   }
   __syncthreads();
   tc::tc_fence_after();
   if (warp == 0) tc::tmem_dealloc(tmem, 512);
-  if (p.split && tid == 0) {          // at most the last unit goes on in the next CTAs
-    Unit<kKeys> un;
-    const auto pc = line.locate(x1 - 1, &un);
-    // (its first tile has to lie in the range, its last one behind it)
-    const bool tail = pc.tile + 1 < un.tr.tiles && x1 - 1 - pc.tile >= x0;
-    p.join[blockIdx.x] = tail ? line.describe(pc, un) : JoinDesc{};
-  }
+  if (p.split == 1 && tid == 0) p.join[blockIdx.x] = line.tail();
   if (p.late) pdl_wait();
   pdl_trigger();
 }
@@ -447,6 +501,9 @@ __device__ __forceinline__ void drain_copies(uint64_t* full, int stages, int n) 
     for (int k = 0; k < (1 << 20) && !tc::mbar_test(&full[m % stages], (m / stages) & 1); ++k) {
     }
 }
+
+// The most sequences of the table of split = 2.
+constexpr int kMaxDealtSeqs = 1024;
 
 // The split of the registers adds up only with those that the kernel was to be built with: setmaxnreg would wait
 // for ever with fewer.
@@ -466,10 +523,12 @@ int stream_launch(const typename Src::Dev& d, const SplitDev& p, cudaStream_t st
   using L = StreamLayout<D, Src>;
   static_assert(!Stream<D>::kSplitRegs || L::kThreads == 384, "the split of the registers");
   static_assert(stream_smem<D, Src>(1, kMaxSplitUnits) <= 227 * 1024, "shared memory of a CTA");
+  static_assert(stream_smem<D, Src>(0, 0) + kMaxDealtSeqs * 16 <= 227 * 1024, "shared memory of a CTA");
   static_assert(L::kRest >= int(kMaxSplitUnits * 16), "scratch of the line");
   // at least 116 KB: no two CTAs that allocate TMEM share an SM
-  const size_t bytes = std::max(stream_smem<D, Src>(p.split, p.U), size_t(116 * 1024));
-  const int64_t grid = p.split ? p.grid : int64_t(p.U) * d.K;
+  const size_t table = p.split == 2 ? size_t(d.B) * 16 : 0;
+  const size_t bytes = std::max(stream_smem<D, Src>(p.split == 1, p.U) + table, size_t(116 * 1024));
+  const int64_t pairs = int64_t(p.U) * d.K, grid = p.split == 1 ? p.grid : p.split == 2 ? std::min<int64_t>(p.grid, pairs) : pairs;
   const cudaError_t e = launch_pdl(stream_attn_kernel<D, Src>, dim3(unsigned(grid)), dim3(L::kThreads), bytes, stream, d, p);
   return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? V4A_OK : V4A_ERR_CUDA;
 }
