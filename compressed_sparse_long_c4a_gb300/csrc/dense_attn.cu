@@ -52,7 +52,9 @@ struct Shape {
   static constexpr int kKeys = (kFp8 ? 32 : 16) * (D == 64 ? 2 : 1);   // positions per tile
   static constexpr int kRow = kFp8 ? D : 2 * D;                  // bytes of a row
   static constexpr int kHalf = kKeys * kRow;                     // keys (or values) of a tile: 32 D bytes (64 D at dim 64)
-  static constexpr int kScales = kFmt == V4A_KV_FP8_GROUP ? 16 : kFp8 ? 2 * kKeys * 4 : 0;      // a tile lies in one group
+  // A group's two scales (a tile lies in one) have 256 bytes: stages that start between two rows of banks, as 16
+  // bytes would have it, took 504 us instead of 469 for 32 sequences at 32k to 64k.
+  static constexpr int kScales = kFmt == V4A_KV_FP8_GROUP ? 256 : kFp8 ? 2 * kKeys * 4 : 0;
   static constexpr int kStage = 2 * kHalf + kScales;             // holds R x D fp32 for the merge as well
   static constexpr int kWarps = 4;
   static constexpr int kThreads = 32 * kWarps;

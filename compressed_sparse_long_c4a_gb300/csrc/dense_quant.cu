@@ -23,7 +23,7 @@ namespace {
 constexpr int kThreads = 128;
 
 struct QuantDev {
-  int T, K, tokens;               // tokens: leaders looked for by a CTA
+  int T, K, tokens, planes;       // of a CTA: tokens among which it looks for groups' first ones; KV heads' keys or values
   const int32_t* positions;
   const int64_t* slots;
   const uint16_t *k, *v;
@@ -55,7 +55,8 @@ __device__ __forceinline__ float hi_of(uint32_t w) { return __uint_as_float(w & 
 __device__ __forceinline__ float power(int field) { return __uint_as_float(uint32_t(max(field, 0)) << 23); }
 
 // A CTA takes the groups whose first token of the call is among `tokens` tokens from
-// blockIdx.x * tokens on, for one KV head's keys or values (blockIdx.y).
+// blockIdx.x * tokens on, for `planes` KV heads' keys or values (planes: keys' heads, then values') from blockIdx.y *
+// planes on.
 template <int D>
 __global__ void __launch_bounds__(kThreads) dense_quant_kernel(const __grid_constant__ QuantDev p) {
   constexpr int kChunks = D / 16, kPasses = kGroupPositions * kChunks / kThreads;      // a chunk: 16 elements of a row
@@ -63,7 +64,6 @@ __global__ void __launch_bounds__(kThreads) dense_quant_kernel(const __grid_cons
   __shared__ int64_t slot[kBefore + 8 + kGroupPositions];      // of tokens x0 - kBefore ..; -1: skipped
   __shared__ uint32_t red[kThreads / 32];
   const int tid = threadIdx.x, lane = tid & 31, x0 = blockIdx.x * p.tokens;
-  const int which = int(blockIdx.y) / p.K, h = int(blockIdx.y) % p.K;
   pdl_trigger();
   pdl_wait();
   for (int i = tid; i < kBefore + p.tokens + kGroupPositions; i += kThreads) {
@@ -94,63 +94,66 @@ __global__ void __launch_bounds__(kThreads) dense_quant_kernel(const __grid_cons
     }
     const int t0 = x0 - kBefore + i, in_block = int(first % kBlockPositions) / kGroupPositions;
     uint8_t* block = p.pool + first / kBlockPositions * p.block_bytes;
-    uint8_t* dst = block + (int64_t(which * p.K + h) * kBlockPositions + in_block * kGroupPositions) * D;
-    float* const scale = reinterpret_cast<float*>(block + int64_t(2 * p.K) * kBlockPositions * D) + (which * p.K + h) * kGroupsPerBlock + in_block;
-    const uint16_t* src = which ? p.v + t0 * p.vs + h * D : p.k + t0 * p.ks + h * D;
-    const int64_t stride = which ? p.vs : p.ks;
     const bool anew = rows[0] & 1;
-    const uint32_t old_bits = anew ? 0 : __float_as_uint(*scale);
-    uint4 a[kPasses], b[kPasses];
-    uint32_t top = 0;
+    for (int plane = blockIdx.y * p.planes; plane < min(2 * p.K, int(blockIdx.y + 1) * p.planes); ++plane) {
+      const int which = plane >= p.K, h = which ? plane - p.K : plane;
+      uint8_t* dst = block + (int64_t(plane) * kBlockPositions + in_block * kGroupPositions) * D;
+      float* const scale = reinterpret_cast<float*>(block + int64_t(2 * p.K) * kBlockPositions * D) + plane * kGroupsPerBlock + in_block;
+      const uint16_t* src = which ? p.v + t0 * p.vs + h * D : p.k + t0 * p.ks + h * D;
+      const int64_t stride = which ? p.vs : p.ks;
+      const uint32_t old_bits = anew ? 0 : __float_as_uint(*scale);
+      uint4 a[kPasses], b[kPasses];
+      uint32_t top = 0;
 #pragma unroll
-    for (int k = 0; k < kPasses; ++k) {
-      const int c = tid + k * kThreads, r = c / kChunks, ch = c % kChunks;
-      a[k] = b[k] = make_uint4(0, 0, 0, 0);
-      if (member[r >> 5] >> (r & 31) & 1) {
-        const uint4* x = reinterpret_cast<const uint4*>(src + r * stride + ch * 16);
-        a[k] = x[0];
-        b[k] = x[1];
-      }
-    }
-#pragma unroll
-    for (int k = 0; k < kPasses; ++k) {
-      top = finite_max(finite_max(finite_max(finite_max(top, a[k].x), a[k].y), a[k].z), a[k].w);
-      top = finite_max(finite_max(finite_max(finite_max(top, b[k].x), b[k].y), b[k].z), b[k].w);
-    }
-    top = __reduce_max_sync(0xffffffffu, max(top >> 16, top & 0xffffu));
-    if (lane == 0) red[tid >> 5] = top;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) top = max(top, red[w]);
-    // exponent fields of the scales: 448 = 1.75 x 2^8, and a bf16's mantissa of 0.75 is 0x60
-    const int old = anew ? 1 : min(253, max(1, int(old_bits >> 23 & 0xff)));
-    const int now = max(old, max(1, int(top >> 7) - 8 + ((top & 0x7f) > 0x60)));
-    if (tid == 0) *scale = power(now);
-    if (now > old && !anew) {
-      const float shrink = power(127 + old - now);
-      for (int c = tid; c < kGroupPositions * kChunks; c += kThreads) {
-        const int r = c / kChunks;
-        if (rows[r >> 5] >> (r & 31) & 1) continue;
-        uint4 w = *reinterpret_cast<const uint4*>(dst + c * 16);
-        uint32_t* const u = &w.x;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float2 x = values2(u[k] & 0xffffu), y = values2(u[k] >> 16);
-          u[k] = codes4(x.x * shrink, x.y * shrink, y.x * shrink, y.y * shrink);
+      for (int k = 0; k < kPasses; ++k) {
+        const int c = tid + k * kThreads, r = c / kChunks, ch = c % kChunks;
+        a[k] = b[k] = make_uint4(0, 0, 0, 0);
+        if (member[r >> 5] >> (r & 31) & 1) {
+          const uint4* x = reinterpret_cast<const uint4*>(src + r * stride + ch * 16);
+          a[k] = x[0];
+          b[k] = x[1];
         }
-        *reinterpret_cast<uint4*>(dst + c * 16) = w;
       }
-    }
-    const float inv = power(254 - now);
 #pragma unroll
-    for (int k = 0; k < kPasses; ++k) {
-      const int c = tid + k * kThreads, r = c / kChunks, ch = c % kChunks;
-      if (!(member[r >> 5] >> (r & 31) & 1)) continue;
-      auto four = [&](uint32_t x, uint32_t y) { return codes4(lo_of(x) * inv, hi_of(x) * inv, lo_of(y) * inv, hi_of(y) * inv); };
-      *reinterpret_cast<uint4*>(dst + int64_t(slot[i + r] % kGroupPositions) * D + ch * 16) =
-          make_uint4(four(a[k].x, a[k].y), four(a[k].z, a[k].w), four(b[k].x, b[k].y), four(b[k].z, b[k].w));
+      for (int k = 0; k < kPasses; ++k) {
+        top = finite_max(finite_max(finite_max(finite_max(top, a[k].x), a[k].y), a[k].z), a[k].w);
+        top = finite_max(finite_max(finite_max(finite_max(top, b[k].x), b[k].y), b[k].z), b[k].w);
+      }
+      top = __reduce_max_sync(0xffffffffu, max(top >> 16, top & 0xffffu));
+      if (lane == 0) red[tid >> 5] = top;
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < kThreads / 32; ++w) top = max(top, red[w]);
+      // exponent fields of the scales: 448 = 1.75 x 2^8, and a bf16's mantissa of 0.75 is 0x60
+      const int old = anew ? 1 : min(253, max(1, int(old_bits >> 23 & 0xff)));
+      const int now = max(old, max(1, int(top >> 7) - 8 + ((top & 0x7f) > 0x60)));
+      if (tid == 0) *scale = power(now);
+      if (now > old && !anew) {
+        const float shrink = power(127 + old - now);
+        for (int c = tid; c < kGroupPositions * kChunks; c += kThreads) {
+          const int r = c / kChunks;
+          if (rows[r >> 5] >> (r & 31) & 1) continue;
+          uint4 w = *reinterpret_cast<const uint4*>(dst + c * 16);
+          uint32_t* const u = &w.x;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float2 x = values2(u[k] & 0xffffu), y = values2(u[k] >> 16);
+            u[k] = codes4(x.x * shrink, x.y * shrink, y.x * shrink, y.y * shrink);
+          }
+          *reinterpret_cast<uint4*>(dst + c * 16) = w;
+        }
+      }
+      const float inv = power(254 - now);
+#pragma unroll
+      for (int k = 0; k < kPasses; ++k) {
+        const int c = tid + k * kThreads, r = c / kChunks, ch = c % kChunks;
+        if (!(member[r >> 5] >> (r & 31) & 1)) continue;
+        auto four = [&](uint32_t x, uint32_t y) { return codes4(lo_of(x) * inv, hi_of(x) * inv, lo_of(y) * inv, hi_of(y) * inv); };
+        *reinterpret_cast<uint4*>(dst + int64_t(slot[i + r] % kGroupPositions) * D + ch * 16) =
+            make_uint4(four(a[k].x, a[k].y), four(a[k].z, a[k].w), four(b[k].x, b[k].y), four(b[k].z, b[k].w));
+      }
+      __syncthreads();                             // `red` is read
     }
-    __syncthreads();                               // `red` is read
   }
 }
 
@@ -241,13 +244,16 @@ int dense_quant(const v4a_dense_insert_args& a, const uint16_t* k_out, int64_t k
   d.T = a.num_tokens; d.K = a.kv.num_kv_heads;
   // few tokens: most are alone in their group, and a CTA each takes them side by side
   d.tokens = a.num_tokens <= 1024 ? 1 : 8;
+  // CTAs without a first token cost their start: with many, each looks once for four planes
+  const int64_t blocks = (int64_t(d.T) + d.tokens - 1) / d.tokens;
+  d.planes = blocks * d.K >= 8 * 152 * 4 ? 4 : 1;
   d.positions = a.positions; d.slots = a.slots;
   d.k = k_out; d.ks = k_out_stride; d.v = a.v; d.vs = a.v_stride;
   d.num_slots = a.kv.num_blocks * kBlockPositions; d.block_bytes = block_bytes;
   d.pool = static_cast<uint8_t*>(a.kv.pool);
   auto kern = a.kv.dim == 64 ? dense_quant_kernel<64> : a.kv.dim == 128 ? dense_quant_kernel<128>
             : a.kv.dim == 192 ? dense_quant_kernel<192> : dense_quant_kernel<256>;
-  const cudaError_t e = launch_pdl(kern, dim3(unsigned((int64_t(d.T) + d.tokens - 1) / d.tokens), unsigned(2 * d.K)), dim3(kThreads), 0, stream, d);
+  const cudaError_t e = launch_pdl(kern, dim3(unsigned(blocks), unsigned((2 * d.K + d.planes - 1) / d.planes)), dim3(kThreads), 0, stream, d);
   return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? V4A_OK : V4A_ERR_CUDA;
 }
 

@@ -296,9 +296,9 @@ class DenseInsert(_Op):
                                None if q_gamma is None else q_gamma.data_ptr(), None if k_gamma is None else k_gamma.data_ptr(),
                                eps, self._rope, cache.struct(), self.status.data_ptr())
         self._bind("v4a_dense_insert", lib().v4a_dense_insert)
-        self._plain = self._where, self._fn, self._call
-        if cache.fmt == KV_FP8_GROUP:
-            self._plain = None
+        self._args = self._call[0]
+        self._plain = None if cache.fmt == KV_FP8_GROUP else (self._where, self._fn, self._call)
+        self._with_rows = "v4a_dense_insert_rows", lib().v4a_dense_insert_rows
 
     def run(self, q, k, v, q_out, positions: torch.Tensor, slots: torch.Tensor, stream=None, k_out=None):
         """q, q_out [T][heads][dim], k, v, k_out [T][KV heads][dim] bf16 (any
@@ -320,7 +320,8 @@ class DenseInsert(_Op):
         a.positions, a.slots = positions.data_ptr(), slots.data_ptr()
         if k_out is not None:
             stride = _rows(k_out, "k_out", dev, c.num_kv_heads, c.dim, n)
-            self._where, self._fn, self._call = "v4a_dense_insert_rows", lib().v4a_dense_insert_rows, (C.byref(a), k_out.data_ptr(), stride)
+            self._where, self._fn = self._with_rows
+            self._call = (self._args, k_out.data_ptr(), stride)
         elif self._plain is None:
             raise ValueError("DenseInsert: a cache with a scale per group needs k_out")
         else:
