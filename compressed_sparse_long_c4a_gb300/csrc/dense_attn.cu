@@ -736,6 +736,7 @@ int dense_attn(const v4a_dense_attn_args* a, void* ws, size_t ws_bytes, cudaStre
   DenseAttnDev d{};
   rc = dense_cache_check(a->kv, &d.block_bytes);
   if (rc) return rc;
+  if (a->kv.format == V4A_KV_FP8_GROUP && d.block_bytes >= int64_t(1) << 40) return V4A_ERR_UNSUPPORTED;      // (a tensor map's strides)
   if (!(a->softmax_scale > 0.f) || !std::isfinite(a->softmax_scale * 1.4426950408889634f) || a->kv.max_blocks < 1) return V4A_ERR_INVALID_ARG;
   if (a->num_tokens == 0 || a->num_seqs == 0) return V4A_OK;
   if (!a->positions || !a->token_starts || !a->kv.block_table || !a->q || !a->out) return V4A_ERR_INVALID_ARG;

@@ -24,7 +24,7 @@ struct DenseAttnDev {
 
 // Sequences of at most this many rows (tokens x heads of a group) go to the
 // form for few rows, which reads the cache once per 16 rows (8 of dim 256), so
-// up to twice for bf16 and four times for fp8; the form for many reads it once
+// up to twice for bf16 and group-scaled fp8 and four times for fp8; the form for many reads it once
 // but converts fp8 codes on the way.  Few / many, 32 + 8 heads
 // of 128, us: bf16, 8 sequences at 8k: 32 rows 69 / 62, 64 rows 123 / 64; one
 // at 8k: 32 rows 22 / 32, 64 rows 28 / 32; 16 at 1k (dim 64): 24 / 26 and
@@ -32,7 +32,10 @@ struct DenseAttnDev {
 // dim 256, 8 at 8k: bf16 16 rows 163 / 107, 32 rows 311 / 107, one at 8k 16 rows
 // 24 / 33; fp8 32 rows 186 / 187, 64 rows 355 / 186.  The limits are those of
 // one sequence, where the second pass costs nothing; with more sequences 9 to
-// 16 rows of dim 256 (bf16) would be faster in the form for many.
+// 16 rows of dim 256 (bf16) would be faster in the form for many.  Group-scaled fp8
+// (its form for many does not convert keys): 8 at 8k: 32 rows 68 / 82, 64 rows 117 /
+// 82; one at 8k: 64 rows 33 / 41, 128 rows 45 / 43; dim 256, 8 at 8k: 16 rows 70 / 70,
+// 32 rows 111 / 72, one at 8k 32 rows 31 / 43.
 constexpr int few_rows(int dim, int format) { return (dim == 256 ? 8 : 16) * (format == V4A_KV_FP8_TOKEN ? 4 : 2); }
 
 // One sequence's tokens of the call: first row, count and first position;

@@ -244,9 +244,11 @@ int dense_quant(const v4a_dense_insert_args& a, const uint16_t* k_out, int64_t k
   d.T = a.num_tokens; d.K = a.kv.num_kv_heads;
   // few tokens: most are alone in their group, and a CTA each takes them side by side
   d.tokens = a.num_tokens <= 1024 ? 1 : 8;
-  // CTAs without a first token cost their start: with many, each looks once for four planes
+  // CTAs without a first token cost their start: with many, each looks once for four planes (of the insert's two
+  // launches, 1, 2, 4, 8 and 16 planes: 16384 tokens, 8 heads of 128, 199, 171, 158, 156 and 169 us; 4097 tokens of 64
+  // dims 42, 37, 36, 38 and 44; 4, 16, 32 or 64 tokens a CTA are no better)
   const int64_t blocks = (int64_t(d.T) + d.tokens - 1) / d.tokens;
-  d.planes = blocks * d.K >= 8 * 152 * 4 ? 4 : 1;
+  d.planes = blocks * 2 * d.K >= 16 * 152 ? 4 : 1;
   d.positions = a.positions; d.slots = a.slots;
   d.k = k_out; d.ks = k_out_stride; d.v = a.v; d.vs = a.v_stride;
   d.num_slots = a.kv.num_blocks * kBlockPositions; d.block_bytes = block_bytes;

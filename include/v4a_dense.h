@@ -292,7 +292,9 @@ V4A_API int v4a_dense_read(const v4a_dense_read_args* args, void* stream);
  * of the tensor cores: to f16 for fp8 caches, to 16 bits for bf16 caches, and
  * to bf16 for the sequences of a bf16 cache that bring more than 32 rows
  * (tokens x heads per KV head; 16 of dim 256) and in the full calls below.  fp8 value scales below 2^-100
- * are read as 2^-100.  Sequences that share tokens (entries not increasing)
+ * are read as 2^-100.  Over a V4A_KV_FP8_GROUP cache the sequences of more than
+ * 32 rows (16 of dim 256), and those of the full calls, take an element of a
+ * query to within 2^-17 of its row's largest (exactly down to 2^-9 of that).  Sequences that share tokens (entries not increasing)
  * set V4A_DEV_BAD_BATCH once they are more than the call has room for, and
  * what their rows hold then is not defined.
  *
@@ -303,7 +305,8 @@ V4A_API int v4a_dense_read(const v4a_dense_read_args* args, void* stream);
  * form for chunks (probabilities in bf16 over bf16 caches, about twice the
  * time); a num_tokens below that, by one token of padding less for instance,
  * keeps each kind its own.  V4A_ERR_UNSUPPORTED: max_new_per_seq
- * * num_heads / num_kv_heads of 2^30 rows or more.
+ * * num_heads / num_kv_heads of 2^30 rows or more, V4A_KV_FP8_GROUP blocks of
+ * 2^40 bytes or more.
  */
 typedef struct {
   int32_t num_tokens;          /* T >= 0: rows of q and out */

@@ -52,6 +52,10 @@ def test_insert_rows_refuses_arguments(lib, kw, code):  # noqa: F811
     assert lib.v4a_dense_insert_rows(C.byref(_insert(_group(), num_tokens=0)), None, 0, None) == 0
 
 
+def test_attention_refuses_wide_blocks(lib):  # noqa: F811
+    assert lib.v4a_dense_attn(C.byref(_attn(_group(block_bytes=1 << 40))), 0x1000, 1 << 30, None) == UNSUPPORTED
+
+
 def _read(cache=None, **kw):
     f = dict(num_rows=5, num_seqs=3, row_starts=0x10, first=0x20, kv=cache or _group(), k=0x100, k_stride=256, v=0x200, v_stride=256, status=None)
     f.update(kw)
