@@ -119,8 +119,33 @@ struct GroupCache {
     return fmaxf(a.scale_log2 * down, 0x1p-126f);
   }
 
-  // The copies of a step's codes, issued by one lane kLead steps ahead.  Table entries are read two steps before they
-  // are used and the scales one step.
+  // Who issues the copies of the value codes: with two tiles Feed, beside the keys' (4096 tokens over 28672, 32 + 8 heads
+  // of 128: 1605 us; the converting warps, whose lanes then wait for the one that issues: 1957), with one tile the
+  // converting warps, as soon as a buffer is read (2048 over 10240, 16 + 4 heads of 256: 371 us; Feed, which then holds
+  // the keys' copies back: 412).
+  template <int D>
+  static constexpr bool copiers_issue() { return Stream<D>::kTiles == 1; }
+  // Issues the copy of the value codes of step i of the segment, step n of the CTA (one lane).
+  template <int D>
+  static __device__ __forceinline__ bool issue_values(const Dev& a, const Unit<Stream<D>::kKeys>& un, int hk, int tile, int i, int n, int32_t page,
+                                                      uint8_t* base, StreamSmem& s) {
+    using L = StreamLayout<D, GroupCache>;
+    if (!wait_for(&s.raw_free[n % 2], ((n / 2) & 1) ^ 1, a.status, &s.abort_flag)) return false;
+    const bool gone = page < 0 || page >= a.num_blocks;
+    s.raw_missing[n % 2] = gone;
+    if (gone) {
+      tc::mbar_arrive(&s.raw_full[n % 2]);
+    } else {
+      const int at = hk * kBlockPositions + un.tr.at(tile + i) * Stream<D>::kKeys % kBlockPositions;       // first row of the step
+      tc::mbar_arrive_expect_tx(&s.raw_full[n % 2], L::kKeyBytes);
+      tc::bulk_load(base + L::kExtra + (n % 2) * L::kKeyBytes, a.pool + page * a.block_bytes + (int64_t(a.K) * kBlockPositions + at) * D,
+                    L::kKeyBytes, &s.raw_full[n % 2]);
+    }
+    return true;
+  }
+
+  // The copies of a step's key codes, issued by one lane kLead steps ahead.  Table entries are read two steps before
+  // they are used and the scales one step.
   template <int D>
   struct Feed {
     using W = Stream<D>;
@@ -161,9 +186,7 @@ struct GroupCache {
     // Issues the copies of step i of the segment, step n of the CTA.
     __device__ __forceinline__ bool issue(int i, int n) {
       constexpr int SK = key_stages<D>();
-      bool ok = wait_for(&s.k_free[n % SK], ((n / SK) & 1) ^ 1, a.status, &s.abort_flag) &&
-                wait_for(&s.raw_free[n % 2], ((n / 2) & 1) ^ 1, a.status, &s.abort_flag);
-      if (!__all_sync(0xffffffffu, ok)) return false;
+      if (!__all_sync(0xffffffffu, wait_for(&s.k_free[n % SK], ((n / SK) & 1) ^ 1, a.status, &s.abort_flag))) return false;
       if (lane() < 2 * kGroups) {
         const int which = lane() / kGroups, g = lane() % kGroups;
         float* const to = s.scales[n & 7][g];
@@ -180,7 +203,6 @@ struct GroupCache {
       if (lane() == 0) {
         if (page < 0) {
           tc::mbar_arrive(&s.k_full[n % SK]);
-          tc::mbar_arrive(&s.raw_full[n % 2]);
         } else {
           const int at = hk * kBlockPositions + un->tr.at(tile + i) * W::kKeys % kBlockPositions;       // first row of the step
           uint8_t* const keys = base + L::kKeys + (n % SK) * L::kKeyBytes;
@@ -188,12 +210,12 @@ struct GroupCache {
 #pragma unroll
           for (int c = 0; c < D / block<D>(); ++c)
             tc::tma_load_3d(keys + c * (W::kKeys * block<D>()), &a.km, c * block<D>(), at, page, &s.k_full[n % SK]);
-          tc::mbar_arrive_expect_tx(&s.raw_full[n % 2], L::kKeyBytes);
-          tc::bulk_load(base + L::kExtra + (n % 2) * L::kKeyBytes,
-                        a.pool + page * a.block_bytes + (int64_t(a.K) * kBlockPositions + at) * D, L::kKeyBytes, &s.raw_full[n % 2]);
         }
       }
+      bool ok = true;
+      if (!copiers_issue<D>() && lane() == 0) ok = issue_values<D>(a, *un, hk, tile, i, n, page, base, s);
       issued = n + 1;
+      if (!__all_sync(0xffffffffu, ok)) return false;
       advance(i + 1);
       return true;
     }
@@ -209,13 +231,13 @@ struct GroupCache {
     __device__ __forceinline__ bool step(int i, int n) { return i + kLead >= count || issue(i + kLead, n + kLead); }
     __device__ __forceinline__ void drain() {
       drain_copies(s.k_full, key_stages<D>(), issued);
-      drain_copies(s.raw_full, 2, issued);
+      if (!copiers_issue<D>()) drain_copies(s.raw_full, 2, issued);
     }
   };
 
   // Value codes of `count` steps from tile `tile` of the unit on, step n of the CTA first, as f16.
   template <int D>
-  static __device__ __forceinline__ bool copy(const Dev& a, const Unit<Stream<D>::kKeys>& un, int, int tile, int count, int n, int lt,
+  static __device__ __forceinline__ bool copy(const Dev& a, const Unit<Stream<D>::kKeys>& un, int hk, int tile, int count, int n, int lt,
                                               uint8_t* base, StreamSmem& s) {
     using L = StreamLayout<D, GroupCache>;
     constexpr int SV = value_stages<D>(), kKeys = Stream<D>::kKeys, kPerRow = D / 16, kStep = copiers<D>() / kPerRow, kPasses = kKeys / kStep;
@@ -224,13 +246,29 @@ struct GroupCache {
     const uint32_t values = tc::smem_u32(base + L::kValues);
     const uint32_t even = values + stream_chunk<kKeys>(r0, 2 * ch), odd = values + stream_chunk<kKeys>(r0, 2 * ch + 1);
     volatile int* abort_flag = &s.abort_flag;
+    auto entry = [&](int i) {        // step i's table entry, read a step ahead of its use
+      return i < count && lt == 0 ? __ldcg(a.bt + int64_t(un.b) * a.max_blocks + un.tr.at(tile + i) / (kBlockPositions / kKeys)) : -1;
+    };
+    constexpr bool kIssue = copiers_issue<D>();
+    auto fail = [&](int issued) {
+      if (kIssue && lt == 0) drain_copies(s.raw_full, 2, issued);
+      return false;
+    };
+    int32_t next = -1;
+    if (kIssue && lt == 0) {         // two steps ahead
+      const int32_t first = entry(0), second = entry(1);
+      if (!issue_values<D>(a, un, hk, tile, 0, n, first, base, s) || (count > 1 && !issue_values<D>(a, un, hk, tile, 1, n + 1, second, base, s)))
+        return fail(n + 1);
+      next = entry(2);
+    }
     for (int i = 0; i < count; ++i, ++n) {
-      if (!wait_for(&s.raw_full[n % 2], (n / 2) & 1, a.status, abort_flag)) return false;
+      const int issued = n + min(count - i, 2);
+      if (!wait_for(&s.raw_full[n % 2], (n / 2) & 1, a.status, abort_flag)) return fail(issued);
       const int j0 = un.tr.at(tile + i) * kKeys;
       // rows up to hi, and of those the ones behind lo or before sk, are values, the others zeros
-      const int hi = s.missing[n & 7] ? -1 : un.m_hi - j0, lo = a.window ? un.m_lo - a.window - j0 : -1, sk = a.window ? a.sinks - j0 : 0;
+      const int hi = s.raw_missing[n % 2] ? -1 : un.m_hi - j0, lo = a.window ? un.m_lo - a.window - j0 : -1, sk = a.window ? a.sinks - j0 : 0;
       const uint4* raw = reinterpret_cast<const uint4*>(base + L::kExtra + (n % 2) * L::kKeyBytes) + lt;
-      if (!wait_for(&s.v_free[n % SV], ((n / SV) & 1) ^ 1, a.status, abort_flag)) return false;
+      if (!wait_for(&s.v_free[n % SV], ((n / SV) & 1) ^ 1, a.status, abort_flag)) return fail(issued);
       const uint32_t to = (n % SV) * Stream<D>::kStepBytes;
 #pragma unroll
       for (int k = 0; k < kPasses; ++k) {
@@ -243,6 +281,10 @@ struct GroupCache {
       tc::mbar_arrive(&s.raw_free[n % 2]);
       tc::fence_proxy_async();
       tc::mbar_arrive(&s.v_full[n % SV]);
+      if (kIssue && lt == 0 && i + 2 < count) {
+        if (!issue_values<D>(a, un, hk, tile, i + 2, n + 2, next, base, s)) return fail(issued);
+        next = entry(i + 3);
+      }
     }
     return true;
   }

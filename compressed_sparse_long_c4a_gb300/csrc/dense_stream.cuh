@@ -57,7 +57,7 @@ struct StreamSmem {
   int abort_flag;
   // step n at [n % 8] (a buffer's step can be six steps ahead of the slowest softmax): its page is missing;
   // of its groups of 64 keys: softmax scale x log2(e) x key scale, log2 of the value scale, its inverse
-  int missing[8];
+  int missing[8], raw_missing[2];
   alignas(16) float scales[8][2][4];
 };
 
