@@ -11,6 +11,11 @@
 //
 // Bound: memory.  The rows of a group (64 x dim bf16, 16 KB at dim 128) lie in a
 // CTA's registers between the maximum and the codes, so they are read once.
+// Measured: the insert's two launches, 16384 tokens of 64 + 8 + 8 heads of 128 158 us
+// (the first alone 127, this one 40; a CTA waits for its rows and then for the
+// maximum, and loading the next plane ahead took 164), 4097 tokens of 64 dims 36 us, 64
+// tokens 10.8; the read back of 133 thousand positions of 8 heads of 128 135 us (6.0 TB/s
+// of the 6.7 that a copy reaches).
 #include <algorithm>
 
 #include "tc_common.cuh"

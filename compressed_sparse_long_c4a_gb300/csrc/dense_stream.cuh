@@ -21,6 +21,17 @@
 // is formed against is raised only when a row's logits pass it by 2^kRaise, so the
 // accumulator is rescaled a few times per row.
 //
+// Bound: a step is a chain of score, softmax and product for each tile, in which the
+// two tiles alternate.  Of about 2,850 clocks a step of 128 keys at dim 128 takes
+// (prompts), the products are 2,048 at the tensor cores' rate; a tile's chain is
+// 520 for its scores' load and maximum of the first 64 keys and as much for the
+// rest, 400 for the exponentials of each half, 300 until the issuer has seen P, 700
+// to issue the products and 330 until the next scores are there.  Measured and not
+// kept: scores in two buffers of 64 columns at dim 128 (1722 us for a prompt of
+// 16384 tokens, 32 + 8 heads, instead of 1373) and 64 (the same), an issuing warp per
+// tile (1994), polling without suspension (1745), the exponentials beside the search
+// for the maximum (1753), the second half's load beside the first's maximum (1387).
+//
 // What differs is in the source, a class: the arguments, the operands of the
 // scores (scores), the queries' way into shared memory (load_q, or Feed's), what
 // the waiting warp copies (Feed) and what the copying warps do (copy).
@@ -135,6 +146,21 @@ struct Segments : Line<R, kTile, kThreads, Dev> {
 // moved there for each.
 template <typename T>
 __device__ __forceinline__ T uniform(T x) { return __shfl_sync(0xffffffffu, x, 0); }
+
+// One step of the exchange of four lanes' four pieces (lane l's v[k] becomes lane k's v[l] with steps 1 and 2): pieces
+// whose number differs from the lane's in bit kBit change places with the partner's.
+template <int kBit>
+__device__ __forceinline__ void exchange(uint4 (&v)[4], int lane) {
+  const bool high = lane & kBit;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if (k & kBit) continue;
+    const uint4 give = high ? v[k] : v[k + kBit];
+    const uint4 got = make_uint4(__shfl_xor_sync(0xffffffffu, give.x, kBit), __shfl_xor_sync(0xffffffffu, give.y, kBit),
+                                 __shfl_xor_sync(0xffffffffu, give.z, kBit), __shfl_xor_sync(0xffffffffu, give.w, kBit));
+    if (high) v[k] = got; else v[k + kBit] = got;
+  }
+}
 
 // The n lowest bits (none for n <= 0, all from 32 on).
 __device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? ~0u : (1u << max(n, 0)) - 1u; }
@@ -350,16 +376,27 @@ stream_attn_kernel(const __grid_constant__ typename Src::Dev a, const SplitDev p
         const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;
         const int64_t at = row_of(a, un, sg.hk, min(row, un.rows - 1));
         const int64_t slot = int64_t(blockIdx.x) * 2 + (begins ? 1 : 0), part = slot * W::kUnit + row;
+        // A lane has a row; four lanes exchange their rows' 16-byte pieces, so that a store covers 64 bytes of each of
+        // eight rows instead of 16 of each of 32 (32 prompts of 300 to 700 tokens 143 us instead of 160).
+        int64_t to[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) to[k] = __shfl_sync(0xffffffffu, at, (lane & ~3) + k) * D + (lane & 3) * 8;
+        const int live = un.rows - (row & ~3);         // of the four rows
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
           float o[32];
           tmem_ld32(o_at + c, o);
-          if (row < un.rows && whole) {
+          if (whole) {
+            uint4 v[4];
 #pragma unroll
-            for (int k = 0; k < 32; k += 8)
-              *reinterpret_cast<uint4*>(a.out + at * D + c + k) =
-                  make_uint4(pack_bf16(o[k] * inv, o[k + 1] * inv), pack_bf16(o[k + 2] * inv, o[k + 3] * inv),
-                             pack_bf16(o[k + 4] * inv, o[k + 5] * inv), pack_bf16(o[k + 6] * inv, o[k + 7] * inv));
+            for (int k = 0; k < 4; ++k)
+              v[k] = make_uint4(pack_bf16(o[8 * k] * inv, o[8 * k + 1] * inv), pack_bf16(o[8 * k + 2] * inv, o[8 * k + 3] * inv),
+                                pack_bf16(o[8 * k + 4] * inv, o[8 * k + 5] * inv), pack_bf16(o[8 * k + 6] * inv, o[8 * k + 7] * inv));
+            exchange<1>(v, lane);
+            exchange<2>(v, lane);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (k < live) *reinterpret_cast<uint4*>(a.out + to[k] + c) = v[k];
           } else if (row < un.rows) {
 #pragma unroll
             for (int k = 0; k < 32; k += 4)      // [slot][dim / 4][row][4]: a warp's rows side by side
