@@ -53,13 +53,14 @@ __device__ __forceinline__ float2 e4m3x2_values(uint32_t codes) {
 
 struct GroupCache {
   using Dev = GroupDev;
-  static constexpr bool kScaled = true, kPaged = true;
+  static constexpr bool kScaled = true, kPaged = true, kShortUnits = false;
   static constexpr int kLead = 2;                  // steps that copies are issued ahead
   template <int D> static constexpr int copiers() { return D == 192 ? 96 : D == 256 ? 128 : 64; }
   template <int D> static constexpr int key_stages() { return 3; }
   template <int D> static constexpr int value_stages() { return 2; }
   template <int D> static constexpr int key_bytes() { return Stream<D>::kKeys * D; }
-  template <int D> static constexpr int extra_bytes() { return 2 * key_bytes<D>(); }       // value codes
+  template <int D> static constexpr int raw_stages() { return 2; }        // of value codes as they are
+  template <int D> static constexpr int extra_bytes() { return raw_stages<D>() * key_bytes<D>(); }
   template <int D> static constexpr int value_arrivals() { return copiers<D>(); }
   // Codes of an operand lie in blocks of this many bytes a row, the span of its swizzle.
   template <int D> static constexpr int block() { return D % 128 ? 64 : 128; }
@@ -138,16 +139,17 @@ struct GroupCache {
   static __device__ __forceinline__ bool issue_values(const Dev& a, const Unit<Stream<D>::kKeys>& un, int hk, int tile, int i, int n, int32_t page,
                                                       uint8_t* base, StreamSmem& s) {
     using L = StreamLayout<D, GroupCache>;
-    if (!wait_for(&s.raw_free[n % 2], ((n / 2) & 1) ^ 1, a.status, &s.abort_flag)) return false;
+    constexpr int SR = raw_stages<D>();
+    if (!wait_for(&s.raw_free[n % SR], ((n / SR) & 1) ^ 1, a.status, &s.abort_flag)) return false;
     const bool gone = page < 0 || page >= a.num_blocks;
-    s.raw_missing[n % 2] = gone;
+    s.raw_missing[n % SR] = gone;
     if (gone) {
-      tc::mbar_arrive(&s.raw_full[n % 2]);
+      tc::mbar_arrive(&s.raw_full[n % SR]);
     } else {
       const int at = hk * kBlockPositions + un.tr.at(tile + i) * Stream<D>::kKeys % kBlockPositions;       // first row of the step
-      tc::mbar_arrive_expect_tx(&s.raw_full[n % 2], L::kKeyBytes);
-      tc::bulk_load(base + L::kExtra + (n % 2) * L::kKeyBytes, a.pool + page * a.block_bytes + (int64_t(a.K) * kBlockPositions + at) * D,
-                    L::kKeyBytes, &s.raw_full[n % 2]);
+      tc::mbar_arrive_expect_tx(&s.raw_full[n % SR], L::kKeyBytes);
+      tc::bulk_load(base + L::kExtra + (n % SR) * L::kKeyBytes, a.pool + page * a.block_bytes + (int64_t(a.K) * kBlockPositions + at) * D,
+                    L::kKeyBytes, &s.raw_full[n % SR]);
     }
     return true;
   }
@@ -236,10 +238,11 @@ struct GroupCache {
         if (!issue(i, n + i)) return false;
       return true;
     }
+    // (4096 tokens over 28672 with three stages of value codes and two of keys, issued behind step i's announcement: 1716 us)
     __device__ __forceinline__ bool step(int i, int n) { return i + kLead >= count || issue(i + kLead, n + kLead); }
     __device__ __forceinline__ void drain() {
       drain_copies(s.k_full, key_stages<D>(), issued);
-      if (!copiers_issue<D>()) drain_copies(s.raw_full, 2, issued);
+      if (!copiers_issue<D>()) drain_copies(s.raw_full, raw_stages<D>(), issued);
     }
   };
 
@@ -248,7 +251,7 @@ struct GroupCache {
   static __device__ __forceinline__ bool copy(const Dev& a, const Unit<Stream<D>::kKeys>& un, int hk, int tile, int count, int n, int lt,
                                               uint8_t* base, StreamSmem& s) {
     using L = StreamLayout<D, GroupCache>;
-    constexpr int SV = value_stages<D>(), kKeys = Stream<D>::kKeys, kPerRow = D / 16, kStep = copiers<D>() / kPerRow, kPasses = kKeys / kStep;
+    constexpr int SV = value_stages<D>(), SR = raw_stages<D>(), kKeys = Stream<D>::kKeys, kPerRow = D / 16, kStep = copiers<D>() / kPerRow, kPasses = kKeys / kStep;
     static_assert(kStep % 8 == 0 && copiers<D>() % kPerRow == 0 && kKeys % kStep == 0, "a thread's chunks lie at the same place of the swizzle");
     const int r0 = lt / kPerRow, ch = lt % kPerRow;
     const uint32_t values = tc::smem_u32(base + L::kValues);
@@ -259,7 +262,7 @@ struct GroupCache {
     };
     constexpr bool kIssue = copiers_issue<D>();
     auto fail = [&](int issued) {
-      if (kIssue && lt == 0) drain_copies(s.raw_full, 2, issued);
+      if (kIssue && lt == 0) drain_copies(s.raw_full, SR, issued);
       return false;
     };
     int32_t next = -1;
@@ -271,11 +274,11 @@ struct GroupCache {
     }
     for (int i = 0; i < count; ++i, ++n) {
       const int issued = n + min(count - i, 2);
-      if (!wait_for(&s.raw_full[n % 2], (n / 2) & 1, a.status, abort_flag)) return fail(issued);
+      if (!wait_for(&s.raw_full[n % SR], (n / SR) & 1, a.status, abort_flag)) return fail(issued);
       const int j0 = un.tr.at(tile + i) * kKeys;
       // rows up to hi, and of those the ones behind lo or before sk, are values, the others zeros
-      const int hi = s.raw_missing[n % 2] ? -1 : un.m_hi - j0, lo = a.window ? un.m_lo - a.window - j0 : -1, sk = a.window ? a.sinks - j0 : 0;
-      const uint4* raw = reinterpret_cast<const uint4*>(base + L::kExtra + (n % 2) * L::kKeyBytes) + lt;
+      const int hi = s.raw_missing[n % SR] ? -1 : un.m_hi - j0, lo = a.window ? un.m_lo - a.window - j0 : -1, sk = a.window ? a.sinks - j0 : 0;
+      const uint4* raw = reinterpret_cast<const uint4*>(base + L::kExtra + (n % SR) * L::kKeyBytes) + lt;
       if (!wait_for(&s.v_free[n % SV], ((n / SV) & 1) ^ 1, a.status, abort_flag)) return fail(issued);
       const uint32_t to = (n % SV) * Stream<D>::kStepBytes;
 #pragma unroll
@@ -286,7 +289,7 @@ struct GroupCache {
         st_shared16(even + to + k * (kStep * 128), f16_of(w.x), f16_of(w.y));
         st_shared16(odd + to + k * (kStep * 128), f16_of(w.z), f16_of(w.w));
       }
-      tc::mbar_arrive(&s.raw_free[n % 2]);
+      tc::mbar_arrive(&s.raw_free[n % SR]);
       tc::fence_proxy_async();
       tc::mbar_arrive(&s.v_full[n % SV]);
       if (kIssue && lt == 0 && i + 2 < count) {
