@@ -23,10 +23,10 @@
 // Bound: as prompts (dense_stream.cuh); the conversions share the softmax's
 // schedulers (as integer operations instead of cvt: 2362 us for 1605; four warps of
 // them among 512 threads: 1708), and the second e4m3 of the query takes 3% of the
-// time.  Measured, 32 + 8 heads of 128: 4096 tokens over 28672 1605 to 1660 us (1260
-// TFLOP/s; ncu, 2048 over 4096: tensor pipe 41% busy), 1000 over 4000 94 us; 16 + 4
-// heads of 256, 2048 over 10240 365 us (1035; row scales 505), of 192 330 us; heads of
-// 64 over 28672 1340 us (770).
+// time.  Measured, 32 + 8 heads of 128: 4096 tokens over 28672 1610 us (1281 TFLOP/s;
+// ncu, 2048 over 4096: tensor pipe 41% busy), 1000 over 4000 94 us; 16 + 4 heads of 256,
+// 2048 over 10240 365 us (1037; row scales 505), of 192 320 us (887); heads of 64 over
+// 28672 1348 us (765).
 #include "dense_stream.cuh"
 
 namespace v4a {

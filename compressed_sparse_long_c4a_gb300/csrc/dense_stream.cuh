@@ -507,11 +507,8 @@ stream_attn_kernel(const __grid_constant__ typename Src::Dev a, const SplitDev p
         ok = __all_sync(0xffffffffu, wait(&s.k_full[(n + j) % SK], (n + j) / SK));
       for (int i = 0; i < count && ok; ++i, ++n, ++e) {
         uint64_t* const p_first = &s.p_full[0][kBuffers == 2 ? e & 1 : 0];
-        auto keys = [&] { return i + kBuffers >= count || wait(&s.k_full[(n + kBuffers) % SK], (n + kBuffers) / SK); };
-        // what is there early is waited for first (keys of a step that Feed has still to issue behind it)
-        ok = (kBuffers == 2 || keys()) && feed.step(i, n) && (kBuffers == 1 || keys()) &&
-             (e < kBuffers || wait(p_first, e / kBuffers - 1)) &&      // (the arrival is for this phase)
-             wait(&s.v_full[n % SV], n / SV);
+        ok = feed.step(i, n) && (i + kBuffers >= count || wait(&s.k_full[(n + kBuffers) % SK], (n + kBuffers) / SK)) &&
+             wait(&s.v_full[n % SV], n / SV) && (e < kBuffers || wait(p_first, e / kBuffers - 1));        // (the arrival is for this phase)
         ok = __all_sync(0xffffffffu, ok);
         if (ok && lane == 0) tc::mbar_arrive(p_first);
       }

@@ -8,10 +8,10 @@
 //
 // Bound: 4 dim flops per visible pair on the tensor cores, which are 53% busy (ncu,
 // 4096 tokens; issue slots 35%, DRAM 6%): dense_stream.cuh says what the rest is.
-// Measured, 32 + 8 heads of 128: 16384 tokens 1366 us (1610 TFLOP/s), 4096 111 us
+// Measured, 32 + 8 heads of 128: 16384 tokens 1360 us (1617 TFLOP/s), 4096 111 us
 // (1243), 64 prompts of 1 to 256 (16 + 4 heads) 45 us; 16 + 4 heads of 256, 8192
-// tokens 420 us (1310); heads of 64, 16384 tokens 1250 us (880: half of the flops for
-// the same softmax); 8 prompts of 1000 to 4096, 64 + 8 heads of 64, window 1024 680 us.
+// tokens 420 us (1310), of 192 336 (1228); heads of 64, 16384 tokens 1202 us (915: half
+// of the flops for the same softmax); 8 prompts of 1000 to 4096, 64 + 8 heads of 64, window 1024 680 us.
 #include "dense_stream.cuh"
 
 namespace v4a {
