@@ -36,6 +36,8 @@
 // scores (scores), the queries' way into shared memory (load_q, or Feed's), what
 // the waiting warp copies (Feed) and what the copying warps do (copy).
 #pragma once
+#include <new>
+
 #include "dense_prefill_common.cuh"
 
 namespace v4a {
@@ -64,6 +66,7 @@ constexpr int stream_unit(int dim) { return dim <= 128 ? 256 : 128; }
 struct StreamSmem {
   uint64_t q_full[2], s_full[2][2], p_full[2][2], o_full[2], k_full[4], k_free[4], v_full[4], v_free[4], raw_full[2], raw_free[2], drain;
   int64_t scan[16];
+  alignas(16) uint8_t line[128];     // the CTA's Segments: what they hold would take every role's registers
   uint32_t tmem_base;
   int abort_flag;
   // step n at [n % 8] (a buffer's step can be six steps ahead of the slowest softmax): its page is missing;
@@ -112,28 +115,29 @@ struct Segments : Line<R, kTile, kThreads, Dev> {
     pairs = unsigned(units) * unsigned(a.K);        // (below 2^31: stream_plan)
     const unsigned turns = pairs / gridDim.x, rest = pairs % gridDim.x;
     x0 = 0;
-    x1 = turns + (seat(turns) < rest);
+    x1 = turns + (seat(a, turns) < rest);
     return x1 > 0;
   }
-  __device__ __forceinline__ unsigned seat(unsigned turn) const { return a.B == 1 && turn & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x; }
-  // The segment at x, and x moved behind it.
-  __device__ __forceinline__ Segment next(int64_t* x, Unit<kTile>* un) const {
-    if (p.split != 2) {
+  __device__ __forceinline__ unsigned seat(const Dev& d, unsigned turn) const { return d.B == 1 && turn & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x; }
+  // The segment at x, and x moved behind it.  (d, split: the kernel's arguments, nearer than what lies beside the line.)
+  __device__ __forceinline__ Segment next(const Dev& d, int split, int64_t* x, Unit<kTile>* un) const {
+    if (split != 2) {
       const auto pc = this->locate(*x, un);
       const int count = int(min(int64_t(un->tr.tiles - pc.tile), x1 - *x));
       *x += count;
       return Segment{pc.hk, pc.tile, count, pc.tile == 0 && count == un->tr.tiles};
     }
-    const unsigned turn = unsigned(*x), place = turn * gridDim.x + seat(turn), pair = a.B == 1 ? pairs - 1 - place : place;
-    const int u = int(pair / unsigned(a.K));
+    const unsigned turn = unsigned(*x), place = turn * gridDim.x + seat(d, turn), pair = d.B == 1 ? pairs - 1 - place : place;
+    const int u = int(pair / unsigned(d.K));
     int lo = 0;                                     // the unit's sequence: the last whose first <= u (empty ones precede)
-    for (int hi = a.B; hi - lo > 1;) {
+    for (int hi = d.B; hi - lo > 1;) {
       const int mid = (lo + hi) >> 1;
       if (seqs[mid].first <= u) lo = mid; else hi = mid;
     }
-    *un = make_unit<R, kTile>(a, this->ref(lo, u - seqs[lo].first, seqs[lo].r));
+    const SeqRun r = seqs[lo].r;
+    *un = make_unit<R, kTile>(d, UnitRef{lo, r.s0, r.p0, int(min(int64_t(r.n) * d.G, (int64_t(u - seqs[lo].first) + 1) * R)) - 1});
     ++*x;
-    return Segment{int(pair % unsigned(a.K)), 0, un->tr.tiles, true};
+    return Segment{int(pair % unsigned(d.K)), 0, un->tr.tiles, true};
   }
   __device__ __forceinline__ JoinDesc tail() const {      // (split = 1) what the CTA leaves to the next ones
     Unit<kTile> un;
@@ -180,7 +184,7 @@ struct StreamLayout {
 
 template <int D, class Src>
 __global__ void __launch_bounds__(StreamLayout<D, Src>::kThreads, 1)
-stream_attn_kernel(const __grid_constant__ typename Src::Dev a, const SplitDev p) {
+stream_attn_kernel(const __grid_constant__ typename Src::Dev a, const __grid_constant__ SplitDev p) {
   using W = Stream<D>;
   using L = StreamLayout<D, Src>;
   constexpr int kThreads = L::kThreads, SK = L::kKeyStages, SV = L::kValueStages;
@@ -194,12 +198,17 @@ stream_attn_kernel(const __grid_constant__ typename Src::Dev a, const SplitDev p
   volatile int* abort_flag = &s.abort_flag;
 
   if (!p.late) pdl_wait();
-  Segments<W::kUnit, kKeys, kThreads, typename Src::Dev> line(a, p, &s + 1);
-  if (!line.init(s.scan, base, W::kMinSteps)) {
-    if (p.late) pdl_wait();
-    return;
+  using Line = Segments<W::kUnit, kKeys, kThreads, typename Src::Dev>;
+  static_assert(sizeof(Line) <= sizeof(StreamSmem::line), "room for the line");
+  {
+    Line mine(a, p, &s + 1);
+    if (!mine.init(s.scan, base, W::kMinSteps)) {
+      if (p.late) pdl_wait();
+      return;
+    }
+    if (tid == 0) new (s.line) Line(mine);
   }
-  const int64_t x0 = line.x0, x1 = line.x1;
+  const Line& line = *reinterpret_cast<const Line*>(s.line);
   const bool q_copied = Src::q_copied(a);      // the queries come with Feed, ahead of the unit before's output
 
   if (tid == 0) {
@@ -245,9 +254,9 @@ stream_attn_kernel(const __grid_constant__ typename Src::Dev a, const SplitDev p
     const uint32_t s_at = tmem + 128 * t + lanes, o_at = tmem_o + D * t + lanes;
     bool ok = true;
     int n = 0, e = 0, g = 0;
-    for (int64_t x = x0; x < x1 && ok;) {
+    for (int64_t x = line.x0; x < line.x1 && ok;) {
       Unit<kKeys> un;
-      const auto sg = line.next(&x, &un);
+      const auto sg = line.next(a, p.split, &x, &un);
       const int count = sg.count;
       if (un.rows <= t * kTileRows) {
         n += count;
@@ -435,9 +444,9 @@ stream_attn_kernel(const __grid_constant__ typename Src::Dev a, const SplitDev p
     auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_for(bar, parity, a.status, abort_flag); };
     bool ok = true;
     int n = 0, e[2] = {0, 0}, g[2] = {0, 0};
-    for (int64_t x = x0; x < x1 && ok;) {
+    for (int64_t x = line.x0; x < line.x1 && ok;) {
       Unit<kKeys> un;
-      const auto sg = line.next(&x, &un);
+      const auto sg = line.next(a, p.split, &x, &un);
       const int count = uniform(sg.count);
       const int tiles = uniform(W::kTiles == 2 && un.rows > kTileRows ? 2 : 1);
       for (int j = 0; j < min(count, kBuffers) && ok; ++j) {
@@ -498,9 +507,9 @@ stream_attn_kernel(const __grid_constant__ typename Src::Dev a, const SplitDev p
     auto wait = [&](uint64_t* bar, int phase) { return wait_for(bar, phase & 1, a.status, abort_flag); };
     bool ok = true;
     int n = 0, e = 0;
-    for (int64_t x = x0; x < x1 && ok;) {
+    for (int64_t x = line.x0; x < line.x1 && ok;) {
       Unit<kKeys> un;
-      const auto sg = line.next(&x, &un);
+      const auto sg = line.next(a, p.split, &x, &un);
       const int count = sg.count;
       ok = feed.begin(un, sg.hk, sg.tile, count, n);
       for (int j = 0; j < min(count, kBuffers) && ok; ++j)      // (a phase is asked for when the one before it has been)
@@ -518,9 +527,9 @@ stream_attn_kernel(const __grid_constant__ typename Src::Dev a, const SplitDev p
     // ---- the copying warps ----
     bool ok = true;
     int n = 0;
-    for (int64_t x = x0; x < x1 && ok;) {
+    for (int64_t x = line.x0; x < line.x1 && ok;) {
       Unit<kKeys> un;
-      const auto sg = line.next(&x, &un);
+      const auto sg = line.next(a, p.split, &x, &un);
       const int count = sg.count;
       ok = Src::template copy<D>(a, un, sg.hk, sg.tile, count, n, tid - W::kSoftmax - 64, base, s);
       n += count;
