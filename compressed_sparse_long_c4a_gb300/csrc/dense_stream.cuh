@@ -23,14 +23,15 @@
 //
 // Bound: a step is a chain of score, softmax and product for each tile, in which the
 // two tiles alternate.  Of about 2,850 clocks a step of 128 keys at dim 128 takes
-// (prompts), the products are 2,048 at the tensor cores' rate; a tile's chain is
+// (prompts, by time stamps), the products are 2,048 at the tensor cores' rate; a tile's chain is
 // 520 for its scores' load and maximum of the first 64 keys and as much for the
 // rest, 400 for the exponentials of each half, 300 until the issuer has seen P, 700
 // to issue the products and 330 until the next scores are there.  Measured and not
 // kept: scores in two buffers of 64 columns at dim 128 (1722 us for a prompt of
 // 16384 tokens, 32 + 8 heads, instead of 1373) and 64 (the same), an issuing warp per
-// tile (1994), polling without suspension (1745), the exponentials beside the search
-// for the maximum (1753), the second half's load beside the first's maximum (1387).
+// tile (1994 for 1688), polling without suspension (1745 for 1665), the exponentials
+// beside the search for the maximum (1436 for 1341), the second half's load beside the
+// first's maximum (1413).
 //
 // What differs is in the source, a class: the arguments, the operands of the
 // scores (scores), the queries' way into shared memory (load_q, or Feed's), what

@@ -7,11 +7,11 @@
 // sequence's cannot reach a product, and are copied by the warp.
 //
 // Bound: 4 dim flops per visible pair on the tensor cores, which are 53% busy (ncu,
-// 4096 tokens; issue slots 35%, DRAM 6%): dense_stream.cuh says what the rest is.
-// Measured, 32 + 8 heads of 128: 16384 tokens 1360 us (1617 TFLOP/s), 4096 111 us
-// (1243), 64 prompts of 1 to 256 (16 + 4 heads) 45 us; 16 + 4 heads of 256, 8192
-// tokens 420 us (1310), of 192 336 (1228); heads of 64, 16384 tokens 1202 us (915: half
-// of the flops for the same softmax); 8 prompts of 1000 to 4096, 64 + 8 heads of 64, window 1024 680 us.
+// 4096 tokens; XU pipe 27%, DRAM 6%): dense_stream.cuh says what the rest is.
+// Measured, 32 + 8 heads of 128: 16384 tokens 1341 us (1639 TFLOP/s), 4096 113 us
+// (1220), 64 prompts of 1 to 256 (16 + 4 heads) 46 us; 16 + 4 heads of 256, 8192
+// tokens 420 us (1310), of 192 336 (1228); heads of 64, 16384 tokens 1215 us (905: half
+// of the flops for the same softmax); 8 prompts of 1000 to 4096, 64 + 8 heads of 64, window 1024 666 us.
 #include "dense_stream.cuh"
 
 namespace v4a {
