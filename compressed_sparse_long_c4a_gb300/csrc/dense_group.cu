@@ -106,7 +106,8 @@ struct GroupCache {
     }
     top = max(top >> 16, top & 0xffffu);
     const int e = top == 0 ? 127 : min(253, max(1, 261 - int(top >> 7)));      // the power's exponent field
-    const float up = live ? __int_as_float(e << 23) : 0.f, down = __int_as_float((254 - e) << 23);
+    // (a row with an infinity becomes NaN: e4m3 has none, and would make it 448)
+    const float up = !live ? 0.f : top >= 0x7f80 ? NAN : __int_as_float(e << 23), down = __int_as_float((254 - e) << 23);
 #pragma unroll 4
     for (int ch = 0; ch < D / 16; ++ch) {
       const uint4 u = __ldcg(q + 2 * ch), w = __ldcg(q + 2 * ch + 1);

@@ -233,6 +233,27 @@ def test_nan_query_stays_in_its_row(dim):
     assert torch.equal(*outs)
 
 
+@pytest.mark.parametrize("new", [1, 300])
+@pytest.mark.parametrize("dim", [64, 128, 192, 256])
+def test_infinite_query_is_not_made_finite(dim, new):
+    """Infinite logits of both signs have no softmax: the row is NaN, the others keep their results."""
+    layer = GroupLayer((400,), 4, 2, dim, seed=16)
+    pos, st = torch.arange(400 - new, 400, **I32), torch.tensor([0, new], **I32)
+    q = layer.query(new)
+    at, outs, lses = new // 2, [], []
+    for _ in range(2):
+        out, lse = torch.empty_like(q), torch.empty(q.shape[:2], device=DEV)
+        _dense().DenseAttention(layer.cache, 4, new, new).run(q, out, pos, st, lse=lse)
+        outs.append(out)
+        lses.append(lse)
+        q[at, 2, 5] = math.inf
+    torch.cuda.synchronize()
+    assert outs[0].isfinite().all() and outs[1][at, 2].isnan().all() and lses[1][at, 2].isnan()
+    for x, y in (outs, lses):
+        y[at, 2] = x[at, 2]
+        assert torch.equal(x, y)
+
+
 @pytest.mark.parametrize("new", [1, 60])
 def test_nan_code_reaches_the_queries_that_see_it(new):
     """A NaN that was inserted comes out, also where the scale is finite."""
