@@ -383,6 +383,7 @@ stream_attn_kernel(const __grid_constant__ typename Src::Dev a, const __grid_con
       if (ok) {
         tc::tc_fence_after();
         const bool begins = sg.tile == 0, whole = sg.whole;
+        if (any && l == 0.f) l = NAN;                  // the largest logit is past fp32: it has no weight against itself
         const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;
         const int64_t at = row_of(a, un, sg.hk, min(row, un.rows - 1));
         const int64_t slot = int64_t(blockIdx.x) * 2 + (begins ? 1 : 0), part = slot * W::kUnit + row;

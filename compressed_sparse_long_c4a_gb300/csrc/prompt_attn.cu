@@ -253,7 +253,7 @@ int prompt_attn(const v4a_prompt_attn_args* a, void* ws, size_t ws_bytes, cudaSt
   d.out = a->out; d.lse = a->lse; d.status = a->status;
   d.scale_log2 = std::max(a->softmax_scale * 1.4426950408889634f, 0x1p-126f);      // (a subnormal one would be flushed)
   SplitDev p{};
-  rc = stream_plan(d, a->dim, 0, (d.Tk + d.B - 1) / d.B, d.causal != 0, ws, &p);
+  rc = stream_plan(d, a->dim, 0, (int64_t(d.Tk) + d.B - 1) / d.B, d.causal != 0, ws, &p);
   if (rc) return rc;
   if (a->num_kv_tokens > 0 && (!make_map(&d.km, a->k, d.Tk, d.K, a->dim, d.ks) || !make_map(&d.vm, a->v, d.Tk, d.K, a->dim, d.vs))) return V4A_ERR_CUDA;
   d.q_copied = kTileRows % d.G == 0;

@@ -254,6 +254,38 @@ def test_infinite_query_is_not_made_finite(dim, new):
         assert torch.equal(x, y)
 
 
+@pytest.mark.parametrize("form", ["prompt", "chunk"])
+@pytest.mark.parametrize("dim", [64, 256])
+def test_logits_past_fp32_give_nan(dim, form):
+    """Scores of 2^126 with a softmax scale of 8: the row is NaN, never zeros, and the others keep their results."""
+    starts, kv, q, k, v = _prompt(((0, 300),), 4, 2, dim, seed=17, pad=0)
+    k, v = k[1:301].contiguous(), v[1:301].contiguous()
+    k[:, 1, 5] = 2.0 ** 62
+    outs = []
+    if form == "chunk":
+        D = _dense()
+        pool = torch.zeros((2, OG.block_bytes(2, dim)), dtype=torch.uint8, device=DEV)
+        cache = D.DenseCache(pool, torch.tensor([[0, 1]], **I32), 2, dim, D.KV_FP8_GROUP)
+        pos = torch.arange(300, **I32)
+        D.DenseInsert(cache, 0, None).run(None, k, v, None, pos, torch.arange(300, device=DEV), k_out=torch.empty_like(k))
+    q[:, 2:, 5] = 0
+    for _ in range(2):
+        if form == "prompt":
+            out, lse = _run_prompt(starts, None, q, k, v, scale=8.0)[1:]
+        else:
+            x = q.contiguous()
+            out, lse = torch.empty_like(x), torch.empty(x.shape[:2], device=DEV)
+            D.DenseAttention(cache, 4, 300, 300, scale=8.0).run(x, out, pos, torch.tensor([0, 300], **I32), lse=lse)
+            torch.cuda.synchronize()
+        outs.append((out, lse))
+        q[77, 2] = 0
+        q[77, 2, 5] = 2.0 ** 64
+    assert outs[0][0].isfinite().all() and outs[1][0][77, 2].isnan().all() and outs[1][1][77, 2].isnan()
+    for x, y in zip(*outs):
+        y[77, 2] = x[77, 2]
+        assert torch.equal(x, y)
+
+
 @pytest.mark.parametrize("new", [1, 60])
 def test_nan_code_reaches_the_queries_that_see_it(new):
     """A NaN that was inserted comes out, also where the scale is finite."""
