@@ -356,7 +356,7 @@ int stream_plan(const DenseAttnDev& d, int dim, int rows_from, int64_t keys, boo
   const double longest = double(d.window ? std::min<int64_t>(keys, d.window + 256) : keys) / 128;
   const double mean = causal_whole && !d.window ? longest / 2 : longest, rounds = double(p.U) * d.K / kSms;
   const double even = rounds * mean + 11, dealt = causal_whole && !d.window ? std::max(longest, rounds * mean) : std::ceil(rounds) * mean;
-  const bool can_split = std::max(p.U, d.B) <= kMaxSplitUnits, can_deal = d.B <= kMaxDealtSeqs;
+  const bool can_split = std::max(p.U, d.B) <= kMaxSplitUnits, can_deal = d.B <= kMaxDealtSeqs && (units * d.K / kSms + 1) * int(sizeof(DealtUnit<128>)) <= dealt_bytes(unit);
   p.split = can_split && (even < dealt || !can_deal) ? 1 : can_deal ? 2 : 0;
   split_carve(&p, ws, unit, dim, kSms, dim <= 128 ? Stream<128>::kCost : Stream<256>::kCost);
   *out = p;

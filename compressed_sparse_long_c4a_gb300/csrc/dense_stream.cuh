@@ -38,6 +38,7 @@
 // the waiting warp copies (Feed) and what the copying warps do (copy).
 #pragma once
 #include <new>
+#include <type_traits>
 
 #include "dense_prefill_common.cuh"
 
@@ -82,68 +83,115 @@ __device__ __forceinline__ uint32_t stream_chunk(int r, int ch) {
   return uint32_t((ch >> 3) * (kN * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4));
 }
 
-// The CTA's segments (parts of units), one after the other.  SplitDev::split = 0 and 1 as in Line; 2: whole units, the
-// (unit, KV head) pairs dealt out to the CTAs and found through a table of the sequences.  One sequence's go from the
-// last on, forth and back, since a causal prompt's last units are its longest (a prompt of 16384 tokens, 32 + 8 heads
-// of 128: 1378 us, from the first on 1468); several sequences' in their order (16 of 1000 to 3000: 568 us, the other
-// way 604).
+// Whether all queries of a sequence are at its run's first position.
+__device__ __forceinline__ bool one_position(const DenseAttnDev&) { return false; }
+
+// Units dealt out (split = 2): a CTA's list lies in shared memory or, longer, in its part of the workspace.
+template <int kTile>
+struct DealtUnit { Unit<kTile> un; int hk; };
+constexpr int kDealtItems = 400, kDealtBytes = kDealtItems * int(sizeof(DealtUnit<128>));
+constexpr int kMaxDealtSeqs = 4096, kLengthEntries = 8192;      // of the table they are found in
+__host__ __device__ constexpr int dealt_bytes(int unit) { return int(split_workspace(unit, 64, 1)); }      // of the workspace, for a CTA
+
+struct Segment { int hk, tile, count; bool whole; };      // tile: the first of `count`; whole: the unit's all
+
+// The CTA's segments (parts of units), one after the other: of SplitDev::split = 0 and 1.
 template <int R, int kTile, int kThreads, typename Dev>
 struct Segments : Line<R, kTile, kThreads, Dev> {
   using Base = Line<R, kTile, kThreads, Dev>;
-  using Base::a, Base::p, Base::x0, Base::x1;
-  struct Segment { int hk, tile, count; bool whole; };      // tile: the first of `count`; whole: the unit's all
-  typename Base::Seq* seqs;
-  unsigned pairs;
+  using Base::x0, Base::x1;
 
-  __device__ __forceinline__ Segments(const Dev& a_, const SplitDev& p_, void* mem) : Base(a_, p_, mem), seqs(static_cast<typename Base::Seq*>(mem)), pairs(0) {}
-  __device__ __forceinline__ bool init(int64_t* scan, void* scratch, int min_tiles) {
-    if (p.split != 2) return Base::init(scan, scratch, min_tiles);
-    const int tid = threadIdx.x;
-    int32_t* st = blockIdx.x == 0 ? a.status : nullptr;     // one CTA reports the batch's faults
-    for (int b = tid; b < a.B; b += kThreads) seqs[b] = typename Base::Seq{this->run(b, st), 0};
-    __syncthreads();
-    const int per = (a.B + kThreads - 1) / kThreads, b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
-    int64_t n = 0, all;
-    for (int b = b0; b < b1; ++b) n += this->groups(seqs[b].r.s0, seqs[b].r.s0 + seqs[b].r.n);
-    int64_t at = this->before(n, scan, &all);
-    const int units = int(min(all, int64_t(p.U)));
-    for (int b = b0; b < b1; ++b) {
-      seqs[b].first = int(min(at, int64_t(units)));
-      at += this->groups(seqs[b].r.s0, seqs[b].r.s0 + seqs[b].r.n);
-    }
-    if (st && tid == 0 && all > p.U) report(st, V4A_DEV_BAD_BATCH);         // sequences that share tokens
-    __syncthreads();
-    pairs = unsigned(units) * unsigned(a.K);        // (below 2^31: stream_plan)
-    const unsigned turns = pairs / gridDim.x, rest = pairs % gridDim.x;
-    x0 = 0;
-    x1 = turns + (seat(a, turns) < rest);
-    return x1 > 0;
-  }
-  __device__ __forceinline__ unsigned seat(const Dev& d, unsigned turn) const { return d.B == 1 && turn & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x; }
-  // The segment at x, and x moved behind it.  (d, split: the kernel's arguments, nearer than what lies beside the line.)
-  __device__ __forceinline__ Segment next(const Dev& d, int split, int64_t* x, Unit<kTile>* un) const {
-    if (split != 2) {
-      const auto pc = this->locate(*x, un);
-      const int count = int(min(int64_t(un->tr.tiles - pc.tile), x1 - *x));
-      *x += count;
-      return Segment{pc.hk, pc.tile, count, pc.tile == 0 && count == un->tr.tiles};
-    }
-    const unsigned turn = unsigned(*x), place = turn * gridDim.x + seat(d, turn), pair = d.B == 1 ? pairs - 1 - place : place;
-    const int u = int(pair / unsigned(d.K));
-    int lo = 0;                                     // the unit's sequence: the last whose first <= u (empty ones precede)
-    for (int hi = d.B; hi - lo > 1;) {
-      const int mid = (lo + hi) >> 1;
-      if (seqs[mid].first <= u) lo = mid; else hi = mid;
-    }
-    const SeqRun r = seqs[lo].r;
-    *un = make_unit<R, kTile>(d, UnitRef{lo, r.s0, r.p0, int(min(int64_t(r.n) * d.G, (int64_t(u - seqs[lo].first) + 1) * R)) - 1});
-    ++*x;
-    return Segment{int(pair % unsigned(d.K)), 0, un->tr.tiles, true};
+  __device__ __forceinline__ Segments(const Dev& a_, const SplitDev& p_, void* mem) : Base(a_, p_, mem) {}
+  // The segment at x, and x moved behind it.
+  __device__ __forceinline__ Segment next(int64_t* x, Unit<kTile>* un) const {
+    const auto pc = this->locate(*x, un);
+    const int count = int(min(int64_t(un->tr.tiles - pc.tile), x1 - *x));
+    *x += count;
+    return Segment{pc.hk, pc.tile, count, pc.tile == 0 && count == un->tr.tiles};
   }
   __device__ __forceinline__ JoinDesc tail() const {      // (split = 1) what the CTA leaves to the next ones
     Unit<kTile> un;
     const auto pc = this->locate(x1 - 1, &un);      // at most the last unit goes on: its first tile has to lie in the range, its last one behind it
     return pc.tile + 1 < un.tr.tiles && x1 - 1 - pc.tile >= x0 ? this->describe(pc, un) : JoinDesc{};
+  }
+};
+
+// Those of split = 2: whole units, the (unit, KV head) pairs dealt out to the CTAs in turn, forth and back, the longest
+// units first.  A unit's length is the tile that its last row sees last (up to the window's length, behind which all are
+// alike), or several tiles are one where the table, an entry for each length and sequence, would be too long.
+template <int R, int kTile, int kThreads, typename Dev>
+struct DealtUnits : Line<R, kTile, kThreads, Dev> {
+  using Base = Line<R, kTile, kThreads, Dev>;
+  using Base::a, Base::p, Base::x0, Base::x1;
+  DealtUnit<kTile>* list;
+
+  __device__ __forceinline__ DealtUnits(const Dev& a_, const SplitDev& p_, void* mem) : Base(a_, p_, mem), list(static_cast<DealtUnit<kTile>*>(mem)) {}
+  __device__ __forceinline__ bool init(int64_t* scan, void* scratch, int) {
+    SeqRun* const runs = static_cast<SeqRun*>(scratch);
+    int* const table = reinterpret_cast<int*>(runs + a.B);      // [length, longest first][B] units before the sequence's
+    const int tid = threadIdx.x;
+    int32_t* st = blockIdx.x == 0 ? a.status : nullptr;     // one CTA reports the batch's faults
+    int top = 0;
+    for (int b = tid; b < a.B; b += kThreads) {
+      const SeqRun r = runs[b] = this->run(b, st);
+      if (r.n > 0) top = max(top, (r.p0 + (one_position(a) ? 0 : r.n - 1)) / kTile);
+    }
+    int lengths = 1, shift = 0;      // a length: 2^shift tiles
+    if (int64_t(p.U) * a.K > gridDim.x) {
+      top = __reduce_max_sync(0xffffffffu, top);
+      if ((tid & 31) == 0) scan[tid >> 5] = top;
+      __syncthreads();
+      for (int w = 0; w < kThreads / 32; ++w) top = max(top, int(scan[w]));
+      if (a.window) top = min(top, (a.window + kTile - 1) / kTile);
+      while (int64_t((top >> shift) + 1) * a.B > kLengthEntries) ++shift;
+      lengths = (top >> shift) + 1;
+    }
+    __syncthreads();
+    auto shorter = [&](const SeqRun& r, int len) {      // units of a sequence that are shorter than length `len`
+      const int64_t all = this->groups(r.s0, r.s0 + r.n), m = (int64_t(len) << shift) * kTile;      // the first position of this length
+      if (len <= 0) return int64_t(0);
+      if (len >= lengths || r.p0 + (one_position(a) ? 1 : r.n) <= m) return all;
+      return one_position(a) ? 0 : max(int64_t(0), m - r.p0) * a.G / R;
+    };
+    const int entries = lengths * a.B, per = (entries + kThreads - 1) / kThreads, e0 = min(entries, tid * per), e1 = min(entries, e0 + per);
+    int64_t n = 0, all;
+    for (int pass = 0; pass < 2; ++pass) {              // counted, then written
+      int64_t at = 0;
+      if (pass == 1) at = this->before(n, scan, &all);
+      for (int e = e0, b = e0 % a.B, len = lengths - 1 - e0 / a.B; e < e1; ++e) {
+        const int64_t units = shorter(runs[b], len + 1) - shorter(runs[b], len);
+        if (pass == 1) table[e] = int(min(at, int64_t(p.U)));
+        at += units;
+        if (++b == a.B) b = 0, --len;
+      }
+      n = at;
+    }
+    if (st && tid == 0 && all > p.U) report(st, V4A_DEV_BAD_BATCH);         // sequences that share tokens
+    __syncthreads();
+    const unsigned pairs = unsigned(min(all, int64_t(p.U))) * unsigned(a.K), turns = pairs / gridDim.x;        // (below 2^31: stream_plan)
+    auto pair_of = [&](unsigned turn) { return turn * gridDim.x + (turn & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x); };
+    x0 = 0;
+    x1 = turns + (pair_of(turns) < pairs);
+    if (turns >= kDealtItems) list = reinterpret_cast<DealtUnit<kTile>*>(reinterpret_cast<uint8_t*>(p.join) + blockIdx.x * dealt_bytes(R));
+    for (int i = tid; i < x1; i += kThreads) {
+      const unsigned pair = pair_of(i);
+      const int u = int(pair / unsigned(a.K));
+      int lo = 0;                                     // the last entry <= u (those without units precede)
+      for (int hi = entries; hi - lo > 1;) {
+        const int mid = (lo + hi) >> 1;
+        if (table[mid] <= u) lo = mid; else hi = mid;
+      }
+      const int b = lo % a.B, rg = int(shorter(runs[b], lengths - 1 - lo / a.B)) + u - table[lo];
+      list[i] = DealtUnit<kTile>{make_unit<R, kTile>(a, this->ref(b, rg, runs[b])), int(pair % unsigned(a.K))};
+    }
+    __syncthreads();
+    return x1 > 0;
+  }
+  __device__ __forceinline__ Segment next(int64_t* x, Unit<kTile>* un) const {
+    const DealtUnit<kTile>& it = list[*x];
+    *un = it.un;
+    ++*x;
+    return Segment{it.hk, 0, un->tr.tiles, true};
   }
 };
 
@@ -183,9 +231,8 @@ struct StreamLayout {
   static_assert(kKeyStages <= 4 && kValueStages <= 4 && kKeyBytes % 1024 == 0, "stages");
 };
 
-template <int D, class Src>
-__global__ void __launch_bounds__(StreamLayout<D, Src>::kThreads, 1)
-stream_attn_kernel(const __grid_constant__ typename Src::Dev a, const __grid_constant__ SplitDev p) {
+template <int D, class Src, bool kDealt>
+__device__ __forceinline__ void stream_attn(const typename Src::Dev& a, const SplitDev& p) {
   using W = Stream<D>;
   using L = StreamLayout<D, Src>;
   constexpr int kThreads = L::kThreads, SK = L::kKeyStages, SV = L::kValueStages;
@@ -199,7 +246,7 @@ stream_attn_kernel(const __grid_constant__ typename Src::Dev a, const __grid_con
   volatile int* abort_flag = &s.abort_flag;
 
   if (!p.late) pdl_wait();
-  using Line = Segments<W::kUnit, kKeys, kThreads, typename Src::Dev>;
+  using Line = std::conditional_t<kDealt, DealtUnits<W::kUnit, kKeys, kThreads, typename Src::Dev>, Segments<W::kUnit, kKeys, kThreads, typename Src::Dev>>;
   static_assert(sizeof(Line) <= sizeof(StreamSmem::line), "room for the line");
   {
     Line mine(a, p, &s + 1);
@@ -257,7 +304,7 @@ stream_attn_kernel(const __grid_constant__ typename Src::Dev a, const __grid_con
     int n = 0, e = 0, g = 0;
     for (int64_t x = line.x0; x < line.x1 && ok;) {
       Unit<kKeys> un;
-      const auto sg = line.next(a, p.split, &x, &un);
+      const auto sg = line.next(&x, &un);
       const int count = sg.count;
       if (un.rows <= t * kTileRows) {
         n += count;
@@ -448,7 +495,7 @@ stream_attn_kernel(const __grid_constant__ typename Src::Dev a, const __grid_con
     int n = 0, e[2] = {0, 0}, g[2] = {0, 0};
     for (int64_t x = line.x0; x < line.x1 && ok;) {
       Unit<kKeys> un;
-      const auto sg = line.next(a, p.split, &x, &un);
+      const auto sg = line.next(&x, &un);
       const int count = uniform(sg.count);
       const int tiles = uniform(W::kTiles == 2 && un.rows > kTileRows ? 2 : 1);
       for (int j = 0; j < min(count, kBuffers) && ok; ++j) {
@@ -511,7 +558,7 @@ stream_attn_kernel(const __grid_constant__ typename Src::Dev a, const __grid_con
     int n = 0, e = 0;
     for (int64_t x = line.x0; x < line.x1 && ok;) {
       Unit<kKeys> un;
-      const auto sg = line.next(a, p.split, &x, &un);
+      const auto sg = line.next(&x, &un);
       const int count = sg.count;
       ok = feed.begin(un, sg.hk, sg.tile, count, n);
       for (int j = 0; j < min(count, kBuffers) && ok; ++j)      // (a phase is asked for when the one before it has been)
@@ -531,7 +578,7 @@ stream_attn_kernel(const __grid_constant__ typename Src::Dev a, const __grid_con
     int n = 0;
     for (int64_t x = line.x0; x < line.x1 && ok;) {
       Unit<kKeys> un;
-      const auto sg = line.next(a, p.split, &x, &un);
+      const auto sg = line.next(&x, &un);
       const int count = sg.count;
       ok = Src::template copy<D>(a, un, sg.hk, sg.tile, count, n, tid - W::kSoftmax - 64, base, s);
       n += count;
@@ -540,9 +587,24 @@ stream_attn_kernel(const __grid_constant__ typename Src::Dev a, const __grid_con
   __syncthreads();
   tc::tc_fence_after();
   if (warp == 0) tc::tmem_dealloc(tmem, 512);
-  if (p.split == 1 && tid == 0) p.join[blockIdx.x] = line.tail();
+  if constexpr (!kDealt) {
+    if (p.split == 1 && tid == 0) p.join[blockIdx.x] = line.tail();
+  }
   if (p.late) pdl_wait();
   pdl_trigger();
+}
+
+// Two kernels, since what finds the segments of an even split costs the other form time (its code and registers: chunks over
+// a long cache 1632 us for 1812 in one kernel).
+template <int D, class Src>
+__global__ void __launch_bounds__(StreamLayout<D, Src>::kThreads, 1)
+stream_attn_kernel(const __grid_constant__ typename Src::Dev a, const __grid_constant__ SplitDev p) {
+  stream_attn<D, Src, false>(a, p);
+}
+template <int D, class Src>
+__global__ void __launch_bounds__(StreamLayout<D, Src>::kThreads, 1)
+dealt_attn_kernel(const __grid_constant__ typename Src::Dev a, const __grid_constant__ SplitDev p) {
+  stream_attn<D, Src, true>(a, p);
 }
 
 template <int D, class Src>
@@ -555,19 +617,18 @@ __device__ __forceinline__ void drain_copies(uint64_t* full, int stages, int n) 
     }
 }
 
-// The most sequences of the table of split = 2.
-constexpr int kMaxDealtSeqs = 1024;
-
 // The split of the registers adds up only with those that the kernel was to be built with: setmaxnreg would wait
 // for ever with fewer.
 template <int D, class Src>
 bool stream_ready() {
   static std::atomic<uint64_t> done{0};
   return once_per_device(&done, [] {
-    auto kern = stream_attn_kernel<D, Src>;
-    cudaFuncAttributes attr;
-    return (!Stream<D>::kSplitRegs || (cudaFuncGetAttributes(&attr, kern) == cudaSuccess && attr.numRegs == kStreamLaunchRegs)) &&
-           raise_smem(kern, 227 * 1024);
+    auto fits = [](auto kern) {
+      cudaFuncAttributes attr;
+      return (!Stream<D>::kSplitRegs || (cudaFuncGetAttributes(&attr, kern) == cudaSuccess && attr.numRegs == kStreamLaunchRegs)) &&
+             raise_smem(kern, 227 * 1024);
+    };
+    return fits(stream_attn_kernel<D, Src>) && fits(dealt_attn_kernel<D, Src>);
   });
 }
 
@@ -576,13 +637,14 @@ int stream_launch(const typename Src::Dev& d, const SplitDev& p, cudaStream_t st
   using L = StreamLayout<D, Src>;
   static_assert(!Stream<D>::kSplitRegs || L::kThreads == 384, "the split of the registers");
   static_assert(stream_smem<D, Src>(1, kMaxSplitUnits) <= 227 * 1024, "shared memory of a CTA");
-  static_assert(stream_smem<D, Src>(0, 0) + kMaxDealtSeqs * 16 <= 227 * 1024, "shared memory of a CTA");
+  static_assert(stream_smem<D, Src>(0, 0) + kDealtBytes <= 227 * 1024, "shared memory of a CTA");
   static_assert(L::kRest >= int(kMaxSplitUnits * 16), "scratch of the line");
+  static_assert(L::kRest >= kMaxDealtSeqs * int(sizeof(SeqRun)) + kLengthEntries * 4, "scratch of the dealt units");
   // at least 116 KB: no two CTAs that allocate TMEM share an SM
-  const size_t table = p.split == 2 ? size_t(d.B) * 16 : 0;
+  const size_t table = p.split == 2 ? kDealtBytes : 0;
   const size_t bytes = std::max(stream_smem<D, Src>(p.split == 1, p.U) + table, size_t(116 * 1024));
   const int64_t pairs = int64_t(p.U) * d.K, grid = p.split == 1 ? p.grid : p.split == 2 ? std::min<int64_t>(p.grid, pairs) : pairs;
-  const cudaError_t e = launch_pdl(stream_attn_kernel<D, Src>, dim3(unsigned(grid)), dim3(L::kThreads), bytes, stream, d, p);
+  const cudaError_t e = launch_pdl(p.split == 2 ? dealt_attn_kernel<D, Src> : stream_attn_kernel<D, Src>, dim3(unsigned(grid)), dim3(L::kThreads), bytes, stream, d, p);
   return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? V4A_OK : V4A_ERR_CUDA;
 }
 

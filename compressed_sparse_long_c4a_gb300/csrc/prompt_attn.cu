@@ -41,6 +41,8 @@ __device__ __forceinline__ SeqRun seq_run(const PromptDev& a, int64_t rows_from,
   return r;
 }
 
+__device__ __forceinline__ bool one_position(const PromptDev& a) { return !a.causal; }
+
 template <int R, int kTile>
 __device__ __forceinline__ Unit<kTile> make_unit(const PromptDev& a, const UnitRef& f) {
   Unit<kTile> u{f.b, 0, 0, f.s0, 0, 0, {0, 0, 0}};
