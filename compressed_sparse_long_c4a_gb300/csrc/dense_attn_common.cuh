@@ -368,9 +368,9 @@ bool dense_prefill_ready(const v4a_dense_attn_args* a, const DenseAttnDev& d);
 int dense_prefill(const v4a_dense_attn_args* a, const DenseAttnDev& d, const SplitDev& p, cudaStream_t stream);
 
 // The same for caches with a scale per group (dense_group.cu).  The division is shared with whole prompts
-// (prompt_attn.cu); keys: what a sequence has at most or on the average, causal_whole: its queries are all of them.
+// (prompt_attn.cu); keys: what a sequence has at most or on the average, causal: its later queries see more.
 size_t stream_workspace(int dim);
-int stream_plan(const DenseAttnDev& d, int dim, int rows_from, int64_t keys, bool causal_whole, void* ws, SplitDev* p);
+int stream_plan(const DenseAttnDev& d, int dim, int rows_from, int64_t keys, bool causal, void* ws, SplitDev* p);
 bool dense_group_ready(int dim, const DenseAttnDev& d);
 int dense_group(int dim, const DenseAttnDev& d, const SplitDev& p, cudaStream_t stream);
 

@@ -338,11 +338,12 @@ int dense_group(int dim, const DenseAttnDev& d, const SplitDev& p, cudaStream_t 
 size_t stream_workspace(int dim) { return split_workspace(stream_unit(dim), dim, kSms); }
 
 // Whole units are dealt out unless an even split of the steps should take less time: that has no idle CTAs, but cut units
-// leave pieces to be joined, which costs the time of about 11 steps of 128 keys.  Even split / dealt out, us, 32 + 8
-// heads of 128: prompts of 16384 tokens 1450 / 1372, 2048 61 / 43, 4 + 1 heads 8192 78 / 109, 4096 45 / 61, 16384 207 /
-// 205; 32 of 300 to 700 tokens 209 / 150; a window of 1024 over 16384 301 / 266; group caches, 4096 tokens over 28672
-// 1599 / 1776, 1000 over 4000 111 / 94.
-int stream_plan(const DenseAttnDev& d, int dim, int rows_from, int64_t keys, bool causal_whole, void* ws, SplitDev* out) {
+// leave pieces to be joined, which costs the time of about 11 steps of 128 keys, and its CTAs walk several sequences'
+// keys at different places.  Even split / dealt out, us, 32 + 8 heads of 128: prompts of 16384 tokens 1450 / 1325, 2048
+// 57 / 39, 4 + 1 heads 8192 74 / 107, 4096 41 / 57, 16384 197 / 201; 4 of 1500 to 2500 143 / 98; a window of 1024 over
+// 16384 293 / 225; group caches, 4096 tokens over 28672 1642 / 1798, over none 279 / 172, 1000 over 4000 115 / 94, 4
+// sequences of 1000 over 8000 561 / 565, of 500 to 2000 over up to 8000 392 / 323, 16 of 256 over 1000 to 30000 1008 / 840.
+int stream_plan(const DenseAttnDev& d, int dim, int rows_from, int64_t keys, bool causal, void* ws, SplitDev* out) {
   const int unit = stream_unit(dim);
   SplitDev p{};
   p.RG = int((int64_t(d.max_new) * d.G + unit - 1) / unit);
@@ -352,10 +353,14 @@ int stream_plan(const DenseAttnDev& d, int dim, int rows_from, int64_t keys, boo
   const int64_t units = units_bound(d, rows_from, p.RG, unit);
   if (units > INT32_MAX || units * d.K > INT32_MAX) return V4A_ERR_UNSUPPORTED;
   p.U = int(units);
-  // times in steps of 128 keys: of the longest unit, of an average one, of the call in either form
-  const double longest = double(d.window ? std::min<int64_t>(keys, d.window + 256) : keys) / 128;
-  const double mean = causal_whole && !d.window ? longest / 2 : longest, rounds = double(p.U) * d.K / kSms;
-  const double even = rounds * mean + 11, dealt = causal_whole && !d.window ? std::max(longest, rounds * mean) : std::ceil(rounds) * mean;
+  // Times in steps of 128 keys.  Units' lengths are taken to be spread evenly: of one sequence between its first and its
+  // last query's, of several between none and the longest.  Dealt out, the full turns have the longest of them, and the
+  // last turn's first is the next.
+  const double longest = double(d.window ? std::min<int64_t>(keys, int64_t(d.window) + 256) : keys) / 128;
+  const double spread = d.window ? 0 : d.B > 1 ? longest : causal ? std::min(longest, double(d.max_new) / 128) : 0;
+  const double rounds = double(p.U) * d.K / kSms, full = std::floor(rounds);
+  const double even = (rounds * (longest - spread / 2) + 11) * (d.B > 1 ? 1.15 : 1);
+  const double dealt = full * (longest - spread * full / (2 * rounds)) + (rounds > full ? longest - spread * full / rounds : 0);
   const bool can_split = std::max(p.U, d.B) <= kMaxSplitUnits, can_deal = d.B <= kMaxDealtSeqs && (units * d.K / kSms + 1) * int(sizeof(DealtUnit<128>)) <= dealt_bytes(unit);
   p.split = can_split && (even < dealt || !can_deal) ? 1 : can_deal ? 2 : 0;
   split_carve(&p, ws, unit, dim, kSms, dim <= 128 ? Stream<128>::kCost : Stream<256>::kCost);

@@ -497,7 +497,7 @@ size_t dense_prefill_workspace(const v4a_dense_attn_args* a) {
 }
 
 int dense_prefill_plan(const v4a_dense_attn_args* a, const DenseAttnDev& d, int rows_from, void* ws, SplitDev* out) {
-  if (a->kv.format == V4A_KV_FP8_GROUP) return stream_plan(d, a->kv.dim, rows_from, int64_t(d.max_blocks) * kBlockPositions, false, ws, out);
+  if (a->kv.format == V4A_KV_FP8_GROUP) return stream_plan(d, a->kv.dim, rows_from, int64_t(d.max_blocks) * kBlockPositions, true, ws, out);
   const bool wide = a->kv.dim > 128;
   const int unit = wide ? kWideUnit : kUnit;
   SplitDev p{};

@@ -19,6 +19,7 @@ def test_registers_of_two_tile_kernels(tmp_path, source):
     r = subprocess.run([B._nvcc(), *B.ARCH, *B.FLAGS, "-Xptxas", "-v", "-I", B.INCLUDE, "-I", B.CSRC, "-c", os.path.join(B.CSRC, source),
                         "-o", str(tmp_path / "x.o")], capture_output=True, text=True)
     assert r.returncode == 0, r.stderr
-    found = re.findall(r"entry function '\w*stream_attn_kernelILi(\d+)E.*?Used (\d+) registers", r.stdout + r.stderr, re.S)
-    assert sorted(int(d) for d, _ in found) == [64, 128, 192, 256]
-    assert {int(n) for d, n in found if int(d) <= 128} == {want}
+    for kernel in ("stream_attn_kernel", "dealt_attn_kernel"):
+        found = re.findall(rf"entry function '\w*{kernel}ILi(\d+)E.*?Used (\d+) registers", r.stdout + r.stderr, re.S)
+        assert sorted(int(d) for d, _ in found) == [64, 128, 192, 256]
+        assert {int(n) for d, n in found if int(d) <= 128} == {want}

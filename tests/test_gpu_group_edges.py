@@ -154,7 +154,7 @@ def test_handles_on_other_streams():
 
 @pytest.mark.parametrize("B", [900, 1100])
 def test_prompts_of_many_sequences(B):
-    """With and without a table of the sequences; some of them empty."""
+    """Many sequences, some of them empty."""
     g = torch.Generator().manual_seed(B)
     runs = [(int(c), int(n)) for c, n in zip(torch.randint(0, 40, (B,), generator=g), torch.randint(0, 90, (B,), generator=g))]
     starts, kv, q, k, v = _prompt(runs, 4, 2, 64, seed=B)
@@ -162,6 +162,33 @@ def test_prompts_of_many_sequences(B):
     assert int(op.status.item()) == 0
     _check_prompt(starts, kv, q, k, v, out, lse, True, 0, 0, op.args.softmax_scale, set(range(0, starts[-1], 397)))
     assert (out[starts[-1]:] == 7.0).all()
+
+
+@pytest.mark.parametrize("B,H,K,window,long", [
+    (4096, 2, 1, 0, 900),          # the most sequences that are dealt out, lengths of several tiles each
+    (4097, 2, 1, 0, 900),
+    (1000, 64, 64, 0, 0),          # more units a CTA than its list in shared memory holds
+    (300, 16, 2, 0, 5000), (40, 16, 2, 700, 6000), (40, 12, 4, 0, 3000),
+])
+@pytest.mark.parametrize("causal", [True, False])
+def test_dealt_units_of_ragged_batches(B, H, K, window, long, causal):
+    """Every row is written once and by its own unit, whatever the order in which units are dealt out."""
+    if window and not causal:
+        pytest.skip("a window is causal")
+    g = torch.Generator().manual_seed(B + H)
+    few = 4 if B > 900 else 60
+    runs = [[int(c), int(n)] for c, n in zip(torch.randint(-2, 40, (B,), generator=g), torch.randint(0, few, (B,), generator=g))]
+    runs = [[max(c, -n), n] for c, n in runs]
+    if long:                       # some long ones among them: all queries, a prefix, both
+        runs[B // 3], runs[B // 2], runs[-1] = [0, long // 3], [long, 3], [long // 2, long // 2]
+    starts, kv, q, k, v = _prompt(runs, H, K, 64, seed=B)
+    op, out, lse = _run_prompt(starts, kv, q, k, v, causal=causal, window=window, sinks=window // 9)
+    assert int(op.status.item()) == 0 and (out[starts[-1]:] == 7.0).all() and (lse[starts[-1]:] == 7.0).all()
+    assert not (lse[:starts[-1]] == 7.0).any() and out[:starts[-1]].isfinite().all()
+    tokens = set(range(0, starts[-1], max(1, starts[-1] * H // 4000)))
+    _check_prompt(starts, kv, q, k, v, out, lse, causal, window, window // 9, op.args.softmax_scale, tokens)
+    again = _run_prompt(starts, kv, q, k, v, causal=causal, window=window, sinks=window // 9)
+    assert torch.equal(out, again[1]) and torch.equal(lse, again[2])
 
 
 @pytest.mark.parametrize("B", [41, 601, 1101])
