@@ -63,6 +63,10 @@ struct Stream {
 // A softmax thread of a 128-key step holds 128 scores: the 384 threads of a CTA of two tiles give it registers.
 constexpr int kStreamLaunchRegs = 168, kStreamSoftmaxRegs = 200, kStreamRestRegs = 104;
 static_assert(kStreamSoftmaxRegs * 256 + kStreamRestRegs * 128 == kStreamLaunchRegs * 384, "the split of the registers");
+// P in bf16 has fp32's range, so its maximum may lag far behind: the first keys of a window, few for some rows, would have
+// most rows raised at the next step (8 prompts of 1000 to 4096 tokens, window 1024: 2^8 614 us, 2^24 584).  Values up to
+// 2^100 stay finite.
+constexpr float kRaiseRows = 24.f;
 constexpr int stream_unit(int dim) { return dim <= 128 ? 256 : 128; }
 
 struct StreamSmem {
@@ -344,11 +348,12 @@ __device__ __forceinline__ void stream_attn(const typename Src::Dev& a, const Sp
         // columns up to hi, and of those the ones behind lo or before sk; a warp whose rows see all skips each side
         const int hi = gone ? -1 : m - j0, lo = a.window ? m - a.window - j0 : -1, sk = a.window ? a.sinks - j0 : 0;
         auto mask = [&](float* z, int h) {             // (part h)
-          if (!hides || __all_sync(0xffffffffu, hi >= 64 * h + 63 && lo < 64 * h)) return;
+          if ((W::kParts == 1 && !hides) || __all_sync(0xffffffffu, hi >= 64 * h + 63 && lo < 64 * h)) return;
 #pragma unroll
           for (int w = 0; w < 2; ++w) {
             const int c0 = 64 * h + 32 * w;
             const uint32_t keep = low_bits(hi + 1 - c0) & (~low_bits(lo + 1 - c0) | low_bits(sk - c0));
+            if (__all_sync(0xffffffffu, keep == ~0u)) continue;
 #pragma unroll
             for (int c = 0; c < 32; ++c) z[32 * w + c] = keep & (1u << c) ? z[32 * w + c] : -INFINITY;
           }
@@ -384,15 +389,16 @@ __device__ __forceinline__ void stream_attn(const typename Src::Dev& a, const Sp
           if (lane == 0) tc::mbar_arrive(&s.p_full[t][kBuffers == 2 ? e & 1 : h]);
         };
         float z[kKeys];
-        tc::tmem_ld64(at, z);
-        mask(z, 0);
-        top = fmaxf(top, largest(z, 0));
-        if constexpr (W::kParts == 2) {
-          tc::tmem_ld64(at + 64, z + 64);
-          mask(z + 64, 1);
-          top = fmaxf(top, largest(z + 64, 1));
-        }
-        const bool raise = top > -INFINITY && (!any || top > ref + (kScaled ? kRaiseFp8 : kRaise));
+        auto find = [&](auto masked) {
+#pragma unroll
+          for (int h = 0; h < W::kParts; ++h) {
+            tc::tmem_ld64(at + 64 * h, z + 64 * h);
+            if constexpr (decltype(masked)::value) mask(z + 64 * h, h);
+            top = fmaxf(top, largest(z + 64 * h, h));
+          }
+        };
+        if (W::kParts == 1 || hides) find(std::true_type{}); else find(std::false_type{});
+        const bool raise = top > -INFINITY && (!any || top > ref + (kScaled ? kRaiseFp8 : kRaiseRows));
         if (__any_sync(0xffffffffu, raise && any)) {       // (so i > 0)
           if constexpr (kBuffers == 2) {      // the step before has to leave the accumulator, which frees its values (one buffer: S says so)
             ok = __all_sync(0xffffffffu, wait_for(&s.v_free[(n - 1) % SV], ((n - 1) / SV) & 1, a.status, abort_flag));

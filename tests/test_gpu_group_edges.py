@@ -334,6 +334,18 @@ def test_nan_code_reaches_the_queries_that_see_it(new):
             assert bool(out[:n].isfinite().all()) and bool((out[:n] == 1).all())
 
 
+@pytest.mark.parametrize("grow", [0.02, 0.1, 1.0])
+@pytest.mark.parametrize("dim", [64, 128, 192, 256])
+def test_logits_that_grow_along_the_keys(dim, grow):
+    """Later keys' logits pass the earlier ones' by little and by much: the running maximum lags, and is raised."""
+    starts, kv, q, k, v = _prompt(((0, 700), (500, 60)), 8, 2, dim, seed=18)
+    k.mul_((1 + grow * torch.arange(k.shape[0], device=DEV)).view(-1, 1, 1).to(torch.bfloat16))
+    for window, sinks in ((0, 0), (300, 40)):
+        op, out, lse = _run_prompt(starts, kv, q, k, v, window=window, sinks=sinks)
+        assert int(op.status.item()) == 0
+        _check_prompt(starts, kv, q, k, v, out, lse, True, window, sinks, op.args.softmax_scale, set(range(0, starts[-1], 23)))
+
+
 @pytest.mark.parametrize("H,K,dim", [(128, 1, 64), (256, 2, 128), (96, 1, 128), (1024, 1024, 64), (5, 5, 256)])
 def test_prompts_of_odd_head_counts(H, K, dim):
     starts, kv, q, k, v = _prompt(((0, 50), (20, 9), (0, 1)), H, K, dim, seed=H)
