@@ -23,10 +23,10 @@
 // Bound: as prompts (dense_stream.cuh); the conversions share the softmax's
 // schedulers (as integer operations instead of cvt: 2362 us for 1605; four warps of
 // them among 512 threads: 1708), and the second e4m3 of the query takes 3% of the
-// time.  Measured, 32 + 8 heads of 128: 4096 tokens over 28672 1622 us (1271 TFLOP/s;
-// ncu, 2048 over 8192: tensor pipe 46% busy), 1000 over 4000 94 us; 16 + 4 heads of 256,
-// 2048 over 10240 368 us (1025; row scales 505), of 192 324 us (876); heads of 64 over
-// 28672 1284 us (803).
+// time.  Measured, 32 + 8 heads of 128: 4096 tokens over 28672 1612 us (1279 TFLOP/s;
+// ncu, 2048 over 8192: tensor pipe 46% busy), 1000 over 4000 94 us, 4096 over none 168; 16 + 4 heads of 256,
+// 2048 over 10240 367 us (1031; row scales 505), of 192 325 us (872); heads of 64 over
+// 28672 1249 us (825).
 #include "dense_stream.cuh"
 
 namespace v4a {

@@ -6,12 +6,13 @@
 // its sequence: its rows behind the last are zeros, so that the next
 // sequence's cannot reach a product, and are copied by the warp.
 //
-// Bound: 4 dim flops per visible pair on the tensor cores, which are 53% busy (ncu,
-// 4096 tokens; XU pipe 27%, DRAM 6%): dense_stream.cuh says what the rest is.
-// Measured, 32 + 8 heads of 128: 16384 tokens 1341 us (1639 TFLOP/s), 4096 113 us
-// (1220), 64 prompts of 1 to 256 (16 + 4 heads) 46 us; 16 + 4 heads of 256, 8192
-// tokens 420 us (1310), of 192 336 (1228); heads of 64, 16384 tokens 1215 us (905: half
-// of the flops for the same softmax); 8 prompts of 1000 to 4096, 64 + 8 heads of 64, window 1024 666 us.
+// Bound: 4 dim flops per visible pair on the tensor cores, which are 62% busy (ncu,
+// 4096 tokens; XU pipe 29%, DRAM 7%): dense_stream.cuh says what the rest is.
+// Measured, 32 + 8 heads of 128: 16384 tokens 1303 us (1688 TFLOP/s), 4096 104 us
+// (1316), 16 prompts of 1000 to 3000 453 (1322), 64 of 1 to 256 (16 + 4 heads) 37 us; 16 +
+// 4 heads of 256, 8192 tokens 412 us (1336), of 192 324 (1274); heads of 64, 16384 tokens
+// 1161 us (947: half of the flops for the same softmax); 8 prompts of 1000 to 4096, 64 + 8
+// heads of 64, window 1024 584 us (650, of which masks take about 40 us).
 #include "dense_stream.cuh"
 
 namespace v4a {
