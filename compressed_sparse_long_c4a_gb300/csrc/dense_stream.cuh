@@ -64,8 +64,10 @@ struct Stream {
 constexpr int kStreamLaunchRegs = 168, kStreamSoftmaxRegs = 200, kStreamRestRegs = 104;
 static_assert(kStreamSoftmaxRegs * 256 + kStreamRestRegs * 128 == kStreamLaunchRegs * 384, "the split of the registers");
 // P in bf16 has fp32's range, so its maximum may lag far behind: the first keys of a window, few for some rows, would have
-// most rows raised at the next step (8 prompts of 1000 to 4096 tokens, window 1024: 2^8 614 us, 2^24 584).  Values up to
-// 2^100 stay finite.
+// most rows raised at the next step (8 prompts of 1000 to 4096 tokens, window 1024: 2^8 614 us, 2^24 584).  The maximum in
+// use is set that far above the largest logit, so that no weight passes one and the accumulator stays below the sum of the
+// values' sizes, as with a maximum that does not lag; what it loses are elements of an output below 2^-102, which it may
+// hold as less than 2^-126.
 constexpr float kRaiseRows = 24.f;
 constexpr int stream_unit(int dim) { return dim <= 128 ? 256 : 128; }
 
@@ -398,14 +400,15 @@ __device__ __forceinline__ void stream_attn(const typename Src::Dev& a, const Sp
           }
         };
         if (W::kParts == 1 || hides) find(std::true_type{}); else find(std::false_type{});
-        const bool raise = top > -INFINITY && (!any || top > ref + (kScaled ? kRaiseFp8 : kRaiseRows));
+        const bool raise = top > -INFINITY && (!any || top > ref + (kScaled ? kRaiseFp8 : 0.f));
+        const float next = kScaled ? top : top + kRaiseRows;      // what the maximum in use is raised to
         if (__any_sync(0xffffffffu, raise && any)) {       // (so i > 0)
           if constexpr (kBuffers == 2) {      // the step before has to leave the accumulator, which frees its values (one buffer: S says so)
             ok = __all_sync(0xffffffffu, wait_for(&s.v_free[(n - 1) % SV], ((n - 1) / SV) & 1, a.status, abort_flag));
             if (!ok) break;
             tc::tc_fence_after();
           }
-          const float w = raise && any ? exp2f(ref - top) : 1.f;
+          const float w = raise && any ? exp2f(ref - next) : 1.f;
           l *= w;
 #pragma unroll 1
           for (int c = 0; c < D; c += 32) {
@@ -418,7 +421,7 @@ __device__ __forceinline__ void stream_attn(const typename Src::Dev& a, const Sp
           tmem_wait_st();
         }
         if (raise) {
-          ref = top;
+          ref = next;
           any = true;
         }
         float sum = weights(z, 0);

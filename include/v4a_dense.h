@@ -347,7 +347,9 @@ V4A_API int v4a_dense_attn(const v4a_dense_attn_args* args, void* workspace, siz
  * is not defined).  Rows outside [kv_starts[b], kv_starts[b + 1]) do not reach
  * sequence b's outputs whatever they hold; a NaN or infinity inside may reach
  * any of them.  Dot products and sums are fp32; the probabilities are rounded
- * to bf16, the output once.
+ * to bf16, the output once.  The sum over the values precedes the division: it
+ * holds while the |value| of a row's visible keys sum up to less than 2^127, and
+ * elements of an output below 2^-102 may be zeros.
  */
 typedef struct {
   int32_t num_tokens;          /* T >= 0: rows of q and out */
