@@ -11,9 +11,9 @@
 // the keys at twice the 16-bit rate.  A bf16 has 8 bits, a nearest e4m3 4 of them
 // and the rest at most 4, so the sum is exact down to 2^-9 of the row's largest
 // element and within 2^-17 of that element below.  Value codes become f16, exactly:
-// P in 8 bits would be too coarse.  P is f16 and holds 2^11 2^{w - m}, w the logit
-// plus log2 of the value scale: weights down to 2^-25 of the largest are rounded
-// to 11 bits.
+// P in 8 bits would be too coarse.  P is f16 and holds 2^{w - m}, w the logit plus
+// log2 of the value scale, times a power that makes 2^11 to 2^15 of the largest:
+// weights down to 2^-25 of it are rounded to 11 bits.
 //
 // Copies: one lane has TMA bring the key codes into the swizzle that the MMA reads,
 // and the value codes as they are; two to four warps convert the latter from shared

@@ -69,6 +69,11 @@ static_assert(kStreamSoftmaxRegs * 256 + kStreamRestRegs * 128 == kStreamLaunchR
 // values' sizes, as with a maximum that does not lag; what it loses are elements of an output below 2^-102, which it may
 // hold as less than 2^-126.
 constexpr float kRaiseRows = 24.f;
+// P in f16 is 2^kTopFp8 2^{w - m}, m again the lag above the largest logit: from 2^11 to 2^15 for the largest weight.  The
+// sum is kept without that factor, so groups of zeros, whose value scale is read as 2^-100, add 2^100 a key at most (with
+// the factor and a maximum below the logits 2^13 of them, with it alone 2^17, made an infinite lse).
+constexpr float kTopFp8 = kShiftFp8 + kRaiseFp8, kTopFp8Inv = 0x1p-15f;
+static_assert(kTopFp8 == 15.f, "its inverse");
 constexpr int stream_unit(int dim) { return dim <= 128 ? 256 : 128; }
 
 struct StreamSmem {
@@ -371,7 +376,7 @@ __device__ __forceinline__ void stream_attn(const typename Src::Dev& a, const Sp
         uint32_t pk[32];
         auto weights = [&](const float* z, int h) {    // P of part h into pk; their sum
           float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-          const float up = kScaled ? lv[h] + kShiftFp8 - ref : -ref;
+          const float up = kScaled ? lv[h] + kTopFp8 - ref : -ref;
           const float2 f2 = make_float2(fk[h], fk[h]), r2 = make_float2(up, up);
 #pragma unroll
           for (int c = 0; c < 64; c += 2) {
@@ -381,7 +386,8 @@ __device__ __forceinline__ void stream_attn(const typename Src::Dev& a, const Sp
             sum[(c >> 1) & 1] = add2(sum[(c >> 1) & 1], y);
             pk[c >> 1] = kScaled ? pack_f16(y.x, y.y) : pack_bf16(y.x, y.y);
           }
-          return ((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y)) * inv_v[h];
+          const float all = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+          return kScaled ? all * inv_v[h] * kTopFp8Inv : all;
         };
         auto announce = [&](int h) {
           tmem_st32(at + 32 * h, pk);
@@ -400,8 +406,8 @@ __device__ __forceinline__ void stream_attn(const typename Src::Dev& a, const Sp
           }
         };
         if (W::kParts == 1 || hides) find(std::true_type{}); else find(std::false_type{});
-        const bool raise = top > -INFINITY && (!any || top > ref + (kScaled ? kRaiseFp8 : 0.f));
-        const float next = kScaled ? top : top + kRaiseRows;      // what the maximum in use is raised to
+        const bool raise = top > -INFINITY && (!any || top > ref);
+        const float next = top + (kScaled ? kRaiseFp8 : kRaiseRows);      // what the maximum in use is raised to
         if (__any_sync(0xffffffffu, raise && any)) {       // (so i > 0)
           if constexpr (kBuffers == 2) {      // the step before has to leave the accumulator, which frees its values (one buffer: S says so)
             ok = __all_sync(0xffffffffu, wait_for(&s.v_free[(n - 1) % SV], ((n - 1) / SV) & 1, a.status, abort_flag));
@@ -457,6 +463,10 @@ __device__ __forceinline__ void stream_attn(const typename Src::Dev& a, const Sp
         for (int c = 0; c < D; c += 32) {
           float o[32];
           tmem_ld32(o_at + c, o);
+          if constexpr (kScaled) {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] *= kTopFp8Inv;
+          }
           if (whole) {
             uint4 v[4];
 #pragma unroll
@@ -480,9 +490,9 @@ __device__ __forceinline__ void stream_attn(const typename Src::Dev& a, const Sp
         }
         if (row < un.rows) {
           if (whole) {
-            if (a.lse) a.lse[at] = any ? (ref - (kScaled ? kShiftFp8 : 0.f) + log2f(l)) * 0.6931471805599453f : l == 0.f ? -INFINITY : l;
+            if (a.lse) a.lse[at] = any ? (ref + log2f(l)) * 0.6931471805599453f : l == 0.f ? -INFINITY : l;
           } else {       // a piece without a key leaves nothing; one whose logits are all NaN is passed on
-            p.part_ml[part * 2] = any || l != 0.f ? ref - (kScaled ? kShiftFp8 : 0.f) : -INFINITY;
+            p.part_ml[part * 2] = any || l != 0.f ? ref : -INFINITY;
             p.part_ml[part * 2 + 1] = l;
           }
         }

@@ -8,7 +8,8 @@ import math
 import pytest
 import torch
 
-from tests.test_gpu_group import _check_prompt, _prompt, _run_prompt
+from oracle import dense_group as OG
+from tests.test_gpu_group import DEV, I32, _check_prompt, _check_token, _dense, _f64, _prompt, _run_prompt
 
 pytestmark = pytest.mark.gpu
 
@@ -28,3 +29,53 @@ def test_prompts_of_large_and_small_values(dim, exponent, runs):
     op, out, lse = _run_prompt(starts, kv, q, k, v, scale=math.log(2))
     assert int(op.status.item()) == 0 and bool(out.isfinite().all())
     _check_prompt(starts, kv, q, k, v, out, lse, True, 0, 0, op.args.softmax_scale, set(range(0, starts[-1], 29)))
+
+
+def _line_cache(keys, values, tight=True):
+    """One sequence's rows, inserted through the public call; a table as wide as the sequence, or far wider."""
+    D = _dense()
+    n, K, dim = keys.shape
+    blocks = -(-n // 256)
+    pool = torch.zeros((blocks, OG.block_bytes(K, dim)), dtype=torch.uint8, device=DEV)
+    table = torch.full((1, blocks if tight else 8 * blocks), -1, **I32)
+    table[0, :blocks] = torch.arange(blocks, **I32)
+    cache = D.DenseCache(pool, table, K, dim, D.KV_FP8_GROUP)
+    op = D.DenseInsert(cache, 0, None)
+    op.run(None, keys, values, None, torch.arange(n, **I32), torch.arange(n, device=DEV), k_out=torch.empty_like(keys))
+    return cache
+
+
+@pytest.mark.parametrize("values", ["zero", "fresh", "tiny", "some"])
+@pytest.mark.parametrize("dim,K,new,n,grow", [
+    (64, 1, 1, 20000, 3.5), (64, 1, 40, 20000, 3.5), (192, 1, 50, 20000, 3.5), (256, 1, 100, 20000, 3.5),
+    # whole units a CTA: one sum over all keys
+    (64, 8, 1200, 20000, 3.5), (128, 8, 1200, 20000, 3.5), (192, 8, 600, 20000, 3.5), (256, 8, 600, 20000, 3.5),
+    (64, 1, 1, 140000, 0.0), (128, 1, 40, 140000, 0.0)])
+def test_sums_over_groups_of_the_least_scales(dim, K, new, n, grow, values):
+    """Groups of zeros (stored with the least scale, or 0 in a pool that was never written) and of the least values that are
+    read as they are: out and lse hold over any number of them.  In log2 units the logits are 0 for the first 256 keys and
+    `grow` for the others, below what has the maximum raised."""
+    D = _dense()
+    keys = torch.zeros((n, K, dim), dtype=torch.bfloat16, device=DEV)
+    keys[256:, :, 0] = grow
+    x = torch.zeros_like(keys)
+    if values == "tiny":
+        x[:] = 2.0 ** -92                          # its group's scale is 2^-100
+    if values == "some":
+        x[n - 5000:] = 1.0
+    cache = _line_cache(keys, x, tight=K == 8)
+    if values == "fresh":
+        cache.pool[:, 2 * K * 256 * dim + 16 * K:2 * K * 256 * dim + 32 * K] = 0
+    q = torch.zeros((new, 4 * K, dim), dtype=torch.bfloat16, device=DEV)
+    q[..., 0] = 1.0
+    op = D.DenseAttention(cache, 4 * K, new, new, scale=math.log(2))
+    out, lse = torch.empty_like(q), torch.empty((new, 4 * K), device=DEV)
+    op.run(q, out, torch.arange(n - new, n, **I32), torch.tensor([0, new], **I32), lse)
+    torch.cuda.synchronize()
+    assert int(op.status.item()) == 0 and bool(lse.isfinite().all()) and bool(out.isfinite().all())
+    kh, vh = _f64(keys[:, 0]), _f64(x[:, 0])
+    for t in {0, new // 2, new - 1}:
+        m = n - new + t + 1
+        _check_token(q[t], out[t], lse[t], lambda w, h: (vh if w else kh)[:m], K, op.args.softmax_scale, 2.0 ** -11, t, 2.0 ** -17)
+    if values in ("zero", "fresh"):
+        assert not out.any()
