@@ -56,6 +56,12 @@ __device__ __forceinline__ float2 values2(uint32_t codes) {
 }
 __device__ __forceinline__ float lo_of(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi_of(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+// x s with x or the product below 2^-126 kept (the library's fast math would take them as zeros).
+__device__ __forceinline__ float times(float x, float s) {
+  float r;
+  asm("mul.rn.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(s));
+  return r;
+}
 // 2^(field - 127), 0 below the normal numbers.
 __device__ __forceinline__ float power(int field) { return __uint_as_float(uint32_t(max(field, 0)) << 23); }
 
@@ -153,7 +159,7 @@ __global__ void __launch_bounds__(kThreads) dense_quant_kernel(const __grid_cons
       for (int k = 0; k < kPasses; ++k) {
         const int c = tid + k * kThreads, r = c / kChunks, ch = c % kChunks;
         if (!(member[r >> 5] >> (r & 31) & 1)) continue;
-        auto four = [&](uint32_t x, uint32_t y) { return codes4(lo_of(x) * inv, hi_of(x) * inv, lo_of(y) * inv, hi_of(y) * inv); };
+        auto four = [&](uint32_t x, uint32_t y) { return codes4(times(lo_of(x), inv), times(hi_of(x), inv), times(lo_of(y), inv), times(hi_of(y), inv)); };
         *reinterpret_cast<uint4*>(dst + int64_t(slot[i + r] % kGroupPositions) * D + ch * 16) =
             make_uint4(four(a[k].x, a[k].y), four(a[k].z, a[k].w), four(b[k].x, b[k].y), four(b[k].z, b[k].w));
       }

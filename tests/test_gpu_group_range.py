@@ -5,11 +5,13 @@ from __future__ import annotations
 
 import math
 
+import numpy as np
 import pytest
 import torch
 
 from oracle import dense_group as OG
-from tests.test_gpu_group import DEV, I32, _check_prompt, _check_token, _dense, _f64, _prompt, _run_prompt
+from oracle import formats as F
+from tests.test_gpu_group import DEV, I32, _check_prompt, _check_token, _dense, _f64, _prompt, _run_prompt, _same_cache
 
 pytestmark = pytest.mark.gpu
 
@@ -79,3 +81,28 @@ def test_sums_over_groups_of_the_least_scales(dim, K, new, n, grow, values):
         _check_token(q[t], out[t], lse[t], lambda w, h: (vh if w else kh)[:m], K, op.args.softmax_scale, 2.0 ** -11, t, 2.0 ** -17)
     if values in ("zero", "fresh"):
         assert not out.any()
+
+
+@pytest.mark.parametrize("top", [-117, -112])
+@pytest.mark.parametrize("dim", [64, 128, 192, 256])
+def test_codes_of_the_least_values(dim, top):
+    """Every bf16 below 2^-116, the ones below 2^-126 among them, in groups of the least scale and of 2^-120: byte for byte."""
+    D = _dense()
+    bits = torch.arange(0, 11 << 7, dtype=torch.int32)
+    bits = torch.cat([bits, bits | 0x8000])
+    bits = bits[torch.randperm(len(bits), generator=torch.Generator().manual_seed(dim))]
+    n = -(-len(bits) // dim)
+    bits = torch.cat([bits, torch.zeros(n * dim - len(bits), dtype=torch.int32)])
+    bits = torch.where(bits > 0x7fff, bits - 0x10000, bits).to(torch.int16)
+    x = bits.view(torch.bfloat16).view(n, 1, dim).to(DEV)
+    x[n // 2, 0, 5] = 2.0 ** top
+    pool = torch.zeros((1, OG.block_bytes(1, dim)), dtype=torch.uint8, device=DEV)
+    want = pool.cpu().numpy().copy()
+    slots = list(range(n))               # one group
+    op = D.DenseInsert(D.DenseCache(pool, None, 1, dim, D.KV_FP8_GROUP), 0, None)
+    k_out = torch.empty_like(x)
+    op.run(None, x, x.flip(0).contiguous(), None, torch.arange(n, **I32), torch.tensor(slots, device=DEV), k_out=k_out)
+    assert torch.equal(k_out.view(torch.int16), x.view(torch.int16))
+    rows = F.bf16_decode(x.cpu().view(torch.int16).numpy().view(np.uint16))
+    OG.insert(want, 1, dim, slots, (rows, rows[::-1]))
+    _same_cache(pool, want, 1, dim)
