@@ -186,6 +186,17 @@ __device__ __forceinline__ uint32_t two(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&x);
 }
 
+// x s for a code x and a row's scale s, so that rounding the result to bf16 rounds the product once.  The product has 28
+// bits, of which fp32 keeps 24; cut off, the last bit set says that it is larger.  That bit may be set for an exact
+// product too unless this is a tie of bf16, which takes a scale of at most nine bits: those have exact products (and an
+// infinite scale is one of them).  Both neighbours of the product, to see whether it is exact, took 165 us for 132.
+__device__ __forceinline__ uint32_t lost_bit(float s) { return (__float_as_uint(s) & 0x7fffu) != 0; }
+__device__ __forceinline__ float times_to_odd(float x, float s, uint32_t lost) {
+  float r;
+  asm("mul.rz.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(s));
+  return __uint_as_float(__float_as_uint(r) | lost);
+}
+
 // A CTA takes `rows` packed rows, a thread 16 elements of one at a time.
 template <int kFmt>
 __global__ void __launch_bounds__(kReadThreads) dense_read_kernel(const __grid_constant__ ReadDev p) {
@@ -234,9 +245,11 @@ __global__ void __launch_bounds__(kReadThreads) dense_read_kernel(const __grid_c
       const uint4 w = *reinterpret_cast<const uint4*>(block + row * p.D + ch * 16);
       const float* scales = reinterpret_cast<const float*>(block + int64_t(2 * p.K) * kBlockPositions * p.D);
       const float s = scales[kFmt == V4A_KV_FP8_GROUP ? row / kGroupPositions : row];
+      const uint32_t lost = lost_bit(s);
       auto pair = [&](uint32_t codes) {
         const float2 x = values2(codes);
-        return two(x.x * s, x.y * s);
+        // (a code times a power of two is exact)
+        return kFmt == V4A_KV_FP8_GROUP ? two(times(x.x, s), times(x.y, s)) : two(times_to_odd(x.x, s, lost), times_to_odd(x.y, s, lost));
       };
       a = make_uint4(pair(w.x & 0xffffu), pair(w.x >> 16), pair(w.y & 0xffffu), pair(w.y >> 16));
       b = make_uint4(pair(w.z & 0xffffu), pair(w.z >> 16), pair(w.w & 0xffffu), pair(w.w >> 16));

@@ -244,8 +244,8 @@ V4A_API int v4a_dense_insert(const v4a_dense_insert_args* args, void* stream);
 V4A_API int v4a_dense_insert_rows(const v4a_dense_insert_args* args, uint16_t* k_out, int64_t k_out_stride, void* stream);
 
 /*
- * Cached rows as packed bf16 rows, each code times its scale rounded once
- * (V4A_KV_BF16 and V4A_KV_FP8_GROUP: exactly, above 2^-126).  Row r with
+ * Cached rows as packed bf16 rows, each code times its scale rounded once (above
+ * 2^-126; V4A_KV_BF16 rows and V4A_KV_FP8_GROUP products exactly).  Row r with
  * row_starts[b] <= r < row_starts[b + 1] receives sequence b's position
  * first[b] + r - row_starts[b].  A row whose block is unallocated or out of
  * range (V4A_DEV_BAD_BLOCK) or whose position is negative or past max_blocks

@@ -106,3 +106,34 @@ def test_codes_of_the_least_values(dim, top):
     rows = F.bf16_decode(x.cpu().view(torch.int16).numpy().view(np.uint16))
     OG.insert(want, 1, dim, slots, (rows, rows[::-1]))
     _same_cache(pool, want, 1, dim)
+
+
+def test_read_rounds_a_row_scaled_product_once():
+    """Products of a code and a scale that lie beside a tie of bf16, nearer to it than fp32 resolves: rounded to fp32 first, half
+    of them would go to the even neighbour from the wrong side."""
+    D = _dense()
+    K, dim = 1, 64
+    # 1.875 = 15 / 8: with s = S / 2^23, 15 S is beside a tie of bf16, T = (2 i + 1) 2^19 for a product in [2^27, 2^28)
+    ties = (2 * torch.arange(128, 256, dtype=torch.int64) + 1) * (1 << 19)
+    scales = torch.round(ties.double() / 15).long()
+    scales = scales[scales < 1 << 24]
+    # scales of nine bits: with codes that are powers of two the product is a tie
+    scales = torch.cat([scales, (2 * torch.arange(128, 256, dtype=torch.int64) + 1) << 15])
+    assert 200 < len(scales) <= 256
+    pool = torch.zeros((1, D.block_bytes(K, dim, D.KV_FP8_TOKEN)), dtype=torch.uint8)
+    codes = torch.tensor([1.875, -1.875, 240.0, -30.0, 0.0, -0.0, 448.0, 2.0 ** -9] * 8).to(torch.float8_e4m3fn).view(torch.uint8)
+    n = len(scales)
+    pool[0, :2 * 256 * dim].view(512, dim)[:] = codes
+    for which in (0, 1):           # (the same mantissas at two sizes)
+        at = 2 * 256 * dim + which * 1024
+        pool[0, at:at + 4 * n] = (scales.double() * 2.0 ** (-30 + 40 * which)).float().view(torch.uint8)
+    k, v = (torch.empty((n, K, dim), dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    D.DenseRead(D.DenseCache(pool.to(DEV), torch.zeros((1, 1), **I32), K, dim, D.KV_FP8_TOKEN)).run(torch.tensor([0, n], **I32), k, v)
+    c = F.e4m3_decode(codes.numpy())
+    twice = 0
+    for which, got in ((0, k), (1, v)):
+        product = c[None] * (scales.double().numpy() * 2.0 ** (-30 + 40 * which))[:, None]        # exact: 28 bits
+        want = F.bf16_encode(product)
+        twice += int((F.bf16_encode(product.astype(np.float32)) != want).sum())
+        assert np.array_equal(got[:, 0].cpu().view(torch.int16).numpy().view(np.uint16), want)
+    assert twice > 100             # the inputs do tell one rounding from two
