@@ -347,7 +347,7 @@ __global__ void __launch_bounds__(Shape<D, NT, kFmt>::kThreads, Shape<D, NT, kFm
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) fz[nt][e] = kGroup ? fmaxf(fq[nt][e] * scale[0], 0x1p-126f) : fq[nt][e];
+        for (int e = 0; e < 2; ++e) fz[nt][e] = kGroup ? logit_factor(fq[nt][e] * scale[0]) : fq[nt][e];
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
         if constexpr (kGroup) {

@@ -82,6 +82,14 @@ __device__ __forceinline__ TileRange<kTile> tile_range(const DenseAttnDev& a, in
   return r;
 }
 
+// A positive factor of logits, at least the smallest normal number (flushed to zero, it would make NaNs of hidden keys'
+// -inf); a NaN stays one.
+__device__ __forceinline__ float logit_factor(float f) {
+  float r;
+  asm("max.NaN.f32 %0, %1, 0f00800000;" : "=f"(r) : "f"(f));
+  return r;
+}
+
 // Whether a row at position m sees position j.
 __device__ __forceinline__ bool visible(const DenseAttnDev& a, int m, int j) {
   return j <= m && (a.window == 0 || j > m - a.window || j < a.sinks);

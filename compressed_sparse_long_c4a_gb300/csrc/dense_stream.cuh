@@ -344,7 +344,7 @@ __device__ __forceinline__ void stream_attn(const typename Src::Dev& a, const Sp
           inv_v[h] = 1.f;
           if constexpr (kScaled) {
             const float4 sc = *reinterpret_cast<const float4*>(s.scales[n & 7][h]);
-            fk[h] = fmaxf(f * sc.x, 0x1p-126f);        // (flushed to zero, it would make NaNs of hidden keys' -inf)
+            fk[h] = logit_factor(f * sc.x);
             lv[h] = sc.y;
             inv_v[h] = sc.z;
           }

@@ -137,3 +137,41 @@ def test_read_rounds_a_row_scaled_product_once():
         twice += int((F.bf16_encode(product.astype(np.float32)) != want).sum())
         assert np.array_equal(got[:, 0].cpu().view(torch.int16).numpy().view(np.uint16), want)
     assert twice > 100             # the inputs do tell one rounding from two
+
+
+@pytest.mark.parametrize("dim", [64, 128, 192, 256])
+@pytest.mark.parametrize("new", [1, 60])
+def test_nan_scale_is_not_made_finite(dim, new):
+    """A group whose key (or value) scale is NaN gives NaN to the queries that see it, and nothing to other sequences."""
+    D = _dense()
+    g = torch.Generator().manual_seed(dim)
+    n, K = 500, 2
+    x = torch.randn((2 * n, 2 * K, dim), generator=g).to(torch.bfloat16).to(DEV)
+    pool = torch.zeros((4, OG.block_bytes(K, dim)), dtype=torch.uint8, device=DEV)
+    cache = D.DenseCache(pool, torch.tensor([[0, 2], [1, 3]], **I32), K, dim, D.KV_FP8_GROUP)
+    pos = torch.arange(n, **I32).repeat(2)
+    slots = (cache.block_table.long()[torch.arange(2, device=DEV).repeat_interleave(n), pos.long() // 256] * 256 + pos % 256)
+    D.DenseInsert(cache, 0, None).run(None, x[:, :K].contiguous(), x[:, K:].contiguous(), None, pos, slots,
+                                      k_out=torch.empty((2 * n, K, dim), dtype=torch.bfloat16, device=DEV))
+    q = torch.randn((2 * new, 4, dim), generator=g).to(torch.bfloat16).to(DEV)
+    at = torch.cat([torch.arange(n - new, n, **I32)] * 2)
+    op = D.DenseAttention(cache, 4, 2 * new, new)
+
+    def run():
+        out, lse = torch.empty_like(q), torch.empty((2 * new, 4), device=DEV)
+        op.run(q, out, at, torch.tensor([0, new, 2 * new], **I32), lse)
+        torch.cuda.synchronize()
+        return out, lse
+    want, want_l = run()
+    assert bool(want.isfinite().all())
+    body = 2 * K * 256 * dim
+    scales = pool[:, body:body + 32 * K].view(torch.float32).view(4, 2, K, 4)      # [block][key, value][head][group]
+    for which in (0, 1):
+        old = float(scales[0, which, 1, 3])
+        scales[0, which, 1, 3] = math.nan          # positions 192..255 of the first sequence, KV head 1
+        out, lse = run()
+        assert bool(out[:new, 2:].isnan().all()) and (which == 1 or bool(lse[:new, 2:].isnan().all()))      # (lse is of the keys alone)
+        assert torch.equal(out[:new, :2], want[:new, :2]) and torch.equal(out[new:], want[new:])
+        assert torch.equal(lse[:new, :2], want_l[:new, :2]) and torch.equal(lse[new:], want_l[new:])
+        scales[0, which, 1, 3] = old
+    assert torch.equal(run()[0], want)
