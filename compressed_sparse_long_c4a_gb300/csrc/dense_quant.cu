@@ -266,8 +266,12 @@ __global__ void __launch_bounds__(kReadThreads) dense_read_kernel(const __grid_c
 int dense_quant(const v4a_dense_insert_args& a, const uint16_t* k_out, int64_t k_out_stride, int64_t block_bytes, cudaStream_t stream) {
   QuantDev d{};
   d.T = a.num_tokens; d.K = a.kv.num_kv_heads;
-  // few tokens: most are alone in their group, and a CTA each takes them side by side
-  d.tokens = a.num_tokens <= 1024 ? 1 : 8;
+  // A CTA takes its tokens' groups one after the other, which suits prompts, where most tokens begin none, and not steps
+  // of single tokens, where all do; the host cannot tell them apart.  The insert's two launches with 1, 2 and 8 tokens a
+  // CTA, us, 64 + 8 + 8 heads of 128: single tokens, 512 25, 29, 33; 1025 44, 46, 54; 2048 86, 87, 108; 4096 171, 171, 185;
+  // one prompt, 600 tokens 11.7, 11.3, 9.9; 1025 16, 15, 14; 2000 27, 24, 24; 4097 51, 45, 43.  Single tokens of 8 + 1 + 1
+  // heads of 64, 1024 8, 9, 26; 4096 19, 19, 28.
+  d.tokens = a.num_tokens <= 1024 ? 1 : a.num_tokens <= 4096 ? 2 : 8;
   // CTAs without a first token cost their start: with many, each looks once for four planes (of the insert's two
   // launches, 1, 2, 4, 8 and 16 planes: 16384 tokens, 8 heads of 128, 199, 171, 158, 156 and 169 us; 4097 tokens of 64
   // dims 42, 37, 36, 38 and 44; 4, 16, 32 or 64 tokens a CTA are no better)

@@ -175,3 +175,26 @@ def test_nan_scale_is_not_made_finite(dim, new):
         assert torch.equal(lse[:new, :2], want_l[:new, :2]) and torch.equal(lse[new:], want_l[new:])
         scales[0, which, 1, 3] = old
     assert torch.equal(run()[0], want)
+
+
+@pytest.mark.parametrize("T,single", [(1025, True), (4097, True), (1025, False), (4096, False), (4097, False)])
+@pytest.mark.parametrize("dim,K", [(64, 1), (128, 3)])
+def test_insert_around_the_sizes_of_its_forms(dim, K, T, single):
+    """Steps of single tokens, each in a group of its own, and one prompt: how many tokens a CTA takes changes nothing."""
+    D = _dense()
+    g = torch.Generator().manual_seed(T)
+    blocks = T if single else T // 256 + 2
+    slots = (torch.randperm(T, generator=g) * 256 + torch.randint(0, 256, (T,), generator=g)).tolist() if single else list(range(37, 37 + T))
+    body = 2 * K * 256 * dim
+    pool = torch.zeros((blocks, OG.block_bytes(K, dim)), dtype=torch.uint8, device=DEV)
+    pool[:, body:] = torch.exp2(torch.randint(-10, -5, (blocks, 8 * K), generator=g).float()).view(torch.uint8).to(DEV)
+    x = (torch.randn((T, 2 * K, dim), generator=g) * 2).to(torch.bfloat16).to(DEV)
+    want = pool.cpu().numpy().copy()
+    op = D.DenseInsert(D.DenseCache(pool, None, K, dim, D.KV_FP8_GROUP), 0, None)
+    k_out = torch.empty((T, K, dim), dtype=torch.bfloat16, device=DEV)
+    op.run(None, x[:, :K], x[:, K:], None, torch.zeros(T, **I32), torch.tensor(slots, device=DEV), k_out=k_out)
+    assert int(op.status.item()) == 0
+    some = [*range(0, T, 13), T - 1] if single else range(T)
+    OG.insert(want, K, dim, [slots[t] for t in some], (_f64(x[some, :K]), _f64(x[some, K:])))
+    at = sorted({slots[t] // 256 for t in some})
+    _same_cache(pool[at], want[at], K, dim)
