@@ -47,7 +47,7 @@ struct InsertDev {
   const int32_t* positions;
   const int64_t* slots;
   const uint16_t *q, *k, *v;
-  uint16_t *q_out, *k_out;         // k_out: the keys as packed rows, or nullptr
+  uint16_t *q_out, *k_out;         // k_out: the keys as packed rows (kPacked)
   int64_t qs, qos, ks, vs, kos;
   const float *qg, *kg;
   uint8_t* pool;
@@ -67,10 +67,12 @@ __device__ __forceinline__ uint2 pack4(const float* x) {
 }
 
 // kLanes: lanes of one row (dim / 8, or 32 with the last eight idle at dim 192).
-// kMode: what the cache gets, bf16 rows, fp8 rows with a scale each, or nothing (keys go to k_out alone, values are not read).
+// kMode: what the cache gets, bf16 rows, fp8 rows with a scale each, or nothing (values are not read).
+// kPacked: the keys go to k_out too (a test of the pointer cost calls without it 4 to 6%: 16384 tokens of 64 + 8 + 8 heads,
+// bf16 128 us against 123, fp8 156 against 147).
 // kShare: several tokens of few rows in a CTA (the division costs the others 5%: 121 us against 127).
 enum { kBf16, kFp8Rows, kRowsOnly };
-template <int kLanes, int kMode, bool kShare>
+template <int kLanes, int kMode, bool kPacked, bool kShare>
 __global__ void __launch_bounds__(kThreads, 8) dense_insert_kernel(const __grid_constant__ InsertDev p) {
   constexpr bool kFp8 = kMode == kFp8Rows;
   constexpr int kRows = kThreads / kLanes;      // rows per pass
@@ -178,7 +180,7 @@ __global__ void __launch_bounds__(kThreads, 8) dense_insert_kernel(const __grid_
         for (int e = 0; e < 4; ++e) turn(x[2 * e], x[2 * e + 1], co[e], sn[e]);
       }
     }
-    if (p.k_out && !is_q && !is_v && live) {
+    if (kPacked && !is_q && !is_v && live) {
       uint16_t* dst = p.k_out + int64_t(t) * p.kos + (r - p.H) * D;
       *reinterpret_cast<uint2*>(dst + d0) = pack4(x);
       *reinterpret_cast<uint2*>(dst + d1) = pack4(x + 4);
@@ -311,15 +313,19 @@ int dense_insert(const v4a_dense_insert_args* a, bool with_rows, uint16_t* k_out
   d.tokens = a->num_tokens;
   auto passes = [&](int share) { return (d.NR + (rows >> share) - 1) / (rows >> share); };
   while (y == 1 && d.share < 2 && passes(d.share + 1) <= kPasses && a->num_tokens >> (d.share + 1) >= 152 * 8) d.passes = passes(++d.share);
-  auto pick = [&](auto mode, auto share) {
+  auto pick = [&](auto mode, auto packed, auto share) {
     constexpr int kMode = decltype(mode)::value;
-    constexpr bool kShare = decltype(share)::value;
-    return lanes == 8 ? dense_insert_kernel<8, kMode, kShare> : lanes == 16 ? dense_insert_kernel<16, kMode, kShare> : dense_insert_kernel<32, kMode, kShare>;
+    constexpr bool kPacked = decltype(packed)::value, kShare = decltype(share)::value;
+    return lanes == 8    ? dense_insert_kernel<8, kMode, kPacked, kShare>
+           : lanes == 16 ? dense_insert_kernel<16, kMode, kPacked, kShare>
+                         : dense_insert_kernel<32, kMode, kPacked, kShare>;
   };
   auto pick_mode = [&](auto share) {
-    return group ? pick(std::integral_constant<int, kRowsOnly>{}, share)
-           : a->kv.format == V4A_KV_FP8_TOKEN ? pick(std::integral_constant<int, kFp8Rows>{}, share)
-                                              : pick(std::integral_constant<int, kBf16>{}, share);
+    const std::integral_constant<int, kBf16> bf16;
+    const std::integral_constant<int, kFp8Rows> fp8;
+    if (group) return pick(std::integral_constant<int, kRowsOnly>{}, std::true_type{}, share);
+    if (a->kv.format == V4A_KV_FP8_TOKEN) return with_rows ? pick(fp8, std::true_type{}, share) : pick(fp8, std::false_type{}, share);
+    return with_rows ? pick(bf16, std::true_type{}, share) : pick(bf16, std::false_type{}, share);
   };
   auto kern = d.share ? pick_mode(std::true_type{}) : pick_mode(std::false_type{});
   const cudaError_t e = launch_pdl(kern, dim3(unsigned(a->num_tokens + (int64_t(1) << d.share) - 1) >> d.share, y), dim3(kThreads), 0, stream, d);
