@@ -53,7 +53,7 @@ __device__ __forceinline__ float2 e4m3x2_values(uint32_t codes) {
 
 struct GroupCache {
   using Dev = GroupDev;
-  static constexpr bool kScaled = true, kPaged = true, kShortUnits = false;
+  static constexpr bool kScaled = true, kPaged = true;
   static constexpr int kLead = 2;                  // steps that copies are issued ahead
   template <int D> static constexpr int copiers() { return D == 192 ? 96 : D == 256 ? 128 : 64; }
   template <int D> static constexpr int key_stages() { return 3; }

@@ -449,16 +449,13 @@ __device__ __forceinline__ void stream_attn(const typename Src::Dev& a, const Sp
         const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;
         const int64_t at = row_of(a, un, sg.hk, min(row, un.rows - 1));
         const int64_t slot = int64_t(blockIdx.x) * 2 + (begins ? 1 : 0), part = slot * W::kUnit + row;
-        // A lane has a row; where units are short, four lanes exchange their rows' 16-byte pieces, so that a store covers
-        // 64 bytes of each of eight rows instead of 16 of each of 32 (32 prompts of 300 to 700 tokens 143 us instead of 160;
-        // chunks over a long cache gain nothing, and the compiler's registers for dim 64 lose: 1520 us for 1320).
-        int64_t to[4] = {at * D, 0, 0, 0};
-        int live = un.rows - row;                      // of the four rows (or of the one)
-        if constexpr (Src::kShortUnits) {
-          live = un.rows - (row & ~3);
+        // A lane has a row; four lanes exchange their rows' 16-byte pieces, so that a store covers 64 bytes of each of
+        // eight rows instead of 16 of each of 32 (32 prompts of 300 to 700 tokens 111 us instead of 135; chunks of 4096
+        // tokens over 28672, heads of 64, 1157 instead of 1208, of 128 1558 and 1565).
+        int64_t to[4];
+        const int live = un.rows - (row & ~3);         // of the four rows
 #pragma unroll
-          for (int k = 0; k < 4; ++k) to[k] = __shfl_sync(0xffffffffu, at, (lane & ~3) + k) * D + (lane & 3) * 8;
-        }
+        for (int k = 0; k < 4; ++k) to[k] = __shfl_sync(0xffffffffu, at, (lane & ~3) + k) * D + (lane & 3) * 8;
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
           float o[32];
@@ -473,13 +470,11 @@ __device__ __forceinline__ void stream_attn(const typename Src::Dev& a, const Sp
             for (int k = 0; k < 4; ++k)
               v[k] = make_uint4(pack_bf16(o[8 * k] * inv, o[8 * k + 1] * inv), pack_bf16(o[8 * k + 2] * inv, o[8 * k + 3] * inv),
                                 pack_bf16(o[8 * k + 4] * inv, o[8 * k + 5] * inv), pack_bf16(o[8 * k + 6] * inv, o[8 * k + 7] * inv));
-            if constexpr (Src::kShortUnits) {
-              exchange<1>(v, lane);
-              exchange<2>(v, lane);
-            }
+            exchange<1>(v, lane);
+            exchange<2>(v, lane);
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              if ((Src::kShortUnits ? k : 0) < live) *reinterpret_cast<uint4*>(a.out + (Src::kShortUnits ? to[k] : to[0] + 8 * k) + c) = v[k];
+              if (k < live) *reinterpret_cast<uint4*>(a.out + to[k] + c) = v[k];
           } else if (row < un.rows) {
 #pragma unroll
             for (int k = 0; k < 32; k += 4)      // [slot][dim / 4][row][4]: a warp's rows side by side

@@ -66,7 +66,7 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, i
 
 struct PackedRows {
   using Dev = PromptDev;
-  static constexpr bool kScaled = false, kPaged = false, kShortUnits = true;
+  static constexpr bool kScaled = false, kPaged = false;
   template <int D> static constexpr int copiers() { return 64; }       // a warp for the keys, one for the values
   template <int D> static constexpr int key_stages() { return D == 64 ? 4 : D == 192 ? 3 : 2; }
   template <int D> static constexpr int value_stages() { return key_stages<D>(); }
