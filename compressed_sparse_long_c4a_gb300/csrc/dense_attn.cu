@@ -27,9 +27,9 @@
 // has just read.  Pieces of a unit that several CTAs hold go to the workspace
 // and are joined by a second kernel in CTA order.
 //
-// A cache with a scale per group has one pair of scales a tile: 4 sequences at 1M, 16 +
-// 2 heads of 128, 350 us (6.1 TB/s; a scale per row 360), 32 at 32k to 64k, 64 + 8
-// heads, 469 us (6.4 TB/s; 526).
+// A cache with a scale per group has one pair of scales a tile, which lies within a
+// group: 4 sequences at 1M, 16 + 2 heads of 128, 320 to 327 us (a scale per row 332), 32
+// at 32k to 64k, 64 + 8 heads, 439 to 448 us: 6.6 to 6.8 TB/s, a copy's rate.
 //
 // bf16 caches: P is taken as the sum of two bf16 operands (16 bits), since the
 // tensor cores have the time; fp8 caches: P in f16, with the values' scales in

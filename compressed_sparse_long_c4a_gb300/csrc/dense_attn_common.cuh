@@ -30,12 +30,13 @@ struct DenseAttnDev {
 // at 8k: 32 rows 22 / 32, 64 rows 28 / 32; 16 at 1k (dim 64): 24 / 26 and
 // 35 / 26; fp8, 8 at 8k: 32 rows 63 / 130, 64 rows 111 / 131, 128 rows 203 / 132;
 // dim 256, 8 at 8k: bf16 16 rows 163 / 107, 32 rows 311 / 107, one at 8k 16 rows
-// 24 / 33; fp8 32 rows 186 / 187, 64 rows 355 / 186.  The limits are those of
+// 24 / 33; fp8 32 rows 186 / 187, 64 rows 355 / 186.  These limits are those of
 // one sequence, where the second pass costs nothing; with more sequences 9 to
-// 16 rows of dim 256 (bf16) would be faster in the form for many.  Group-scaled fp8
-// (its form for many does not convert keys): 8 at 8k: 32 rows 68 / 82, 64 rows 117 /
-// 82; one at 8k: 64 rows 33 / 41, 128 rows 45 / 43; dim 256, 8 at 8k: 16 rows 70 / 70,
-// 32 rows 111 / 72, one at 8k 32 rows 31 / 43.
+// 16 rows of dim 256 (bf16) would be faster in the form for many.  The limits of
+// group-scaled fp8 (its form for many does not convert keys) are those of several
+// sequences: 8 at 8k: 32 rows 68 / 82, 64 rows 117 / 82; dim 256: 16 rows 70 / 70, 32
+// rows 111 / 72.  One sequence alone would gain from twice as many: at 8k 64 rows 33 /
+// 41, 128 rows 45 / 43; dim 256, 32 rows 31 / 43.
 constexpr int few_rows(int dim, int format) { return (dim == 256 ? 8 : 16) * (format == V4A_KV_FP8_TOKEN ? 4 : 2); }
 
 // One sequence's tokens of the call: first row, count and first position;

@@ -23,10 +23,11 @@
 // Bound: as prompts (dense_stream.cuh); the conversions share the softmax's
 // schedulers (as integer operations instead of cvt: 2362 us for 1605; four warps of
 // them among 512 threads: 1708), and the second e4m3 of the query takes 3% of the
-// time.  Measured, 32 + 8 heads of 128: 4096 tokens over 28672 1612 us (1279 TFLOP/s;
-// ncu, 2048 over 8192: tensor pipe 46% busy), 1000 over 4000 94 us, 4096 over none 168; 16 + 4 heads of 256,
-// 2048 over 10240 367 us (1031; row scales 505), of 192 325 us (872); heads of 64 over
-// 28672 1249 us (825).
+// time.  Measured, 32 + 8 heads of 128: 4096 tokens over 28672 1568 us (1314 TFLOP/s;
+// ncu, 2048 over 8192: tensor pipe 47% busy), 1000 over 4000 92 us, 4096 over none 168 (both
+// with a table no wider than the sequence: stream_plan); 16 + 4 heads of 256,
+// 2048 over 10240 367 us (1030; row scales 505), of 192 330 us (860); heads of 64 over
+// 28672 1157 us (891).
 #include "dense_stream.cuh"
 
 namespace v4a {
@@ -339,10 +340,14 @@ size_t stream_workspace(int dim) { return split_workspace(stream_unit(dim), dim,
 
 // Whole units are dealt out unless an even split of the steps should take less time: that has no idle CTAs, but cut units
 // leave pieces to be joined, which costs the time of about 11 steps of 128 keys, and its CTAs walk several sequences'
-// keys at different places.  Even split / dealt out, us, 32 + 8 heads of 128: prompts of 16384 tokens 1450 / 1325, 2048
-// 57 / 39, 4 + 1 heads 8192 74 / 107, 4096 41 / 57, 16384 197 / 201; 4 of 1500 to 2500 143 / 98; a window of 1024 over
-// 16384 293 / 225; group caches, 4096 tokens over 28672 1642 / 1798, over none 279 / 172, 1000 over 4000 115 / 94, 4
-// sequences of 1000 over 8000 561 / 565, of 500 to 2000 over up to 8000 392 / 323, 16 of 256 over 1000 to 30000 1008 / 840.
+// keys at different places.  Even split / dealt out, us, 32 + 8 heads of 128: prompts of 16384 tokens 1348 / 1276, 2048
+// 57 / 37, 4 + 1 heads 8192 74 / 104, 4096 41 / 57, 16384 195 / 195; 4 of 1500 to 2500 139 / 96; a window of 1024 over
+// 16384 276 / 217; group caches, 4096 tokens over 28672 1565 / 1806, over none 277 / 168, 2048 over 2000 156 / 125, 1000
+// over 4000 111 / 94, 4 sequences of 1000 over 8000 533 / 557, of 500 to 2000 over up to 8000 378 / 314, 16 of 256 over
+// 1000 to 30000 963 / 846.
+// `keys` of a paged cache is the width of its block table, the only bound on the lengths that the host has.  Where the
+// table is far wider than its sequences they look long, and chunks that would gain from being dealt out are split evenly:
+// with a table of 8192 positions or more the chunks over none, 2000 and 4000 above take the first of the two times.
 int stream_plan(const DenseAttnDev& d, int dim, int rows_from, int64_t keys, bool causal, void* ws, SplitDev* out) {
   const int unit = stream_unit(dim);
   SplitDev p{};

@@ -17,9 +17,9 @@
 // and the fp8 row maximum are shuffles inside the row's lanes.  A CTA takes one
 // token (or part of its rows when tokens are few): its angles are computed once
 // and shared by all its heads, and all its loads are issued before the first use.
-// Measured, 64 + 8 + 8 heads of 128: 16384 tokens, bf16 120 us (671 MB: 5.6
-// TB/s of the 6.8 that a copy reaches), fp8 143 us (the row maxima and the
-// codes); one token 2.1 us.
+// Measured, 64 + 8 + 8 heads of 128, one call behind the other: 16384 tokens, bf16
+// 123 us (671 MB: 5.5 TB/s of the 6.7 that a copy reaches), fp8 147 us (the row
+// maxima and the codes); one token 2.9 us.  With packed keys 129 and 152 us.
 //
 // A cache with a scale per group takes two launches (v4a_dense_insert_rows): this
 // kernel for queries and keys as rows, then dense_quant.cu for the codes, which

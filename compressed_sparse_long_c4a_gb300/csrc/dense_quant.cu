@@ -11,11 +11,12 @@
 //
 // Bound: memory.  The rows of a group (64 x dim bf16, 16 KB at dim 128) lie in a
 // CTA's registers between the maximum and the codes, so they are read once.
-// Measured: the insert's two launches, 16384 tokens of 64 + 8 + 8 heads of 128 158 us
-// (the first alone 127, this one 40; a CTA waits for its rows and then for the
-// maximum, and loading the next plane ahead took 164), 4097 tokens of 64 dims 36 us, 64
-// tokens 10.8; the read back of 133 thousand positions of 8 heads of 128 135 us (6.0 TB/s
-// of the 6.7 that a copy reaches).
+// Measured: the insert's two launches, 16384 tokens of 64 + 8 + 8 heads of 128 150 us
+// (ncu, half of the tokens, each alone: 61 and 25; a CTA waits for its rows and then
+// for the maximum, and loading the next plane ahead was slower), 4097 tokens of 64
+// dims 27 us, 64 tokens of 16 + 4 + 4 heads 6 (one call behind the other; alone and from cold
+// caches 154, 35 and 10.9); the read back of 133 thousand positions of 8 heads of 128
+// 133 us (6.1 TB/s of the 6.7 that a copy reaches), of row-scaled ones 136.
 #include <algorithm>
 
 #include "tc_common.cuh"
@@ -272,9 +273,9 @@ int dense_quant(const v4a_dense_insert_args& a, const uint16_t* k_out, int64_t k
   // one prompt, 600 tokens 11.7, 11.3, 9.9; 1025 16, 15, 14; 2000 27, 24, 24; 4097 51, 45, 43.  Single tokens of 8 + 1 + 1
   // heads of 64, 1024 8, 9, 26; 4096 19, 19, 28.
   d.tokens = a.num_tokens <= 1024 ? 1 : a.num_tokens <= 4096 ? 2 : 8;
-  // CTAs without a first token cost their start: with many, each looks once for four planes (of the insert's two
-  // launches, 1, 2, 4, 8 and 16 planes: 16384 tokens, 8 heads of 128, 199, 171, 158, 156 and 169 us; 4097 tokens of 64
-  // dims 42, 37, 36, 38 and 44; 4, 16, 32 or 64 tokens a CTA are no better)
+  // CTAs without a first token cost their start: with many, each looks once for four planes (the insert's two
+  // launches from cold caches, 1, 2, 4, 8 and 16 planes: 16384 tokens, 8 heads of 128, 197, 167, 154, 152 and 165 us; 4097
+  // tokens of 64 dims 42, 36, 36, 38 and 44)
   const int64_t blocks = (int64_t(d.T) + d.tokens - 1) / d.tokens;
   d.planes = blocks * 2 * d.K >= 16 * 152 ? 4 : 1;
   d.positions = a.positions; d.slots = a.slots;

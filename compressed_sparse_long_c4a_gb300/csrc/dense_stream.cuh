@@ -27,11 +27,11 @@
 // 520 for its scores' load and maximum of the first 64 keys and as much for the
 // rest, 400 for the exponentials of each half, 300 until the issuer has seen P, 700
 // to issue the products and 330 until the next scores are there.  Measured and not
-// kept: scores in two buffers of 64 columns at dim 128 (1722 us for a prompt of
-// 16384 tokens, 32 + 8 heads, instead of 1373) and 64 (the same), an issuing warp per
-// tile (1994 for 1688), polling without suspension (1745 for 1665), the exponentials
-// beside the search for the maximum (1436 for 1341), the second half's load beside the
-// first's maximum (1413).
+// kept: against the form of its time, for a prompt of 16384 tokens, 32 + 8 heads: scores
+// in two buffers of 64 columns at dim 128 (1722 us for 1373) and 64 (the same), an
+// issuing warp per tile (1994 for 1688), polling without suspension (1745 for 1665), the
+// exponentials beside the search for the maximum (1436 for 1341), the second half's load
+// beside the first's maximum (1413 for 1341).
 //
 // What differs is in the source, a class: the arguments, the operands of the
 // scores (scores), the queries' way into shared memory (load_q, or Feed's), what
@@ -64,7 +64,7 @@ struct Stream {
 constexpr int kStreamLaunchRegs = 168, kStreamSoftmaxRegs = 200, kStreamRestRegs = 104;
 static_assert(kStreamSoftmaxRegs * 256 + kStreamRestRegs * 128 == kStreamLaunchRegs * 384, "the split of the registers");
 // P in bf16 has fp32's range, so its maximum may lag far behind: the first keys of a window, few for some rows, would have
-// most rows raised at the next step (8 prompts of 1000 to 4096 tokens, window 1024: 2^8 614 us, 2^24 584).  The maximum in
+// most rows raised at the next step (8 prompts of 1000 to 4096 tokens, window 1024: 2^8 608 us, 2^24 575).  The maximum in
 // use is set that far above the largest logit, so that no weight passes one and the accumulator stays below the sum of the
 // values' sizes, as with a maximum that does not lag; what it loses are elements of an output below 2^-102, which it may
 // hold as less than 2^-126.

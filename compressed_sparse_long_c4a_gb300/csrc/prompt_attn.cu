@@ -6,13 +6,14 @@
 // its sequence: its rows behind the last are zeros, so that the next
 // sequence's cannot reach a product, and are copied by the warp.
 //
-// Bound: 4 dim flops per visible pair on the tensor cores, which are 62% busy (ncu,
-// 4096 tokens; XU pipe 29%, DRAM 7%): dense_stream.cuh says what the rest is.
-// Measured, 32 + 8 heads of 128: 16384 tokens 1303 us (1688 TFLOP/s), 4096 104 us
-// (1316), 16 prompts of 1000 to 3000 453 (1322), 64 of 1 to 256 (16 + 4 heads) 37 us; 16 +
-// 4 heads of 256, 8192 tokens 412 us (1336), of 192 324 (1274); heads of 64, 16384 tokens
-// 1161 us (947: half of the flops for the same softmax); 8 prompts of 1000 to 4096, 64 + 8
-// heads of 64, window 1024 584 us (650, of which masks take about 40 us).
+// Bound: 4 dim flops per visible pair on the tensor cores, which are 63% busy (ncu,
+// 4096 tokens; XU pipe 32%, DRAM 7%): dense_stream.cuh says what the rest is.
+// Measured alone (calls one behind the other heat the GPU: the longest takes 1413 us
+// then, 1556 TFLOP/s), 32 + 8 heads of 128: 16384 tokens 1292 us (1702 TFLOP/s), 4096 104
+// us (1316), 16 prompts of 1000 to 3000 447 (1340), 64 of 1 to 256 (16 + 4 heads) 37 us; 16 +
+// 4 heads of 256, 8192 tokens 412 us (1336), of 192 326 (1266); heads of 64, 16384 tokens
+// 1141 us (964: half of the flops for the same softmax); 8 prompts of 1000 to 4096, 64 + 8
+// heads of 64, window 1024 575 us (660, of which masks take about 40 us).
 #include "dense_stream.cuh"
 
 namespace v4a {

@@ -364,6 +364,8 @@ class DenseAttention(_Op):
     max_new_per_seq: the most tokens one sequence brings in a call.  A run of
     T >= sequences x max_new_per_seq tokens is taken as one where each brings
     that many, padded or not: shorter sequences then take the chunks' form.
+    Chunks over a KV_FP8_GROUP cache are divided as if sequences filled the
+    block table's columns: a table far wider than they are costs time.
     window: 0 for every earlier position, else the last `window` ones (own
     included) and the first `sinks`.  scale defaults to 1 / sqrt(dim).
     """

@@ -291,7 +291,10 @@ V4A_API int v4a_dense_read(const v4a_dense_read_args* args, void* stream);
  * Dot products and sums are fp32; the probabilities are rounded as an operand
  * of the tensor cores: to f16 for fp8 caches, to 16 bits for bf16 caches, and
  * to bf16 for the sequences of a bf16 cache that bring more than 32 rows
- * (tokens x heads per KV head; 16 of dim 256) and in the full calls below.
+ * (tokens x heads per KV head; 16 of dim 256) and in the full calls below.  The
+ * sum over the values precedes the division: over a bf16 cache it holds while the
+ * |value| of a row's visible keys sum up to less than 2^127 (2^119 for those
+ * sequences and calls).
  * fp8 value scales below 2^-100 are read as 2^-100; sums over up to 2^26
  * positions of such scales hold (2^13 over a V4A_KV_FP8_TOKEN cache for the
  * sequences of more than 64 rows, 32 of dim 256, and in the full calls).  Over a
@@ -309,7 +312,10 @@ V4A_API int v4a_dense_read(const v4a_dense_read_args* args, void* stream);
  * in a batch padded that far, sequences of few rows are attended to in the
  * form for chunks (probabilities in bf16 over bf16 caches, about twice the
  * time); a num_tokens below that, by one token of padding less for instance,
- * keeps each kind its own.  V4A_ERR_UNSUPPORTED: max_new_per_seq
+ * keeps each kind its own.  Over V4A_KV_FP8_GROUP caches chunks take
+ * kv.max_blocks for the sequences' length when their work is divided: with a
+ * table far wider than its sequences short ones take up to 1.7 times as long
+ * (results are the same but for the order of sums).  V4A_ERR_UNSUPPORTED: max_new_per_seq
  * * num_heads / num_kv_heads of 2^30 rows or more, V4A_KV_FP8_GROUP blocks of
  * 2^40 bytes or more.
  */
