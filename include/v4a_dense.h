@@ -297,11 +297,11 @@ V4A_API int v4a_dense_read(const v4a_dense_read_args* args, void* stream);
  * sequences and calls).
  * fp8 value scales below 2^-100 are read as 2^-100; sums over up to 2^26
  * positions of such scales hold (2^13 over a V4A_KV_FP8_TOKEN cache for the
- * sequences of more than 64 rows, 32 of dim 256, and in the full calls).  Over a
- * V4A_KV_FP8_GROUP cache the sequences of more than 32 rows (16 of dim 256), and
- * those of the full calls, take an element of a query to within 2^-17 of its
- * row's largest (exactly down to 2^-9 of that), and leave out keys whose exp(z_j)
- * times value scale is below 2^-137 of the largest one.
+ * sequences of more than 64 rows, 32 of dim 256, and in the full calls).  Keys of
+ * an fp8 cache whose exp(z_j) times value scale is below 2^-120 of the largest one
+ * may be left out, of lse too.  Over a V4A_KV_FP8_GROUP cache the sequences of more
+ * than 32 rows (16 of dim 256), and those of the full calls, take an element of a
+ * query to within 2^-17 of its row's largest (exactly down to 2^-9 of that).
  * Sequences that share tokens (entries not increasing)
  * set V4A_DEV_BAD_BATCH once they are more than the call has room for, and
  * what their rows hold then is not defined.
