@@ -299,7 +299,8 @@ V4A_API int v4a_dense_read(const v4a_dense_read_args* args, void* stream);
  * positions of such scales hold (2^13 over a V4A_KV_FP8_TOKEN cache for the
  * sequences of more than 64 rows, 32 of dim 256, and in the full calls).  Keys of
  * an fp8 cache whose exp(z_j) times value scale is below 2^-120 of the largest one
- * may be left out, of lse too.  Over a V4A_KV_FP8_GROUP cache the sequences of more
+ * may be left out, of lse too, and beside value scales above 2^96 (values past
+ * 2^104) more of them.  Over a V4A_KV_FP8_GROUP cache the sequences of more
  * than 32 rows (16 of dim 256), and those of the full calls, take an element of a
  * query to within 2^-17 of its row's largest (exactly down to 2^-9 of that).
  * Sequences that share tokens (entries not increasing)

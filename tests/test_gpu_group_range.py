@@ -11,7 +11,8 @@ import torch
 
 from oracle import dense_group as OG
 from oracle import formats as F
-from tests.test_gpu_group import DEV, I32, _check_prompt, _check_token, _dense, _f64, _prompt, _run_prompt, _same_cache
+from tests.test_gpu_dense import _attend, _runs
+from tests.test_gpu_group import DEV, I32, GroupLayer, _check_prompt, _check_token, _dense, _f64, _prompt, _run_prompt, _same_cache
 
 pytestmark = pytest.mark.gpu
 
@@ -198,3 +199,13 @@ def test_insert_around_the_sizes_of_its_forms(dim, K, T, single):
     OG.insert(want, K, dim, [slots[t] for t in some], (_f64(x[some, :K]), _f64(x[some, K:])))
     at = sorted({slots[t] // 256 for t in some})
     _same_cache(pool[at], want[at], K, dim)
+
+
+@pytest.mark.parametrize("new", [1, 90])
+@pytest.mark.parametrize("dim", [64, 128, 192, 256])
+@pytest.mark.parametrize("exponents,q_std", [((86, 95), 2.0 ** -96), ((-99, -92), 2.0 ** 88)])
+def test_scales_far_from_one(exponents, q_std, dim, new):
+    """Keys and values of sizes up to 2^104 and down to 2^-108, under queries that bring the logits back to ordinary ones."""
+    pos, starts = _runs((900 - new, 400 - new), (new, new))
+    layer = GroupLayer((900, 400), 8, 2, dim, seed=5, exponents=exponents, q_std=q_std)
+    _attend(layer, pos, starts, tokens={0, new // 2, new - 1, new, 2 * new - 1})
